@@ -72,6 +72,14 @@ class PagedCfg(ctypes.Structure):
     _fields_ = [("B", _i32), ("n_new", _i32), ("block_size", _i32), ("max_blocks", _i32), ("n_blocks", _i32)]
 
 
+class RaggedCfg(ctypes.Structure):
+    _fields_ = [("B", _i32), ("T", _i32), ("block_size", _i32), ("max_blocks", _i32), ("n_blocks", _i32)]
+
+
+class VerifyCfg(ctypes.Structure):
+    _fields_ = [("B", _i32), ("T", _i32), ("V", _i32), ("dtype", _i32)]
+
+
 class StreamResult(ctypes.Structure):
     _fields_ = [("loss", _f32), ("total_norm", _f32), ("clip_coef", _f32)]
 
@@ -122,6 +130,15 @@ _SIGNATURES = {
     "kl_layer_forward_paged_ws_bytes": (_sz, [_P(LayerCfg), _P(PagedCfg)]),
     "kl_layer_forward_paged": (ctypes.c_int, [_P(LayerCfg), _P(PagedCfg), _P(LayerWeights), _vp, _vp, _vp, _vp,
                                               _vp, _vp, _vp, _sz, _vp]),
+    "kl_ragged_plan": (ctypes.c_int, [_P(RaggedCfg)] + [_vp] * 11),
+    "kl_ragged_qkv_rope": (ctypes.c_int, [_P(RaggedCfg), _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _f32, _f32,
+                                          _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "kl_ragged_attention_ws_bytes": (_sz, [_P(RaggedCfg), _i32, _i32, _i32]),
+    "kl_ragged_attention": (ctypes.c_int, [_P(RaggedCfg), _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                           _vp, _vp, _sz, _vp]),
+    "kl_draft_verify": (ctypes.c_int, [_P(VerifyCfg), _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "kl_layer_forward_ragged_ws_bytes": (_sz, [_P(LayerCfg), _P(RaggedCfg)]),
+    "kl_layer_forward_ragged": (ctypes.c_int, [_P(LayerCfg), _P(RaggedCfg), _P(LayerWeights)] + [_vp] * 10 + [_sz, _vp]),
     "kl_profile_enable": (ctypes.c_int, [_i32]),
     "kl_profile_read": (_i32, [_vp, _i32]),
     "kl_launch_count": (ctypes.c_uint64, []),
@@ -322,6 +339,45 @@ def kl_layer_forward_paged(cfg: LayerCfg, pc: PagedCfg, w: LayerWeights, X, Y, k
                            ws_bytes, stream=None) -> None:
     check(load().kl_layer_forward_paged(ctypes.byref(cfg), ctypes.byref(pc), ctypes.byref(w), X, Y, k_pool, v_pool,
                                         table, ctx, ws, ws_bytes, _stream(stream)))
+
+
+def kl_ragged_plan(rc: RaggedCfg, n_new, ctx, table, held, free_list, n_free, cu_rows, pos, slots, missing,
+                   stream=None) -> None:
+    check(load().kl_ragged_plan(ctypes.byref(rc), n_new, ctx, table, held, free_list, n_free, cu_rows, pos, slots,
+                                missing, _stream(stream)))
+
+
+def kl_ragged_qkv_rope(rc: RaggedCfg, Hq, Hkv, d, dtype, q_pre, k_pre, v, gamma_q, gamma_k, eps, rope_base,
+                       rope_interleaved, cu_rows, pos, slots, q_out, k_pool, v_pool, stream=None) -> None:
+    check(load().kl_ragged_qkv_rope(ctypes.byref(rc), Hq, Hkv, d, dtype, q_pre, k_pre, v, gamma_q, gamma_k, eps,
+                                    rope_base, rope_interleaved, cu_rows, pos, slots, q_out, k_pool, v_pool,
+                                    _stream(stream)))
+
+
+def kl_ragged_attention_ws_bytes(rc: RaggedCfg, Hq, Hkv, d) -> int:
+    return load().kl_ragged_attention_ws_bytes(ctypes.byref(rc), Hq, Hkv, d)
+
+
+def kl_ragged_attention(rc: RaggedCfg, Hq, Hkv, d, dtype, q, k_pool, v_pool, table, cu_rows, ctx, o, lse, ws,
+                        ws_bytes, stream=None) -> None:
+    check(load().kl_ragged_attention(ctypes.byref(rc), Hq, Hkv, d, dtype, q, k_pool, v_pool, table, cu_rows, ctx, o,
+                                     lse, ws, ws_bytes, _stream(stream)))
+
+
+def kl_draft_verify(cfg: VerifyCfg, p, ldp, q, ldq, tokens, cu_rows, u_accept, u_sample, n_accepted, next_token,
+                    stream=None) -> None:
+    check(load().kl_draft_verify(ctypes.byref(cfg), p, ldp, q, ldq, tokens, cu_rows, u_accept, u_sample, n_accepted,
+                                 next_token, _stream(stream)))
+
+
+def kl_layer_forward_ragged_ws_bytes(cfg: LayerCfg, rc: RaggedCfg) -> int:
+    return load().kl_layer_forward_ragged_ws_bytes(ctypes.byref(cfg), ctypes.byref(rc))
+
+
+def kl_layer_forward_ragged(cfg: LayerCfg, rc: RaggedCfg, w: LayerWeights, X, Y, k_pool, v_pool, table, cu_rows, ctx,
+                            pos, slots, ws, ws_bytes, stream=None) -> None:
+    check(load().kl_layer_forward_ragged(ctypes.byref(cfg), ctypes.byref(rc), ctypes.byref(w), X, Y, k_pool, v_pool,
+                                         table, cu_rows, ctx, pos, slots, ws, ws_bytes, _stream(stream)))
 
 
 def kl_device_status(stream=None) -> int:

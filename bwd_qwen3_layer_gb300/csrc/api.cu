@@ -1,7 +1,8 @@
 // C ABI of libkl (declared in include/kl.h): argument checks, status
 // plumbing, buffer carving and the layer / lm-head orchestration. Every step
-// runs in the kernels of gemm.cu, elementwise.cu, attention.cu and ce.cu on
+// runs in the kernels of the other files on
 // the caller's stream; nothing here synchronises except kl_device_status.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
@@ -212,8 +213,7 @@ void carve_bwd(const Dims& D, Carver& c, BwdWs* w) {
   w->qk_k = D.qk_norm ? c.take(w->qk_k_bytes) : nullptr;
 }
 
-// Workspace of the paged-cache layer forward: the step's activations (T = B *
-// n_new rows), the attention split partials and the GEMMs' last-round scratch.
+// Workspace of a paged or ragged step's layer forward: its activations (T rows), the attention split partials and the GEMMs' last-round scratch.
 struct PagedWs {
   void *h1, *q_pre, *k_pre, *v, *q, *k, *o, *x2, *h2, *g, *u, *m;
   float *rstd1, *rstd2, *rstd_q, *rstd_k;
@@ -223,7 +223,7 @@ struct PagedWs {
   size_t tail_bytes;
 };
 
-void carve_paged(const Dims& D, const kl_paged_cfg& pc, Carver& c, PagedWs* w) {
+void carve_paged(const Dims& D, size_t att_bytes, Carver& c, PagedWs* w) {
   const size_t T = D.T, es = D.es;
   w->h1 = c.take(T * D.H * es);
   w->rstd1 = static_cast<float*>(c.take(T * 4));
@@ -241,7 +241,7 @@ void carve_paged(const Dims& D, const kl_paged_cfg& pc, Carver& c, PagedWs* w) {
   w->g = c.take(T * D.I * es);
   w->u = c.take(T * D.I * es);
   w->m = c.take(T * D.I * es);
-  w->att_bytes = paged_attention_ws(pc, D.Hq, D.Hkv);
+  w->att_bytes = att_bytes;
   w->att = w->att_bytes ? c.take(w->att_bytes) : nullptr;
   w->tail_bytes = gemm_tail_ws_bytes();
   w->tail = c.take(w->tail_bytes);
@@ -251,6 +251,15 @@ kl_status check_ptrs(std::initializer_list<const void*> ptrs, const char* what) 
   for (const void* p : ptrs) {
     if (!p) return set_error(KL_ERR_INVALID_ARG, "%s: null pointer", what);
     if (!al16(p)) return set_error(KL_ERR_INVALID_ARG, "%s: pointer not 16-byte aligned", what);
+  }
+  return KL_OK;
+}
+
+// int32 / fp32 arrays, which may be pieces of a larger buffer: their own alignment is enough
+kl_status check_arrays(std::initializer_list<const void*> ptrs, const char* what) {
+  for (const void* p : ptrs) {
+    if (!p) return set_error(KL_ERR_INVALID_ARG, "%s: null pointer", what);
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return set_error(KL_ERR_INVALID_ARG, "%s: pointer not 4-byte aligned", what);
   }
   return KL_OK;
 }
@@ -736,13 +745,55 @@ kl_status kl_paged_attention(const kl_paged_cfg* pc, int32_t Hq, int32_t Hkv, in
                          static_cast<cudaStream_t>(stream));
 }
 
+// The two halves of a paged step's layer around its rotation and attention:
+// h1 = norm(X) and the q / k / v projections ...
+static kl_status paged_qkv(const Dims& D, const kl_layer_weights* w, const void* X, float eps, const PagedWs& b,
+                    cudaStream_t st) {
+  const int T = D.T, H = D.H, dt = D.dt;
+  KL_TRY(rmsnorm_fwd(T, H, dt, X, w->gamma1, eps, b.h1, b.rstd1, st));
+  {
+    GemmSpec g[3] = {proj(T, D.Dq, H, b.h1, H, w->wq, H, b.q_pre, D.Dq, dt),
+                     proj(T, D.Dkv, H, b.h1, H, w->wk, H, b.k_pre, D.Dkv, dt),
+                     proj(T, D.Dkv, H, b.h1, H, w->wv, H, b.v, D.Dkv, dt)};
+    with_tail(g, 3, b.tail, b.tail_bytes);
+    KL_TRY(run_gemms(dt, g, 3, st, "gemm.paged_qkv"));
+  }
+  return KL_OK;
+}
+// ... and x2 = X + O W_o^T, then Y = x2 + the MLP of norm(x2).
+static kl_status paged_out_mlp(const Dims& D, const kl_layer_weights* w, const void* X, void* Y, float eps, const PagedWs& b,
+                        cudaStream_t st) {
+  const int T = D.T, H = D.H, I = D.I, dt = D.dt;
+  {
+    GemmSpec g = proj(T, H, D.Dq, b.o, D.Dq, w->wo, D.Dq, b.x2, H, dt, X, dt);
+    with_tail(&g, 1, b.tail, b.tail_bytes);
+    KL_TRY(run_gemms(dt, &g, 1, st, "gemm.paged_o"));
+  }
+  KL_TRY(rmsnorm_fwd(T, H, dt, b.x2, w->gamma2, eps, b.h2, b.rstd2, st));
+  {
+    GemmSpec g = proj(T, I, H, b.h2, H, w->wg, H, b.g, I, dt);
+    g.epi = GEMM_EPI_SWIGLU;
+    g.B2 = w->wu;
+    g.C2 = b.u;
+    g.C3 = b.m;
+    with_tail(&g, 1, b.tail, b.tail_bytes);
+    KL_TRY(run_gemms(dt, &g, 1, st, "gemm.paged_gateup"));
+  }
+  {
+    GemmSpec g = proj(T, H, I, b.m, I, w->wd, I, Y, H, dt, b.x2, dt);
+    with_tail(&g, 1, b.tail, b.tail_bytes);
+    KL_TRY(run_gemms(dt, &g, 1, st, "gemm.paged_down"));
+  }
+  return KL_OK;
+}
+
 size_t kl_layer_forward_paged_ws_bytes(const kl_layer_cfg* cfg, const kl_paged_cfg* pc) {
   Dims D;
   if (check_cfg(cfg, &D) != KL_OK || paged_check(pc, D.Hq, D.Hkv, D.d, D.dt) != KL_OK) return 0;
   if (cfg->B != pc->B || cfg->S != pc->n_new) return 0;
   Carver c(nullptr);
   PagedWs w;
-  carve_paged(D, *pc, c, &w);
+  carve_paged(D, paged_attention_ws(*pc, D.Hq, D.Hkv), c, &w);
   return c.off;
 }
 
@@ -765,42 +816,126 @@ kl_status kl_layer_forward_paged(const kl_layer_cfg* cfg, const kl_paged_cfg* pc
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Carver c(ws);
   PagedWs b;
-  carve_paged(D, *pc, c, &b);
-  const int T = D.T, H = D.H, I = D.I, dt = D.dt;
-  KL_TRY(rmsnorm_fwd(T, H, dt, X, w->gamma1, cfg->eps, b.h1, b.rstd1, st));
-  {
-    GemmSpec g[3] = {proj(T, D.Dq, H, b.h1, H, w->wq, H, b.q_pre, D.Dq, dt),
-                     proj(T, D.Dkv, H, b.h1, H, w->wk, H, b.k_pre, D.Dkv, dt),
-                     proj(T, D.Dkv, H, b.h1, H, w->wv, H, b.v, D.Dkv, dt)};
-    with_tail(g, 3, b.tail, b.tail_bytes);
-    KL_TRY(run_gemms(dt, g, 3, st, "gemm.paged_qkv"));
-  }
+  carve_paged(D, paged_attention_ws(*pc, D.Hq, D.Hkv), c, &b);
+  KL_TRY(paged_qkv(D, w, X, cfg->eps, b, st));
   // optional per-head norm, the rotation at the tokens' absolute positions ctx[b] + i, and the new keys
   // and values written into their cache slots: one launch
   KL_TRY(paged_qkv_rope(*pc, D.Hq, D.Hkv, D.d, b.q_pre, b.k_pre, b.v, w->gamma_q, w->gamma_k, cfg->eps, D.qk_norm,
                         D.inter, cfg->rope_base, table, ctx, b.q, k_pool, v_pool, st));
   KL_TRY(paged_attention(*pc, D.Hq, D.Hkv, b.q, k_pool, v_pool, table, ctx, b.o, nullptr, b.att, b.att_bytes, st));
-  {
-    GemmSpec g = proj(T, H, D.Dq, b.o, D.Dq, w->wo, D.Dq, b.x2, H, dt, X, dt);
-    with_tail(&g, 1, b.tail, b.tail_bytes);
-    KL_TRY(run_gemms(dt, &g, 1, st, "gemm.paged_o"));
-  }
-  KL_TRY(rmsnorm_fwd(T, H, dt, b.x2, w->gamma2, cfg->eps, b.h2, b.rstd2, st));
-  {
-    GemmSpec g = proj(T, I, H, b.h2, H, w->wg, H, b.g, I, dt);
-    g.epi = GEMM_EPI_SWIGLU;
-    g.B2 = w->wu;
-    g.C2 = b.u;
-    g.C3 = b.m;
-    with_tail(&g, 1, b.tail, b.tail_bytes);
-    KL_TRY(run_gemms(dt, &g, 1, st, "gemm.paged_gateup"));
-  }
-  {
-    GemmSpec g = proj(T, H, I, b.m, I, w->wd, I, Y, H, dt, b.x2, dt);
-    with_tail(&g, 1, b.tail, b.tail_bytes);
-    KL_TRY(run_gemms(dt, &g, 1, st, "gemm.paged_down"));
-  }
+  return paged_out_mlp(D, w, X, Y, cfg->eps, b, st);
+}
+
+kl_status kl_ragged_plan(const kl_ragged_cfg* rc, const int32_t* n_new, const int32_t* ctx, int32_t* table,
+                         int32_t* held, int32_t* free_list, int32_t* n_free, int32_t* cu_rows, int32_t* pos,
+                         int32_t* slots, int32_t* missing, void* stream) {
+  KL_TRY(ragged_check(rc));
+  KL_TRY(check_arrays({n_new, ctx, table, held, free_list, n_free, cu_rows, pos, slots, missing}, "ragged_plan"));
+  return ragged_plan(*rc, n_new, ctx, table, held, free_list, n_free, cu_rows, pos, slots, missing,
+                     static_cast<cudaStream_t>(stream));
+}
+
+kl_status kl_ragged_qkv_rope(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
+                             const void* q_pre, const void* k_pre, const void* v, const void* gamma_q,
+                             const void* gamma_k, float eps, float rope_base, int32_t rope_interleaved,
+                             const int32_t* cu_rows, const int32_t* pos, const int32_t* slots, void* q_out,
+                             void* k_pool, void* v_pool, void* stream) {
+  KL_TRY(ragged_heads_check(rc, Hq, Hkv, d, dtype));
+  KL_TRY(check_ptrs({q_pre, k_pre, v, q_out, k_pool, v_pool}, "ragged_qkv_rope"));
+  KL_TRY(check_arrays({cu_rows, pos, slots}, "ragged_qkv_rope"));
+  if (!gamma_q != !gamma_k) return set_error(KL_ERR_INVALID_ARG, "ragged_qkv_rope: one of gamma_q, gamma_k is null");
+  if (gamma_q) KL_TRY(check_ptrs({gamma_q, gamma_k}, "ragged_qkv_rope gains"));
+  // rates below 1 / (2 pi) turns per position fit the fixed-point angle
+  if (!(rope_base >= 1.f) || !(rope_base < INFINITY) || !(eps >= 0.f) || !(eps < INFINITY) ||
+      (rope_interleaved != 0 && rope_interleaved != 1))
+    return set_error(KL_ERR_INVALID_ARG, "ragged_qkv_rope: base %g, eps %g, interleaved %d", rope_base, eps,
+                     rope_interleaved);
+  return ragged_qkv_rope(*rc, Hq, Hkv, q_pre, k_pre, v, gamma_q, gamma_k, eps, rope_base, rope_interleaved, cu_rows,
+                         pos, slots, q_out, k_pool, v_pool, static_cast<cudaStream_t>(stream));
+}
+
+size_t kl_ragged_attention_ws_bytes(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d) {
+  if (ragged_heads_check(rc, Hq, Hkv, d, KL_BF16) != KL_OK) return 0;
+  return ragged_attention_ws();
+}
+
+kl_status kl_ragged_attention(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
+                              const void* q, const void* k_pool, const void* v_pool, const int32_t* table,
+                              const int32_t* cu_rows, const int32_t* ctx, void* o, float* lse, void* ws,
+                              size_t ws_bytes, void* stream) {
+  KL_TRY(ragged_heads_check(rc, Hq, Hkv, d, dtype));
+  KL_TRY(check_ptrs({q, k_pool, v_pool, o}, "ragged_attention"));
+  KL_TRY(check_arrays({table, cu_rows, ctx}, "ragged_attention"));
+  if (reinterpret_cast<uintptr_t>(lse) & 3u)
+    return set_error(KL_ERR_INVALID_ARG, "ragged_attention: lse not 4-byte aligned");
+  return ragged_attention(*rc, Hq, Hkv, q, k_pool, v_pool, table, cu_rows, ctx, o, lse, ws, ws_bytes,
+                          static_cast<cudaStream_t>(stream));
+}
+
+kl_status kl_draft_verify(const kl_verify_cfg* c, const void* p, int64_t ldp, const void* q, int64_t ldq,
+                          const int32_t* tokens, const int32_t* cu_rows, const float* u_accept, const float* u_sample,
+                          int32_t* n_accepted, int32_t* next_token, void* stream) {
+  if (!c) return set_error(KL_ERR_INVALID_ARG, "draft_verify: null configuration");
+  if (c->B < 1 || c->T < 1 || c->V < 1 || ldp < c->V || (q && ldq < c->V))
+    return set_error(KL_ERR_INVALID_ARG, "draft_verify: bad sizes (B %d, T %d, V %d, row strides %lld, %lld)", c->B, c->T,
+                     c->V, static_cast<long long>(ldp), static_cast<long long>(ldq));
+  if (c->dtype != KL_F32 && c->dtype != KL_BF16)
+    return set_error(KL_ERR_INVALID_ARG, "draft_verify: bad dtype %d", c->dtype);
+  if (c->B > (1 << 24) || c->T > (1 << 24))
+    return set_error(KL_ERR_UNSUPPORTED, "draft_verify: too many requests or rows (%d, %d)", c->B, c->T);
+  KL_TRY(check_ptrs({p}, "draft_verify p"));
+  if (q) KL_TRY(check_ptrs({q}, "draft_verify q"));
+  KL_TRY(check_arrays({tokens, cu_rows, u_accept, u_sample, n_accepted, next_token}, "draft_verify"));
+  return draft_verify(*c, p, ldp, q, ldq, tokens, cu_rows, u_accept, u_sample, n_accepted, next_token,
+                      static_cast<cudaStream_t>(stream));
+}
+
+// A ragged step's layer: T rows as one run (cfg->B 1, cfg->S = rc->T).
+static kl_status ragged_layer_check(const kl_layer_cfg* cfg, const kl_ragged_cfg* rc, Dims* D) {
+  KL_TRY(check_cfg(cfg, D));
+  KL_TRY(ragged_heads_check(rc, D->Hq, D->Hkv, D->d, D->dt));
+  if (cfg->B != 1 || cfg->S != rc->T)
+    return set_error(KL_ERR_INVALID_ARG, "layer_forward_ragged: cfg B, S must be 1 and the step's rows");
+  if (!(cfg->rope_base >= 1.f))
+    return set_error(KL_ERR_INVALID_ARG, "layer_forward_ragged: rope base %g below 1", cfg->rope_base);
   return KL_OK;
+}
+
+size_t kl_layer_forward_ragged_ws_bytes(const kl_layer_cfg* cfg, const kl_ragged_cfg* rc) {
+  Dims D;
+  if (ragged_layer_check(cfg, rc, &D) != KL_OK) return 0;
+  Carver c(nullptr);
+  PagedWs w;
+  carve_paged(D, ragged_attention_ws(), c, &w);
+  return c.off;
+}
+
+kl_status kl_layer_forward_ragged(const kl_layer_cfg* cfg, const kl_ragged_cfg* rc, const kl_layer_weights* w,
+                                  const void* X, void* Y, void* k_pool, void* v_pool, const int32_t* table,
+                                  const int32_t* cu_rows, const int32_t* ctx, const int32_t* pos, const int32_t* slots,
+                                  void* ws, size_t ws_bytes, void* stream) {
+  Dims D;
+  KL_TRY(ragged_layer_check(cfg, rc, &D));
+  if (!w) return set_error(KL_ERR_INVALID_ARG, "layer_forward_ragged: null weights");
+  KL_TRY(check_ptrs({w->gamma1, w->wq, w->wk, w->wv, w->wo, w->gamma2, w->wg, w->wu, w->wd},
+                    "layer_forward_ragged weights"));
+  if (D.qk_norm) KL_TRY(check_ptrs({w->gamma_q, w->gamma_k}, "layer_forward_ragged q/k norm gains"));
+  KL_TRY(check_ptrs({X, Y, k_pool, v_pool}, "layer_forward_ragged buffers"));
+  KL_TRY(check_arrays({table, cu_rows, ctx, pos, slots}, "layer_forward_ragged"));
+  const size_t need = kl_layer_forward_ragged_ws_bytes(cfg, rc);
+  if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return set_error(KL_ERR_NO_MEMORY, "layer_forward_ragged: workspace too small or not 256-byte aligned");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Carver c(ws);
+  PagedWs b;
+  carve_paged(D, ragged_attention_ws(), c, &b);
+  KL_TRY(paged_qkv(D, w, X, cfg->eps, b, st));
+  KL_TRY(ragged_qkv_rope(*rc, D.Hq, D.Hkv, b.q_pre, b.k_pre, b.v, D.qk_norm ? w->gamma_q : nullptr,
+                         D.qk_norm ? w->gamma_k : nullptr, cfg->eps, cfg->rope_base, D.inter, cu_rows, pos, slots, b.q,
+                         k_pool, v_pool, st));
+  KL_TRY(ragged_attention(*rc, D.Hq, D.Hkv, b.q, k_pool, v_pool, table, cu_rows, ctx, b.o, nullptr, b.att, b.att_bytes,
+                          st));
+  return paged_out_mlp(D, w, X, Y, cfg->eps, b, st);
 }
 
 }  // extern "C"

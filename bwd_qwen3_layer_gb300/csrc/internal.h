@@ -157,6 +157,24 @@ kl_status paged_kv_write(const kl_paged_cfg& pc, int Hkv, const void* k_new, con
 kl_status paged_attention(const kl_paged_cfg& pc, int Hq, int Hkv, const void* q, const void* kp, const void* vp,
                           const int32_t* table, const int32_t* ctx, void* o, float* lse, void* ws, size_t ws_bytes,
                           cudaStream_t st);
+
+// ragged.cu, ragged_attn.cu: a ragged step over the paged cache (bf16, d = 128)
+kl_status ragged_check(const kl_ragged_cfg* rc);
+kl_status ragged_heads_check(const kl_ragged_cfg* rc, int Hq, int Hkv, int d, int dtype);
+kl_status ragged_plan(const kl_ragged_cfg& rc, const int32_t* n_new, const int32_t* ctx, int32_t* table, int32_t* held,
+                      int32_t* free_list, int32_t* n_free, int32_t* cu, int32_t* pos, int32_t* slots, int32_t* missing,
+                      cudaStream_t st);
+kl_status ragged_qkv_rope(const kl_ragged_cfg& rc, int Hq, int Hkv, const void* q_pre, const void* k_pre, const void* v,
+                          const void* gq, const void* gk, float eps, float base, int inter, const int32_t* cu,
+                          const int32_t* pos, const int32_t* slots, void* q_out, void* kp, void* vp, cudaStream_t st);
+size_t ragged_attention_ws();
+kl_status ragged_attention(const kl_ragged_cfg& rc, int Hq, int Hkv, const void* q, const void* kp, const void* vp,
+                           const int32_t* table, const int32_t* cu, const int32_t* ctx, void* o, float* lse, void* ws,
+                           size_t ws_bytes, cudaStream_t st);
+// verify.cu: drafted tokens against the target's probabilities
+kl_status draft_verify(const kl_verify_cfg& c, const void* p, int64_t ldp, const void* q, int64_t ldq,
+                       const int32_t* tokens, const int32_t* cu, const float* ua, const float* us, int32_t* acc,
+                       int32_t* next, cudaStream_t st);
 kl_status swiglu_fwd(int64_t n, int dtype, const void* g, const void* u, void* m, cudaStream_t st);
 kl_status swiglu_bwd(int64_t n, int dtype, const void* dm, const void* g, const void* u, void* dg,
                      void* du, cudaStream_t st);

@@ -1,0 +1,836 @@
+// Attention of a ragged step over a paged key/value cache, on the 5th-generation
+// tensor cores: request b feeds n_b = cu_rows[b+1] - cu_rows[b] new tokens (one
+// when it decodes, a few drafted ones, a chunk of its prompt), and new token i
+// attends to positions 0 .. ctx[b] + i of its request's pages:
+//   o_i = sum_j softmax_j(q_i . k_j / sqrt(d)) v_j,  lse_i = log sum_j exp(q_i . k_j / sqrt(d)).
+//
+// Tiles. An item is (request, kv head, query tile). The G = Hq / Hkv query heads
+// of a kv head read the same keys, so a query tile packs TQ = floor(128 / G)
+// tokens x G heads into the 128 rows of one tcgen05 tile (row = token * G +
+// head): each key and value tile is fetched once for all of them, and one shape
+// of work covers decoding (G rows of 128 used: bound by HBM, the idle rows cost
+// tensor-core time that the loads hide) and prompts (bound by the tensor cores).
+//
+// Work split. Lengths are on the device only, so the grid is one CTA per SM and
+// every CTA finds its own work: the items' key tiles of 128 (plus one unit for
+// an item's start and end) laid end to end are W units, and CTA c takes units
+// [c P, c P + P), P = ceil(W / CTAs). Every CTA thus streams the same number of
+// key tiles whatever the lengths are. A CTA's first and last item may be cut; it
+// leaves such a piece unnormalised (fp32 O, running max and sum per row) in the
+// workspace and ragged_combine_kernel joins an item's pieces in CTA order, so
+// results repeat bit for bit. The workspace holds two pieces per CTA and does
+// not depend on the lengths.
+//
+// Roles (6 warps): warp 0 looks up the pages and issues the copies, warp 1
+// issues the products, warps 2..5 are the softmax (thread = query row = TMEM
+// lane): the scheme of the training forward's persistent kernel.
+// Pages: with block_size a multiple of 8 a key tile is 128 / box TMA boxes of
+// box = gcd(block_size, 128) rows, each found through the table; a box past the
+// context, past its table row or whose table entry lies outside the pool starts
+// past the tensor's last row and is filled with zeros by the copy. Other block
+// sizes gather row by row with 16-byte cp.async. Slots behind a context's end
+// may hold anything (NaN too): their scores are masked, and the last tile's
+// value rows behind the end are zeroed before the product reads them.
+#include <cudaTypedefs.h>
+#include <math.h>
+#include <string.h>
+
+#include <type_traits>
+
+#include "internal.h"
+#include "kl_common.cuh"
+
+namespace kl {
+namespace {
+
+constexpr int RA_D = 128;        // head dim
+constexpr int RA_BQ = 128;       // rows of a query tile
+constexpr int RA_BKV = 128;      // keys per tile
+constexpr int RA_THREADS = 192;
+constexpr uint32_t RA_TILE = 128 * 128 * 2;   // 32 KB: two 64-column swizzle blocks of 16 KB
+constexpr int RA_NST = 2;                     // stages of the K and of the V ring
+constexpr uint32_t RA_OFF_Q = 0;
+constexpr uint32_t RA_OFF_K = RA_OFF_Q + RA_TILE;
+constexpr uint32_t RA_OFF_V = RA_OFF_K + RA_NST * RA_TILE;
+constexpr uint32_t RA_OFF_BAR = RA_OFF_V + RA_NST * RA_TILE;
+constexpr size_t RA_SMEM = 1024 + RA_OFF_BAR + 512;
+constexpr int RA_ITEM_UNITS = 1;              // units an item's start and end count for
+constexpr int RA_MIN_UNITS = 3;               // units per CTA at least
+constexpr float RA_LOG2E = 1.4426950408889634f;
+constexpr float RA_LN2 = 0.6931471805599453f;
+
+// Where a CTA's run of units starts: an item and the unit inside it.
+struct RaStart {
+  int b, g, qt, pad;
+  long long off;    // unit within the item
+  long long P;      // units per CTA
+};
+
+struct RaParams {
+  CUtensorMap tmQ, tmK, tmV;
+  const __nv_bfloat16* kp;
+  const __nv_bfloat16* vp;
+  const int32_t* table;
+  const int32_t* cu;
+  const int32_t* ctx;
+  __nv_bfloat16* o;
+  float* lse;            // [T, Hq] or null
+  float* part_o;         // [CTA][2][128][128] unnormalised pieces
+  float* part_ml;        // [CTA][2][128][2] (max in log2 units, sum)
+  RaStart* starts;       // [CTA]
+  int B, T, Hq, Hkv, G, TQ;
+  int bs, max_blocks, n_blocks;
+  int box;               // rows per TMA box
+  float scale_log2;
+  uint32_t* err;
+};
+
+__device__ __forceinline__ float ra_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// K-major operand (two 64-column swizzle blocks of 128 rows), k-step kk of 16 columns
+__device__ __forceinline__ uint64_t ra_desc_k(uint32_t base, int kk) {
+  return smem_desc_sw128(base + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024);
+}
+// V as the MN-major B operand: n = head dim in two 64-wide blocks, k-step kk of 16 keys
+__device__ __forceinline__ uint64_t ra_desc_v(uint32_t base, int kk) {
+  return smem_desc_sw128(base + kk * 2048, 16384, 1024);
+}
+__device__ __forceinline__ void ra_tma_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void ra_cp16(uint32_t dst, const void* src, bool valid) {
+  const int sz = valid ? 16 : 0;   // zero-fill
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(sz) : "memory");
+}
+
+// One request's rows and context, every value brought into range.
+struct RaReq {
+  int r0, n, ctx;
+};
+__device__ __forceinline__ RaReq ra_req(const RaParams& p, int b) {
+  RaReq q;
+  q.r0 = min(max(p.cu[b], 0), p.T);
+  q.n = min(max(p.cu[b + 1], q.r0), p.T) - q.r0;
+  q.ctx = max(p.ctx[b], 0);
+  return q;
+}
+// Key tiles of query tile qt (its last token's limit decides).
+__device__ __forceinline__ int ra_tiles(const RaReq& q, int TQ, int qt) {
+  const long long last = static_cast<long long>(q.ctx) + min(static_cast<long long>(q.n), (qt + 1LL) * TQ) - 1;
+  return static_cast<int>(last / RA_BKV) + 1;
+}
+// Units of query tiles 0 .. m-1, all but the request's last one:
+//   sum_{k=1}^{m} (floor((ctx - 1 + k TQ) / 128) + 1 + RA_ITEM_UNITS).
+// The quotients repeat with period 128 / gcd(TQ, 128) up to a constant step, so
+// whole periods are summed in closed form.
+__device__ long long ra_units_before(int ctx, int TQ, long long m) {
+  const int low = TQ & -TQ;                       // gcd(TQ, 128), TQ <= 128
+  const int period = RA_BKV / low, step = TQ / low;
+  const long long a = static_cast<long long>(ctx) - 1;
+  const long long c = m / period;
+  const int r = static_cast<int>(m - c * period);
+  long long full = 0, part = 0;
+  for (int k = 1; k <= (c ? period : r); ++k) {
+    const long long v = (a + static_cast<long long>(k) * TQ) >> 7;
+    full += v;
+    if (k <= r) part += v;
+  }
+  return m * (1 + RA_ITEM_UNITS) + (c ? c * full + static_cast<long long>(period) * step * (c * (c - 1) / 2) : 0) +
+         part + static_cast<long long>(r) * step * c;
+}
+__device__ __forceinline__ long long ra_head_units(const RaReq& q, int TQ) {
+  if (q.n <= 0) return 0;
+  const int QT = (q.n + TQ - 1) / TQ;
+  return ra_units_before(q.ctx, TQ, QT - 1) + ra_tiles(q, TQ, QT - 1) + RA_ITEM_UNITS;
+}
+
+// The pieces of one CTA's run, in order. Every role walks the same list.
+struct RaWalk {
+  int b, g, qt;            // where the walk stands: request (its lengths: q), kv head, query tile,
+  long long off, left;     // unit inside the item, units left of the run
+  RaReq q;
+  int ib, ig, iq;          // the piece that next() found: request (its lengths: rq), kv head, query tile
+  RaReq rq;
+  int tiles, ta, tb;       // the item's key tiles; the piece's [ta, tb)
+  int idx;                 // items met so far: the first one's pieces take slot 0, a later one's slot 1
+
+  __device__ __forceinline__ void init(const RaParams& p, const RaStart& s, long long units) {
+    b = s.b;
+    g = s.g;
+    qt = s.qt;
+    off = s.off;
+    left = units;
+    idx = -1;
+    if (left > 0) q = ra_req(p, b);
+  }
+  // the next piece with at least one key tile, or false
+  __device__ __forceinline__ bool next(const RaParams& p) {
+    while (left > 0) {
+      tiles = ra_tiles(q, p.TQ, qt);
+      const long long len = tiles + RA_ITEM_UNITS;
+      const long long take = min(left, len - off);
+      const long long e = off + take;
+      ta = static_cast<int>(max(off - RA_ITEM_UNITS, 0LL));
+      tb = static_cast<int>(max(e - RA_ITEM_UNITS, 0LL));
+      left -= take;
+      ++idx;
+      ib = b;
+      ig = g;
+      iq = qt;
+      rq = q;
+      if (left > 0) {      // the item ends here: on to the next
+        off = 0;
+        if (static_cast<long long>(qt + 1) * p.TQ < q.n) {
+          ++qt;
+        } else {
+          qt = 0;
+          if (++g == p.Hkv) {
+            g = 0;
+            do {
+              if (++b >= p.B) {      // cannot happen: the run lies inside the W units
+                left = 0;
+                break;
+              }
+              q = ra_req(p, b);
+            } while (q.n <= 0);
+          }
+        }
+      }
+      if (tb > ta) return true;
+    }
+    return false;
+  }
+};
+
+template <bool TMA>
+__global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid_constant__ RaParams p) {
+  pdl_enter();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sb = smem_u32(smem);
+  const uint32_t bar = sb + RA_OFF_BAR;
+  // barriers; those of a pair serve the steps (or pieces) of one parity each, so
+  // that a warp which runs a step ahead of another cannot count for its phase
+  const uint32_t q_full = bar + 0, q_empty = bar + 8, drain = bar + 16;
+  auto k_full = [&](int s) { return bar + 24 + 8 * s; };
+  auto k_empty = [&](int s) { return bar + 40 + 8 * s; };
+  auto v_full = [&](int s) { return bar + 56 + 8 * s; };
+  auto v_empty = [&](int s) { return bar + 72 + 8 * s; };
+  auto s_full = [&](int s) { return bar + 88 + 8 * s; };    // S_n computed
+  auto s_free = [&](int s) { return bar + 104 + 8 * s; };   // S_n read
+  auto p_full = [&](int s) { return bar + 120 + 8 * s; };   // P_n written (and V_n's tail cleared)
+  auto p_done = [&](int s) { return bar + 136 + 8 * s; };   // O += P_n V_n computed
+  auto o_empty = [&](int s) { return bar + 152 + 8 * s; };  // a piece's O read
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + RA_OFF_BAR + 168);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + RA_OFF_BAR + 172);
+  RaStart* start = reinterpret_cast<RaStart*>(smem + RA_OFF_BAR + 176);
+  long long* wsum = reinterpret_cast<long long*>(smem + RA_OFF_BAR + 256);   // [8]: the warps' unit sums, then W
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = blockIdx.x, ctas = gridDim.x;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(k_full(s), TMA ? 1 : 32);
+      mbar_init(k_empty(s), 1);
+      mbar_init(v_full(s), TMA ? 1 : 32);
+      mbar_init(v_empty(s), 1);
+      mbar_init(s_full(s), 1);
+      mbar_init(s_free(s), 4);
+      mbar_init(p_full(s), 4);
+      mbar_init(p_done(s), 1);
+      mbar_init(o_empty(s), 4);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_holder), 512);
+    tmem_relinquish();
+  }
+
+  // ---- this CTA's run: prefix sums of the requests' units, then the item at unit cta * P ----
+  {
+    const int per = (p.B + RA_THREADS - 1) / RA_THREADS;
+    const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += ra_head_units(ra_req(p, b), p.TQ) * p.Hkv;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    long long before = 0, W = 0;
+    for (int w = 0; w < RA_THREADS / 32; ++w) {
+      if (w < warp) before += wsum[w];
+      W += wsum[w];
+    }
+    const long long P = max((W + ctas - 1) / ctas, static_cast<long long>(RA_MIN_UNITS));
+    const long long u0 = cta * P;
+    if (threadIdx.x == 0) {
+      wsum[7] = max(0LL, min(P, W - u0));     // units of this CTA
+      start->P = P;
+      if (u0 >= W) start->b = -1;
+    }
+    long long lo = before + incl - mine;      // units before this thread's requests
+    if (mine > 0 && u0 >= lo && u0 < lo + mine && u0 < W) {
+      int b = b0;
+      long long hu = 0;
+      for (; b < b1; ++b) {
+        hu = ra_head_units(ra_req(p, b), p.TQ);
+        if (u0 < lo + hu * p.Hkv) break;
+        lo += hu * p.Hkv;
+      }
+      const long long x = u0 - lo;
+      const RaReq q = ra_req(p, b);
+      const int g = static_cast<int>(x / hu);
+      const long long y = x - g * hu;
+      int m0 = 0, m1 = (q.n + p.TQ - 1) / p.TQ;      // the query tile: units_before(m0) <= y < units_before(m1)
+      while (m1 - m0 > 1) {
+        const int m = (m0 + m1) >> 1;
+        if (ra_units_before(q.ctx, p.TQ, m) <= y) m0 = m; else m1 = m;
+      }
+      start->b = b;
+      start->g = g;
+      start->qt = m0;
+      start->off = y - ra_units_before(q.ctx, p.TQ, m0);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;   // S[0] at column 0, S[1] at 128, O[0] at 256, O[1] at 384
+  const RaStart st = *start;
+  const long long units = wsum[7];
+  if (threadIdx.x == 0) p.starts[cta] = st;
+  const int GT = p.G * p.TQ;            // rows of a full query tile
+
+  if (warp == 0) {
+    // ---------------- copies (whole warp: lane = page box of a tile) ----------------
+    const bool el = elect_one();
+    if (el) {
+      tma_prefetch_desc(&p.tmQ);
+      if (TMA) {
+        tma_prefetch_desc(&p.tmK);
+        tma_prefetch_desc(&p.tmV);
+      }
+    }
+    const int nbox = RA_BKV / p.box;
+    const int no_row = p.n_blocks * p.bs;         // past the pool's last row: filled with zeros
+    int issued_q = 0, issued_k = 0, issued_v = 0, arrived = 0;
+    bool ok = true;
+    // the pool row of position pos, or no_row
+    auto pool_row = [&](int b, long long pos, long long L) {
+      if (pos >= L) return no_row;
+      const int lb = static_cast<int>(pos / p.bs);
+      const int blk = lb < p.max_blocks ? p.table[static_cast<int64_t>(b) * p.max_blocks + lb] : -1;
+      if (blk < 0 || blk >= p.n_blocks) {
+        record_error(p.err, KL_DEVERR_PAGE);
+        return no_row;
+      }
+      return blk * p.bs + static_cast<int>(pos - static_cast<long long>(lb) * p.bs);
+    };
+    // cp.async: the K (or V) rows of one tile; row[k] of lane l is the pool row of key 32 k + l
+    auto gather = [&](uint32_t dst, const __nv_bfloat16* pool, int g, const int (&row)[4]) {
+      const int ch = lane & 15;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+#pragma unroll 4
+        for (int it = 0; it < 16; ++it) {
+          const int key = 32 * k + 2 * it + (lane >> 4);
+          const int src = __shfl_sync(0xffffffffu, row[k], 2 * it + (lane >> 4));
+          const uint32_t off = (ch >> 3) * 16384 + key * 128 + (((ch & 7) ^ (key & 7)) << 4);
+          const bool valid = src != no_row;
+          ra_cp16(dst + off, pool + (static_cast<int64_t>(valid ? src : 0) * p.Hkv + g) * RA_D + ch * 8, valid);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // cp.async: once at most N copy groups are under way the oldest tile's K and V
+    // have landed; made visible to the tensor core, then announced
+    auto announce = [&](auto pending) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(decltype(pending)::value) : "memory");
+      fence_async_shared();
+      mbar_arrive(k_full(arrived & 1));
+      mbar_arrive(v_full(arrived & 1));
+      ++arrived;
+    };
+    RaWalk w;
+    w.init(p, st, units);
+    while (ok && w.next(p)) {
+      // Q: the buffer is free once the previous item's last S product is done
+      if (!mbar_wait_warp(q_empty, (issued_q & 1) ^ 1u, p.err, abort_flag)) { ok = false; break; }
+      if (el) {
+        mbar_arrive_expect_tx(q_full, 2u * GT * 128u);
+        const int t0 = w.rq.r0 + w.iq * p.TQ;
+        ra_tma_3d(sb + RA_OFF_Q, &p.tmQ, 0, w.ig * p.G, t0, q_full);
+        ra_tma_3d(sb + RA_OFF_Q + 16384, &p.tmQ, 64, w.ig * p.G, t0, q_full);
+      }
+      __syncwarp();
+      ++issued_q;
+      const long long L = static_cast<long long>(w.rq.ctx) + w.rq.n;
+      int row[4];
+      auto lookup = [&](int j) {
+        if (TMA) {
+          row[0] = lane < nbox ? pool_row(w.ib, static_cast<long long>(j) * RA_BKV + lane * p.box, L) : no_row;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) row[k] = pool_row(w.ib, static_cast<long long>(j) * RA_BKV + k * 32 + lane, L);
+        }
+      };
+      lookup(w.ta);
+      for (int j = w.ta; j < w.tb; ++j) {
+        const int s = issued_k & 1;
+        const uint32_t ph = (issued_k >> 1) & 1;
+        const uint32_t kd = sb + RA_OFF_K + s * RA_TILE, vd = sb + RA_OFF_V + s * RA_TILE;
+        const int col = w.ig * RA_D;
+        if (!mbar_wait_warp(k_empty(s), ph ^ 1u, p.err, abort_flag)) { ok = false; break; }
+        if (TMA) {
+          if (el) mbar_arrive_expect_tx(k_full(s), RA_TILE);
+          __syncwarp();
+          if (lane < nbox) {
+            tma_load_2d(kd + lane * p.box * 128, &p.tmK, col, row[0], k_full(s));
+            tma_load_2d(kd + 16384 + lane * p.box * 128, &p.tmK, col + 64, row[0], k_full(s));
+          }
+          __syncwarp();
+        } else {
+          gather(kd, p.kp, w.ig, row);
+          // tile j - 1 (all but the newest group), before the wait for room for V_j,
+          // which comes from a product behind S_(j-1)
+          if (j > w.ta) announce(std::integral_constant<int, 1>());
+        }
+        ++issued_k;
+        if (!mbar_wait_warp(v_empty(s), ph ^ 1u, p.err, abort_flag)) { ok = false; break; }
+        if (TMA) {
+          if (el) mbar_arrive_expect_tx(v_full(s), RA_TILE);
+          __syncwarp();
+          if (lane < nbox) {
+            tma_load_2d(vd + lane * p.box * 128, &p.tmV, col, row[0], v_full(s));
+            tma_load_2d(vd + 16384 + lane * p.box * 128, &p.tmV, col + 64, row[0], v_full(s));
+          }
+          __syncwarp();
+        } else {
+          gather(vd, p.vp, w.ig, row);
+        }
+        ++issued_v;
+        if (j + 1 < w.tb) lookup(j + 1);
+      }
+      // the piece's last tile: its products free Q, which the next piece waits for
+      if (!TMA && ok) announce(std::integral_constant<int, 0>());
+    }
+    if (!ok) *abort_flag = 1;
+    // copies still in flight must land before exit
+    if (issued_q > 0) mbar_wait(q_full, (issued_q - 1) & 1, p.err);
+    if (TMA) {
+      for (int j = (issued_k > 2 ? issued_k - 2 : 0); j < issued_k; ++j) mbar_wait(k_full(j & 1), (j >> 1) & 1, p.err);
+      for (int j = (issued_v > 2 ? issued_v - 2 : 0); j < issued_v; ++j) mbar_wait(v_full(j & 1), (j >> 1) & 1, p.err);
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA (whole warp; the elected lane issues) ----------------
+    // Step n (over all pieces) issues S_n, then the P V product of step n - 1,
+    // which may be the previous piece's last.
+    const bool el = elect_one();
+    const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);
+    const uint32_t idesc_pv = idesc_bf16_f32(128, 128, 0, 1);
+    auto issue_pv = [&](int gp, int ob, bool first) -> bool {
+      const int s = gp & 1;
+      const uint32_t ph = (gp >> 1) & 1;
+      if (!mbar_wait_warp(p_full(s), ph, p.err, abort_flag)) return false;
+      if (!mbar_wait_warp(v_full(s), ph, p.err, abort_flag)) return false;
+      tc_fence_after();
+      if (el) {
+        for (int kk = 0; kk < RA_BKV / 16; ++kk)   // P from TMEM (the first 64 columns of S[s])
+          umma_bf16_ta(tmem + 256 + ob * 128, tmem + s * 128 + kk * 8, ra_desc_v(sb + RA_OFF_V + s * RA_TILE, kk),
+                       idesc_pv, (!first || kk > 0) ? 1u : 0u);
+        umma_commit(v_empty(s));
+        umma_commit(p_done(s));
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = true;
+    int n = 0, k = 0, pend_n = -1, pend_ob = 0;
+    bool pend_first = false;
+    RaWalk w;
+    w.init(p, st, units);
+    for (; ok && w.next(p); ++k) {
+      const int ob = k & 1;
+      if (!mbar_wait_warp(q_full, k & 1, p.err, abort_flag)) { ok = false; break; }
+      for (int j = w.ta; j < w.tb; ++j, ++n) {
+        const int s = n & 1;
+        const uint32_t ph = (n >> 1) & 1;
+        if (!mbar_wait_warp(k_full(s), ph, p.err, abort_flag) ||
+            (n >= 2 && !mbar_wait_warp(s_free(s), ph ^ 1u, p.err, abort_flag))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (el) {
+          for (int kk = 0; kk < RA_D / 16; ++kk)
+            umma_bf16(tmem + s * 128, ra_desc_k(sb + RA_OFF_Q, kk), ra_desc_k(sb + RA_OFF_K + s * RA_TILE, kk), idesc_s,
+                      kk > 0);
+          umma_commit(k_empty(s));
+          umma_commit(s_full(s));
+          if (j == w.tb - 1) umma_commit(q_empty);   // the piece's last use of Q
+        }
+        __syncwarp();
+        if (pend_n >= 0 && !issue_pv(pend_n, pend_ob, pend_first)) { ok = false; break; }
+        // O[ob] takes this piece's first P V: the epilogue of piece k - 2 must have read it
+        if (j == w.ta && !mbar_wait_warp(o_empty(ob), ((k >> 1) & 1) ^ 1u, p.err, abort_flag)) { ok = false; break; }
+        pend_n = n;
+        pend_ob = ob;
+        pend_first = j == w.ta;
+      }
+    }
+    if (ok && pend_n >= 0 && !issue_pv(pend_n, pend_ob, pend_first)) ok = false;
+    if (!ok) *abort_flag = 1;
+    if (el) umma_commit(drain);
+    __syncwarp();
+    mbar_wait(drain, 0, p.err);
+  } else {
+    // ---------------- softmax / correction / epilogue ----------------
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;           // row within the tile = TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const int tok = r / p.G, hh = r - tok * p.G;
+    bool ok = true;
+    int n = 0, k = 0;
+    RaWalk w;
+    w.init(p, st, units);
+    for (; ok && w.next(p); ++k) {
+      const int ob = k & 1;
+      const int first_tok = w.iq * p.TQ;
+      const int toks = min(p.TQ, w.rq.n - first_tok);       // tokens of this tile
+      const bool busy = quarter * 32 < toks * p.G;          // some row of this warp is real
+      const bool mine = r < toks * p.G;
+      const long long qpos = static_cast<long long>(w.rq.ctx) + first_tok + min(tok, toks - 1);   // padding rows: the last real row's limit
+      const long long L = static_cast<long long>(w.rq.ctx) + w.rq.n;
+      const uint32_t oadr = tmem + lane_off + 256 + ob * 128;
+      float m = -INFINITY, l = 0.f;
+      for (int j = w.ta; j < w.tb; ++j, ++n) {
+        const int s = n & 1;
+        const uint32_t ph = (n >> 1) & 1;
+        const long long key0 = static_cast<long long>(j) * RA_BKV;
+        // the tile that holds the context's end: the value rows behind it become zero
+        if (TMA && key0 + RA_BKV > L) {
+          if (!mbar_wait_warp(v_full(s), ph, p.err, abort_flag)) { ok = false; break; }
+          if (key0 + r >= L) {
+            const uint32_t va = sb + RA_OFF_V + s * RA_TILE + r * 128;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              st_shared_v4(va + c * 16, 0u, 0u, 0u, 0u);
+              st_shared_v4(va + 16384 + c * 16, 0u, 0u, 0u, 0u);
+            }
+          }
+          fence_async_shared();
+        }
+        if (!mbar_wait_warp(s_full(s), ph, p.err, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t sadr = tmem + lane_off + s * 128;
+        if (!busy) {                               // no real row: P stays whatever it is, its O rows are never read
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(s_free(s));
+            mbar_arrive(p_full(s));
+          }
+          continue;
+        }
+        uint32_t sv[RA_BKV];
+        tmem_ld_32x32b_x32(sadr, *reinterpret_cast<uint32_t(*)[32]>(sv));
+        tmem_ld_32x32b_x32(sadr + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
+        tmem_ld_32x32b_x32(sadr + 64, *reinterpret_cast<uint32_t(*)[32]>(sv + 64));
+        tmem_ld_32x32b_x32(sadr + 96, *reinterpret_cast<uint32_t(*)[32]>(sv + 96));
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free(s));     // S[s] may be overwritten from here on
+        if (key0 + RA_BKV - 1 > w.rq.ctx + first_tok) {   // some row of the tile ends inside these keys
+          const int lim = static_cast<int>(min(qpos - key0, static_cast<long long>(RA_BKV)));   // keys 0 .. lim are kept
+#pragma unroll
+          for (int e = 0; e < RA_BKV; ++e)
+            if (e > lim) sv[e] = __float_as_uint(-INFINITY);
+        }
+        float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < RA_BKV; e += 4) {
+          m0 = fmaxf(m0, __uint_as_float(sv[e]));
+          m1 = fmaxf(m1, __uint_as_float(sv[e + 1]));
+          m2 = fmaxf(m2, __uint_as_float(sv[e + 2]));
+          m3 = fmaxf(m3, __uint_as_float(sv[e + 3]));
+        }
+        const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * p.scale_log2;
+        // The max is only raised when it grows by more than 2^8 (the final O / l
+        // cancels a stale one). A row of a later piece's tile can be fully masked
+        // (its token ends before these keys): mx = -inf, and m stays -inf.
+        const bool raise = mx > m + 8.0f;
+        const float m_new = raise ? mx : m;
+        const float alpha = raise ? ra_ex2(m - m_new) : 1.0f;
+        if (j > w.ta && __any_sync(0xffffffffu, raise)) {
+          if (!mbar_wait_warp(p_done(s ^ 1), ((n - 1) >> 1) & 1, p.err, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(oadr + c * 32, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+            tmem_st_32x32b_x32(oadr + c * 32, v);
+          }
+          tmem_st_wait();
+        }
+        const float neg = m_new > -INFINITY ? -m_new : 0.f;
+        const float sc = p.scale_log2;
+        float r0 = 0.f, r1 = 0.f, r2 = 0.f, r3 = 0.f;
+        uint32_t pk[64];
+#pragma unroll
+        for (int e = 0; e < RA_BKV; e += 4) {
+          const float p0 = ra_ex2(fmaf(__uint_as_float(sv[e]), sc, neg));
+          const float p1 = ra_ex2(fmaf(__uint_as_float(sv[e + 1]), sc, neg));
+          const float p2 = ra_ex2(fmaf(__uint_as_float(sv[e + 2]), sc, neg));
+          const float p3 = ra_ex2(fmaf(__uint_as_float(sv[e + 3]), sc, neg));
+          r0 += p0;
+          r1 += p1;
+          r2 += p2;
+          r3 += p3;
+          pk[e >> 1] = pack_bf16x2(p0, p1);        // P enters its product as bf16: half a step (2^-9) per weight
+          pk[(e >> 1) + 1] = pack_bf16x2(p2, p3);
+        }
+        tmem_st_32x32b_x32(sadr, *reinterpret_cast<uint32_t(*)[32]>(pk));
+        tmem_st_32x32b_x32(sadr + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
+        l = l * alpha + ((r0 + r1) + (r2 + r3));
+        m = m_new;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(s));
+      }
+      if (!ok) break;
+      // the piece's last P V product, step n - 1's
+      if (!mbar_wait_warp(p_done((n - 1) & 1), ((n - 1) >> 1) & 1, p.err, abort_flag)) { ok = false; break; }
+      tc_fence_after();
+      const bool whole = w.ta == 0 && w.tb == w.tiles;
+      if (busy) {
+        const int head = w.ig * p.G + hh;
+        const int64_t orow = static_cast<int64_t>(w.rq.r0 + first_tok + tok) * p.Hq + head;
+        const int64_t pc = (static_cast<int64_t>(cta) * 2 + (w.idx > 0 ? 1 : 0)) * RA_BQ + r;
+        const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(oadr + c * 32, v);
+          tmem_ld_wait();
+          if (!mine) continue;
+          if (whole) {
+            __nv_bfloat16* orow_p = p.o + orow * RA_D + c * 32;
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint4 x;
+              x.x = pack_bf16x2(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv);
+              x.y = pack_bf16x2(__uint_as_float(v[e + 2]) * inv, __uint_as_float(v[e + 3]) * inv);
+              x.z = pack_bf16x2(__uint_as_float(v[e + 4]) * inv, __uint_as_float(v[e + 5]) * inv);
+              x.w = pack_bf16x2(__uint_as_float(v[e + 6]) * inv, __uint_as_float(v[e + 7]) * inv);
+              *reinterpret_cast<uint4*>(orow_p + e) = x;
+            }
+          } else {
+            float* po = p.part_o + pc * RA_D + c * 32;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(po + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          }
+        }
+        if (mine) {
+          if (whole) {
+            if (p.lse) p.lse[orow] = (m + log2f(l)) * RA_LN2;
+          } else {
+            *reinterpret_cast<float2*>(p.part_ml + pc * 2) = make_float2(m, l);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_empty(ob));   // O[ob] may take piece k + 2's products
+    }
+    if (!ok) *abort_flag = 1;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// CTA (c, y): if the run boundary at CTA c's start is the first one that cuts its
+// item with key tiles on both sides, the rows 32 y .. 32 y + 31 of that item's
+// pieces are joined, one warp per row:
+//   O = sum_s O_s 2^(m_s - M) / sum_s l_s 2^(m_s - M).
+// Pieces lie in CTA order: CTA c - 1's (its last item), then c, c + 1, ... (each
+// one's first).
+constexpr int RC_THREADS = 256;
+__global__ void __launch_bounds__(RC_THREADS) ragged_combine_kernel(const __grid_constant__ RaParams p) {
+  pdl_enter();
+  const int c = blockIdx.x + 1;
+  const RaStart st = p.starts[c];
+  if (st.b < 0) return;
+  const long long P = st.P;
+  // not the first cut with tiles before it
+  if (st.off <= RA_ITEM_UNITS || st.off - P > RA_ITEM_UNITS) return;
+  const RaReq q = ra_req(p, st.b);
+  const long long len = ra_tiles(q, p.TQ, st.qt) + RA_ITEM_UNITS;
+  const int np = 1 + static_cast<int>((len - st.off + P - 1) / P);
+  const int first_tok = st.qt * p.TQ;
+  const int rows = min(p.TQ, q.n - first_tok) * p.G;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int slot0 = st.off - P >= 0 ? 0 : 1;       // CTA c - 1 met this item as its first one, or later
+  for (int r = blockIdx.y * 32 + warp; r < min(rows, static_cast<int>(blockIdx.y) * 32 + 32); r += RC_THREADS / 32) {
+    auto piece = [&](int s) { return (static_cast<int64_t>(c - 1 + s) * 2 + (s == 0 ? slot0 : 0)) * RA_BQ + r; };
+    float M = -INFINITY;
+    for (int s = lane; s < np; s += 32) M = fmaxf(M, p.part_ml[piece(s) * 2]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float l = 0.f, a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < np; ++s) {
+      const int64_t pc = piece(s);
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + pc * 2);
+      const float4 v = *reinterpret_cast<const float4*>(p.part_o + pc * RA_D + lane * 4);
+      if (!(ml.x > -INFINITY)) continue;           // a piece whose keys this row does not see
+      const float f = exp2f(ml.x - M);
+      l = fmaf(ml.y, f, l);
+      a0 = fmaf(v.x, f, a0);
+      a1 = fmaf(v.y, f, a1);
+      a2 = fmaf(v.z, f, a2);
+      a3 = fmaf(v.w, f, a3);
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int tok = r / p.G;
+    const int64_t orow = static_cast<int64_t>(q.r0 + first_tok + tok) * p.Hq + st.g * p.G + (r - tok * p.G);
+    uint2 x;
+    x.x = pack_bf16x2(a0 * inv, a1 * inv);
+    x.y = pack_bf16x2(a2 * inv, a3 * inv);
+    *reinterpret_cast<uint2*>(p.o + orow * RA_D + lane * 4) = x;
+    if (p.lse && lane == 0) p.lse[orow] = (M + log2f(l)) * RA_LN2;
+  }
+}
+
+kl_status ra_map(CUtensorMap* m, int rank, const void* ptr, const cuuint64_t* dims, const cuuint64_t* strides,
+                 const cuuint32_t* box) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return set_error(KL_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(KL_ERR_INVALID_ARG, "ragged attention: tensor map encode failed (%d)", (int)r);
+  return KL_OK;
+}
+
+struct RaWs {
+  size_t o, ml, starts, total;
+};
+RaWs ra_ws(int ctas) {
+  RaWs w;
+  w.o = 0;
+  w.ml = w.o + static_cast<size_t>(ctas) * 2 * RA_BQ * RA_D * 4;
+  w.starts = w.ml + align_up(static_cast<size_t>(ctas) * 2 * RA_BQ * 2 * 4, 256);
+  w.total = w.starts + align_up(static_cast<size_t>(ctas) * sizeof(RaStart), 256);
+  return w;
+}
+
+}  // namespace
+
+size_t ragged_attention_ws() { return ra_ws(num_sms()).total; }
+
+kl_status ragged_attention(const kl_ragged_cfg& rc, int Hq, int Hkv, const void* q, const void* kp, const void* vp,
+                           const int32_t* table, const int32_t* cu, const int32_t* ctx, void* o, float* lse, void* ws,
+                           size_t ws_bytes, cudaStream_t st) {
+  const int ctas = num_sms();
+  const RaWs lay = ra_ws(ctas);
+  if (!ws || ws_bytes < lay.total || (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return set_error(KL_ERR_NO_MEMORY, "ragged attention: workspace too small or not 256-byte aligned");
+  RaParams p;
+  memset(&p, 0, sizeof(p));
+  p.G = Hq / Hkv;
+  p.TQ = RA_BQ / p.G;
+  const bool tma = rc.block_size % 8 == 0;
+  p.box = 128;
+  while (tma && rc.block_size % p.box) p.box >>= 1;    // gcd(block_size, 128)
+  {
+    const cuuint64_t dq[3] = {RA_D, static_cast<cuuint64_t>(Hq), static_cast<cuuint64_t>(rc.T)};
+    const cuuint64_t sq[2] = {RA_D * 2, static_cast<cuuint64_t>(Hq) * RA_D * 2};
+    const cuuint32_t bq[3] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(p.TQ)};
+    KL_TRY(ra_map(&p.tmQ, 3, q, dq, sq, bq));
+  }
+  if (tma) {
+    const cuuint64_t dk[2] = {static_cast<cuuint64_t>(Hkv) * RA_D, static_cast<cuuint64_t>(rc.n_blocks) * rc.block_size};
+    const cuuint64_t sk[1] = {static_cast<cuuint64_t>(Hkv) * RA_D * 2};
+    const cuuint32_t bk[2] = {64, static_cast<cuuint32_t>(p.box)};
+    KL_TRY(ra_map(&p.tmK, 2, kp, dk, sk, bk));
+    KL_TRY(ra_map(&p.tmV, 2, vp, dk, sk, bk));
+  }
+  p.kp = static_cast<const __nv_bfloat16*>(kp);
+  p.vp = static_cast<const __nv_bfloat16*>(vp);
+  p.table = table;
+  p.cu = cu;
+  p.ctx = ctx;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  uint8_t* wb = static_cast<uint8_t*>(ws);
+  p.part_o = reinterpret_cast<float*>(wb + lay.o);
+  p.part_ml = reinterpret_cast<float*>(wb + lay.ml);
+  p.starts = reinterpret_cast<RaStart*>(wb + lay.starts);
+  p.B = rc.B;
+  p.T = rc.T;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.bs = rc.block_size;
+  p.max_blocks = rc.max_blocks;
+  p.n_blocks = rc.n_blocks;
+  p.scale_log2 = RA_LOG2E / sqrtf(static_cast<float>(RA_D));
+  p.err = device_error_word();
+  static uint64_t attr_done = 0;
+  int dev = 0;
+  KL_CUDA(cudaGetDevice(&dev));
+  if (dev < 64 && !(attr_done >> dev & 1u)) {
+    KL_CUDA(cudaFuncSetAttribute(ragged_attn_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(RA_SMEM)));
+    KL_CUDA(cudaFuncSetAttribute(ragged_attn_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(RA_SMEM)));
+    attr_done |= uint64_t(1) << dev;
+  }
+  {
+    // the lengths are on the device: the rows' queries and outputs are what the host knows of the traffic
+    ProfScope ps("ragged_attention", st, 0.0, 4.0 * rc.T * Hq * RA_D);
+    if (tma)
+      launch_pdl(ragged_attn_kernel<true>, ctas, RA_THREADS, RA_SMEM, st, p);
+    else
+      launch_pdl(ragged_attn_kernel<false>, ctas, RA_THREADS, RA_SMEM, st, p);
+  }
+  KL_CUDA(cudaGetLastError());
+  if (ctas > 1) {
+    ProfScope ps("ragged_combine", st, 0.0, 4.0 * ctas * RA_D);
+    launch_pdl(ragged_combine_kernel, dim3(ctas - 1, RA_BQ / 32), RC_THREADS, 0, st, p);
+    KL_CUDA(cudaGetLastError());
+  }
+  return KL_OK;
+}
+
+}  // namespace kl

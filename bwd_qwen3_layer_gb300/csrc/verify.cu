@@ -1,0 +1,355 @@
+// Drafted tokens judged by the target's probabilities (speculative decoding's
+// accept-or-resample rule, from given random numbers):
+//   draft t of row r is accepted iff u_r q_r(t) < p_r(t);
+//   at the first rejection the next token is drawn from max(0, p_r - q_r), after
+//   the last accepted draft from p: the smallest index i with
+//   C_i = sum_{j <= i} w_j > u sum_j w_j.
+//
+// Only one row of p (and q) per request is read whole: V x 4 B each, bound by
+// HBM for many requests and by latency for one. A cluster of eight CTAs takes
+// one request: each finds the row itself (at most a few gathers), sums its
+// eighth of the weights, the eight sums meet in distributed shared memory, and
+// the CTA in whose range the cumulative sum crosses u x total looks for the
+// place: its warps' sums name a stretch of about a thousand weights, which the
+// CTA sums once more (from L2), one vector per lane.
+//
+// An index must not depend on how a sum is split, so sums are held far beyond
+// the weights' own precision: p - q as an error-free pair of floats (two-sum,
+// Knuth), accumulated per thread in a pair (about 48 bits), and from there in
+// fp64. fp64 additions for every weight would cost more than the reads (two per
+// clock and SM). The acceptance test is exact: the product of two floats fits
+// a double.
+#include "internal.h"
+#include "kl_common.cuh"
+
+namespace kl {
+namespace {
+
+constexpr int DV_THREADS = 512;
+constexpr int DV_WARPS = DV_THREADS / 32;
+constexpr int DV_CL = 8;           // CTAs (one cluster) per request
+
+struct VerifyParams {
+  const void* p;
+  const void* q;
+  int64_t ldp, ldq;
+  const int32_t* tokens;
+  const int32_t* cu;
+  const float* ua;
+  const float* us;
+  int32_t* acc;
+  int32_t* next;
+  int B, T, V;
+  uint32_t* err;
+};
+
+template <typename T>
+__device__ __forceinline__ float dv_ld(const void* base, int64_t i) {
+  return Elem<T>::to_f(static_cast<const T*>(base)[i]);
+}
+
+// E elements of a row starting at column i (E = 1, or a 16-byte vector): columns
+// outside [0, V) give zero.
+template <typename T, int E>
+__device__ __forceinline__ void dv_load(const T* row, int64_t i, int V, float (&f)[E]) {
+  if constexpr (E == 1) {
+    f[0] = i < V ? Elem<T>::to_f(row[i]) : 0.f;
+  } else {
+    if (i >= 0 && i + E <= V) {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(row + i));
+      if constexpr (sizeof(T) == 4) {
+        f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y);
+        f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
+      } else {
+        const float2 x0 = unpack_bf16x2(a.x), x1 = unpack_bf16x2(a.y), x2 = unpack_bf16x2(a.z), x3 = unpack_bf16x2(a.w);
+        f[0] = x0.x; f[1] = x0.y; f[2] = x1.x; f[3] = x1.y;
+        f[4] = x2.x; f[5] = x2.y; f[6] = x3.x; f[7] = x3.y;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = i + e >= 0 && i + e < V ? Elem<T>::to_f(row[i + e]) : 0.f;
+    }
+  }
+}
+
+// A running sum as an unevaluated pair: hi + lo.
+struct Pair {
+  float hi, lo;
+  __device__ __forceinline__ void add(float x) {
+    const float s = hi + x, b = s - hi;
+    lo += (hi - (s - b)) + (x - b);
+    hi = s;
+  }
+  __device__ __forceinline__ double value() const { return static_cast<double>(hi) + static_cast<double>(lo); }
+};
+
+// Which weights a request's token is drawn from.
+enum { DV_P = 0, DV_REST = 1, DV_REST_LOOKUP = 2 };   // p; max(0, p - q); p without the draft
+
+// The weight p - q (or p) as an error-free pair; zero where it is not positive.
+__device__ __forceinline__ void dv_weight(int kind, float p, float q, int64_t col, int draft, float& w, float& we) {
+  w = p;
+  we = 0.f;
+  if (kind == DV_REST) {
+    w = p - q;
+    const float b = w - p;
+    we = (p - (w - b)) - (q + b);
+  } else if (kind == DV_REST_LOOKUP && col == draft) {
+    w = 0.f;
+  }
+  if (!(w > 0.f)) w = we = 0.f;
+}
+
+__device__ __forceinline__ double dv_warp_sum(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ double dv_warp_scan(double v, int lane) {   // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
+  return v;
+}
+// The two halves of a cluster-wide barrier: shared memory of another CTA may be
+// written once that CTA runs, so every CTA arrives at its start and waits just
+// before its first such write.
+__device__ __forceinline__ void dv_cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void dv_cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+__device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v) {
+  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
+}
+
+// The part of [0, n) whose cumulative sum crosses x: the first i with
+// before + sum_{j <= i} s_j > x; if rounding leaves none, the last one with a
+// positive sum; -1 if there is none. `before` becomes the sum in front of it.
+__device__ __forceinline__ int dv_cross(const double* s, int n, double x, double& before) {
+  int last = -1;
+  double c = before, at = before;
+  for (int i = 0; i < n; ++i) {
+    if (s[i] > 0.0) {
+      last = i;
+      at = c;
+      if (c + s[i] > x) break;
+    }
+    c += s[i];
+  }
+  before = at;
+  return last;
+}
+
+template <typename T, int E>
+__device__ void dv_request(const VerifyParams& p, int b, int rank, const T* prow, const T* qrow, int mis, int kind, int draft,
+                           int accepted, double (*slots)[DV_CL], double* wsum) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // columns in vectors of E: vector j holds columns E j - mis ..
+  const int nv = static_cast<int>((static_cast<int64_t>(p.V) + mis + E - 1) / E);
+  const int per_cta = (nv + DV_CL - 1) / DV_CL;
+  const int per_warp = (per_cta + DV_WARPS - 1) / DV_WARPS;
+  const int c0 = min(nv, rank * per_cta), c1 = min(nv, c0 + per_cta);
+  const int w0 = min(c1, c0 + warp * per_warp), w1 = min(c1, w0 + per_warp);
+  const double u = static_cast<double>(p.us[b]);
+
+  for (int attempt = 0; attempt < 2; ++attempt) {
+    Pair sum = {0.f, 0.f};
+#pragma unroll 4
+    for (int j = w0 + lane; j < w1; j += 32) {
+      const int64_t col = static_cast<int64_t>(j) * E - mis;
+      float fp[E], fq[E] = {};
+      dv_load<T, E>(prow, col, p.V, fp);
+      if (kind == DV_REST) dv_load<T, E>(qrow, col, p.V, fq);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        float w, we;
+        dv_weight(kind, fp[e], fq[e], col + e, draft, w, we);
+        sum.add(w);
+        sum.lo += we;
+      }
+    }
+    const double ws = dv_warp_sum(sum.value());
+    if (lane == 0) wsum[warp] = ws;
+    __syncthreads();
+    double mine = 0.0;
+    for (int w = 0; w < DV_WARPS; ++w) mine += wsum[w];
+    if (attempt == 0) dv_cluster_wait();
+    if (tid < DV_CL) st_cluster_f64(mapa_shared(smem_u32(&slots[attempt][rank]), tid), mine);
+    cluster_sync_all();
+    double total = 0.0;
+    for (int c = 0; c < DV_CL; ++c) total += slots[attempt][c];
+    if (attempt == 0 && kind != DV_P && !(total > 0.0)) {   // nothing left of p - q anywhere: p itself
+      kind = DV_P;
+      __syncthreads();                                      // wsum is written again
+      continue;
+    }
+    const double x = u * total;
+    double before = 0.0;
+    const int owner = total > 0.0 && total < INFINITY ? dv_cross(slots[attempt], DV_CL, x, before) : -1;
+    if (owner < 0) {
+      if (rank == 0 && tid == 0) {
+        p.acc[b] = accepted;
+        p.next[b] = -1;
+      }
+      return;
+    }
+    if (owner != rank) return;
+    const int ow = max(0, dv_cross(wsum, DV_WARPS, x, before));
+    // that warp's stretch once more, spread over the CTA: warp w takes its w-th sixteenth
+    const int s0 = min(c1, c0 + ow * per_warp), s1 = min(c1, s0 + per_warp);
+    const int piece = (s1 - s0 + DV_WARPS - 1) / DV_WARPS;
+    const int p0 = min(s1, s0 + warp * piece), p1 = min(s1, p0 + piece);
+    double part = 0.0;
+    for (int j = p0 + lane; j < p1; j += 32) {
+      const int64_t col = static_cast<int64_t>(j) * E - mis;
+      float fp[E], fq[E] = {};
+      dv_load<T, E>(prow, col, p.V, fp);
+      if (kind == DV_REST) dv_load<T, E>(qrow, col, p.V, fq);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        float w, we;
+        dv_weight(kind, fp[e], fq[e], col + e, draft, w, we);
+        part += static_cast<double>(w) + static_cast<double>(we);
+      }
+    }
+    part = dv_warp_sum(part);
+    __syncthreads();                                        // every thread has read wsum
+    if (lane == 0) wsum[warp] = part;
+    __syncthreads();
+    const int pw = max(0, dv_cross(wsum, DV_WARPS, x, before));
+    if (warp != pw) return;
+    // this warp's piece in order, 32 vectors at a time
+    int64_t found = -1, last = -1;
+    double c = before;
+    for (int j0 = p0; j0 < p1 && found < 0; j0 += 32) {
+      const int j = j0 + lane;
+      const int64_t col = static_cast<int64_t>(j) * E - mis;
+      double w[E], s = 0.0;
+      if (j < p1) {
+        float fp[E], fq[E] = {};
+        dv_load<T, E>(prow, col, p.V, fp);
+        if (kind == DV_REST) dv_load<T, E>(qrow, col, p.V, fq);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          float a, ae;
+          dv_weight(kind, fp[e], fq[e], col + e, draft, a, ae);
+          w[e] = static_cast<double>(a) + static_cast<double>(ae);
+          s += w[e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) w[e] = 0.0;
+      }
+      const double incl = dv_warp_scan(s, lane);
+      double at = c + (incl - s);
+      int64_t hit = -1, pos = -1;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        at += w[e];
+        if (w[e] > 0.0) {
+          pos = col + e;
+          if (hit < 0 && at > x) hit = col + e;
+        }
+      }
+      const unsigned hits = __ballot_sync(0xffffffffu, hit >= 0), any = __ballot_sync(0xffffffffu, pos >= 0);
+      if (hits) found = __shfl_sync(0xffffffffu, hit, __ffs(hits) - 1);
+      if (any) last = __shfl_sync(0xffffffffu, pos, 31 - __clz(any));
+      c += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) {
+      p.acc[b] = accepted;
+      p.next[b] = static_cast<int32_t>(found >= 0 ? found : last);   // rounding at the very end: the last positive weight
+    }
+    return;
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(DV_THREADS) draft_verify_kernel(const VerifyParams p) {
+  pdl_enter();
+  __shared__ double slots[2][DV_CL];
+  __shared__ double wsum[DV_WARPS];
+  __shared__ int s_acc;
+  const int b = blockIdx.x / DV_CL, rank = static_cast<int>(cluster_ctarank());
+  const int r0 = min(max(p.cu[b], 0), p.T), r1 = min(max(p.cu[b + 1], r0), p.T);
+  if (r1 <= r0) {                       // the whole cluster leaves here
+    if (rank == 0 && threadIdx.x == 0) {
+      p.acc[b] = 0;
+      p.next[b] = -1;
+    }
+    return;
+  }
+  dv_cluster_arrive();
+  if (threadIdx.x < 32) {
+    // the first draft that is not accepted, 32 at a time
+    int acc = r1 - 1 - r0;
+    for (int i0 = 0; i0 < r1 - 1 - r0; i0 += 32) {
+      const int i = i0 + static_cast<int>(threadIdx.x);
+      bool no = false;
+      if (i < r1 - 1 - r0) {
+        const int64_t row = r0 + i;
+        const int t = p.tokens[row + 1];
+        no = true;
+        if (t >= 0 && t < p.V) {
+          const double pt = dv_ld<T>(p.p, row * p.ldp + t);
+          const double qt = p.q ? dv_ld<T>(p.q, row * p.ldq + t) : 1.f;
+          no = !(static_cast<double>(p.ua[row]) * qt < pt);
+        } else if (rank == 0) {
+          record_error(p.err, KL_DEVERR_TARGET);
+        }
+      }
+      const unsigned m = __ballot_sync(0xffffffffu, no);
+      if (m) {
+        acc = i0 + __ffs(m) - 1;
+        break;
+      }
+    }
+    if (threadIdx.x == 0) s_acc = acc;
+  }
+  __syncthreads();
+  const int accepted = s_acc;
+  const int64_t row = r0 + accepted;
+  const bool rejected = row < r1 - 1;
+  const int kind = !rejected ? DV_P : p.q ? DV_REST : DV_REST_LOOKUP;
+  const int draft = rejected ? p.tokens[row + 1] : -1;
+  const T* prow = static_cast<const T*>(p.p) + row * p.ldp;
+  const T* qrow = kind == DV_REST ? static_cast<const T*>(p.q) + row * p.ldq : nullptr;
+  constexpr int E = 16 / sizeof(T);
+  // 16-byte vectors where both rows start at the same place of one (a whole row
+  // of an odd vocabulary starts anywhere); element by element where they do not
+  const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(prow) & 15u) / sizeof(T));
+  if (!qrow || mis == static_cast<int>((reinterpret_cast<uintptr_t>(qrow) & 15u) / sizeof(T)))
+    dv_request<T, E>(p, b, rank, prow, qrow, mis, kind, draft, accepted, slots, wsum);
+  else
+    dv_request<T, 1>(p, b, rank, prow, qrow, 0, kind, draft, accepted, slots, wsum);
+}
+
+}  // namespace
+
+kl_status draft_verify(const kl_verify_cfg& c, const void* p, int64_t ldp, const void* q, int64_t ldq,
+                       const int32_t* tokens, const int32_t* cu, const float* ua, const float* us, int32_t* acc,
+                       int32_t* next, cudaStream_t st) {
+  VerifyParams v = {p, q, ldp, ldq, tokens, cu, ua, us, acc, next, c.B, c.T, c.V, device_error_word()};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = DV_CL;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(c.B * DV_CL);
+  cfg.blockDim = dim3(DV_THREADS);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const double es = static_cast<double>(dtype_size(c.dtype));
+  ProfScope ps("draft_verify", st, 0.0, static_cast<double>(c.B) * c.V * es * (q ? 2 : 1));
+  if (c.dtype == KL_F32)
+    KL_CUDA(cudaLaunchKernelEx(&cfg, draft_verify_kernel<float>, v));
+  else
+    KL_CUDA(cudaLaunchKernelEx(&cfg, draft_verify_kernel<__nv_bfloat16>, v));
+  return KL_OK;
+}
+
+}  // namespace kl

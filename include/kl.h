@@ -80,6 +80,8 @@ typedef enum kl_dtype { KL_F32 = 0, KL_BF16 = 1 } kl_dtype;
 #define KL_DEVERR_PAGE 0x8u         /* a paged-cache position past its block-table row,
                                        or a table entry outside the pool (the access
                                        was skipped)                                   */
+#define KL_DEVERR_ROWS 0x10u        /* a ragged step has more new tokens than its tensors
+                                       have rows (the rows past the last were dropped) */
 
 KL_API const char* kl_version(void);
 KL_API const char* kl_status_str(kl_status s);
@@ -461,6 +463,121 @@ KL_API kl_status kl_layer_forward_paged(const kl_layer_cfg* cfg, const kl_paged_
                                         const kl_layer_weights* w, const void* X, void* Y, void* k_pool,
                                         void* v_pool, const int32_t* table, const int32_t* ctx, void* ws,
                                         size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* A ragged step over the paged cache: requests that decode, feed drafted     */
+/* tokens or feed a chunk of their prompt, side by side in one step. The      */
+/* pages' paged-KV paragraph in the form a server needs; the lengths live on  */
+/* the device, so a captured step serves every later one.                     */
+/* ------------------------------------------------------------------------ */
+
+/* Request b feeds cu_rows[b+1] - cu_rows[b] new tokens (zero or more); the
+ * step's tensors are ragged: row cu_rows[b] + i is request b's new token i, at
+ * position ctx[b] + i (ctx below zero counts as zero). cu_rows [B+1] int32 on
+ * the device, starting at 0 and not decreasing; rows from cu_rows[B] on are
+ * neither read nor written. Pools and tables are those of kl_paged_cfg. bf16,
+ * head dim 128, Hq / Hkv <= 128; pool rows (n_blocks * block_size * Hkv) below
+ * 2^31; T at most 2^24. int32 and fp32 arrays of these entry points need only
+ * 4-byte alignment (they may be pieces of one buffer). */
+typedef struct kl_ragged_cfg {
+  int32_t B;           /* requests in the step                               */
+  int32_t T;           /* rows of the step's tensors (room for all requests) */
+  int32_t block_size;  /* tokens per cache block                             */
+  int32_t max_blocks;  /* length of each block-table row                     */
+  int32_t n_blocks;    /* blocks in each pool                                */
+} kl_ragged_cfg;
+
+/* A step's block tables, row offsets, positions and cache slots from the
+ * requests' lengths, in one launch. All arrays are int32 on the device.
+ *   n_new [B]      new tokens of each request; 0: none this step; below 0: the
+ *                  request has ended and gives its blocks back
+ *   ctx [B]        tokens already in the cache
+ * Updated in place (the state a server keeps):
+ *   table [B*max_blocks], held [B]  each request's blocks and how many it holds
+ *                  (a request may hold more than ctx[b] fills, after rejected
+ *                  drafts: those are used first)
+ *   free_list [n_blocks], n_free [1]  the free blocks, taken from the end
+ * Written:
+ *   cu_rows [B+1]  row offsets (at most T)
+ *   pos, slots [T] each row's position and its pool slot block * block_size +
+ *                  offset; -1 where the row has no block
+ *   missing [1]    blocks that were wanted and not there
+ * Request b wants ceil((ctx + n_new) / block_size) blocks (max_blocks at most)
+ * when it feeds tokens. In request order each takes what it lacks, the k-th
+ * block taken being free_list[n_free - 1 - k]; from the first request on that
+ * cannot have all its blocks none is taken any more, such a request's new table
+ * entries become -1 and the blocks it lacks count in *missing. Then the blocks
+ * of ended requests are appended to the list, in request order and table order.
+ * Rows beyond T are dropped (KL_DEVERR_ROWS); a position past its table row
+ * has slot -1 (KL_DEVERR_PAGE). */
+KL_API kl_status kl_ragged_plan(const kl_ragged_cfg* rc, const int32_t* n_new, const int32_t* ctx, int32_t* table,
+                                int32_t* held, int32_t* free_list, int32_t* n_free, int32_t* cu_rows, int32_t* pos,
+                                int32_t* slots, int32_t* missing, void* stream);
+/* The new tokens' q and k heads: RMSNorm over each head with the gains gamma_q,
+ * gamma_k [d] (both NULL: no norm), then the rotation at position pos[row] with
+ * planes (i, i + d/2) or, rope_interleaved, (2i, 2i + 1). q goes to q_out (may
+ * be q_pre), k and the unchanged v to slot slots[row] of the pools, all in one
+ * launch. q_pre, q_out [T, Hq*d], k_pre, v [T, Hkv*d]; rope_base at least 1. A row whose slot is below
+ * zero leaves the pools alone; a slot past the pool is skipped and reported
+ * (KL_DEVERR_PAGE). Two rows must not have the same slot. */
+KL_API kl_status kl_ragged_qkv_rope(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
+                                    const void* q_pre, const void* k_pre, const void* v, const void* gamma_q,
+                                    const void* gamma_k, float eps, float rope_base, int32_t rope_interleaved,
+                                    const int32_t* cu_rows, const int32_t* pos, const int32_t* slots, void* q_out,
+                                    void* k_pool, void* v_pool, void* stream);
+/* Causal GQA attention of every new token over its request's cache: row
+ * cu_rows[b] + i sees positions 0 .. ctx[b] + i, whose keys and values
+ * (this step's too) are already written. Scale 1/sqrt(d); query head h reads kv
+ * head floor(h * Hkv / Hq). q, o [T, Hq*d]; lse [T, Hq] fp32 (natural log) or
+ * NULL. Slots behind a request's last token may hold anything. A position past
+ * its table row, or whose table entry lies outside the pool, reads as a zero key
+ * and value and is reported (KL_DEVERR_PAGE). The workspace (256-byte aligned)
+ * does not depend on the lengths; steps that may run at the same time need one
+ * each. o and lse must not overlap the inputs. */
+KL_API size_t kl_ragged_attention_ws_bytes(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d);
+KL_API kl_status kl_ragged_attention(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
+                                     const void* q, const void* k_pool, const void* v_pool, const int32_t* table,
+                                     const int32_t* cu_rows, const int32_t* ctx, void* o, float* lse, void* ws,
+                                     size_t ws_bytes, void* stream);
+
+/* Drafted tokens judged by the target's probabilities. Request b's rows
+ * r0 = cu_rows[b] .. r1 - 1 (r1 = cu_rows[b+1]) were fed tokens[r0] (its last
+ * token) and the drafts tokens[r0+1 .. r1-1]. p [T, V] holds the target's
+ * probabilities after each row (row stride ldp), q [T, V] the draft's own (row
+ * r is what the draft of row r + 1 was drawn from; stride ldq; a request's last
+ * row is not read), or NULL for drafts that were not drawn (a lookup, a greedy
+ * draft: q is one at the draft). u_accept [T], u_sample [B]: uniform random
+ * numbers in [0, 1), fp32.
+ * The draft t of row r + 1 is accepted iff u_accept[r] * q[r, t] < p[r, t];
+ * n_accepted[b] counts the drafts before the first one that is not. The next
+ * token comes from the row r0 + n_accepted[b] with weights max(0, p - q) after a
+ * rejection (p alone if that is zero everywhere) and p when every draft was
+ * accepted or none was given: next_token[b] is the smallest index whose
+ * cumulative weight exceeds u_sample[b] times the sum. Probabilities need not
+ * sum to one; a weight that is NaN counts as zero; -1 where no weight is positive or their sum
+ * is not finite. A request without rows gets 0 and -1. A draft outside [0, V)
+ * is not accepted and reported (KL_DEVERR_TARGET).
+ * Products and sums are held to 48 bits or more. All on the device, p and q of
+ * type dtype (fp32 or bf16). One launch, no workspace. */
+typedef struct kl_verify_cfg {
+  int32_t B;        /* requests                                              */
+  int32_t T;        /* rows of p, q, tokens and u_accept                     */
+  int32_t V;        /* vocabulary                                            */
+  int32_t dtype;    /* kl_dtype of p and q                                   */
+} kl_verify_cfg;
+KL_API kl_status kl_draft_verify(const kl_verify_cfg* cfg, const void* p, int64_t ldp, const void* q, int64_t ldq,
+                                 const int32_t* tokens, const int32_t* cu_rows, const float* u_accept,
+                                 const float* u_sample, int32_t* n_accepted, int32_t* next_token, void* stream);
+/* The layer forward of kl_layer_forward_paged for a ragged step: X, Y [T, H]
+ * with cfg->B = 1 and cfg->S = rc->T (the step's rows as one run of rows);
+ * positions, slots and cu_rows as kl_ragged_plan leaves them. The projections
+ * run over all T rows: rows of Y from cu_rows[B] on are written and mean
+ * nothing, and nothing of such rows reaches the others. */
+KL_API size_t kl_layer_forward_ragged_ws_bytes(const kl_layer_cfg* cfg, const kl_ragged_cfg* rc);
+KL_API kl_status kl_layer_forward_ragged(const kl_layer_cfg* cfg, const kl_ragged_cfg* rc, const kl_layer_weights* w,
+                                         const void* X, void* Y, void* k_pool, void* v_pool, const int32_t* table,
+                                         const int32_t* cu_rows, const int32_t* ctx, const int32_t* pos,
+                                         const int32_t* slots, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -58,3 +58,4 @@ from .paged import (  # noqa: F401,E402
     positions,
     rope_at,
 )
+from .ragged import draft_verify, ragged_attention, ragged_plan  # noqa: F401,E402
