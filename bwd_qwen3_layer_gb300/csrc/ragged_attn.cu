@@ -21,9 +21,9 @@
 // results repeat bit for bit. The workspace holds two pieces per CTA and does
 // not depend on the lengths.
 //
-// Roles (6 warps): warp 0 looks up the pages and issues the copies, warp 1
-// issues the products, warps 2..5 are the softmax (thread = query row = TMEM
-// lane): the scheme of the training forward's persistent kernel.
+// Roles (7 warps): warp 0 looks up the pages and copies Q and the keys, warp 1
+// the values, warp 2 issues the products, warps 3..6 are the softmax (thread =
+// query row = TMEM lane): the scheme of the training forward's persistent kernel.
 // Pages: with block_size a multiple of 8 a key tile is 128 / box TMA boxes of
 // box = gcd(block_size, 128) rows, each found through the table; a box past the
 // context, past its table row or whose table entry lies outside the pool starts
@@ -46,9 +46,13 @@ namespace {
 constexpr int RA_D = 128;        // head dim
 constexpr int RA_BQ = 128;       // rows of a query tile
 constexpr int RA_BKV = 128;      // keys per tile
-constexpr int RA_THREADS = 192;
-constexpr uint32_t RA_TILE = 128 * 128 * 2;   // 32 KB: two 64-column swizzle blocks of 16 KB
-constexpr int RA_NST = 2;                     // stages of the K and of the V ring
+constexpr int RA_WARPS = 7;      // K copies, V copies, products, four of softmax
+constexpr int RA_THREADS = 32 * RA_WARPS;
+// A key or value tile (32 KB) is 16 groups of 8 keys, each group two swizzled
+// blocks of 8 rows x 64 columns (1 KB): a page of 8 m tokens is then one TMA box
+// of m groups x 2 column blocks x 8 rows, one copy instruction instead of two.
+constexpr uint32_t RA_TILE = 128 * 128 * 2;
+constexpr int RA_NST = 3;                     // stages of the K and of the V ring
 constexpr uint32_t RA_OFF_Q = 0;
 constexpr uint32_t RA_OFF_K = RA_OFF_Q + RA_TILE;
 constexpr uint32_t RA_OFF_V = RA_OFF_K + RA_NST * RA_TILE;
@@ -90,19 +94,31 @@ __device__ __forceinline__ float ra_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// K-major operand (two 64-column swizzle blocks of 128 rows), k-step kk of 16 columns
-__device__ __forceinline__ uint64_t ra_desc_k(uint32_t base, int kk) {
+// Q, K-major (two 64-column swizzle blocks of 128 rows), k-step kk of 16 columns
+__device__ __forceinline__ uint64_t ra_desc_q(uint32_t base, int kk) {
   return smem_desc_sw128(base + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024);
 }
-// V as the MN-major B operand: n = head dim in two 64-wide blocks, k-step kk of 16 keys
+// K, K-major, in groups of 8 keys 2 KB apart
+__device__ __forceinline__ uint64_t ra_desc_k(uint32_t base, int kk) {
+  return smem_desc_sw128(base + (kk >> 2) * 1024 + (kk & 3) * 32, 16, 2048);
+}
+// V as the MN-major B operand: n = head dim in two 64-wide blocks 1 KB apart,
+// k-step kk of 16 keys = two groups
 __device__ __forceinline__ uint64_t ra_desc_v(uint32_t base, int kk) {
-  return smem_desc_sw128(base + kk * 2048, 16384, 1024);
+  return smem_desc_sw128(base + kk * 4096, 1024, 2048);
 }
 __device__ __forceinline__ void ra_tma_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void ra_tma_4d(uint32_t dst, const void* tmap, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void ra_cp16(uint32_t dst, const void* src, bool valid) {
@@ -221,18 +237,18 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
   // that a warp which runs a step ahead of another cannot count for its phase
   const uint32_t q_full = bar + 0, q_empty = bar + 8, drain = bar + 16;
   auto k_full = [&](int s) { return bar + 24 + 8 * s; };
-  auto k_empty = [&](int s) { return bar + 40 + 8 * s; };
-  auto v_full = [&](int s) { return bar + 56 + 8 * s; };
-  auto v_empty = [&](int s) { return bar + 72 + 8 * s; };
-  auto s_full = [&](int s) { return bar + 88 + 8 * s; };    // S_n computed
-  auto s_free = [&](int s) { return bar + 104 + 8 * s; };   // S_n read
-  auto p_full = [&](int s) { return bar + 120 + 8 * s; };   // P_n written (and V_n's tail cleared)
-  auto p_done = [&](int s) { return bar + 136 + 8 * s; };   // O += P_n V_n computed
-  auto o_empty = [&](int s) { return bar + 152 + 8 * s; };  // a piece's O read
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + RA_OFF_BAR + 168);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + RA_OFF_BAR + 172);
-  RaStart* start = reinterpret_cast<RaStart*>(smem + RA_OFF_BAR + 176);
-  long long* wsum = reinterpret_cast<long long*>(smem + RA_OFF_BAR + 256);   // [8]: the warps' unit sums, then W
+  auto k_empty = [&](int s) { return bar + 48 + 8 * s; };
+  auto v_full = [&](int s) { return bar + 72 + 8 * s; };
+  auto v_empty = [&](int s) { return bar + 96 + 8 * s; };
+  auto s_full = [&](int s) { return bar + 120 + 8 * s; };   // S_n computed
+  auto s_free = [&](int s) { return bar + 136 + 8 * s; };   // S_n read
+  auto p_full = [&](int s) { return bar + 152 + 8 * s; };   // P_n written (and V_n's tail cleared)
+  auto p_done = [&](int s) { return bar + 168 + 8 * s; };   // O += P_n V_n computed
+  auto o_empty = [&](int s) { return bar + 184 + 8 * s; };  // a piece's O read
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + RA_OFF_BAR + 200);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + RA_OFF_BAR + 204);
+  RaStart* start = reinterpret_cast<RaStart*>(smem + RA_OFF_BAR + 208);
+  long long* wsum = reinterpret_cast<long long*>(smem + RA_OFF_BAR + 256);   // [8]: the warps' unit sums, then this CTA's units
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
@@ -240,11 +256,13 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < RA_NST; ++s) {
       mbar_init(k_full(s), TMA ? 1 : 32);
       mbar_init(k_empty(s), 1);
       mbar_init(v_full(s), TMA ? 1 : 32);
       mbar_init(v_empty(s), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(s_full(s), 1);
       mbar_init(s_free(s), 4);
       mbar_init(p_full(s), 4);
@@ -255,7 +273,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
+  if (warp == 2) {
     tmem_alloc(smem_u32(tmem_holder), 512);
     tmem_relinquish();
   }
@@ -275,7 +293,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     if (lane == 31) wsum[warp] = incl;
     __syncthreads();
     long long before = 0, W = 0;
-    for (int w = 0; w < RA_THREADS / 32; ++w) {
+    for (int w = 0; w < RA_WARPS; ++w) {
       if (w < warp) before += wsum[w];
       W += wsum[w];
     }
@@ -319,19 +337,22 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
   if (threadIdx.x == 0) p.starts[cta] = st;
   const int GT = p.G * p.TQ;            // rows of a full query tile
 
-  if (warp == 0) {
-    // ---------------- copies (whole warp: lane = page box of a tile) ----------------
+  if (warp < 2) {
+    // ------- copies (warp 0: Q and K, warp 1: V; lane = page box of a tile) -------
+    const bool is_k = warp == 0;
     const bool el = elect_one();
+    const CUtensorMap* tm = is_k ? &p.tmK : &p.tmV;
+    const __nv_bfloat16* pool = is_k ? p.kp : p.vp;
+    const uint32_t ring = sb + (is_k ? RA_OFF_K : RA_OFF_V);
+    const uint32_t full0 = is_k ? k_full(0) : v_full(0), empty0 = is_k ? k_empty(0) : v_empty(0);
     if (el) {
-      tma_prefetch_desc(&p.tmQ);
-      if (TMA) {
-        tma_prefetch_desc(&p.tmK);
-        tma_prefetch_desc(&p.tmV);
-      }
+      if (is_k) tma_prefetch_desc(&p.tmQ);
+      if (TMA) tma_prefetch_desc(tm);
     }
     const int nbox = RA_BKV / p.box;
     const int no_row = p.n_blocks * p.bs;         // past the pool's last row: filled with zeros
-    int issued_q = 0, issued_k = 0, issued_v = 0, arrived = 0;
+    int issued_q = 0, issued = 0, s = 0, as = 0;  // s: the ring's stage; as: the next one to announce
+    uint32_t ph = 1;                              // parity that an empty stage's wait passes with
     bool ok = true;
     // the pool row of position pos, or no_row
     auto pool_row = [&](int b, long long pos, long long L) {
@@ -344,8 +365,8 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
       }
       return blk * p.bs + static_cast<int>(pos - static_cast<long long>(lb) * p.bs);
     };
-    // cp.async: the K (or V) rows of one tile; row[k] of lane l is the pool row of key 32 k + l
-    auto gather = [&](uint32_t dst, const __nv_bfloat16* pool, int g, const int (&row)[4]) {
+    // cp.async: the rows of one tile; row[k] of lane l is the pool row of key 32 k + l
+    auto gather = [&](uint32_t dst, int g, const int (&row)[4]) {
       const int ch = lane & 15;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -353,35 +374,36 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
         for (int it = 0; it < 16; ++it) {
           const int key = 32 * k + 2 * it + (lane >> 4);
           const int src = __shfl_sync(0xffffffffu, row[k], 2 * it + (lane >> 4));
-          const uint32_t off = (ch >> 3) * 16384 + key * 128 + (((ch & 7) ^ (key & 7)) << 4);
+          const uint32_t off = (key >> 3) * 2048 + (ch >> 3) * 1024 + (key & 7) * 128 + (((ch & 7) ^ (key & 7)) << 4);
           const bool valid = src != no_row;
           ra_cp16(dst + off, pool + (static_cast<int64_t>(valid ? src : 0) * p.Hkv + g) * RA_D + ch * 8, valid);
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    // cp.async: once at most N copy groups are under way the oldest tile's K and V
-    // have landed; made visible to the tensor core, then announced
+    // cp.async: once at most N copy groups are under way the oldest tile has
+    // landed; made visible to the tensor core, then announced
     auto announce = [&](auto pending) {
       asm volatile("cp.async.wait_group %0;" ::"n"(decltype(pending)::value) : "memory");
       fence_async_shared();
-      mbar_arrive(k_full(arrived & 1));
-      mbar_arrive(v_full(arrived & 1));
-      ++arrived;
+      mbar_arrive(full0 + 8 * as);
+      as = as == RA_NST - 1 ? 0 : as + 1;
     };
     RaWalk w;
     w.init(p, st, units);
     while (ok && w.next(p)) {
-      // Q: the buffer is free once the previous item's last S product is done
-      if (!mbar_wait_warp(q_empty, (issued_q & 1) ^ 1u, p.err, abort_flag)) { ok = false; break; }
-      if (el) {
-        mbar_arrive_expect_tx(q_full, 2u * GT * 128u);
-        const int t0 = w.rq.r0 + w.iq * p.TQ;
-        ra_tma_3d(sb + RA_OFF_Q, &p.tmQ, 0, w.ig * p.G, t0, q_full);
-        ra_tma_3d(sb + RA_OFF_Q + 16384, &p.tmQ, 64, w.ig * p.G, t0, q_full);
+      if (is_k) {
+        // Q: the buffer is free once the previous piece's last S product is done
+        if (!mbar_wait_warp(q_empty, (issued_q & 1) ^ 1u, p.err, abort_flag)) { ok = false; break; }
+        if (el) {
+          mbar_arrive_expect_tx(q_full, 2u * GT * 128u);
+          const int t0 = w.rq.r0 + w.iq * p.TQ;
+          ra_tma_3d(sb + RA_OFF_Q, &p.tmQ, 0, w.ig * p.G, t0, q_full);
+          ra_tma_3d(sb + RA_OFF_Q + 16384, &p.tmQ, 64, w.ig * p.G, t0, q_full);
+        }
+        __syncwarp();
+        ++issued_q;
       }
-      __syncwarp();
-      ++issued_q;
       const long long L = static_cast<long long>(w.rq.ctx) + w.rq.n;
       int row[4];
       auto lookup = [&](int j) {
@@ -394,39 +416,22 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
       };
       lookup(w.ta);
       for (int j = w.ta; j < w.tb; ++j) {
-        const int s = issued_k & 1;
-        const uint32_t ph = (issued_k >> 1) & 1;
-        const uint32_t kd = sb + RA_OFF_K + s * RA_TILE, vd = sb + RA_OFF_V + s * RA_TILE;
-        const int col = w.ig * RA_D;
-        if (!mbar_wait_warp(k_empty(s), ph ^ 1u, p.err, abort_flag)) { ok = false; break; }
+        if (!mbar_wait_warp(empty0 + 8 * s, ph, p.err, abort_flag)) { ok = false; break; }
+        const uint32_t dst = ring + s * RA_TILE;
         if (TMA) {
-          if (el) mbar_arrive_expect_tx(k_full(s), RA_TILE);
+          if (el) mbar_arrive_expect_tx(full0 + 8 * s, RA_TILE);
           __syncwarp();
-          if (lane < nbox) {
-            tma_load_2d(kd + lane * p.box * 128, &p.tmK, col, row[0], k_full(s));
-            tma_load_2d(kd + 16384 + lane * p.box * 128, &p.tmK, col + 64, row[0], k_full(s));
-          }
+          if (lane < nbox) ra_tma_4d(dst + lane * p.box * 256, tm, 0, 0, 2 * w.ig, row[0] >> 3, full0 + 8 * s);
           __syncwarp();
         } else {
-          gather(kd, p.kp, w.ig, row);
-          // tile j - 1 (all but the newest group), before the wait for room for V_j,
-          // which comes from a product behind S_(j-1)
-          if (j > w.ta) announce(std::integral_constant<int, 1>());
+          gather(dst, w.ig, row);
+          if (j > w.ta) announce(std::integral_constant<int, 1>());   // the tile before
         }
-        ++issued_k;
-        if (!mbar_wait_warp(v_empty(s), ph ^ 1u, p.err, abort_flag)) { ok = false; break; }
-        if (TMA) {
-          if (el) mbar_arrive_expect_tx(v_full(s), RA_TILE);
-          __syncwarp();
-          if (lane < nbox) {
-            tma_load_2d(vd + lane * p.box * 128, &p.tmV, col, row[0], v_full(s));
-            tma_load_2d(vd + 16384 + lane * p.box * 128, &p.tmV, col + 64, row[0], v_full(s));
-          }
-          __syncwarp();
-        } else {
-          gather(vd, p.vp, w.ig, row);
+        ++issued;
+        if (++s == RA_NST) {
+          s = 0;
+          ph ^= 1u;
         }
-        ++issued_v;
         if (j + 1 < w.tb) lookup(j + 1);
       }
       // the piece's last tile: its products free Q, which the next piece waits for
@@ -436,32 +441,36 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     // copies still in flight must land before exit
     if (issued_q > 0) mbar_wait(q_full, (issued_q - 1) & 1, p.err);
     if (TMA) {
-      for (int j = (issued_k > 2 ? issued_k - 2 : 0); j < issued_k; ++j) mbar_wait(k_full(j & 1), (j >> 1) & 1, p.err);
-      for (int j = (issued_v > 2 ? issued_v - 2 : 0); j < issued_v; ++j) mbar_wait(v_full(j & 1), (j >> 1) & 1, p.err);
+      for (int j = max(0, issued - RA_NST); j < issued; ++j) mbar_wait(full0 + 8 * (j % RA_NST), (j / RA_NST) & 1, p.err);
     } else {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
-  } else if (warp == 1) {
+  } else if (warp == 2) {
     // ---------------- MMA (whole warp; the elected lane issues) ----------------
     // Step n (over all pieces) issues S_n, then the P V product of step n - 1,
     // which may be the previous piece's last.
     const bool el = elect_one();
     const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);
     const uint32_t idesc_pv = idesc_bf16_f32(128, 128, 0, 1);
+    int vs = 0, ks = 0;                       // stages of the V and K rings
+    uint32_t vph = 0, kph = 0;
     auto issue_pv = [&](int gp, int ob, bool first) -> bool {
       const int s = gp & 1;
-      const uint32_t ph = (gp >> 1) & 1;
-      if (!mbar_wait_warp(p_full(s), ph, p.err, abort_flag)) return false;
-      if (!mbar_wait_warp(v_full(s), ph, p.err, abort_flag)) return false;
+      if (!mbar_wait_warp(p_full(s), (gp >> 1) & 1, p.err, abort_flag)) return false;
+      if (!mbar_wait_warp(v_full(vs), vph, p.err, abort_flag)) return false;
       tc_fence_after();
       if (el) {
         for (int kk = 0; kk < RA_BKV / 16; ++kk)   // P from TMEM (the first 64 columns of S[s])
-          umma_bf16_ta(tmem + 256 + ob * 128, tmem + s * 128 + kk * 8, ra_desc_v(sb + RA_OFF_V + s * RA_TILE, kk),
+          umma_bf16_ta(tmem + 256 + ob * 128, tmem + s * 128 + kk * 8, ra_desc_v(sb + RA_OFF_V + vs * RA_TILE, kk),
                        idesc_pv, (!first || kk > 0) ? 1u : 0u);
-        umma_commit(v_empty(s));
+        umma_commit(v_empty(vs));
         umma_commit(p_done(s));
       }
       __syncwarp();
+      if (++vs == RA_NST) {
+        vs = 0;
+        vph ^= 1u;
+      }
       return true;
     };
     bool ok = true;
@@ -474,22 +483,25 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
       if (!mbar_wait_warp(q_full, k & 1, p.err, abort_flag)) { ok = false; break; }
       for (int j = w.ta; j < w.tb; ++j, ++n) {
         const int s = n & 1;
-        const uint32_t ph = (n >> 1) & 1;
-        if (!mbar_wait_warp(k_full(s), ph, p.err, abort_flag) ||
-            (n >= 2 && !mbar_wait_warp(s_free(s), ph ^ 1u, p.err, abort_flag))) {
+        if (!mbar_wait_warp(k_full(ks), kph, p.err, abort_flag) ||
+            (n >= 2 && !mbar_wait_warp(s_free(s), ((n >> 1) & 1) ^ 1u, p.err, abort_flag))) {
           ok = false;
           break;
         }
         tc_fence_after();
         if (el) {
           for (int kk = 0; kk < RA_D / 16; ++kk)
-            umma_bf16(tmem + s * 128, ra_desc_k(sb + RA_OFF_Q, kk), ra_desc_k(sb + RA_OFF_K + s * RA_TILE, kk), idesc_s,
+            umma_bf16(tmem + s * 128, ra_desc_q(sb + RA_OFF_Q, kk), ra_desc_k(sb + RA_OFF_K + ks * RA_TILE, kk), idesc_s,
                       kk > 0);
-          umma_commit(k_empty(s));
+          umma_commit(k_empty(ks));
           umma_commit(s_full(s));
           if (j == w.tb - 1) umma_commit(q_empty);   // the piece's last use of Q
         }
         __syncwarp();
+        if (++ks == RA_NST) {
+          ks = 0;
+          kph ^= 1u;
+        }
         if (pend_n >= 0 && !issue_pv(pend_n, pend_ob, pend_first)) { ok = false; break; }
         // O[ob] takes this piece's first P V: the epilogue of piece k - 2 must have read it
         if (j == w.ta && !mbar_wait_warp(o_empty(ob), ((k >> 1) & 1) ^ 1u, p.err, abort_flag)) { ok = false; break; }
@@ -529,13 +541,14 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
         const long long key0 = static_cast<long long>(j) * RA_BKV;
         // the tile that holds the context's end: the value rows behind it become zero
         if (TMA && key0 + RA_BKV > L) {
-          if (!mbar_wait_warp(v_full(s), ph, p.err, abort_flag)) { ok = false; break; }
+          const int vs = n % RA_NST;
+          if (!mbar_wait_warp(v_full(vs), (n / RA_NST) & 1, p.err, abort_flag)) { ok = false; break; }
           if (key0 + r >= L) {
-            const uint32_t va = sb + RA_OFF_V + s * RA_TILE + r * 128;
+            const uint32_t va = sb + RA_OFF_V + vs * RA_TILE + (r >> 3) * 2048 + (r & 7) * 128;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               st_shared_v4(va + c * 16, 0u, 0u, 0u, 0u);
-              st_shared_v4(va + 16384 + c * 16, 0u, 0u, 0u, 0u);
+              st_shared_v4(va + 1024 + c * 16, 0u, 0u, 0u, 0u);
             }
           }
           fence_async_shared();
@@ -671,7 +684,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 2) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -735,7 +748,7 @@ kl_status ra_map(CUtensorMap* m, int rank, const void* ptr, const cuuint64_t* di
                  const cuuint32_t* box) {
   auto fn = tensor_map_encoder();
   if (!fn) return set_error(KL_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
-  const cuuint32_t estr[3] = {1, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -780,11 +793,14 @@ kl_status ragged_attention(const kl_ragged_cfg& rc, int Hq, int Hkv, const void*
     KL_TRY(ra_map(&p.tmQ, 3, q, dq, sq, bq));
   }
   if (tma) {
-    const cuuint64_t dk[2] = {static_cast<cuuint64_t>(Hkv) * RA_D, static_cast<cuuint64_t>(rc.n_blocks) * rc.block_size};
-    const cuuint64_t sk[1] = {static_cast<cuuint64_t>(Hkv) * RA_D * 2};
-    const cuuint32_t bk[2] = {64, static_cast<cuuint32_t>(p.box)};
-    KL_TRY(ra_map(&p.tmK, 2, kp, dk, sk, bk));
-    KL_TRY(ra_map(&p.tmV, 2, vp, dk, sk, bk));
+    // (64 columns, 8 rows, column blocks, groups of 8 rows)
+    const cuuint64_t pitch = static_cast<cuuint64_t>(Hkv) * RA_D * 2;
+    const cuuint64_t dk[4] = {64, 8, static_cast<cuuint64_t>(Hkv) * 2,
+                              static_cast<cuuint64_t>(rc.n_blocks) * rc.block_size / 8};
+    const cuuint64_t sk[3] = {pitch, 128, 8 * pitch};
+    const cuuint32_t bk[4] = {64, 8, 2, static_cast<cuuint32_t>(p.box / 8)};
+    KL_TRY(ra_map(&p.tmK, 4, kp, dk, sk, bk));
+    KL_TRY(ra_map(&p.tmV, 4, vp, dk, sk, bk));
   }
   p.kp = static_cast<const __nv_bfloat16*>(kp);
   p.vp = static_cast<const __nv_bfloat16*>(vp);
