@@ -272,11 +272,10 @@ __device__ __forceinline__ uint4 rq_pack(const float (&f)[8]) {
 // 64 + 8 l .. (planes (i, i + 64)), or 16 l .. 16 l + 15 (planes (2i, 2i + 1)).
 // Heads in the order q, k, v; each element is read and written by one thread,
 // so q_out may be q_pre.
-__global__ void __launch_bounds__(RQ_THREADS) ragged_qkv_kernel(const __grid_constant__ QkvParams p) {
+__global__ void __launch_bounds__(RQ_THREADS, 4) ragged_qkv_kernel(const __grid_constant__ QkvParams p) {
   pdl_enter();
   __shared__ float2 cs[RQ_D / 2];
   const int row = blockIdx.x;
-  if (row >= min(p.cu[p.B], p.T)) return;
   const int heads = p.Hq + 2 * p.Hkv;
   const int l = threadIdx.x % RQ_LANES, h0 = threadIdx.x / RQ_LANES;
   constexpr int STEP = RQ_THREADS / RQ_LANES;
@@ -286,12 +285,9 @@ __global__ void __launch_bounds__(RQ_THREADS) ragged_qkv_kernel(const __grid_con
            : h < p.Hq + p.Hkv ? p.k_pre + (static_cast<int64_t>(row) * p.Hkv + (h - p.Hq)) * RQ_D
                               : p.v + (static_cast<int64_t>(row) * p.Hkv + (h - p.Hq - p.Hkv)) * RQ_D;
   };
-  const int pos = p.pos[row];
+  // a row past the last request is read too (the tensors have it), not written
+  const int rows = p.cu[p.B], pos = p.pos[row];
   int slot = p.slots[row];
-  if (slot >= p.pool_rows) {
-    if (threadIdx.x == 0) record_error(p.err, KL_DEVERR_PAGE);
-    slot = -1;
-  }
   for (int base = 0; base < heads; base += RQ_MAX * STEP) {
     uint4 xa[RQ_MAX], xb[RQ_MAX];
 #pragma unroll
@@ -305,6 +301,11 @@ __global__ void __launch_bounds__(RQ_THREADS) ragged_qkv_kernel(const __grid_con
       }
     }
     if (base == 0) {
+      if (row >= rows) return;
+      if (slot >= p.pool_rows) {
+        if (threadIdx.x == 0) record_error(p.err, KL_DEVERR_PAGE);
+        slot = -1;
+      }
       if (threadIdx.x < RQ_D / 2) {
         float c, sn;
         rope_cos_sin(pos, p.f.turn[threadIdx.x], 1.0f, &c, &sn);

@@ -15,10 +15,11 @@
 //
 // An index must not depend on how a sum is split, so sums are held far beyond
 // the weights' own precision: p - q as an error-free pair of floats (two-sum,
-// Knuth), accumulated per thread in a pair (about 48 bits), and from there in
-// fp64. fp64 additions for every weight would cost more than the reads (two per
-// clock and SM). The acceptance test is exact: the product of two floats fits
-// a double.
+// Knuth), accumulated per thread and over a warp in pairs (about 48 bits), and
+// from there by single warps in fp64 (an SM adds two doubles a clock: fp64 sums
+// in every thread took most of the time, 82 us for 64 requests of 151936 classes
+// against the reads' 11.5). The acceptance test is exact: the product of two
+// floats fits a double.
 #include "internal.h"
 #include "kl_common.cuh"
 
@@ -82,6 +83,16 @@ struct Pair {
   }
   __device__ __forceinline__ double value() const { return static_cast<double>(hi) + static_cast<double>(lo); }
 };
+// The sum of the warp's 32 pairs, in every lane.
+__device__ __forceinline__ Pair dv_warp_sum(Pair v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float hi = __shfl_xor_sync(0xffffffffu, v.hi, o), lo = __shfl_xor_sync(0xffffffffu, v.lo, o);
+    v.add(hi);
+    v.lo += lo;
+  }
+  return v;
+}
 
 // Which weights a request's token is drawn from.
 enum { DV_P = 0, DV_REST = 1, DV_REST_LOOKUP = 2 };   // p; max(0, p - q); p without the draft
@@ -100,11 +111,6 @@ __device__ __forceinline__ void dv_weight(int kind, float p, float q, int64_t co
   if (!(w > 0.f)) w = we = 0.f;
 }
 
-__device__ __forceinline__ double dv_warp_sum(double v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
 __device__ __forceinline__ double dv_warp_scan(double v, int lane) {   // inclusive
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -122,27 +128,53 @@ __device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v) {
   asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
 }
 
-// The part of [0, n) whose cumulative sum crosses x: the first i with
-// before + sum_{j <= i} s_j > x; if rounding leaves none, the last one with a
-// positive sum; -1 if there is none. `before` becomes the sum in front of it.
-__device__ __forceinline__ int dv_cross(const double* s, int n, double x, double& before) {
-  int last = -1;
-  double c = before, at = before;
-  for (int i = 0; i < n; ++i) {
-    if (s[i] > 0.0) {
-      last = i;
-      at = c;
-      if (c + s[i] > x) break;
+// One warp: lane i < n holds the sum of part i. The part whose cumulative sum
+// crosses x: the first i with before + sum_{j <= i} s_j > x; if rounding leaves
+// none, the last one with a positive sum; -1 if there is none. `before` becomes
+// the sum in front of it.
+__device__ __forceinline__ int dv_cross(double s, int lane, double x, double& before) {
+  const double incl = before + dv_warp_scan(s, lane);
+  const unsigned some = __ballot_sync(0xffffffffu, s > 0.0);
+  const unsigned over = __ballot_sync(0xffffffffu, s > 0.0 && incl > x);
+  if (!some) return -1;
+  const int i = over ? __ffs(over) - 1 : 31 - __clz(some);
+  before = __shfl_sync(0xffffffffu, incl - s, i);
+  return i;
+}
+
+// What the first warp tells the others: the part to look into (below 0: none),
+// the sum in front of it and the value to cross.
+struct VerifySmem {
+  double slots[2][DV_CL];        // the CTAs' sums, written by each of them (one array per attempt)
+  double parts[DV_WARPS];        // the warps' sums
+  double before, x;
+  int part, accepted, kind;
+};
+
+// Sum of this lane's vectors j0 + lane, + 32, ... of [j0, j1).
+template <typename T, int E>
+__device__ __forceinline__ Pair dv_sum(const T* prow, const T* qrow, int mis, int V, int kind, int draft, int j0, int j1) {
+  Pair sum = {0.f, 0.f};
+#pragma unroll 4
+  for (int j = j0 + static_cast<int>(threadIdx.x & 31); j < j1; j += 32) {
+    const int64_t col = static_cast<int64_t>(j) * E - mis;
+    float fp[E], fq[E] = {};
+    dv_load<T, E>(prow, col, V, fp);
+    if (kind == DV_REST) dv_load<T, E>(qrow, col, V, fq);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      float w, we;
+      dv_weight(kind, fp[e], fq[e], col + e, draft, w, we);
+      sum.add(w);
+      sum.lo += we;
     }
-    c += s[i];
   }
-  before = at;
-  return last;
+  return dv_warp_sum(sum);
 }
 
 template <typename T, int E>
-__device__ void dv_request(const VerifyParams& p, int b, int rank, const T* prow, const T* qrow, int mis, int kind, int draft,
-                           int accepted, double (*slots)[DV_CL], double* wsum) {
+__device__ __forceinline__ void dv_request(const VerifyParams& p, VerifySmem& s, int b, int rank, const T* prow, const T* qrow, int mis,
+                           int kind, int draft, int accepted) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // columns in vectors of E: vector j holds columns E j - mis ..
   const int nv = static_cast<int>((static_cast<int64_t>(p.V) + mis + E - 1) / E);
@@ -150,103 +182,94 @@ __device__ void dv_request(const VerifyParams& p, int b, int rank, const T* prow
   const int per_warp = (per_cta + DV_WARPS - 1) / DV_WARPS;
   const int c0 = min(nv, rank * per_cta), c1 = min(nv, c0 + per_cta);
   const int w0 = min(c1, c0 + warp * per_warp), w1 = min(c1, w0 + per_warp);
-  const double u = static_cast<double>(p.us[b]);
+  const float u = p.us[b];
 
   for (int attempt = 0; attempt < 2; ++attempt) {
-    Pair sum = {0.f, 0.f};
-#pragma unroll 4
-    for (int j = w0 + lane; j < w1; j += 32) {
-      const int64_t col = static_cast<int64_t>(j) * E - mis;
-      float fp[E], fq[E] = {};
-      dv_load<T, E>(prow, col, p.V, fp);
-      if (kind == DV_REST) dv_load<T, E>(qrow, col, p.V, fq);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        float w, we;
-        dv_weight(kind, fp[e], fq[e], col + e, draft, w, we);
-        sum.add(w);
-        sum.lo += we;
-      }
-    }
-    const double ws = dv_warp_sum(sum.value());
-    if (lane == 0) wsum[warp] = ws;
+    const Pair sum = dv_sum<T, E>(prow, qrow, mis, p.V, kind, draft, w0, w1);
+    if (lane == 0) s.parts[warp] = sum.value();
+    if (attempt == 0) dv_cluster_wait();
     __syncthreads();
     double mine = 0.0;
-    for (int w = 0; w < DV_WARPS; ++w) mine += wsum[w];
-    if (attempt == 0) dv_cluster_wait();
-    if (tid < DV_CL) st_cluster_f64(mapa_shared(smem_u32(&slots[attempt][rank]), tid), mine);
+    if (warp == 0) {
+      mine = lane < DV_WARPS ? s.parts[lane] : 0.0;
+      const double cta = __shfl_sync(0xffffffffu, dv_warp_scan(mine, lane), 31);
+      if (lane < DV_CL) st_cluster_f64(mapa_shared(smem_u32(&s.slots[attempt][rank]), lane), cta);
+    }
     cluster_sync_all();
-    double total = 0.0;
-    for (int c = 0; c < DV_CL; ++c) total += slots[attempt][c];
-    if (attempt == 0 && kind != DV_P && !(total > 0.0)) {   // nothing left of p - q anywhere: p itself
+    if (warp == 0) {
+      const double part = lane < DV_CL ? s.slots[attempt][lane] : 0.0;
+      const double total = __shfl_sync(0xffffffffu, dv_warp_scan(part, lane), 31);
+      const double x = static_cast<double>(u) * total;
+      double before = 0.0;
+      int next = kind;
+      int owner = total > 0.0 && total < INFINITY ? dv_cross(part, lane, x, before) : -1;
+      if (owner < 0 && attempt == 0 && kind != DV_P && !(total > 0.0)) {
+        next = -1;                                   // nothing left of p - q anywhere: p itself
+      } else if (owner < 0) {
+        if (rank == 0 && lane == 0) {
+          p.acc[b] = accepted;
+          p.next[b] = -1;
+        }
+      } else if (owner == rank) {
+        owner = max(0, dv_cross(mine, lane, x, before));
+        if (lane == 0) {
+          s.before = before;
+          s.x = x;
+        }
+      } else {
+        owner = -1;
+      }
+      if (lane == 0) {
+        s.part = owner;
+        s.kind = next;
+      }
+    }
+    __syncthreads();
+    if (s.kind < 0) {
       kind = DV_P;
-      __syncthreads();                                      // wsum is written again
       continue;
     }
-    const double x = u * total;
-    double before = 0.0;
-    const int owner = total > 0.0 && total < INFINITY ? dv_cross(slots[attempt], DV_CL, x, before) : -1;
-    if (owner < 0) {
-      if (rank == 0 && tid == 0) {
-        p.acc[b] = accepted;
-        p.next[b] = -1;
-      }
-      return;
-    }
-    if (owner != rank) return;
-    const int ow = max(0, dv_cross(wsum, DV_WARPS, x, before));
+    const int ow = s.part;
+    if (ow < 0) return;
     // that warp's stretch once more, spread over the CTA: warp w takes its w-th sixteenth
     const int s0 = min(c1, c0 + ow * per_warp), s1 = min(c1, s0 + per_warp);
     const int piece = (s1 - s0 + DV_WARPS - 1) / DV_WARPS;
     const int p0 = min(s1, s0 + warp * piece), p1 = min(s1, p0 + piece);
-    double part = 0.0;
-    for (int j = p0 + lane; j < p1; j += 32) {
-      const int64_t col = static_cast<int64_t>(j) * E - mis;
-      float fp[E], fq[E] = {};
-      dv_load<T, E>(prow, col, p.V, fp);
-      if (kind == DV_REST) dv_load<T, E>(qrow, col, p.V, fq);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        float w, we;
-        dv_weight(kind, fp[e], fq[e], col + e, draft, w, we);
-        part += static_cast<double>(w) + static_cast<double>(we);
-      }
-    }
-    part = dv_warp_sum(part);
-    __syncthreads();                                        // every thread has read wsum
-    if (lane == 0) wsum[warp] = part;
+    const Pair part = dv_sum<T, E>(prow, qrow, mis, p.V, kind, draft, p0, p1);
+    if (lane == 0) s.parts[warp] = part.value();
     __syncthreads();
-    const int pw = max(0, dv_cross(wsum, DV_WARPS, x, before));
+    const double x = s.x;
+    double before = s.before;
+    const int pw = max(0, dv_cross(lane < DV_WARPS ? s.parts[lane] : 0.0, lane, x, before));
     if (warp != pw) return;
     // this warp's piece in order, 32 vectors at a time
     int64_t found = -1, last = -1;
-    double c = before;
     for (int j0 = p0; j0 < p1 && found < 0; j0 += 32) {
       const int j = j0 + lane;
       const int64_t col = static_cast<int64_t>(j) * E - mis;
-      double w[E], s = 0.0;
+      float w[E], we[E];
+      Pair sum = {0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < E; ++e) w[e] = we[e] = 0.f;
       if (j < p1) {
         float fp[E], fq[E] = {};
         dv_load<T, E>(prow, col, p.V, fp);
         if (kind == DV_REST) dv_load<T, E>(qrow, col, p.V, fq);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          float a, ae;
-          dv_weight(kind, fp[e], fq[e], col + e, draft, a, ae);
-          w[e] = static_cast<double>(a) + static_cast<double>(ae);
-          s += w[e];
+          dv_weight(kind, fp[e], fq[e], col + e, draft, w[e], we[e]);
+          sum.add(w[e]);
+          sum.lo += we[e];
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) w[e] = 0.0;
       }
-      const double incl = dv_warp_scan(s, lane);
-      double at = c + (incl - s);
+      const double mine2 = sum.value();
+      const double incl = before + dv_warp_scan(mine2, lane);
+      double at = incl - mine2;
       int64_t hit = -1, pos = -1;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        at += w[e];
-        if (w[e] > 0.0) {
+        at += static_cast<double>(w[e]) + static_cast<double>(we[e]);
+        if (w[e] > 0.f) {
           pos = col + e;
           if (hit < 0 && at > x) hit = col + e;
         }
@@ -254,7 +277,7 @@ __device__ void dv_request(const VerifyParams& p, int b, int rank, const T* prow
       const unsigned hits = __ballot_sync(0xffffffffu, hit >= 0), any = __ballot_sync(0xffffffffu, pos >= 0);
       if (hits) found = __shfl_sync(0xffffffffu, hit, __ffs(hits) - 1);
       if (any) last = __shfl_sync(0xffffffffu, pos, 31 - __clz(any));
-      c += __shfl_sync(0xffffffffu, incl, 31);
+      before = __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) {
       p.acc[b] = accepted;
@@ -267,9 +290,7 @@ __device__ void dv_request(const VerifyParams& p, int b, int rank, const T* prow
 template <typename T>
 __global__ void __launch_bounds__(DV_THREADS) draft_verify_kernel(const VerifyParams p) {
   pdl_enter();
-  __shared__ double slots[2][DV_CL];
-  __shared__ double wsum[DV_WARPS];
-  __shared__ int s_acc;
+  __shared__ VerifySmem s;
   const int b = blockIdx.x / DV_CL, rank = static_cast<int>(cluster_ctarank());
   const int r0 = min(max(p.cu[b], 0), p.T), r1 = min(max(p.cu[b + 1], r0), p.T);
   if (r1 <= r0) {                       // the whole cluster leaves here
@@ -304,10 +325,10 @@ __global__ void __launch_bounds__(DV_THREADS) draft_verify_kernel(const VerifyPa
         break;
       }
     }
-    if (threadIdx.x == 0) s_acc = acc;
+    if (threadIdx.x == 0) s.accepted = acc;
   }
   __syncthreads();
-  const int accepted = s_acc;
+  const int accepted = s.accepted;
   const int64_t row = r0 + accepted;
   const bool rejected = row < r1 - 1;
   const int kind = !rejected ? DV_P : p.q ? DV_REST : DV_REST_LOOKUP;
@@ -319,9 +340,9 @@ __global__ void __launch_bounds__(DV_THREADS) draft_verify_kernel(const VerifyPa
   // of an odd vocabulary starts anywhere); element by element where they do not
   const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(prow) & 15u) / sizeof(T));
   if (!qrow || mis == static_cast<int>((reinterpret_cast<uintptr_t>(qrow) & 15u) / sizeof(T)))
-    dv_request<T, E>(p, b, rank, prow, qrow, mis, kind, draft, accepted, slots, wsum);
+    dv_request<T, E>(p, s, b, rank, prow, qrow, mis, kind, draft, accepted);
   else
-    dv_request<T, 1>(p, b, rank, prow, qrow, 0, kind, draft, accepted, slots, wsum);
+    dv_request<T, 1>(p, s, b, rank, prow, qrow, 0, kind, draft, accepted);
 }
 
 }  // namespace
