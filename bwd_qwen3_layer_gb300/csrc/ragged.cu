@@ -384,6 +384,9 @@ kl_status ragged_check(const kl_ragged_cfg* rc) {
   const double rows = static_cast<double>(rc->n_blocks) * rc->block_size;
   if (rows >= 2147483647.0)
     return set_error(KL_ERR_UNSUPPORTED, "ragged: pool rows (%.0f) beyond 32-bit indexing", rows);
+  if (static_cast<double>(rc->max_blocks) * rc->block_size > 1073741824.0)
+    return set_error(KL_ERR_UNSUPPORTED, "ragged: a table row of %d blocks of %d tokens above 2^30 positions", rc->max_blocks,
+                     rc->block_size);
   return KL_OK;
 }
 

@@ -57,7 +57,9 @@ constexpr uint32_t RA_OFF_Q = 0;
 constexpr uint32_t RA_OFF_K = RA_OFF_Q + RA_TILE;
 constexpr uint32_t RA_OFF_V = RA_OFF_K + RA_NST * RA_TILE;
 constexpr uint32_t RA_OFF_BAR = RA_OFF_V + RA_NST * RA_TILE;
-constexpr size_t RA_SMEM = 1024 + RA_OFF_BAR + 512;
+constexpr size_t RA_SMEM = 1024 + RA_OFF_BAR + 1536;
+// Tensor memory: S of two steps, P (bf16 pairs), O, Q (bf16 pairs): all 512 columns.
+constexpr uint32_t RA_TM_P = 256, RA_TM_O = 320, RA_TM_Q = 448;
 constexpr int RA_ITEM_UNITS = 1;              // units an item's start and end count for
 constexpr int RA_MIN_UNITS = 3;               // units per CTA at least
 constexpr float RA_LOG2E = 1.4426950408889634f;
@@ -94,9 +96,29 @@ __device__ __forceinline__ float ra_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Q, K-major (two 64-column swizzle blocks of 128 rows), k-step kk of 16 columns
-__device__ __forceinline__ uint64_t ra_desc_q(uint32_t base, int kk) {
-  return smem_desc_sw128(base + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024);
+// Pairs of floats in one 64-bit register: one instruction for two elements.
+__device__ __forceinline__ uint64_t ra_pair(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void ra_unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t ra_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t ra_add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float ra_max3(float a, uint32_t b, uint32_t c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+  return d;
 }
 // K, K-major, in groups of 8 keys 2 KB apart
 __device__ __forceinline__ uint64_t ra_desc_k(uint32_t base, int kk) {
@@ -126,7 +148,26 @@ __device__ __forceinline__ void ra_cp16(uint32_t dst, const void* src, bool vali
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(sz) : "memory");
 }
 
-// One request's rows and context, every value brought into range.
+// mbar_wait_warp for a copy warp, which is a ring ahead of the products: between
+// probes it sleeps, so that its issue slots go to the softmax warp beside it.
+__device__ __forceinline__ bool ra_wait_copy(uint32_t bar, uint32_t parity, uint32_t* err, volatile int* abort_flag) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0; !__all_sync(0xffffffffu, mbar_test_wait(bar, parity)); ++i) {
+    __nanosleep(100);
+    if ((i & 63u) == 63u) {
+      const uint64_t t = global_timer_ns();
+      if (i == 63u) t0 = t;
+      const bool late = t - t0 > KL_WAIT_LIMIT_NS;
+      if (late) record_error(err, KL_DEVERR_TIMEOUT);
+      if (__any_sync(0xffffffffu, late || *abort_flag)) return false;
+    }
+  }
+  return true;
+}
+
+// One request's rows and context, every value brought into range (no table row
+// is as long as RA_MAX_CTX, so a context beyond it is past its table anyway).
+constexpr int RA_MAX_CTX = 1 << 30;
 struct RaReq {
   int r0, n, ctx;
 };
@@ -134,24 +175,23 @@ __device__ __forceinline__ RaReq ra_req(const RaParams& p, int b) {
   RaReq q;
   q.r0 = min(max(p.cu[b], 0), p.T);
   q.n = min(max(p.cu[b + 1], q.r0), p.T) - q.r0;
-  q.ctx = max(p.ctx[b], 0);
+  q.ctx = min(max(p.ctx[b], 0), RA_MAX_CTX);
   return q;
 }
 // Key tiles of query tile qt (its last token's limit decides).
 __device__ __forceinline__ int ra_tiles(const RaReq& q, int TQ, int qt) {
-  const long long last = static_cast<long long>(q.ctx) + min(static_cast<long long>(q.n), (qt + 1LL) * TQ) - 1;
-  return static_cast<int>(last / RA_BKV) + 1;
+  return (q.ctx + min(q.n, (qt + 1) * TQ) - 1) / RA_BKV + 1;
 }
 // Units of query tiles 0 .. m-1, all but the request's last one:
 //   sum_{k=1}^{m} (floor((ctx - 1 + k TQ) / 128) + 1 + RA_ITEM_UNITS).
 // The quotients repeat with period 128 / gcd(TQ, 128) up to a constant step, so
 // whole periods are summed in closed form.
 __device__ long long ra_units_before(int ctx, int TQ, long long m) {
-  const int low = TQ & -TQ;                       // gcd(TQ, 128), TQ <= 128
-  const int period = RA_BKV / low, step = TQ / low;
+  const int sh = __ffs(TQ) - 1;                   // gcd(TQ, 128) = 2^sh, TQ <= 128
+  const int period = RA_BKV >> sh, step = TQ >> sh;
   const long long a = static_cast<long long>(ctx) - 1;
-  const long long c = m / period;
-  const int r = static_cast<int>(m - c * period);
+  const long long c = m >> (7 - sh);
+  const int r = static_cast<int>(m & (period - 1));
   long long full = 0, part = 0;
   for (int k = 1; k <= (c ? period : r); ++k) {
     const long long v = (a + static_cast<long long>(k) * TQ) >> 7;
@@ -165,6 +205,12 @@ __device__ __forceinline__ long long ra_head_units(const RaReq& q, int TQ) {
   if (q.n <= 0) return 0;
   const int QT = (q.n + TQ - 1) / TQ;
   return ra_units_before(q.ctx, TQ, QT - 1) + ra_tiles(q, TQ, QT - 1) + RA_ITEM_UNITS;
+}
+
+// Quotient of non-negative numbers; most fit 32 bits, whose division is several times faster.
+__device__ __forceinline__ long long ra_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
 }
 
 // The pieces of one CTA's run, in order. Every role walks the same list.
@@ -203,7 +249,7 @@ struct RaWalk {
       rq = q;
       if (left > 0) {      // the item ends here: on to the next
         off = 0;
-        if (static_cast<long long>(qt + 1) * p.TQ < q.n) {
+        if ((qt + 1) * p.TQ < q.n) {
           ++qt;
         } else {
           qt = 0;
@@ -225,6 +271,16 @@ struct RaWalk {
   }
 };
 
+// What a softmax warp keeps of a piece, in shared memory: its registers are full
+// of scores, and every one more costs the steps (with the walk and 64-bit
+// positions in registers the steps took 1950 cycles).
+struct RaPiece {
+  int row0, toks, head0;   // the tile's first row of the step, its tokens, its first head
+  int pos0, L;             // position of its first token; keys of the request
+  int ta, tb;              // key tiles; tb = 0: there is no such piece
+  int flags;               // 1: all of the item's tiles; 2: the piece goes to slot 1
+};
+
 template <bool TMA>
 __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid_constant__ RaParams p) {
   pdl_enter();
@@ -233,9 +289,10 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sb = smem_u32(smem);
   const uint32_t bar = sb + RA_OFF_BAR;
-  // barriers; those of a pair serve the steps (or pieces) of one parity each, so
-  // that a warp which runs a step ahead of another cannot count for its phase
-  const uint32_t q_full = bar + 0, q_empty = bar + 8, drain = bar + 16;
+  // barriers; those of a pair serve the steps of one parity each, so that a warp
+  // which runs a step ahead of another cannot count for its phase
+  const uint32_t q_full = bar + 0, drain = bar + 8;
+  const uint32_t q_tm = bar + 16;                           // a piece's Q copied to tensor memory
   auto k_full = [&](int s) { return bar + 24 + 8 * s; };
   auto k_empty = [&](int s) { return bar + 48 + 8 * s; };
   auto v_full = [&](int s) { return bar + 72 + 8 * s; };
@@ -244,18 +301,21 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
   auto s_free = [&](int s) { return bar + 136 + 8 * s; };   // S_n read
   auto p_full = [&](int s) { return bar + 152 + 8 * s; };   // P_n written (and V_n's tail cleared)
   auto p_done = [&](int s) { return bar + 168 + 8 * s; };   // O += P_n V_n computed
-  auto o_empty = [&](int s) { return bar + 184 + 8 * s; };  // a piece's O read
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + RA_OFF_BAR + 200);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + RA_OFF_BAR + 204);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + RA_OFF_BAR + 184);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + RA_OFF_BAR + 188);
   RaStart* start = reinterpret_cast<RaStart*>(smem + RA_OFF_BAR + 208);
   long long* wsum = reinterpret_cast<long long*>(smem + RA_OFF_BAR + 256);   // [8]: the warps' unit sums, then this CTA's units
+
+  RaWalk* walks = reinterpret_cast<RaWalk*>(smem + RA_OFF_BAR + 320);        // [4], of the softmax warps
+  RaPiece* pieces = reinterpret_cast<RaPiece*>(smem + RA_OFF_BAR + 1024);    // [4][2]
+  static_assert(4 * sizeof(RaWalk) <= 704 && 8 * sizeof(RaPiece) <= 512, "shared-memory layout");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_tm, 4);
     for (int s = 0; s < RA_NST; ++s) {
       mbar_init(k_full(s), TMA ? 1 : 32);
       mbar_init(k_empty(s), 1);
@@ -267,7 +327,6 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
       mbar_init(s_free(s), 4);
       mbar_init(p_full(s), 4);
       mbar_init(p_done(s), 1);
-      mbar_init(o_empty(s), 4);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -297,7 +356,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
       if (w < warp) before += wsum[w];
       W += wsum[w];
     }
-    const long long P = max((W + ctas - 1) / ctas, static_cast<long long>(RA_MIN_UNITS));
+    const long long P = max(ra_div(W + ctas - 1, ctas), static_cast<long long>(RA_MIN_UNITS));
     const long long u0 = cta * P;
     if (threadIdx.x == 0) {
       wsum[7] = max(0LL, min(P, W - u0));     // units of this CTA
@@ -315,7 +374,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
       }
       const long long x = u0 - lo;
       const RaReq q = ra_req(p, b);
-      const int g = static_cast<int>(x / hu);
+      const int g = static_cast<int>(ra_div(x, hu));
       const long long y = x - g * hu;
       int m0 = 0, m1 = (q.n + p.TQ - 1) / p.TQ;      // the query tile: units_before(m0) <= y < units_before(m1)
       while (m1 - m0 > 1) {
@@ -331,7 +390,8 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_holder;   // S[0] at column 0, S[1] at 128, O[0] at 256, O[1] at 384
+  const uint32_t tmem = *tmem_holder;
+  const uint32_t tmP = tmem + RA_TM_P, tmO = tmem + RA_TM_O, tmQ = tmem + RA_TM_Q;
   const RaStart st = *start;
   const long long units = wsum[7];
   if (threadIdx.x == 0) p.starts[cta] = st;
@@ -355,15 +415,15 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     uint32_t ph = 1;                              // parity that an empty stage's wait passes with
     bool ok = true;
     // the pool row of position pos, or no_row
-    auto pool_row = [&](int b, long long pos, long long L) {
+    auto pool_row = [&](int b, int pos, int L) {
       if (pos >= L) return no_row;
-      const int lb = static_cast<int>(pos / p.bs);
+      const int lb = pos / p.bs;
       const int blk = lb < p.max_blocks ? p.table[static_cast<int64_t>(b) * p.max_blocks + lb] : -1;
       if (blk < 0 || blk >= p.n_blocks) {
         record_error(p.err, KL_DEVERR_PAGE);
         return no_row;
       }
-      return blk * p.bs + static_cast<int>(pos - static_cast<long long>(lb) * p.bs);
+      return blk * p.bs + (pos - lb * p.bs);
     };
     // cp.async: the rows of one tile; row[k] of lane l is the pool row of key 32 k + l
     auto gather = [&](uint32_t dst, int g, const int (&row)[4]) {
@@ -393,8 +453,8 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     w.init(p, st, units);
     while (ok && w.next(p)) {
       if (is_k) {
-        // Q: the buffer is free once the previous piece's last S product is done
-        if (!mbar_wait_warp(q_empty, (issued_q & 1) ^ 1u, p.err, abort_flag)) { ok = false; break; }
+        // Q: the buffer is free once the previous piece's Q is in tensor memory
+        if (!ra_wait_copy(q_tm, (issued_q & 1) ^ 1u, p.err, abort_flag)) { ok = false; break; }
         if (el) {
           mbar_arrive_expect_tx(q_full, 2u * GT * 128u);
           const int t0 = w.rq.r0 + w.iq * p.TQ;
@@ -404,19 +464,19 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
         __syncwarp();
         ++issued_q;
       }
-      const long long L = static_cast<long long>(w.rq.ctx) + w.rq.n;
+      const int L = w.rq.ctx + w.rq.n;
       int row[4];
       auto lookup = [&](int j) {
         if (TMA) {
-          row[0] = lane < nbox ? pool_row(w.ib, static_cast<long long>(j) * RA_BKV + lane * p.box, L) : no_row;
+          row[0] = lane < nbox ? pool_row(w.ib, j * RA_BKV + lane * p.box, L) : no_row;
         } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) row[k] = pool_row(w.ib, static_cast<long long>(j) * RA_BKV + k * 32 + lane, L);
+          for (int k = 0; k < 4; ++k) row[k] = pool_row(w.ib, j * RA_BKV + k * 32 + lane, L);
         }
       };
       lookup(w.ta);
       for (int j = w.ta; j < w.tb; ++j) {
-        if (!mbar_wait_warp(empty0 + 8 * s, ph, p.err, abort_flag)) { ok = false; break; }
+        if (!ra_wait_copy(empty0 + 8 * s, ph, p.err, abort_flag)) { ok = false; break; }
         const uint32_t dst = ring + s * RA_TILE;
         if (TMA) {
           if (el) mbar_arrive_expect_tx(full0 + 8 * s, RA_TILE);
@@ -447,70 +507,81 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     }
   } else if (warp == 2) {
     // ---------------- MMA (whole warp; the elected lane issues) ----------------
-    // Step n (over all pieces) issues S_n, then the P V product of step n - 1,
-    // which may be the previous piece's last.
+    // S_n = Q K_n^T into S[n % 2] as soon as K_n is there and the softmax warps
+    // have read S_(n-2); O += P_n V_n as soon as P_n and V_n are there: whichever
+    // is ready first, so that a late key tile does not hold up the products that
+    // would free a value tile.
     const bool el = elect_one();
     const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);
     const uint32_t idesc_pv = idesc_bf16_f32(128, 128, 0, 1);
+    auto ready = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(b, parity)); };
     int vs = 0, ks = 0;                       // stages of the V and K rings
     uint32_t vph = 0, kph = 0;
-    auto issue_pv = [&](int gp, int ob, bool first) -> bool {
-      const int s = gp & 1;
-      if (!mbar_wait_warp(p_full(s), (gp >> 1) & 1, p.err, abort_flag)) return false;
-      if (!mbar_wait_warp(v_full(vs), vph, p.err, abort_flag)) return false;
-      tc_fence_after();
-      if (el) {
-        for (int kk = 0; kk < RA_BKV / 16; ++kk)   // P from TMEM (the first 64 columns of S[s])
-          umma_bf16_ta(tmem + 256 + ob * 128, tmem + s * 128 + kk * 8, ra_desc_v(sb + RA_OFF_V + vs * RA_TILE, kk),
-                       idesc_pv, (!first || kk > 0) ? 1u : 0u);
-        umma_commit(v_empty(vs));
-        umma_commit(p_done(s));
-      }
-      __syncwarp();
-      if (++vs == RA_NST) {
-        vs = 0;
-        vph ^= 1u;
-      }
-      return true;
-    };
+    int sn = 0, pn = 0, k = 0;                // next step of S and of P V; the S products' piece
+    uint32_t firsts = 0;                      // bit n % 4: step n begins a piece
+    uint64_t t0 = 0;
+    uint32_t spins = 0;
     bool ok = true;
-    int n = 0, k = 0, pend_n = -1, pend_ob = 0;
-    bool pend_first = false;
     RaWalk w;
     w.init(p, st, units);
-    for (; ok && w.next(p); ++k) {
-      const int ob = k & 1;
-      if (!mbar_wait_warp(q_full, k & 1, p.err, abort_flag)) { ok = false; break; }
-      for (int j = w.ta; j < w.tb; ++j, ++n) {
-        const int s = n & 1;
-        if (!mbar_wait_warp(k_full(ks), kph, p.err, abort_flag) ||
-            (n >= 2 && !mbar_wait_warp(s_free(s), ((n >> 1) & 1) ^ 1u, p.err, abort_flag))) {
-          ok = false;
-          break;
-        }
+    bool more = w.next(p);
+    int j = more ? w.ta : 0;
+    while (more || pn < sn) {
+      bool idle = true;
+      if (more && (j > w.ta || ready(q_tm, k & 1)) && ready(k_full(ks), kph) &&
+          (sn < 2 || ready(s_free(sn & 1), ((sn >> 1) & 1) ^ 1u))) {
         tc_fence_after();
         if (el) {
           for (int kk = 0; kk < RA_D / 16; ++kk)
-            umma_bf16(tmem + s * 128, ra_desc_q(sb + RA_OFF_Q, kk), ra_desc_k(sb + RA_OFF_K + ks * RA_TILE, kk), idesc_s,
-                      kk > 0);
+            umma_bf16_ta(tmem + (sn & 1) * 128, tmQ + kk * 8, ra_desc_k(sb + RA_OFF_K + ks * RA_TILE, kk), idesc_s, kk > 0);
           umma_commit(k_empty(ks));
-          umma_commit(s_full(s));
-          if (j == w.tb - 1) umma_commit(q_empty);   // the piece's last use of Q
+          umma_commit(s_full(sn & 1));
         }
         __syncwarp();
+        const uint32_t bit = 1u << (sn & 3);
+        firsts = j == w.ta ? firsts | bit : firsts & ~bit;
         if (++ks == RA_NST) {
           ks = 0;
           kph ^= 1u;
         }
-        if (pend_n >= 0 && !issue_pv(pend_n, pend_ob, pend_first)) { ok = false; break; }
-        // O[ob] takes this piece's first P V: the epilogue of piece k - 2 must have read it
-        if (j == w.ta && !mbar_wait_warp(o_empty(ob), ((k >> 1) & 1) ^ 1u, p.err, abort_flag)) { ok = false; break; }
-        pend_n = n;
-        pend_ob = ob;
-        pend_first = j == w.ta;
+        ++sn;
+        if (++j == w.tb) {
+          more = w.next(p);
+          j = w.ta;
+          ++k;
+        }
+        idle = false;
+      }
+      if (pn < sn && ready(p_full(pn & 1), (pn >> 1) & 1) && ready(v_full(vs), vph)) {
+        tc_fence_after();
+        if (el) {
+          const bool first = firsts >> (pn & 3) & 1u;
+          for (int kk = 0; kk < RA_BKV / 16; ++kk)
+            umma_bf16_ta(tmO, tmP + kk * 8, ra_desc_v(sb + RA_OFF_V + vs * RA_TILE, kk), idesc_pv, (!first || kk > 0) ? 1u : 0u);
+          umma_commit(v_empty(vs));
+          umma_commit(p_done(pn & 1));
+        }
+        __syncwarp();
+        if (++vs == RA_NST) {
+          vs = 0;
+          vph ^= 1u;
+        }
+        ++pn;
+        idle = false;
+      }
+      if (!idle) {
+        spins = 0;
+      } else if (__nanosleep(20), (++spins & 255u) == 0) {     // bounded, as every wait
+        const uint64_t t = global_timer_ns();
+        if (spins == 256u) t0 = t;
+        const bool late = t - t0 > KL_WAIT_LIMIT_NS;
+        if (late && el) record_error(p.err, KL_DEVERR_TIMEOUT);
+        if (__any_sync(0xffffffffu, late || *abort_flag)) {
+          ok = false;
+          break;
+        }
       }
     }
-    if (ok && pend_n >= 0 && !issue_pv(pend_n, pend_ob, pend_first)) ok = false;
     if (!ok) *abort_flag = 1;
     if (el) umma_commit(drain);
     __syncwarp();
@@ -520,30 +591,75 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;           // row within the tile = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const int tok = r / p.G, hh = r - tok * p.G;
-    bool ok = true;
-    int n = 0, k = 0;
-    RaWalk w;
-    w.init(p, st, units);
-    for (; ok && w.next(p); ++k) {
-      const int ob = k & 1;
-      const int first_tok = w.iq * p.TQ;
-      const int toks = min(p.TQ, w.rq.n - first_tok);       // tokens of this tile
-      const bool busy = quarter * 32 < toks * p.G;          // some row of this warp is real
-      const bool mine = r < toks * p.G;
-      const long long qpos = static_cast<long long>(w.rq.ctx) + first_tok + min(tok, toks - 1);   // padding rows: the last real row's limit
-      const long long L = static_cast<long long>(w.rq.ctx) + w.rq.n;
-      const uint32_t oadr = tmem + lane_off + 256 + ob * 128;
+    const uint32_t oadr = tmO + lane_off, padr = tmP + lane_off;
+    RaWalk& walk = walks[quarter];
+    auto piece = [&](int k) -> RaPiece& { return pieces[quarter * 2 + (k & 1)]; };
+    // piece k of this CTA into its place; false if there is none
+    auto find = [&](int k) -> bool {
+      __syncwarp();                                // every lane is done with piece k - 2
+      if (lane == 0) {
+        RaPiece& c = piece(k);
+        c.tb = 0;
+        if (walk.next(p)) {
+          const int first = walk.iq * p.TQ;
+          c.row0 = walk.rq.r0 + first;
+          c.toks = min(p.TQ, walk.rq.n - first);
+          c.head0 = walk.ig * p.G;
+          c.pos0 = walk.rq.ctx + first;
+          c.L = walk.rq.ctx + walk.rq.n;
+          c.ta = walk.ta;
+          c.tb = walk.tb;
+          c.flags = (walk.ta == 0 && walk.tb == walk.tiles ? 1 : 0) | (walk.idx > 0 ? 2 : 0);
+        }
+      }
+      __syncwarp();
+      return piece(k).tb > 0;
+    };
+    // this row's Q (two 128-byte-swizzled 64-column blocks) to tensor memory, the
+    // A operand of its piece's score products
+    auto copy_q = [&](int k) -> bool {
+      if (!mbar_wait_warp(q_full, k & 1, p.err, abort_flag)) return false;
+      const uint8_t* qs = smem + RA_OFF_Q + r * 128;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t qa[32];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint4 x = *reinterpret_cast<const uint4*>(qs + c * 16384 + ((e ^ (r & 7)) << 4));
+          qa[4 * e] = x.x; qa[4 * e + 1] = x.y; qa[4 * e + 2] = x.z; qa[4 * e + 3] = x.w;
+        }
+        tmem_st_32x32b_x32(tmQ + lane_off + c * 32, qa);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_tm);
+      return true;
+    };
+    if (lane == 0) walk.init(p, st, units);
+    bool have = find(0);
+    bool ok = !have || copy_q(0);
+    const float scale = p.scale_log2;
+    int n = 0;
+    for (int k = 0; ok && have; ++k) {
+      int left, lim, over, end;                    // tiles left; the row's last key, the tile's first row's, and the
+      bool busy;                                   // context's end, counted from the tile's first key
+      {
+        const RaPiece& c = piece(k);
+        left = c.tb - c.ta;
+        over = c.pos0 - c.ta * RA_BKV;
+        lim = over + min(r / p.G, c.toks - 1);     // padding rows: the last real row's limit
+        end = c.L - c.ta * RA_BKV;
+        busy = quarter * 32 < c.toks * p.G;        // some row of this warp is real
+      }
       float m = -INFINITY, l = 0.f;
-      for (int j = w.ta; j < w.tb; ++j, ++n) {
+      for (bool first = true; left > 0; --left, ++n, first = false) {
         const int s = n & 1;
-        const uint32_t ph = (n >> 1) & 1;
-        const long long key0 = static_cast<long long>(j) * RA_BKV;
         // the tile that holds the context's end: the value rows behind it become zero
-        if (TMA && key0 + RA_BKV > L) {
+        if (TMA && end < RA_BKV) {
           const int vs = n % RA_NST;
           if (!mbar_wait_warp(v_full(vs), (n / RA_NST) & 1, p.err, abort_flag)) { ok = false; break; }
-          if (key0 + r >= L) {
+          if (r >= end) {
             const uint32_t va = sb + RA_OFF_V + vs * RA_TILE + (r >> 3) * 2048 + (r & 7) * 128;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
@@ -553,105 +669,123 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
           }
           fence_async_shared();
         }
-        if (!mbar_wait_warp(s_full(s), ph, p.err, abort_flag)) { ok = false; break; }
+        if (!mbar_wait_warp(s_full(s), (n >> 1) & 1, p.err, abort_flag)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t sadr = tmem + lane_off + s * 128;
+        if (left == 1) {                           // the piece's last scores: Q's columns take the next piece's
+          have = find(k + 1);
+          if (have && !copy_q(k + 1)) { ok = false; break; }
+        }
+        // P's columns and O are free once the previous product is done. A warp
+        // without rows waits for that too: it must not count for step n + 2's phase
+        // while another still works on step n.
+        const uint32_t done = p_done(s ^ 1), done_ph = ((n - 1) >> 1) & 1;
         if (!busy) {                               // no real row: P stays whatever it is, its O rows are never read
+          if (n > 0 && !mbar_wait_warp(done, done_ph, p.err, abort_flag)) { ok = false; break; }
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(s_free(s));
             mbar_arrive(p_full(s));
           }
-          continue;
-        }
-        uint32_t sv[RA_BKV];
-        tmem_ld_32x32b_x32(sadr, *reinterpret_cast<uint32_t(*)[32]>(sv));
-        tmem_ld_32x32b_x32(sadr + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
-        tmem_ld_32x32b_x32(sadr + 64, *reinterpret_cast<uint32_t(*)[32]>(sv + 64));
-        tmem_ld_32x32b_x32(sadr + 96, *reinterpret_cast<uint32_t(*)[32]>(sv + 96));
-        tmem_ld_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_free(s));     // S[s] may be overwritten from here on
-        if (key0 + RA_BKV - 1 > w.rq.ctx + first_tok) {   // some row of the tile ends inside these keys
-          const int lim = static_cast<int>(min(qpos - key0, static_cast<long long>(RA_BKV)));   // keys 0 .. lim are kept
+        } else {
+          const uint32_t sadr = tmem + lane_off + s * 128;
+          uint32_t sv[RA_BKV];
+          tmem_ld_32x32b_x32(sadr, *reinterpret_cast<uint32_t(*)[32]>(sv));
+          tmem_ld_32x32b_x32(sadr + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
+          tmem_ld_32x32b_x32(sadr + 64, *reinterpret_cast<uint32_t(*)[32]>(sv + 64));
+          tmem_ld_32x32b_x32(sadr + 96, *reinterpret_cast<uint32_t(*)[32]>(sv + 96));
+          tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free(s));   // S[s] may be overwritten from here on
+          if (over < RA_BKV - 1) {                 // some row of the tile ends inside these keys: 0 .. lim are kept
 #pragma unroll
-          for (int e = 0; e < RA_BKV; ++e)
-            if (e > lim) sv[e] = __float_as_uint(-INFINITY);
-        }
-        float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < RA_BKV; e += 4) {
-          m0 = fmaxf(m0, __uint_as_float(sv[e]));
-          m1 = fmaxf(m1, __uint_as_float(sv[e + 1]));
-          m2 = fmaxf(m2, __uint_as_float(sv[e + 2]));
-          m3 = fmaxf(m3, __uint_as_float(sv[e + 3]));
-        }
-        const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * p.scale_log2;
-        // The max is only raised when it grows by more than 2^8 (the final O / l
-        // cancels a stale one). A row of a later piece's tile can be fully masked
-        // (its token ends before these keys): mx = -inf, and m stays -inf.
-        const bool raise = mx > m + 8.0f;
-        const float m_new = raise ? mx : m;
-        const float alpha = raise ? ra_ex2(m - m_new) : 1.0f;
-        if (j > w.ta && __any_sync(0xffffffffu, raise)) {
-          if (!mbar_wait_warp(p_done(s ^ 1), ((n - 1) >> 1) & 1, p.err, abort_flag)) { ok = false; break; }
-          tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(oadr + c * 32, v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-            tmem_st_32x32b_x32(oadr + c * 32, v);
+            for (int e = 0; e < RA_BKV; ++e)
+              if (e > lim) sv[e] = __float_as_uint(-INFINITY);
           }
-          tmem_st_wait();
-        }
-        const float neg = m_new > -INFINITY ? -m_new : 0.f;
-        const float sc = p.scale_log2;
-        float r0 = 0.f, r1 = 0.f, r2 = 0.f, r3 = 0.f;
-        uint32_t pk[64];
+          float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < RA_BKV; e += 4) {
-          const float p0 = ra_ex2(fmaf(__uint_as_float(sv[e]), sc, neg));
-          const float p1 = ra_ex2(fmaf(__uint_as_float(sv[e + 1]), sc, neg));
-          const float p2 = ra_ex2(fmaf(__uint_as_float(sv[e + 2]), sc, neg));
-          const float p3 = ra_ex2(fmaf(__uint_as_float(sv[e + 3]), sc, neg));
-          r0 += p0;
-          r1 += p1;
-          r2 += p2;
-          r3 += p3;
-          pk[e >> 1] = pack_bf16x2(p0, p1);        // P enters its product as bf16: half a step (2^-9) per weight
-          pk[(e >> 1) + 1] = pack_bf16x2(p2, p3);
+          for (int e = 0; e < RA_BKV; e += 8) {
+            m0 = ra_max3(m0, sv[e], sv[e + 1]);
+            m1 = ra_max3(m1, sv[e + 2], sv[e + 3]);
+            m2 = ra_max3(m2, sv[e + 4], sv[e + 5]);
+            m3 = ra_max3(m3, sv[e + 6], sv[e + 7]);
+          }
+          const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * scale;
+          // The max is only raised when it grows by more than 2^8 (the final O / l
+          // cancels a stale one). A row of a later piece's tile can be fully masked
+          // (its token ends before these keys): mx = -inf, and m stays -inf.
+          const bool raise = mx > m + 8.0f;
+          const float m_new = raise ? mx : m;
+          const float alpha = raise ? ra_ex2(m - m_new) : 1.0f;
+          if (!first && __any_sync(0xffffffffu, raise)) {
+            if (!mbar_wait_warp(done, done_ph, p.err, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              uint32_t v[16];
+              tmem_ld_32x32b_x16(oadr + c * 16, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+              tmem_st_32x32b_x16(oadr + c * 16, v);
+            }
+          }
+          const uint32_t neg = __float_as_uint(m_new > -INFINITY ? -m_new : 0.f), sc = __float_as_uint(scale);
+          const uint64_t neg2 = ra_pair(neg, neg), sc2 = ra_pair(sc, sc);
+          uint64_t r0 = 0, r1 = 0;
+          uint32_t pk[64];
+#pragma unroll
+          for (int e = 0; e < RA_BKV; e += 4) {
+            float p0, p1, p2, p3;
+            ra_unpair(ra_fma2(ra_pair(sv[e], sv[e + 1]), sc2, neg2), p0, p1);
+            ra_unpair(ra_fma2(ra_pair(sv[e + 2], sv[e + 3]), sc2, neg2), p2, p3);
+            p0 = ra_ex2(p0);
+            p1 = ra_ex2(p1);
+            p2 = ra_ex2(p2);
+            p3 = ra_ex2(p3);
+            r0 = ra_add2(r0, ra_pair(__float_as_uint(p0), __float_as_uint(p1)));
+            r1 = ra_add2(r1, ra_pair(__float_as_uint(p2), __float_as_uint(p3)));
+            pk[e >> 1] = pack_bf16x2(p0, p1);      // P enters its product as bf16: half a step (2^-8 at most) per weight
+            pk[(e >> 1) + 1] = pack_bf16x2(p2, p3);
+          }
+          float a0, a1, a2, a3;
+          ra_unpair(r0, a0, a1);
+          ra_unpair(r1, a2, a3);
+          l = l * alpha + ((a0 + a1) + (a2 + a3));
+          m = m_new;
+          if (n > 0 && !mbar_wait_warp(done, done_ph, p.err, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          tmem_st_32x32b_x32(padr, *reinterpret_cast<uint32_t(*)[32]>(pk));
+          tmem_st_32x32b_x32(padr + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(s));
         }
-        tmem_st_32x32b_x32(sadr, *reinterpret_cast<uint32_t(*)[32]>(pk));
-        tmem_st_32x32b_x32(sadr + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
-        l = l * alpha + ((r0 + r1) + (r2 + r3));
-        m = m_new;
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(s));
+        lim -= RA_BKV;
+        over -= RA_BKV;
+        end -= RA_BKV;
       }
       if (!ok) break;
       // the piece's last P V product, step n - 1's
       if (!mbar_wait_warp(p_done((n - 1) & 1), ((n - 1) >> 1) & 1, p.err, abort_flag)) { ok = false; break; }
       tc_fence_after();
-      const bool whole = w.ta == 0 && w.tb == w.tiles;
       if (busy) {
-        const int head = w.ig * p.G + hh;
-        const int64_t orow = static_cast<int64_t>(w.rq.r0 + first_tok + tok) * p.Hq + head;
-        const int64_t pc = (static_cast<int64_t>(cta) * 2 + (w.idx > 0 ? 1 : 0)) * RA_BQ + r;
+        const RaPiece& c = piece(k);
+        const bool whole = c.flags & 1;
+        const int tok = r / p.G;
+        const bool mine = r < c.toks * p.G;
+        const int64_t orow = static_cast<int64_t>(c.row0 + tok) * p.Hq + c.head0 + (r - tok * p.G);
+        const int64_t pc = (static_cast<int64_t>(cta) * 2 + (c.flags >> 1)) * RA_BQ + r;
         const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int h = 0; h < 4; ++h) {
           uint32_t v[32];
-          tmem_ld_32x32b_x32(oadr + c * 32, v);
+          tmem_ld_32x32b_x32(oadr + h * 32, v);
           tmem_ld_wait();
           if (!mine) continue;
           if (whole) {
-            __nv_bfloat16* orow_p = p.o + orow * RA_D + c * 32;
+            __nv_bfloat16* orow_p = p.o + orow * RA_D + h * 32;
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
               uint4 x;
@@ -662,7 +796,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
               *reinterpret_cast<uint4*>(orow_p + e) = x;
             }
           } else {
-            float* po = p.part_o + pc * RA_D + c * 32;
+            float* po = p.part_o + pc * RA_D + h * 32;
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
               *reinterpret_cast<uint4*>(po + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
@@ -676,9 +810,9 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
           }
         }
       }
+      // the next piece's first P V into O follows this warp's next arrival
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(o_empty(ob));   // O[ob] may take piece k + 2's products
     }
     if (!ok) *abort_flag = 1;
   }

@@ -477,7 +477,7 @@ KL_API kl_status kl_layer_forward_paged(const kl_layer_cfg* cfg, const kl_paged_
  * the device, starting at 0 and not decreasing; rows from cu_rows[B] on are
  * neither read nor written. Pools and tables are those of kl_paged_cfg. bf16,
  * head dim 128, Hq / Hkv <= 128; pool rows (n_blocks * block_size * Hkv) below
- * 2^31; T at most 2^24. int32 and fp32 arrays of these entry points need only
+ * 2^31; T at most 2^24, max_blocks * block_size at most 2^30. int32 and fp32 arrays of these entry points need only
  * 4-byte alignment (they may be pieces of one buffer). */
 typedef struct kl_ragged_cfg {
   int32_t B;           /* requests in the step                               */
