@@ -21,9 +21,15 @@
 // results repeat bit for bit. The workspace holds two pieces per CTA and does
 // not depend on the lengths.
 //
-// Roles (7 warps): warp 0 looks up the pages and copies Q and the keys, warp 1
-// the values, warp 2 issues the products, warps 3..6 are the softmax (thread =
-// query row = TMEM lane): the scheme of the training forward's persistent kernel.
+// Roles (8 warps): warp 0 looks up the pages and copies Q and the keys, warp 1
+// the values, warp 2 issues the score products, warp 3 the P V products, warps
+// 4..7 are the softmax (thread = query row = TMEM lane). A step's chain is
+// scores -> softmax -> P V. S and P have two buffers each: S_(n+2) waits only for
+// S_n to be read, P_n only for the product of step n - 2, so neither product's
+// latency lies on the softmax warps' path. Each kind of product has a warp of
+// its own because a warp's barrier probes queue up behind the products it has
+// issued (measured: 514 cycles for 8 products of 64, 820 with three probes in
+// between): one warp for both kept the tensor core waiting, 1850 cycles a step.
 // Pages: with block_size a multiple of 8 a key tile is 128 / box TMA boxes of
 // box = gcd(block_size, 128) rows, each found through the table; a box past the
 // context, past its table row or whose table entry lies outside the pool starts
@@ -46,7 +52,7 @@ namespace {
 constexpr int RA_D = 128;        // head dim
 constexpr int RA_BQ = 128;       // rows of a query tile
 constexpr int RA_BKV = 128;      // keys per tile
-constexpr int RA_WARPS = 7;      // K copies, V copies, products, four of softmax
+constexpr int RA_WARPS = 8;      // K copies, V copies, score products, P V products, four of softmax
 constexpr int RA_THREADS = 32 * RA_WARPS;
 // A key or value tile (32 KB) is 16 groups of 8 keys, each group two swizzled
 // blocks of 8 rows x 64 columns (1 KB): a page of 8 m tokens is then one TMA box
@@ -58,8 +64,8 @@ constexpr uint32_t RA_OFF_K = RA_OFF_Q + RA_TILE;
 constexpr uint32_t RA_OFF_V = RA_OFF_K + RA_NST * RA_TILE;
 constexpr uint32_t RA_OFF_BAR = RA_OFF_V + RA_NST * RA_TILE;
 constexpr size_t RA_SMEM = 1024 + RA_OFF_BAR + 1536;
-// Tensor memory: S of two steps, P (bf16 pairs), O, Q (bf16 pairs): all 512 columns.
-constexpr uint32_t RA_TM_P = 256, RA_TM_O = 320, RA_TM_Q = 448;
+// Tensor memory: S of two steps, P of two steps (bf16 pairs), O: all 512 columns.
+constexpr uint32_t RA_TM_P = 256, RA_TM_O = 384;
 constexpr int RA_ITEM_UNITS = 1;              // units an item's start and end count for
 constexpr int RA_MIN_UNITS = 3;               // units per CTA at least
 constexpr float RA_LOG2E = 1.4426950408889634f;
@@ -95,6 +101,10 @@ __device__ __forceinline__ float ra_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// Q, K-major (two 64-column swizzle blocks of 128 rows), k-step kk of 16 columns
+__device__ __forceinline__ uint64_t ra_desc_q(uint32_t base, int kk) {
+  return smem_desc_sw128(base + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024);
 }
 // Pairs of floats in one 64-bit register: one instruction for two elements.
 __device__ __forceinline__ uint64_t ra_pair(uint32_t lo, uint32_t hi) {
@@ -292,7 +302,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
   // barriers; those of a pair serve the steps of one parity each, so that a warp
   // which runs a step ahead of another cannot count for its phase
   const uint32_t q_full = bar + 0, drain = bar + 8;
-  const uint32_t q_tm = bar + 16;                           // a piece's Q copied to tensor memory
+  const uint32_t q_empty = bar + 16;                        // a piece's last S product is done with Q
   auto k_full = [&](int s) { return bar + 24 + 8 * s; };
   auto k_empty = [&](int s) { return bar + 48 + 8 * s; };
   auto v_full = [&](int s) { return bar + 72 + 8 * s; };
@@ -301,21 +311,22 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
   auto s_free = [&](int s) { return bar + 136 + 8 * s; };   // S_n read
   auto p_full = [&](int s) { return bar + 152 + 8 * s; };   // P_n written (and V_n's tail cleared)
   auto p_done = [&](int s) { return bar + 168 + 8 * s; };   // O += P_n V_n computed
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + RA_OFF_BAR + 184);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + RA_OFF_BAR + 188);
+  const uint32_t drain_pv = bar + 184;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + RA_OFF_BAR + 192);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + RA_OFF_BAR + 196);
   RaStart* start = reinterpret_cast<RaStart*>(smem + RA_OFF_BAR + 208);
-  long long* wsum = reinterpret_cast<long long*>(smem + RA_OFF_BAR + 256);   // [8]: the warps' unit sums, then this CTA's units
+  long long* wsum = reinterpret_cast<long long*>(smem + RA_OFF_BAR + 256);   // the warps' unit sums, then this CTA's units
 
-  RaWalk* walks = reinterpret_cast<RaWalk*>(smem + RA_OFF_BAR + 320);        // [4], of the softmax warps
+  RaWalk* walks = reinterpret_cast<RaWalk*>(smem + RA_OFF_BAR + 336);        // [4], of the softmax warps
   RaPiece* pieces = reinterpret_cast<RaPiece*>(smem + RA_OFF_BAR + 1024);    // [4][2]
-  static_assert(4 * sizeof(RaWalk) <= 704 && 8 * sizeof(RaPiece) <= 512, "shared-memory layout");
+  static_assert(4 * sizeof(RaWalk) <= 688 && 8 * sizeof(RaPiece) <= 512, "shared-memory layout");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    mbar_init(q_tm, 4);
+    mbar_init(q_empty, 1);
     for (int s = 0; s < RA_NST; ++s) {
       mbar_init(k_full(s), TMA ? 1 : 32);
       mbar_init(k_empty(s), 1);
@@ -329,6 +340,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
       mbar_init(p_done(s), 1);
     }
     mbar_init(drain, 1);
+    mbar_init(drain_pv, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -359,7 +371,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     const long long P = max(ra_div(W + ctas - 1, ctas), static_cast<long long>(RA_MIN_UNITS));
     const long long u0 = cta * P;
     if (threadIdx.x == 0) {
-      wsum[7] = max(0LL, min(P, W - u0));     // units of this CTA
+      wsum[RA_WARPS] = max(0LL, min(P, W - u0));     // units of this CTA
       start->P = P;
       if (u0 >= W) start->b = -1;
     }
@@ -391,9 +403,9 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const uint32_t tmP = tmem + RA_TM_P, tmO = tmem + RA_TM_O, tmQ = tmem + RA_TM_Q;
+  const uint32_t tmP = tmem + RA_TM_P, tmO = tmem + RA_TM_O;
   const RaStart st = *start;
-  const long long units = wsum[7];
+  const long long units = wsum[RA_WARPS];
   if (threadIdx.x == 0) p.starts[cta] = st;
   const int GT = p.G * p.TQ;            // rows of a full query tile
 
@@ -453,8 +465,8 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     w.init(p, st, units);
     while (ok && w.next(p)) {
       if (is_k) {
-        // Q: the buffer is free once the previous piece's Q is in tensor memory
-        if (!ra_wait_copy(q_tm, (issued_q & 1) ^ 1u, p.err, abort_flag)) { ok = false; break; }
+        // Q: the buffer is free once the previous piece's last S product is done
+        if (!ra_wait_copy(q_empty, (issued_q & 1) ^ 1u, p.err, abort_flag)) { ok = false; break; }
         if (el) {
           mbar_arrive_expect_tx(q_full, 2u * GT * 128u);
           const int t0 = w.rq.r0 + w.iq * p.TQ;
@@ -506,79 +518,35 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
   } else if (warp == 2) {
-    // ---------------- MMA (whole warp; the elected lane issues) ----------------
-    // S_n = Q K_n^T into S[n % 2] as soon as K_n is there and the softmax warps
-    // have read S_(n-2); O += P_n V_n as soon as P_n and V_n are there: whichever
-    // is ready first, so that a late key tile does not hold up the products that
-    // would free a value tile.
+    // ---------- S_n = Q K_n^T into S[n % 2] (whole warp; the elected lane issues) ----------
     const bool el = elect_one();
-    const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);
-    const uint32_t idesc_pv = idesc_bf16_f32(128, 128, 0, 1);
-    auto ready = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(b, parity)); };
-    int vs = 0, ks = 0;                       // stages of the V and K rings
-    uint32_t vph = 0, kph = 0;
-    int sn = 0, pn = 0, k = 0;                // next step of S and of P V; the S products' piece
-    uint32_t firsts = 0;                      // bit n % 4: step n begins a piece
-    uint64_t t0 = 0;
-    uint32_t spins = 0;
+    const uint32_t idesc = idesc_bf16_f32(128, 128, 0, 0);
+    int n = 0, k = 0, ks = 0;                 // step, piece, K stage
+    uint32_t kph = 0;
     bool ok = true;
     RaWalk w;
     w.init(p, st, units);
-    bool more = w.next(p);
-    int j = more ? w.ta : 0;
-    while (more || pn < sn) {
-      bool idle = true;
-      if (more && (j > w.ta || ready(q_tm, k & 1)) && ready(k_full(ks), kph) &&
-          (sn < 2 || ready(s_free(sn & 1), ((sn >> 1) & 1) ^ 1u))) {
+    for (; ok && w.next(p); ++k) {
+      if (!mbar_wait_warp(q_full, k & 1, p.err, abort_flag)) { ok = false; break; }
+      for (int j = w.ta; j < w.tb; ++j, ++n) {
+        const int s = n & 1;
+        if ((n >= 2 && !mbar_wait_warp(s_free(s), ((n >> 1) & 1) ^ 1u, p.err, abort_flag)) ||
+            !mbar_wait_warp(k_full(ks), kph, p.err, abort_flag)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
         if (el) {
           for (int kk = 0; kk < RA_D / 16; ++kk)
-            umma_bf16_ta(tmem + (sn & 1) * 128, tmQ + kk * 8, ra_desc_k(sb + RA_OFF_K + ks * RA_TILE, kk), idesc_s, kk > 0);
+            umma_bf16(tmem + s * 128, ra_desc_q(sb + RA_OFF_Q, kk), ra_desc_k(sb + RA_OFF_K + ks * RA_TILE, kk), idesc, kk > 0);
+          umma_commit(s_full(s));
           umma_commit(k_empty(ks));
-          umma_commit(s_full(sn & 1));
+          if (j == w.tb - 1) umma_commit(q_empty);   // the piece's last use of Q
         }
         __syncwarp();
-        const uint32_t bit = 1u << (sn & 3);
-        firsts = j == w.ta ? firsts | bit : firsts & ~bit;
         if (++ks == RA_NST) {
           ks = 0;
           kph ^= 1u;
-        }
-        ++sn;
-        if (++j == w.tb) {
-          more = w.next(p);
-          j = w.ta;
-          ++k;
-        }
-        idle = false;
-      }
-      if (pn < sn && ready(p_full(pn & 1), (pn >> 1) & 1) && ready(v_full(vs), vph)) {
-        tc_fence_after();
-        if (el) {
-          const bool first = firsts >> (pn & 3) & 1u;
-          for (int kk = 0; kk < RA_BKV / 16; ++kk)
-            umma_bf16_ta(tmO, tmP + kk * 8, ra_desc_v(sb + RA_OFF_V + vs * RA_TILE, kk), idesc_pv, (!first || kk > 0) ? 1u : 0u);
-          umma_commit(v_empty(vs));
-          umma_commit(p_done(pn & 1));
-        }
-        __syncwarp();
-        if (++vs == RA_NST) {
-          vs = 0;
-          vph ^= 1u;
-        }
-        ++pn;
-        idle = false;
-      }
-      if (!idle) {
-        spins = 0;
-      } else if (__nanosleep(20), (++spins & 255u) == 0) {     // bounded, as every wait
-        const uint64_t t = global_timer_ns();
-        if (spins == 256u) t0 = t;
-        const bool late = t - t0 > KL_WAIT_LIMIT_NS;
-        if (late && el) record_error(p.err, KL_DEVERR_TIMEOUT);
-        if (__any_sync(0xffffffffu, late || *abort_flag)) {
-          ok = false;
-          break;
         }
       }
     }
@@ -586,6 +554,42 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     if (el) umma_commit(drain);
     __syncwarp();
     mbar_wait(drain, 0, p.err);
+  } else if (warp == 3) {
+    // ---------- O (+)= P_n V_n (whole warp; the elected lane issues) ----------
+    const bool el = elect_one();
+    const uint32_t idesc = idesc_bf16_f32(128, 128, 0, 1);
+    int n = 0, vs = 0;                        // step, V stage
+    uint32_t vph = 0;
+    bool ok = true;
+    RaWalk w;
+    w.init(p, st, units);
+    while (ok && w.next(p)) {
+      for (int j = w.ta; j < w.tb; ++j, ++n) {
+        const int s = n & 1;
+        if (!mbar_wait_warp(v_full(vs), vph, p.err, abort_flag) ||
+            !mbar_wait_warp(p_full(s), (n >> 1) & 1, p.err, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (el) {
+          for (int kk = 0; kk < RA_BKV / 16; ++kk)
+            umma_bf16_ta(tmO, tmP + s * 64 + kk * 8, ra_desc_v(sb + RA_OFF_V + vs * RA_TILE, kk), idesc,
+                         (j > w.ta || kk > 0) ? 1u : 0u);
+          umma_commit(p_done(s));
+          umma_commit(v_empty(vs));
+        }
+        __syncwarp();
+        if (++vs == RA_NST) {
+          vs = 0;
+          vph ^= 1u;
+        }
+      }
+    }
+    if (!ok) *abort_flag = 1;
+    if (el) umma_commit(drain_pv);
+    __syncwarp();
+    mbar_wait(drain_pv, 0, p.err);
   } else {
     // ---------------- softmax / correction / epilogue ----------------
     const int quarter = warp & 3;
@@ -615,33 +619,11 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
       __syncwarp();
       return piece(k).tb > 0;
     };
-    // this row's Q (two 128-byte-swizzled 64-column blocks) to tensor memory, the
-    // A operand of its piece's score products
-    auto copy_q = [&](int k) -> bool {
-      if (!mbar_wait_warp(q_full, k & 1, p.err, abort_flag)) return false;
-      const uint8_t* qs = smem + RA_OFF_Q + r * 128;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t qa[32];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint4 x = *reinterpret_cast<const uint4*>(qs + c * 16384 + ((e ^ (r & 7)) << 4));
-          qa[4 * e] = x.x; qa[4 * e + 1] = x.y; qa[4 * e + 2] = x.z; qa[4 * e + 3] = x.w;
-        }
-        tmem_st_32x32b_x32(tmQ + lane_off + c * 32, qa);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_tm);
-      return true;
-    };
     if (lane == 0) walk.init(p, st, units);
-    bool have = find(0);
-    bool ok = !have || copy_q(0);
+    bool ok = true;
     const float scale = p.scale_log2;
     int n = 0;
-    for (int k = 0; ok && have; ++k) {
+    for (int k = 0; ok && find(k); ++k) {
       int left, lim, over, end;                    // tiles left; the row's last key, the tile's first row's, and the
       bool busy;                                   // context's end, counted from the tile's first key
       {
@@ -671,16 +653,12 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
         }
         if (!mbar_wait_warp(s_full(s), (n >> 1) & 1, p.err, abort_flag)) { ok = false; break; }
         tc_fence_after();
-        if (left == 1) {                           // the piece's last scores: Q's columns take the next piece's
-          have = find(k + 1);
-          if (have && !copy_q(k + 1)) { ok = false; break; }
-        }
-        // P's columns and O are free once the previous product is done. A warp
-        // without rows waits for that too: it must not count for step n + 2's phase
-        // while another still works on step n.
-        const uint32_t done = p_done(s ^ 1), done_ph = ((n - 1) >> 1) & 1;
+        // P's columns are free once the product of step n - 2 is done. A warp
+        // without rows waits for that too: it must not count for step n's phase while
+        // another still works on step n - 2.
+        const uint32_t done_ph = ((n >> 1) & 1) ^ 1u;
         if (!busy) {                               // no real row: P stays whatever it is, its O rows are never read
-          if (n > 0 && !mbar_wait_warp(done, done_ph, p.err, abort_flag)) { ok = false; break; }
+          if (n >= 2 && !mbar_wait_warp(p_done(s), done_ph, p.err, abort_flag)) { ok = false; break; }
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(s_free(s));
@@ -718,7 +696,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
           const float m_new = raise ? mx : m;
           const float alpha = raise ? ra_ex2(m - m_new) : 1.0f;
           if (!first && __any_sync(0xffffffffu, raise)) {
-            if (!mbar_wait_warp(done, done_ph, p.err, abort_flag)) { ok = false; break; }
+            if (!mbar_wait_warp(p_done(s ^ 1), ((n - 1) >> 1) & 1, p.err, abort_flag)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
@@ -753,10 +731,10 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
           ra_unpair(r1, a2, a3);
           l = l * alpha + ((a0 + a1) + (a2 + a3));
           m = m_new;
-          if (n > 0 && !mbar_wait_warp(done, done_ph, p.err, abort_flag)) { ok = false; break; }
+          if (n >= 2 && !mbar_wait_warp(p_done(s), done_ph, p.err, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          tmem_st_32x32b_x32(padr, *reinterpret_cast<uint32_t(*)[32]>(pk));
-          tmem_st_32x32b_x32(padr + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
+          tmem_st_32x32b_x32(padr + s * 64, *reinterpret_cast<uint32_t(*)[32]>(pk));
+          tmem_st_32x32b_x32(padr + s * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
