@@ -63,7 +63,7 @@ constexpr uint32_t RA_OFF_Q = 0;
 constexpr uint32_t RA_OFF_K = RA_OFF_Q + RA_TILE;
 constexpr uint32_t RA_OFF_V = RA_OFF_K + RA_NST * RA_TILE;
 constexpr uint32_t RA_OFF_BAR = RA_OFF_V + RA_NST * RA_TILE;
-constexpr size_t RA_SMEM = 1024 + RA_OFF_BAR + 1536;
+constexpr size_t RA_SMEM = 1024 + RA_OFF_BAR + 2048;
 // Tensor memory: S of two steps, P of two steps (bf16 pairs), O: all 512 columns.
 constexpr uint32_t RA_TM_P = 256, RA_TM_O = 384;
 constexpr int RA_ITEM_UNITS = 1;              // units an item's start and end count for
@@ -71,11 +71,22 @@ constexpr int RA_MIN_UNITS = 3;               // units per CTA at least
 constexpr float RA_LOG2E = 1.4426950408889634f;
 constexpr float RA_LN2 = 0.6931471805599453f;
 
-// Where a CTA's run of units starts: an item and the unit inside it.
+// One request's rows and context, every value brought into range (no table row
+// is as long as RA_MAX_CTX, so a context beyond it is past its table anyway).
+constexpr int RA_MAX_CTX = 1 << 30;
+struct RaReq {
+  int r0, n, ctx;
+};
+
+// Where a CTA's run of units starts: an item and the unit inside it. The cut
+// that the run's start makes, for the joining kernel: pieces of the item, its
+// rows, the first one's row of the step; pieces 0: nothing to join here.
 struct RaStart {
-  int b, g, qt, pad;
+  int b, g, qt;
+  int pieces, rows, row0;
+  int first_slot;   // of the CTA before: 0 if this item was its first
+  RaReq q;
   long long off;    // unit within the item
-  long long P;      // units per CTA
 };
 
 struct RaParams {
@@ -87,7 +98,7 @@ struct RaParams {
   const int32_t* ctx;
   __nv_bfloat16* o;
   float* lse;            // [T, Hq] or null
-  float* part_o;         // [CTA][2][128][128] unnormalised pieces
+  float* part_o;         // [CTA][2][32][128][4] unnormalised pieces: 4 columns of the 128 rows together
   float* part_ml;        // [CTA][2][128][2] (max in log2 units, sum)
   RaStart* starts;       // [CTA]
   int B, T, Hq, Hkv, G, TQ;
@@ -175,12 +186,6 @@ __device__ __forceinline__ bool ra_wait_copy(uint32_t bar, uint32_t parity, uint
   return true;
 }
 
-// One request's rows and context, every value brought into range (no table row
-// is as long as RA_MAX_CTX, so a context beyond it is past its table anyway).
-constexpr int RA_MAX_CTX = 1 << 30;
-struct RaReq {
-  int r0, n, ctx;
-};
 __device__ __forceinline__ RaReq ra_req(const RaParams& p, int b) {
   RaReq q;
   q.r0 = min(max(p.cu[b], 0), p.T);
@@ -196,7 +201,7 @@ __device__ __forceinline__ int ra_tiles(const RaReq& q, int TQ, int qt) {
 //   sum_{k=1}^{m} (floor((ctx - 1 + k TQ) / 128) + 1 + RA_ITEM_UNITS).
 // The quotients repeat with period 128 / gcd(TQ, 128) up to a constant step, so
 // whole periods are summed in closed form.
-__device__ long long ra_units_before(int ctx, int TQ, long long m) {
+__device__ __noinline__ long long ra_units_before(int ctx, int TQ, long long m) {
   const int sh = __ffs(TQ) - 1;                   // gcd(TQ, 128) = 2^sh, TQ <= 128
   const int period = RA_BKV >> sh, step = TQ >> sh;
   const long long a = static_cast<long long>(ctx) - 1;
@@ -218,78 +223,71 @@ __device__ __forceinline__ long long ra_head_units(const RaReq& q, int TQ) {
 }
 
 // Quotient of non-negative numbers; most fit 32 bits, whose division is several times faster.
-__device__ __forceinline__ long long ra_div(long long a, long long b) {
+__device__ __noinline__ long long ra_div(long long a, long long b) {
   if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
   return a / b;
 }
 
-// The pieces of one CTA's run, in order. Every role walks the same list.
-struct RaWalk {
-  int b, g, qt;            // where the walk stands: request (its lengths: q), kv head, query tile,
-  long long off, left;     // unit inside the item, units left of the run
-  RaReq q;
-  int ib, ig, iq;          // the piece that next() found: request (its lengths: rq), kv head, query tile
-  RaReq rq;
-  int tiles, ta, tb;       // the item's key tiles; the piece's [ta, tb)
-  int idx;                 // items met so far: the first one's pieces take slot 0, a later one's slot 1
-
-  __device__ __forceinline__ void init(const RaParams& p, const RaStart& s, long long units) {
-    b = s.b;
-    g = s.g;
-    qt = s.qt;
-    off = s.off;
-    left = units;
-    idx = -1;
-    if (left > 0) q = ra_req(p, b);
-  }
-  // the next piece with at least one key tile, or false
-  __device__ __forceinline__ bool next(const RaParams& p) {
-    while (left > 0) {
-      tiles = ra_tiles(q, p.TQ, qt);
-      const long long len = tiles + RA_ITEM_UNITS;
-      const long long take = min(left, len - off);
-      const long long e = off + take;
-      ta = static_cast<int>(max(off - RA_ITEM_UNITS, 0LL));
-      tb = static_cast<int>(max(e - RA_ITEM_UNITS, 0LL));
-      left -= take;
-      ++idx;
-      ib = b;
-      ig = g;
-      iq = qt;
-      rq = q;
-      if (left > 0) {      // the item ends here: on to the next
-        off = 0;
-        if ((qt + 1) * p.TQ < q.n) {
-          ++qt;
-        } else {
-          qt = 0;
-          if (++g == p.Hkv) {
-            g = 0;
-            do {
-              if (++b >= p.B) {      // cannot happen: the run lies inside the W units
-                left = 0;
-                break;
-              }
-              q = ra_req(p, b);
-            } while (q.n <= 0);
-          }
-        }
-      }
-      if (tb > ta) return true;
-    }
-    return false;
-  }
-};
-
-// What a softmax warp keeps of a piece, in shared memory: its registers are full
-// of scores, and every one more costs the steps (with the walk and 64-bit
-// positions in registers the steps took 1950 cycles).
+// One piece of a CTA's run: the query tile and the range of its key tiles.
 struct RaPiece {
-  int row0, toks, head0;   // the tile's first row of the step, its tokens, its first head
+  int b, g;                // request, kv head
+  int row0, toks;          // the tile's first row of the step, its tokens
   int pos0, L;             // position of its first token; keys of the request
   int ta, tb;              // key tiles; tb = 0: there is no such piece
   int flags;               // 1: all of the item's tiles; 2: the piece goes to slot 1
+  int pad;
 };
+// The walk over a CTA's run. Every role's warp walks for itself, in shared
+// memory: the softmax warps' registers are full of scores, and every one more
+// costs their steps (with the walk in registers they spilled).
+struct RaWalk {
+  int b, g, qt;            // request (its lengths: q), kv head, query tile
+  int idx;                 // items met so far: the first one's pieces take slot 0, a later one's slot 1
+  RaReq q;
+  long long off, left;     // unit inside the item, units left of the run
+};
+// The next piece with at least one key tile into c. Called by one lane; one copy
+// of the code for all roles (a CTA's start is bound by instruction fetches).
+__device__ __noinline__ void ra_next(const RaParams& p, RaWalk& w, RaPiece& c) {
+  c.tb = 0;
+  while (w.left > 0) {
+    const int tiles = ra_tiles(w.q, p.TQ, w.qt);
+    const long long len = tiles + RA_ITEM_UNITS;
+    const long long take = min(w.left, len - w.off), e = w.off + take;
+    const int first = w.qt * p.TQ;
+    c.ta = static_cast<int>(max(w.off - RA_ITEM_UNITS, 0LL));
+    c.tb = static_cast<int>(max(e - RA_ITEM_UNITS, 0LL));
+    c.b = w.b;
+    c.g = w.g;
+    c.row0 = w.q.r0 + first;
+    c.toks = min(p.TQ, w.q.n - first);
+    c.pos0 = w.q.ctx + first;
+    c.L = w.q.ctx + w.q.n;
+    c.flags = (c.ta == 0 && c.tb == tiles ? 1 : 0) | (w.idx > 0 ? 2 : 0);
+    w.left -= take;
+    ++w.idx;
+    if (w.left > 0) {      // the item ends here: on to the next
+      w.off = 0;
+      if (first + p.TQ < w.q.n) {
+        ++w.qt;
+      } else {
+        w.qt = 0;
+        if (++w.g == p.Hkv) {
+          w.g = 0;
+          do {
+            if (++w.b >= p.B) {      // cannot happen: the run lies inside the W units
+              w.left = 0;
+              break;
+            }
+            w.q = ra_req(p, w.b);
+          } while (w.q.n <= 0);
+        }
+      }
+    }
+    if (c.tb > c.ta) return;
+    c.tb = 0;
+  }
+}
 
 template <bool TMA>
 __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid_constant__ RaParams p) {
@@ -317,9 +315,9 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
   RaStart* start = reinterpret_cast<RaStart*>(smem + RA_OFF_BAR + 208);
   long long* wsum = reinterpret_cast<long long*>(smem + RA_OFF_BAR + 256);   // the warps' unit sums, then this CTA's units
 
-  RaWalk* walks = reinterpret_cast<RaWalk*>(smem + RA_OFF_BAR + 336);        // [4], of the softmax warps
-  RaPiece* pieces = reinterpret_cast<RaPiece*>(smem + RA_OFF_BAR + 1024);    // [4][2]
-  static_assert(4 * sizeof(RaWalk) <= 688 && 8 * sizeof(RaPiece) <= 512, "shared-memory layout");
+  RaWalk* walks = reinterpret_cast<RaWalk*>(smem + RA_OFF_BAR + 336);        // [8]
+  RaPiece* pieces = reinterpret_cast<RaPiece*>(smem + RA_OFF_BAR + 912);     // [8][2]
+  static_assert(RA_WARPS * sizeof(RaWalk) <= 576 && RA_WARPS * 2 * sizeof(RaPiece) <= 1136, "shared-memory layout");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
@@ -353,8 +351,13 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
   {
     const int per = (p.B + RA_THREADS - 1) / RA_THREADS;
     const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += ra_head_units(ra_req(p, b), p.TQ) * p.Hkv;
+    long long mine = 0, units = 0;
+    RaReq q = {0, 0, 0};
+    for (int b = b0; b < b1; ++b) {
+      q = ra_req(p, b);
+      units = ra_head_units(q, p.TQ);
+      mine += units * p.Hkv;
+    }
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -363,6 +366,8 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     }
     if (lane == 31) wsum[warp] = incl;
     __syncthreads();
+    if (lane == 0 && warp >= 5 && (TMA || warp == 5))
+      tma_prefetch_desc(warp == 5 ? &p.tmQ : warp == 6 ? &p.tmK : &p.tmV);
     long long before = 0, W = 0;
     for (int w = 0; w < RA_WARPS; ++w) {
       if (w < warp) before += wsum[w];
@@ -370,33 +375,42 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     }
     const long long P = max(ra_div(W + ctas - 1, ctas), static_cast<long long>(RA_MIN_UNITS));
     const long long u0 = cta * P;
-    if (threadIdx.x == 0) {
-      wsum[RA_WARPS] = max(0LL, min(P, W - u0));     // units of this CTA
-      start->P = P;
-      if (u0 >= W) start->b = -1;
+    if (threadIdx.x == 0) wsum[RA_WARPS] = max(0LL, min(P, W - u0));     // units of this CTA
+    if (threadIdx.x == 0 && u0 >= W) {
+      start->b = -1;
+      start->pieces = 0;
     }
     long long lo = before + incl - mine;      // units before this thread's requests
-    if (mine > 0 && u0 >= lo && u0 < lo + mine && u0 < W) {
+    if (mine > 0 && u0 >= lo && u0 < lo + mine) {
       int b = b0;
-      long long hu = 0;
-      for (; b < b1; ++b) {
-        hu = ra_head_units(ra_req(p, b), p.TQ);
-        if (u0 < lo + hu * p.Hkv) break;
-        lo += hu * p.Hkv;
+      if (per > 1) {                          // with one request a thread q and units are its own still
+        for (;; ++b) {
+          q = ra_req(p, b);
+          units = ra_head_units(q, p.TQ);
+          if (u0 < lo + units * p.Hkv) break;
+          lo += units * p.Hkv;
+        }
       }
-      const long long x = u0 - lo;
-      const RaReq q = ra_req(p, b);
-      const int g = static_cast<int>(ra_div(x, hu));
-      const long long y = x - g * hu;
+      const int g = static_cast<int>(ra_div(u0 - lo, units));
+      const long long y = u0 - lo - g * units;
       int m0 = 0, m1 = (q.n + p.TQ - 1) / p.TQ;      // the query tile: units_before(m0) <= y < units_before(m1)
       while (m1 - m0 > 1) {
         const int m = (m0 + m1) >> 1;
         if (ra_units_before(q.ctx, p.TQ, m) <= y) m0 = m; else m1 = m;
       }
+      const long long off = y - (m0 ? ra_units_before(q.ctx, p.TQ, m0) : 0);
       start->b = b;
       start->g = g;
       start->qt = m0;
-      start->off = y - ra_units_before(q.ctx, p.TQ, m0);
+      start->q = q;
+      start->off = off;
+      // the first cut of its item with key tiles on both sides joins the pieces
+      const long long len = ra_tiles(q, p.TQ, m0) + RA_ITEM_UNITS;
+      const bool joins = off > RA_ITEM_UNITS && off - P <= RA_ITEM_UNITS;
+      start->pieces = joins ? 1 + static_cast<int>(ra_div(len - off + P - 1, P)) : 0;
+      start->rows = min(p.TQ, q.n - m0 * p.TQ) * p.G;
+      start->row0 = q.r0 + m0 * p.TQ;
+      start->first_slot = off - P >= 0 ? 0 : 1;
     }
   }
   tc_fence_before();
@@ -409,6 +423,25 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
   if (threadIdx.x == 0) p.starts[cta] = st;
   const int GT = p.G * p.TQ;            // rows of a full query tile
 
+  RaWalk& walk = walks[warp];
+  if (lane == 0) {
+    walk.b = st.b;
+    walk.g = st.g;
+    walk.qt = st.qt;
+    walk.idx = 0;
+    walk.q = st.q;
+    walk.off = st.off;
+    walk.left = units;
+  }
+  auto piece = [&](int k) -> RaPiece& { return pieces[warp * 2 + (k & 1)]; };
+  // piece k of this CTA into its place; false if there is none
+  auto find = [&](int k) -> bool {
+    __syncwarp();                       // every lane is done with piece k - 2
+    if (lane == 0) ra_next(p, walk, piece(k));
+    __syncwarp();
+    return piece(k).tb > 0;
+  };
+
   if (warp < 2) {
     // ------- copies (warp 0: Q and K, warp 1: V; lane = page box of a tile) -------
     const bool is_k = warp == 0;
@@ -417,10 +450,6 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     const __nv_bfloat16* pool = is_k ? p.kp : p.vp;
     const uint32_t ring = sb + (is_k ? RA_OFF_K : RA_OFF_V);
     const uint32_t full0 = is_k ? k_full(0) : v_full(0), empty0 = is_k ? k_empty(0) : v_empty(0);
-    if (el) {
-      if (is_k) tma_prefetch_desc(&p.tmQ);
-      if (TMA) tma_prefetch_desc(tm);
-    }
     const int nbox = RA_BKV / p.box;
     const int no_row = p.n_blocks * p.bs;         // past the pool's last row: filled with zeros
     int issued_q = 0, issued = 0, s = 0, as = 0;  // s: the ring's stage; as: the next one to announce
@@ -461,29 +490,26 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
       mbar_arrive(full0 + 8 * as);
       as = as == RA_NST - 1 ? 0 : as + 1;
     };
-    RaWalk w;
-    w.init(p, st, units);
-    while (ok && w.next(p)) {
+    for (int k = 0; ok && find(k); ++k) {
+      const RaPiece w = piece(k);
       if (is_k) {
         // Q: the buffer is free once the previous piece's last S product is done
         if (!ra_wait_copy(q_empty, (issued_q & 1) ^ 1u, p.err, abort_flag)) { ok = false; break; }
         if (el) {
           mbar_arrive_expect_tx(q_full, 2u * GT * 128u);
-          const int t0 = w.rq.r0 + w.iq * p.TQ;
-          ra_tma_3d(sb + RA_OFF_Q, &p.tmQ, 0, w.ig * p.G, t0, q_full);
-          ra_tma_3d(sb + RA_OFF_Q + 16384, &p.tmQ, 64, w.ig * p.G, t0, q_full);
+          ra_tma_3d(sb + RA_OFF_Q, &p.tmQ, 0, w.g * p.G, w.row0, q_full);
+          ra_tma_3d(sb + RA_OFF_Q + 16384, &p.tmQ, 64, w.g * p.G, w.row0, q_full);
         }
         __syncwarp();
         ++issued_q;
       }
-      const int L = w.rq.ctx + w.rq.n;
       int row[4];
       auto lookup = [&](int j) {
         if (TMA) {
-          row[0] = lane < nbox ? pool_row(w.ib, j * RA_BKV + lane * p.box, L) : no_row;
+          row[0] = lane < nbox ? pool_row(w.b, j * RA_BKV + lane * p.box, w.L) : no_row;
         } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) row[k] = pool_row(w.ib, j * RA_BKV + k * 32 + lane, L);
+          for (int i = 0; i < 4; ++i) row[i] = pool_row(w.b, j * RA_BKV + i * 32 + lane, w.L);
         }
       };
       lookup(w.ta);
@@ -493,10 +519,10 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
         if (TMA) {
           if (el) mbar_arrive_expect_tx(full0 + 8 * s, RA_TILE);
           __syncwarp();
-          if (lane < nbox) ra_tma_4d(dst + lane * p.box * 256, tm, 0, 0, 2 * w.ig, row[0] >> 3, full0 + 8 * s);
+          if (lane < nbox) ra_tma_4d(dst + lane * p.box * 256, tm, 0, 0, 2 * w.g, row[0] >> 3, full0 + 8 * s);
           __syncwarp();
         } else {
-          gather(dst, w.ig, row);
+          gather(dst, w.g, row);
           if (j > w.ta) announce(std::integral_constant<int, 1>());   // the tile before
         }
         ++issued;
@@ -524,11 +550,10 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     int n = 0, k = 0, ks = 0;                 // step, piece, K stage
     uint32_t kph = 0;
     bool ok = true;
-    RaWalk w;
-    w.init(p, st, units);
-    for (; ok && w.next(p); ++k) {
+    for (; ok && find(k); ++k) {
+      const int tiles = piece(k).tb - piece(k).ta;
       if (!mbar_wait_warp(q_full, k & 1, p.err, abort_flag)) { ok = false; break; }
-      for (int j = w.ta; j < w.tb; ++j, ++n) {
+      for (int j = 0; j < tiles; ++j, ++n) {
         const int s = n & 1;
         if ((n >= 2 && !mbar_wait_warp(s_free(s), ((n >> 1) & 1) ^ 1u, p.err, abort_flag)) ||
             !mbar_wait_warp(k_full(ks), kph, p.err, abort_flag)) {
@@ -541,7 +566,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
             umma_bf16(tmem + s * 128, ra_desc_q(sb + RA_OFF_Q, kk), ra_desc_k(sb + RA_OFF_K + ks * RA_TILE, kk), idesc, kk > 0);
           umma_commit(s_full(s));
           umma_commit(k_empty(ks));
-          if (j == w.tb - 1) umma_commit(q_empty);   // the piece's last use of Q
+          if (j == tiles - 1) umma_commit(q_empty);   // the piece's last use of Q
         }
         __syncwarp();
         if (++ks == RA_NST) {
@@ -561,10 +586,9 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     int n = 0, vs = 0;                        // step, V stage
     uint32_t vph = 0;
     bool ok = true;
-    RaWalk w;
-    w.init(p, st, units);
-    while (ok && w.next(p)) {
-      for (int j = w.ta; j < w.tb; ++j, ++n) {
+    for (int k = 0; ok && find(k); ++k) {
+      const int tiles = piece(k).tb - piece(k).ta;
+      for (int j = 0; j < tiles; ++j, ++n) {
         const int s = n & 1;
         if (!mbar_wait_warp(v_full(vs), vph, p.err, abort_flag) ||
             !mbar_wait_warp(p_full(s), (n >> 1) & 1, p.err, abort_flag)) {
@@ -575,7 +599,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
         if (el) {
           for (int kk = 0; kk < RA_BKV / 16; ++kk)
             umma_bf16_ta(tmO, tmP + s * 64 + kk * 8, ra_desc_v(sb + RA_OFF_V + vs * RA_TILE, kk), idesc,
-                         (j > w.ta || kk > 0) ? 1u : 0u);
+                         (j > 0 || kk > 0) ? 1u : 0u);
           umma_commit(p_done(s));
           umma_commit(v_empty(vs));
         }
@@ -596,30 +620,6 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     const int r = quarter * 32 + lane;           // row within the tile = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t oadr = tmO + lane_off, padr = tmP + lane_off;
-    RaWalk& walk = walks[quarter];
-    auto piece = [&](int k) -> RaPiece& { return pieces[quarter * 2 + (k & 1)]; };
-    // piece k of this CTA into its place; false if there is none
-    auto find = [&](int k) -> bool {
-      __syncwarp();                                // every lane is done with piece k - 2
-      if (lane == 0) {
-        RaPiece& c = piece(k);
-        c.tb = 0;
-        if (walk.next(p)) {
-          const int first = walk.iq * p.TQ;
-          c.row0 = walk.rq.r0 + first;
-          c.toks = min(p.TQ, walk.rq.n - first);
-          c.head0 = walk.ig * p.G;
-          c.pos0 = walk.rq.ctx + first;
-          c.L = walk.rq.ctx + walk.rq.n;
-          c.ta = walk.ta;
-          c.tb = walk.tb;
-          c.flags = (walk.ta == 0 && walk.tb == walk.tiles ? 1 : 0) | (walk.idx > 0 ? 2 : 0);
-        }
-      }
-      __syncwarp();
-      return piece(k).tb > 0;
-    };
-    if (lane == 0) walk.init(p, st, units);
     bool ok = true;
     const float scale = p.scale_log2;
     int n = 0;
@@ -753,8 +753,8 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
         const bool whole = c.flags & 1;
         const int tok = r / p.G;
         const bool mine = r < c.toks * p.G;
-        const int64_t orow = static_cast<int64_t>(c.row0 + tok) * p.Hq + c.head0 + (r - tok * p.G);
-        const int64_t pc = (static_cast<int64_t>(cta) * 2 + (c.flags >> 1)) * RA_BQ + r;
+        const int64_t orow = static_cast<int64_t>(c.row0 + tok) * p.Hq + c.g * p.G + (r - tok * p.G);
+        const int64_t pslot = static_cast<int64_t>(cta) * 2 + (c.flags >> 1);
         const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
@@ -774,17 +774,17 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
               *reinterpret_cast<uint4*>(orow_p + e) = x;
             }
           } else {
-            float* po = p.part_o + pc * RA_D + h * 32;
+            float* po = p.part_o + (pslot * RA_D + h * 32) * RA_BQ + r * 4;      // lanes side by side
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(po + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+              *reinterpret_cast<uint4*>(po + e * RA_BQ) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
           }
         }
         if (mine) {
           if (whole) {
             if (p.lse) p.lse[orow] = (m + log2f(l)) * RA_LN2;
           } else {
-            *reinterpret_cast<float2*>(p.part_ml + pc * 2) = make_float2(m, l);
+            *reinterpret_cast<float2*>(p.part_ml + (pslot * RA_BQ + r) * 2) = make_float2(m, l);
           }
         }
       }
@@ -803,9 +803,9 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
   }
 }
 
-// CTA (c, y): if the run boundary at CTA c's start is the first one that cuts its
-// item with key tiles on both sides, the rows 32 y .. 32 y + 31 of that item's
-// pieces are joined, one warp per row:
+// CTA (c - 1, y): the item that CTA c's run start cuts (if that is the item's
+// first cut with key tiles on both sides), rows 32 y .. 32 y + 31, a lane per row
+// and a warp per 16 columns:
 //   O = sum_s O_s 2^(m_s - M) / sum_s l_s 2^(m_s - M).
 // Pieces lie in CTA order: CTA c - 1's (its last item), then c, c + 1, ... (each
 // one's first).
@@ -814,46 +814,61 @@ __global__ void __launch_bounds__(RC_THREADS) ragged_combine_kernel(const __grid
   pdl_enter();
   const int c = blockIdx.x + 1;
   const RaStart st = p.starts[c];
-  if (st.b < 0) return;
-  const long long P = st.P;
-  // not the first cut with tiles before it
-  if (st.off <= RA_ITEM_UNITS || st.off - P > RA_ITEM_UNITS) return;
-  const RaReq q = ra_req(p, st.b);
-  const long long len = ra_tiles(q, p.TQ, st.qt) + RA_ITEM_UNITS;
-  const int np = 1 + static_cast<int>((len - st.off + P - 1) / P);
-  const int first_tok = st.qt * p.TQ;
-  const int rows = min(p.TQ, q.n - first_tok) * p.G;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int slot0 = st.off - P >= 0 ? 0 : 1;       // CTA c - 1 met this item as its first one, or later
-  for (int r = blockIdx.y * 32 + warp; r < min(rows, static_cast<int>(blockIdx.y) * 32 + 32); r += RC_THREADS / 32) {
-    auto piece = [&](int s) { return (static_cast<int64_t>(c - 1 + s) * 2 + (s == 0 ? slot0 : 0)) * RA_BQ + r; };
-    float M = -INFINITY;
-    for (int s = lane; s < np; s += 32) M = fmaxf(M, p.part_ml[piece(s) * 2]);
+  const int lane = threadIdx.x & 31, col = (threadIdx.x >> 5) * 16;
+  const int rows = st.rows - static_cast<int>(blockIdx.y) * 32;
+  if (rows <= 0 || st.pieces == 0) return;
+  // few rows (decoding): the lanes that have none take a share of the pieces
+  const int R = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  const int r = blockIdx.y * 32 + (lane & (R - 1));
+  auto slot = [&](int s) { return static_cast<int64_t>(c - 1 + s) * 2 + (s == 0 ? st.first_slot : 0); };
+  // running max over the pieces, as within a piece
+  float M = -INFINITY, l = 0.f, a[16];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float l = 0.f, a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+  for (int e = 0; e < 16; ++e) a[e] = 0.f;
+  auto add = [&](float m2, float l2, const float (&v)[16]) {
+    if (!(m2 > -INFINITY)) return;                 // a piece whose keys this row does not see
+    const float m_new = fmaxf(M, m2), f0 = exp2f(M - m_new), f = exp2f(m2 - m_new);
+    M = m_new;
+    l = fmaf(l2, f, l * f0);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) a[e] = fmaf(v[e], f, a[e] * f0);
+  };
+  if (r < st.rows) {
 #pragma unroll 4
-    for (int s = 0; s < np; ++s) {
-      const int64_t pc = piece(s);
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + pc * 2);
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + pc * RA_D + lane * 4);
-      if (!(ml.x > -INFINITY)) continue;           // a piece whose keys this row does not see
-      const float f = exp2f(ml.x - M);
-      l = fmaf(ml.y, f, l);
-      a0 = fmaf(v.x, f, a0);
-      a1 = fmaf(v.y, f, a1);
-      a2 = fmaf(v.z, f, a2);
-      a3 = fmaf(v.w, f, a3);
+    for (int s = lane / R; s < st.pieces; s += 32 / R) {
+      const int64_t at = slot(s);
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (at * RA_BQ + r) * 2);
+      const float* po = p.part_o + (at * RA_D + col) * RA_BQ + r * 4;
+      float v[16];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 x = *reinterpret_cast<const float4*>(po + e * 4 * RA_BQ);
+        v[4 * e] = x.x; v[4 * e + 1] = x.y; v[4 * e + 2] = x.z; v[4 * e + 3] = x.w;
+      }
+      add(ml.x, ml.y, v);
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int tok = r / p.G;
-    const int64_t orow = static_cast<int64_t>(q.r0 + first_tok + tok) * p.Hq + st.g * p.G + (r - tok * p.G);
-    uint2 x;
-    x.x = pack_bf16x2(a0 * inv, a1 * inv);
-    x.y = pack_bf16x2(a2 * inv, a3 * inv);
-    *reinterpret_cast<uint2*>(p.o + orow * RA_D + lane * 4) = x;
-    if (p.lse && lane == 0) p.lse[orow] = (M + log2f(l)) * RA_LN2;
   }
+  for (int o = 16; o >= R; o >>= 1) {
+    const float m2 = __shfl_down_sync(0xffffffffu, M, o), l2 = __shfl_down_sync(0xffffffffu, l, o);
+    float v[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = __shfl_down_sync(0xffffffffu, a[e], o);
+    if (lane < o) add(m2, l2, v);
+  }
+  if (lane >= R || r >= st.rows) return;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const int tok = r / p.G;
+  const int64_t orow = static_cast<int64_t>(st.row0 + tok) * p.Hq + st.g * p.G + (r - tok * p.G);
+#pragma unroll
+  for (int e = 0; e < 16; e += 8) {
+    uint4 x;
+    x.x = pack_bf16x2(a[e] * inv, a[e + 1] * inv);
+    x.y = pack_bf16x2(a[e + 2] * inv, a[e + 3] * inv);
+    x.z = pack_bf16x2(a[e + 4] * inv, a[e + 5] * inv);
+    x.w = pack_bf16x2(a[e + 6] * inv, a[e + 7] * inv);
+    *reinterpret_cast<uint4*>(p.o + orow * RA_D + col + e) = x;
+  }
+  if (p.lse && col == 0) p.lse[orow] = (M + log2f(l)) * RA_LN2;
 }
 
 kl_status ra_map(CUtensorMap* m, int rank, const void* ptr, const cuuint64_t* dims, const cuuint64_t* strides,
