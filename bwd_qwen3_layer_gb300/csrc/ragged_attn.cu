@@ -620,129 +620,155 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     const int r = quarter * 32 + lane;           // row within the tile = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t oadr = tmO + lane_off, padr = tmP + lane_off;
+    // The tile that holds the context's end: its value rows behind it become zero
+    // (each of the four warps its 32).
+    auto clear_tail = [&](int end, int n) -> bool {
+      if (end >= RA_BKV) return true;
+      const int vs = n % RA_NST;
+      if (!mbar_wait_warp(v_full(vs), (n / RA_NST) & 1, p.err, abort_flag)) return false;
+      if (r >= end) {
+        const uint32_t va = sb + RA_OFF_V + vs * RA_TILE + (r >> 3) * 2048 + (r & 7) * 128;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          st_shared_v4(va + c * 16, 0u, 0u, 0u, 0u);
+          st_shared_v4(va + 1024 + c * 16, 0u, 0u, 0u, 0u);
+        }
+      }
+      fence_async_shared();
+      return true;
+    };
     bool ok = true;
     const float scale = p.scale_log2;
     int n = 0;
+    float m = -INFINITY, l = 0.f;                  // the row's running max (log2 units) and sum
+    int lim = 0, end = 0;                          // the row's last key and the context's end, from the tile's first key
+    // One step of a warp with rows. CUT: some row of the tile ends inside its keys.
+    // The whole tiles before have a body of their own, without what that takes
+    // (tests and masks cost them ~180 cycles a step).
+    auto step = [&](auto cut, bool first) -> bool {
+      constexpr bool CUT = decltype(cut)::value;
+      const int s = n & 1;
+      if (CUT && TMA && !clear_tail(end, n)) return false;
+      if (!mbar_wait_warp(s_full(s), (n >> 1) & 1, p.err, abort_flag)) return false;
+      tc_fence_after();
+      const uint32_t sadr = tmem + lane_off + s * 128;
+      uint32_t sv[RA_BKV];
+      tmem_ld_32x32b_x32(sadr, *reinterpret_cast<uint32_t(*)[32]>(sv));
+      tmem_ld_32x32b_x32(sadr + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
+      tmem_ld_32x32b_x32(sadr + 64, *reinterpret_cast<uint32_t(*)[32]>(sv + 64));
+      tmem_ld_32x32b_x32(sadr + 96, *reinterpret_cast<uint32_t(*)[32]>(sv + 96));
+      // P's columns are free once the product of step n - 2 is done: probed here,
+      // where the probe's latency costs nothing, and most likely it is
+      const uint32_t done_ph = ((n >> 1) & 1) ^ 1u;
+      const bool p_ready = n < 2 || mbar_test_wait(p_done(s), done_ph);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_free(s));       // S[s] may be overwritten from here on
+      if (CUT) {                                   // keys 0 .. lim are kept
+#pragma unroll
+        for (int e = 0; e < RA_BKV; ++e)
+          if (e > lim) sv[e] = __float_as_uint(-INFINITY);
+      }
+      float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < RA_BKV; e += 8) {
+        m0 = ra_max3(m0, sv[e], sv[e + 1]);
+        m1 = ra_max3(m1, sv[e + 2], sv[e + 3]);
+        m2 = ra_max3(m2, sv[e + 4], sv[e + 5]);
+        m3 = ra_max3(m3, sv[e + 6], sv[e + 7]);
+      }
+      const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * scale;
+      // The max is only raised when it grows by more than 2^8 (the final O / l
+      // cancels a stale one). A row of a later piece's tile can be fully masked
+      // (its token ends before these keys): mx = -inf, and m stays -inf.
+      const bool raise = mx > m + 8.0f;
+      if (__any_sync(0xffffffffu, raise)) {
+        const float m_new = raise ? mx : m;
+        const float alpha = raise ? ra_ex2(m - m_new) : 1.0f;
+        m = m_new;
+        l *= alpha;
+        if (!first) {
+          if (!mbar_wait_warp(p_done(s ^ 1), ((n - 1) >> 1) & 1, p.err, abort_flag)) return false;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(oadr + c * 16, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+            tmem_st_32x32b_x16(oadr + c * 16, v);
+          }
+        }
+      }
+      const uint32_t neg = __float_as_uint(m > -INFINITY ? -m : 0.f), sc = __float_as_uint(scale);
+      const uint64_t neg2 = ra_pair(neg, neg), sc2 = ra_pair(sc, sc);
+      uint64_t r0 = 0, r1 = 0;
+      uint32_t pk[64];
+#pragma unroll
+      for (int e = 0; e < RA_BKV; e += 4) {
+        float p0, p1, p2, p3;
+        ra_unpair(ra_fma2(ra_pair(sv[e], sv[e + 1]), sc2, neg2), p0, p1);
+        ra_unpair(ra_fma2(ra_pair(sv[e + 2], sv[e + 3]), sc2, neg2), p2, p3);
+        p0 = ra_ex2(p0);
+        p1 = ra_ex2(p1);
+        p2 = ra_ex2(p2);
+        p3 = ra_ex2(p3);
+        r0 = ra_add2(r0, ra_pair(__float_as_uint(p0), __float_as_uint(p1)));
+        r1 = ra_add2(r1, ra_pair(__float_as_uint(p2), __float_as_uint(p3)));
+        pk[e >> 1] = pack_bf16x2(p0, p1);          // P enters its product as bf16: half a step (2^-8 at most) per weight
+        pk[(e >> 1) + 1] = pack_bf16x2(p2, p3);
+      }
+      float a0, a1, a2, a3;
+      ra_unpair(r0, a0, a1);
+      ra_unpair(r1, a2, a3);
+      l += (a0 + a1) + (a2 + a3);
+      if (!__all_sync(0xffffffffu, p_ready) && !mbar_wait_warp(p_done(s), done_ph, p.err, abort_flag)) return false;
+      tc_fence_after();
+      tmem_st_32x32b_x32(padr + s * 64, *reinterpret_cast<uint32_t(*)[32]>(pk));
+      tmem_st_32x32b_x32(padr + s * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full(s));
+      lim -= RA_BKV;
+      end -= RA_BKV;
+      ++n;
+      return true;
+    };
     for (int k = 0; ok && find(k); ++k) {
-      int left, lim, over, end;                    // tiles left; the row's last key, the tile's first row's, and the
-      bool busy;                                   // context's end, counted from the tile's first key
+      int left, whole;                             // tiles left; those that every row sees whole
+      bool busy;
       {
         const RaPiece& c = piece(k);
         left = c.tb - c.ta;
-        over = c.pos0 - c.ta * RA_BKV;
+        const int over = c.pos0 - c.ta * RA_BKV;   // the tile's first row's last key
+        whole = min(left, (over + 1) >> 7);        // below zero: none
         lim = over + min(r / p.G, c.toks - 1);     // padding rows: the last real row's limit
         end = c.L - c.ta * RA_BKV;
         busy = quarter * 32 < c.toks * p.G;        // some row of this warp is real
       }
-      float m = -INFINITY, l = 0.f;
-      for (bool first = true; left > 0; --left, ++n, first = false) {
-        const int s = n & 1;
-        // the tile that holds the context's end: the value rows behind it become zero
-        if (TMA && end < RA_BKV) {
-          const int vs = n % RA_NST;
-          if (!mbar_wait_warp(v_full(vs), (n / RA_NST) & 1, p.err, abort_flag)) { ok = false; break; }
-          if (r >= end) {
-            const uint32_t va = sb + RA_OFF_V + vs * RA_TILE + (r >> 3) * 2048 + (r & 7) * 128;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              st_shared_v4(va + c * 16, 0u, 0u, 0u, 0u);
-              st_shared_v4(va + 1024 + c * 16, 0u, 0u, 0u, 0u);
-            }
-          }
-          fence_async_shared();
-        }
-        if (!mbar_wait_warp(s_full(s), (n >> 1) & 1, p.err, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        // P's columns are free once the product of step n - 2 is done. A warp
-        // without rows waits for that too: it must not count for step n's phase while
-        // another still works on step n - 2.
-        const uint32_t done_ph = ((n >> 1) & 1) ^ 1u;
-        if (!busy) {                               // no real row: P stays whatever it is, its O rows are never read
-          if (n >= 2 && !mbar_wait_warp(p_done(s), done_ph, p.err, abort_flag)) { ok = false; break; }
+      m = -INFINITY;
+      l = 0.f;
+      if (busy) {
+        bool first = true;
+        for (int i = 0; ok && i < whole; ++i, first = false) ok = step(std::false_type(), first);
+        for (int i = max(whole, 0); ok && i < left; ++i, first = false) ok = step(std::true_type(), first);
+      } else {
+        // no real row: P stays whatever it is, its O rows are never read. The product
+        // of step n - 2 is waited for all the same: this warp must not count for
+        // step n's phase while another still works on step n - 2.
+        for (int i = 0; ok && i < left; ++i, ++n, end -= RA_BKV) {
+          const int s = n & 1;
+          ok = (!TMA || clear_tail(end, n)) && mbar_wait_warp(s_full(s), (n >> 1) & 1, p.err, abort_flag) &&
+               (n < 2 || mbar_wait_warp(p_done(s), ((n >> 1) & 1) ^ 1u, p.err, abort_flag));
           __syncwarp();
-          if (lane == 0) {
+          if (ok && lane == 0) {
             mbar_arrive(s_free(s));
             mbar_arrive(p_full(s));
           }
-        } else {
-          const uint32_t sadr = tmem + lane_off + s * 128;
-          uint32_t sv[RA_BKV];
-          tmem_ld_32x32b_x32(sadr, *reinterpret_cast<uint32_t(*)[32]>(sv));
-          tmem_ld_32x32b_x32(sadr + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
-          tmem_ld_32x32b_x32(sadr + 64, *reinterpret_cast<uint32_t(*)[32]>(sv + 64));
-          tmem_ld_32x32b_x32(sadr + 96, *reinterpret_cast<uint32_t(*)[32]>(sv + 96));
-          tmem_ld_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(s_free(s));   // S[s] may be overwritten from here on
-          if (over < RA_BKV - 1) {                 // some row of the tile ends inside these keys: 0 .. lim are kept
-#pragma unroll
-            for (int e = 0; e < RA_BKV; ++e)
-              if (e > lim) sv[e] = __float_as_uint(-INFINITY);
-          }
-          float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
-#pragma unroll
-          for (int e = 0; e < RA_BKV; e += 8) {
-            m0 = ra_max3(m0, sv[e], sv[e + 1]);
-            m1 = ra_max3(m1, sv[e + 2], sv[e + 3]);
-            m2 = ra_max3(m2, sv[e + 4], sv[e + 5]);
-            m3 = ra_max3(m3, sv[e + 6], sv[e + 7]);
-          }
-          const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * scale;
-          // The max is only raised when it grows by more than 2^8 (the final O / l
-          // cancels a stale one). A row of a later piece's tile can be fully masked
-          // (its token ends before these keys): mx = -inf, and m stays -inf.
-          const bool raise = mx > m + 8.0f;
-          const float m_new = raise ? mx : m;
-          const float alpha = raise ? ra_ex2(m - m_new) : 1.0f;
-          if (!first && __any_sync(0xffffffffu, raise)) {
-            if (!mbar_wait_warp(p_done(s ^ 1), ((n - 1) >> 1) & 1, p.err, abort_flag)) { ok = false; break; }
-            tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              uint32_t v[16];
-              tmem_ld_32x32b_x16(oadr + c * 16, v);
-              tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-              tmem_st_32x32b_x16(oadr + c * 16, v);
-            }
-          }
-          const uint32_t neg = __float_as_uint(m_new > -INFINITY ? -m_new : 0.f), sc = __float_as_uint(scale);
-          const uint64_t neg2 = ra_pair(neg, neg), sc2 = ra_pair(sc, sc);
-          uint64_t r0 = 0, r1 = 0;
-          uint32_t pk[64];
-#pragma unroll
-          for (int e = 0; e < RA_BKV; e += 4) {
-            float p0, p1, p2, p3;
-            ra_unpair(ra_fma2(ra_pair(sv[e], sv[e + 1]), sc2, neg2), p0, p1);
-            ra_unpair(ra_fma2(ra_pair(sv[e + 2], sv[e + 3]), sc2, neg2), p2, p3);
-            p0 = ra_ex2(p0);
-            p1 = ra_ex2(p1);
-            p2 = ra_ex2(p2);
-            p3 = ra_ex2(p3);
-            r0 = ra_add2(r0, ra_pair(__float_as_uint(p0), __float_as_uint(p1)));
-            r1 = ra_add2(r1, ra_pair(__float_as_uint(p2), __float_as_uint(p3)));
-            pk[e >> 1] = pack_bf16x2(p0, p1);      // P enters its product as bf16: half a step (2^-8 at most) per weight
-            pk[(e >> 1) + 1] = pack_bf16x2(p2, p3);
-          }
-          float a0, a1, a2, a3;
-          ra_unpair(r0, a0, a1);
-          ra_unpair(r1, a2, a3);
-          l = l * alpha + ((a0 + a1) + (a2 + a3));
-          m = m_new;
-          if (n >= 2 && !mbar_wait_warp(p_done(s), done_ph, p.err, abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          tmem_st_32x32b_x32(padr + s * 64, *reinterpret_cast<uint32_t(*)[32]>(pk));
-          tmem_st_32x32b_x32(padr + s * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(p_full(s));
         }
-        lim -= RA_BKV;
-        over -= RA_BKV;
-        end -= RA_BKV;
       }
       if (!ok) break;
       // the piece's last P V product, step n - 1's
