@@ -2,13 +2,13 @@
 // block tables, positions and slots from the requests' lengths, and the new
 // tokens' rotation with the cache write.
 //
-//   ragged_plan_kernel  one cluster. Every CTA scans the requests itself (rows
-//                       and blocks wanted, 1024 requests at a time, the prefix
-//                       sums in its shared memory) and takes its share of the
-//                       rows and of the new table entries; after a cluster
-//                       barrier, when nobody reads the state any more, the
-//                       first CTA updates the counts and the free list. Bound by
-//                       latency: three dependent reads and two scans.
+//   ragged_plan_kernel  one cluster. Every CTA scans the requests itself (rows,
+//                       blocks wanted and given back, 1024 requests at a time,
+//                       the prefix sums in its shared memory) and takes its share
+//                       of the rows, of the new table entries and, after a cluster
+//                       barrier, when nobody reads the list any more, of the
+//                       blocks given back; the first CTA updates the counts.
+//                       Bound by latency: three dependent reads and a scan.
 //   ragged_qkv_kernel   one CTA per row: all its q, k and v heads, 16 bytes a
 //                       thread and plane half, the row's 64 (cos, sin) pairs
 //                       formed once in shared memory while the heads are on
@@ -30,6 +30,7 @@ constexpr int RP_WARPS = RP_THREADS / 32;
 constexpr int RP_CLUSTER = 8;
 constexpr int RP_ONE_CTA_ROWS = 4096;
 
+constexpr long long RP_PAST = 1LL << 30;     // no table row reaches this position
 struct PlanParams {
   const int32_t* n_new;
   const int32_t* ctx;
@@ -66,10 +67,9 @@ __device__ __forceinline__ PlanReq plan_req(const PlanParams& p, int b) {
 }
 
 struct PlanSmem {
-  long long sums[3][RP_WARPS];
+  long long sums[3][RP_WARPS], most[RP_WARPS];
   // the chunk's requests: exclusive prefix sums within the chunk and their lengths
-  long long row[RP_THREADS + 1], take[RP_THREADS + 1];
-  int back[RP_THREADS + 1];
+  long long row[RP_THREADS + 1], take[RP_THREADS + 1], back[RP_THREADS];
   int ctx[RP_THREADS], held[RP_THREADS], want[RP_THREADS];
 };
 
@@ -125,24 +125,26 @@ __global__ void __launch_bounds__(RP_THREADS) ragged_plan_kernel(const PlanParam
   __shared__ PlanSmem s;
   const int rank = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(gridDim.x);
   const int tid = threadIdx.x, gtid = rank * RP_THREADS + tid, gstride = ctas * RP_THREADS;
+  const bool one_round = p.B <= RP_THREADS;
   const int n_free = min(max(*p.n_free, 0), p.n_blocks);
-  long long row0 = 0, take0 = 0;
+  long long row0 = 0, take0 = 0, mine = 0;
   bool bad_page = false;      // a position past its table row, or a block outside the pool
-  auto slot_of = [&](int blk, long long at, long long lb) {
+  auto slot_of = [&](int blk, int at, int lb) {
     if (blk < 0) return -1;
     if (blk >= p.n_blocks) {
       bad_page = true;
       return -1;
     }
-    return blk * p.bs + static_cast<int>(at - lb * p.bs);
+    return blk * p.bs + (at - lb * p.bs);
   };
-
-  for (int base = 0; base < p.B; base += RP_THREADS) {
+  // the chunk's requests, their prefix sums in shared memory
+  auto load = [&](int base, long long (&t)[3]) -> PlanReq {
     const PlanReq r = plan_req(p, base + tid);
-    long long v[3] = {r.n, r.take, 0}, t[3];
+    long long v[3] = {r.n, r.take, r.back};
     plan_scan(s, v, t);
     s.row[tid] = v[0];
     s.take[tid] = v[1];
+    s.back[tid] = v[2];
     s.ctx[tid] = r.ctx;
     s.held[tid] = r.held;
     s.want[tid] = r.want;
@@ -150,9 +152,18 @@ __global__ void __launch_bounds__(RP_THREADS) ragged_plan_kernel(const PlanParam
       s.row[RP_THREADS] = t[0];
       s.take[RP_THREADS] = t[1];
     }
-    if (rank == 0 && base + tid < p.B) p.cu[base + tid] = static_cast<int32_t>(min(row0 + v[0], static_cast<long long>(p.T)));
     __syncthreads();
+    return r;
+  };
+  PlanReq r = {0, 0, 0, 0, 0, 0};
+  long long t[3] = {0, 0, 0};
+
+  for (int base = 0; base < p.B; base += RP_THREADS) {
+    r = load(base, t);
     const int here = min(p.B - base, RP_THREADS);
+    if (rank == 0 && tid < here) p.cu[base + tid] = static_cast<int32_t>(min(row0 + s.row[tid], static_cast<long long>(p.T)));
+    // blocks granted: the largest prefix of the wishes that the list can give
+    if (r.take > 0 && take0 + s.take[tid + 1] <= n_free) mine = take0 + s.take[tid + 1];
     // the new table entries: the k-th block taken comes from the list's end; a
     // request whose last block is not there has none of them
     for (long long k = gtid; k < t[1]; k += gstride) {
@@ -162,12 +173,12 @@ __global__ void __launch_bounds__(RP_THREADS) ragged_plan_kernel(const PlanParam
       p.table[static_cast<int64_t>(base + i) * p.max_blocks + lb] = granted ? p.free_list[n_free - 1 - static_cast<int>(take0 + k)] : -1;
     }
     // the rows
-    const long long rows = min(t[0], static_cast<long long>(p.T) - row0);
-#pragma unroll 2
-    for (long long k = gtid; k < rows; k += gstride) {
+    const int rows = static_cast<int>(max(0LL, min(t[0], static_cast<long long>(p.T) - row0)));
+#pragma unroll 4
+    for (int k = gtid; k < rows; k += gstride) {
       const int i = plan_find(s.row, here, k);
-      const long long at = s.ctx[i] + (k - s.row[i]);
-      const long long lb = at / p.bs;
+      const long long pos = s.ctx[i] + (k - s.row[i]);
+      const int at = static_cast<int>(min(pos, RP_PAST)), lb = at / p.bs;    // RP_PAST: past any table row
       int slot = -1;
       if (lb < s.held[i]) {
         slot = slot_of(p.table[static_cast<int64_t>(base + i) * p.max_blocks + lb], at, lb);
@@ -178,58 +189,48 @@ __global__ void __launch_bounds__(RP_THREADS) ragged_plan_kernel(const PlanParam
       } else {
         bad_page = true;
       }
-      p.pos[row0 + k] = static_cast<int32_t>(at);
+      p.pos[row0 + k] = static_cast<int32_t>(pos);
       p.slots[row0 + k] = slot;
     }
     row0 += t[0];
     take0 += t[1];
   }
   if (bad_page) record_error(p.err, KL_DEVERR_PAGE);
-  if (ctas > 1) cluster_sync_all();                 // nobody reads the state any more
+  // the blocks granted in all, found by every CTA for itself
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine = max(mine, static_cast<long long>(__shfl_xor_sync(0xffffffffu, mine, o)));
+  if ((tid & 31) == 0) s.most[tid >> 5] = mine;
+  if (ctas > 1) cluster_sync_all();                 // nobody reads the list any more
   else __syncthreads();
+  long long granted = 0;
+  for (int w = 0; w < RP_WARPS; ++w) granted = max(granted, s.most[w]);
+
+  // ended requests' blocks go behind what is left of the list
+  long long back = n_free - granted;
+  for (int base = 0; base < p.B; base += RP_THREADS) {
+    if (!one_round) r = load(base, t);
+    const int here = min(p.B - base, RP_THREADS);
+    for (long long k = gtid; k < t[2]; k += gstride) {
+      const int i = plan_find(s.back, here, k);
+      if (back + k < p.n_blocks)                    // a list that was consistent never grows past the pool
+        p.free_list[back + k] = p.table[static_cast<int64_t>(base + i) * p.max_blocks + (k - s.back[i])];
+    }
+    back += t[2];
+  }
+  if (!one_round && ctas > 1) cluster_sync_all();   // nobody reads the counts any more
   if (rank != 0) return;
+  // the counts: with one round of requests they are at hand still
+  long long upto = 0;
+  for (int base = 0; base < p.B; base += RP_THREADS) {
+    if (!one_round) r = load(base, t);
+    if (base + tid < p.B) p.held[base + tid] = r.back ? 0 : upto + s.take[tid + 1] <= granted ? max(r.held, r.want) : r.held;
+    upto += t[1];
+  }
   if (tid == 0) {
     p.cu[p.B] = static_cast<int32_t>(min(row0, static_cast<long long>(p.T)));
+    *p.n_free = static_cast<int32_t>(min(back, static_cast<long long>(p.n_blocks)));
+    *p.missing = static_cast<int32_t>(min(take0 - granted, 2147483647LL));
     if (row0 > p.T) record_error(p.err, KL_DEVERR_ROWS);
-  }
-
-  // counts and the free list. A grant depends only on the sums before it, so the
-  // blocks granted are the sum at the first request that got none.
-  long long granted = 0, missing = 0;
-  take0 = 0;
-  for (int base = 0; base < p.B; base += RP_THREADS) {
-    const PlanReq r = plan_req(p, base + tid);
-    long long v[3] = {0, r.take, 0}, t[3];
-    plan_scan(s, v, t);
-    const bool ok = take0 + v[1] + r.take <= n_free;
-    long long g[3] = {ok ? r.take : 0, ok ? 0 : r.take, 0}, gt[3];
-    plan_scan(s, g, gt);
-    if (base + tid < p.B) p.held[base + tid] = r.back ? r.held : ok ? max(r.held, r.want) : r.held;
-    granted += gt[0];
-    missing += gt[1];
-    take0 += t[1];
-  }
-  const long long left = n_free - granted;
-  long long back0 = 0;
-  for (int base = 0; base < p.B; base += RP_THREADS) {
-    const PlanReq r = plan_req(p, base + tid);
-    long long v[3] = {0, 0, r.back}, t[3];
-    plan_scan(s, v, t);
-    s.back[tid] = static_cast<int>(v[2]);
-    __syncthreads();
-    const int here = min(p.B - base, RP_THREADS);
-    for (long long k = tid; k < t[2]; k += RP_THREADS) {
-      const int i = plan_find(s.back, here, k);
-      const long long at = left + back0 + k;
-      if (at < p.n_blocks)                          // a list that was consistent never grows past the pool
-        p.free_list[at] = p.table[static_cast<int64_t>(base + i) * p.max_blocks + (k - s.back[i])];
-    }
-    if (base + tid < p.B && r.back) p.held[base + tid] = 0;
-    back0 += t[2];
-  }
-  if (tid == 0) {
-    *p.n_free = static_cast<int32_t>(min(left + back0, static_cast<long long>(p.n_blocks)));
-    *p.missing = static_cast<int32_t>(min(missing, 2147483647LL));
   }
 }
 

@@ -26,9 +26,11 @@
 namespace kl {
 namespace {
 
-constexpr int DV_THREADS = 512;
-constexpr int DV_WARPS = DV_THREADS / 32;
 constexpr int DV_CL = 8;           // CTAs (one cluster) per request
+// Warps per CTA: 8 where the requests' CTAs fill the GPU (all of 64 requests'
+// are resident then: 23 us for 64 x 151936; with 16 warps they take two rounds, 30), 16 where
+// every CTA has an SM to itself (one request: 12.0 us; with 32 warps 13.4).
+constexpr int DV_WARPS_MANY = 8, DV_WARPS_FEW = 16;
 
 struct VerifyParams {
   const void* p;
@@ -49,27 +51,31 @@ __device__ __forceinline__ float dv_ld(const void* base, int64_t i) {
   return Elem<T>::to_f(static_cast<const T*>(base)[i]);
 }
 
-// E elements of a row starting at column i (E = 1, or a 16-byte vector): columns
-// outside [0, V) give zero.
+// E elements (one, or a 16-byte vector), all of them in the row.
+template <typename T, int E>
+__device__ __forceinline__ void dv_load_whole(const T* x, float (&f)[E]) {
+  if constexpr (E == 1) {
+    f[0] = Elem<T>::to_f(*x);
+  } else {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(x));
+    if constexpr (sizeof(T) == 4) {
+      f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y);
+      f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
+    } else {
+      const float2 x0 = unpack_bf16x2(a.x), x1 = unpack_bf16x2(a.y), x2 = unpack_bf16x2(a.z), x3 = unpack_bf16x2(a.w);
+      f[0] = x0.x; f[1] = x0.y; f[2] = x1.x; f[3] = x1.y;
+      f[4] = x2.x; f[5] = x2.y; f[6] = x3.x; f[7] = x3.y;
+    }
+  }
+}
+// E elements of a row starting at column i: columns outside [0, V) give zero.
 template <typename T, int E>
 __device__ __forceinline__ void dv_load(const T* row, int64_t i, int V, float (&f)[E]) {
-  if constexpr (E == 1) {
-    f[0] = i < V ? Elem<T>::to_f(row[i]) : 0.f;
+  if (i >= 0 && i + E <= V) {
+    dv_load_whole<T, E>(row + i, f);
   } else {
-    if (i >= 0 && i + E <= V) {
-      const uint4 a = __ldg(reinterpret_cast<const uint4*>(row + i));
-      if constexpr (sizeof(T) == 4) {
-        f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y);
-        f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
-      } else {
-        const float2 x0 = unpack_bf16x2(a.x), x1 = unpack_bf16x2(a.y), x2 = unpack_bf16x2(a.z), x3 = unpack_bf16x2(a.w);
-        f[0] = x0.x; f[1] = x0.y; f[2] = x1.x; f[3] = x1.y;
-        f[4] = x2.x; f[5] = x2.y; f[6] = x3.x; f[7] = x3.y;
-      }
-    } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) f[e] = i + e >= 0 && i + e < V ? Elem<T>::to_f(row[i + e]) : 0.f;
-    }
+    for (int e = 0; e < E; ++e) f[e] = i + e >= 0 && i + e < V ? Elem<T>::to_f(row[i + e]) : 0.f;
   }
 }
 
@@ -146,52 +152,90 @@ __device__ __forceinline__ int dv_cross(double s, int lane, double x, double& be
 // the sum in front of it and the value to cross.
 struct VerifySmem {
   double slots[2][DV_CL];        // the CTAs' sums, written by each of them (one array per attempt)
-  double parts[DV_WARPS];        // the warps' sums
+  double parts[32];              // the warps' sums
   double before, x;
   int part, accepted, kind;
 };
 
-// Sum of this lane's vectors j0 + lane, + 32, ... of [j0, j1).
-template <typename T, int E>
-__device__ __forceinline__ Pair dv_sum(const T* prow, const T* qrow, int mis, int V, int kind, int draft, int j0, int j1) {
-  Pair sum = {0.f, 0.f};
-#pragma unroll 4
-  for (int j = j0 + static_cast<int>(threadIdx.x & 31); j < j1; j += 32) {
-    const int64_t col = static_cast<int64_t>(j) * E - mis;
-    float fp[E], fq[E] = {};
-    dv_load<T, E>(prow, col, V, fp);
-    if (kind == DV_REST) dv_load<T, E>(qrow, col, V, fq);
+// A row (and the draft's): where it starts, its first column's place in a vector.
+template <typename T>
+struct DvRow {
+  const T* p;
+  const T* q;
+  int mis, V, draft;
+};
+
+template <typename T, int E, int KIND>
+__device__ __forceinline__ void dv_add(const DvRow<T>& r, int64_t col, const float (&fp)[E], const float (&fq)[E], Pair& sum) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      float w, we;
-      dv_weight(kind, fp[e], fq[e], col + e, draft, w, we);
-      sum.add(w);
-      sum.lo += we;
-    }
+  for (int e = 0; e < E; ++e) {
+    float w, we;
+    dv_weight(KIND, fp[e], fq[e], col + e, r.draft, w, we);
+    sum.add(w);
+    if (KIND == DV_REST) sum.lo += we;
   }
-  return dv_warp_sum(sum);
 }
 
+// Sum of the warp's vectors j0 .. j1 - 1, lane by lane: the whole ones four at a
+// time, the row's first and last one, which columns outside it may share, apart.
+template <typename T, int E, int KIND>
+__device__ __forceinline__ Pair dv_sum_kind(const DvRow<T>& r, int j0, int j1) {
+  constexpr int U = 4;
+  const int lane = threadIdx.x & 31;
+  const int lo = max(j0, r.mis ? 1 : 0);
+  const int hi = min(j1, static_cast<int>((static_cast<int64_t>(r.V) + r.mis) / E));
+  Pair sum = {0.f, 0.f};
+  auto one = [&](int j) {
+    const int64_t col = static_cast<int64_t>(j) * E - r.mis;
+    float fp[E], fq[E] = {};
+    dv_load<T, E>(r.p, col, r.V, fp);
+    if (KIND == DV_REST) dv_load<T, E>(r.q, col, r.V, fq);
+    dv_add<T, E, KIND>(r, col, fp, fq, sum);
+  };
+  int j = lo + lane;
+  for (; j + 32 * (U - 1) < hi; j += 32 * U) {
+    float fp[U][E], fq[U][E] = {};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t col = static_cast<int64_t>(j + 32 * u) * E - r.mis;
+      dv_load_whole<T, E>(r.p + col, fp[u]);
+      if (KIND == DV_REST) dv_load_whole<T, E>(r.q + col, fq[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) dv_add<T, E, KIND>(r, static_cast<int64_t>(j + 32 * u) * E - r.mis, fp[u], fq[u], sum);
+  }
+  for (; j < hi; j += 32) one(j);
+  if (lane == 0 && j0 < lo && j0 < j1) one(j0);
+  if (lane == 31 && j1 > hi && j1 - 1 >= lo) one(j1 - 1);
+  return dv_warp_sum(sum);
+}
 template <typename T, int E>
-__device__ __forceinline__ void dv_request(const VerifyParams& p, VerifySmem& s, int b, int rank, const T* prow, const T* qrow, int mis,
-                           int kind, int draft, int accepted) {
+__device__ __forceinline__ Pair dv_sum(const DvRow<T>& r, int kind, int j0, int j1) {
+  if (kind == DV_REST) return dv_sum_kind<T, E, DV_REST>(r, j0, j1);
+  if (kind == DV_REST_LOOKUP) return dv_sum_kind<T, E, DV_REST_LOOKUP>(r, j0, j1);
+  return dv_sum_kind<T, E, DV_P>(r, j0, j1);
+}
+
+template <typename T, int E, int WARPS>
+__device__ __forceinline__ void dv_request(const VerifyParams& p, VerifySmem& s, int b, int rank, const DvRow<T>& row, int kind,
+                                           int accepted) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // columns in vectors of E: vector j holds columns E j - mis ..
-  const int nv = static_cast<int>((static_cast<int64_t>(p.V) + mis + E - 1) / E);
+  const int nv = static_cast<int>((static_cast<int64_t>(p.V) + row.mis + E - 1) / E);
   const int per_cta = (nv + DV_CL - 1) / DV_CL;
-  const int per_warp = (per_cta + DV_WARPS - 1) / DV_WARPS;
+  const int per_warp = (per_cta + WARPS - 1) / WARPS;
   const int c0 = min(nv, rank * per_cta), c1 = min(nv, c0 + per_cta);
   const int w0 = min(c1, c0 + warp * per_warp), w1 = min(c1, w0 + per_warp);
   const float u = p.us[b];
 
   for (int attempt = 0; attempt < 2; ++attempt) {
-    const Pair sum = dv_sum<T, E>(prow, qrow, mis, p.V, kind, draft, w0, w1);
+    const Pair sum = dv_sum<T, E>(row, kind, w0, w1);
     if (lane == 0) s.parts[warp] = sum.value();
     if (attempt == 0) dv_cluster_wait();
     __syncthreads();
     double mine = 0.0;
     if (warp == 0) {
-      mine = lane < DV_WARPS ? s.parts[lane] : 0.0;
+      mine = lane < WARPS ? s.parts[lane] : 0.0;
       const double cta = __shfl_sync(0xffffffffu, dv_warp_scan(mine, lane), 31);
       if (lane < DV_CL) st_cluster_f64(mapa_shared(smem_u32(&s.slots[attempt][rank]), lane), cta);
     }
@@ -231,33 +275,33 @@ __device__ __forceinline__ void dv_request(const VerifyParams& p, VerifySmem& s,
     }
     const int ow = s.part;
     if (ow < 0) return;
-    // that warp's stretch once more, spread over the CTA: warp w takes its w-th sixteenth
+    // that warp's stretch once more, spread over the CTA: warp w takes its w-th part
     const int s0 = min(c1, c0 + ow * per_warp), s1 = min(c1, s0 + per_warp);
-    const int piece = (s1 - s0 + DV_WARPS - 1) / DV_WARPS;
+    const int piece = (s1 - s0 + WARPS - 1) / WARPS;
     const int p0 = min(s1, s0 + warp * piece), p1 = min(s1, p0 + piece);
-    const Pair part = dv_sum<T, E>(prow, qrow, mis, p.V, kind, draft, p0, p1);
+    const Pair part = dv_sum<T, E>(row, kind, p0, p1);
     if (lane == 0) s.parts[warp] = part.value();
     __syncthreads();
     const double x = s.x;
     double before = s.before;
-    const int pw = max(0, dv_cross(lane < DV_WARPS ? s.parts[lane] : 0.0, lane, x, before));
+    const int pw = max(0, dv_cross(lane < WARPS ? s.parts[lane] : 0.0, lane, x, before));
     if (warp != pw) return;
     // this warp's piece in order, 32 vectors at a time
     int64_t found = -1, last = -1;
     for (int j0 = p0; j0 < p1 && found < 0; j0 += 32) {
       const int j = j0 + lane;
-      const int64_t col = static_cast<int64_t>(j) * E - mis;
+      const int64_t col = static_cast<int64_t>(j) * E - row.mis;
       float w[E], we[E];
       Pair sum = {0.f, 0.f};
 #pragma unroll
       for (int e = 0; e < E; ++e) w[e] = we[e] = 0.f;
       if (j < p1) {
         float fp[E], fq[E] = {};
-        dv_load<T, E>(prow, col, p.V, fp);
-        if (kind == DV_REST) dv_load<T, E>(qrow, col, p.V, fq);
+        dv_load<T, E>(row.p, col, p.V, fp);
+        if (kind == DV_REST) dv_load<T, E>(row.q, col, p.V, fq);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          dv_weight(kind, fp[e], fq[e], col + e, draft, w[e], we[e]);
+          dv_weight(kind, fp[e], fq[e], col + e, row.draft, w[e], we[e]);
           sum.add(w[e]);
           sum.lo += we[e];
         }
@@ -287,8 +331,8 @@ __device__ __forceinline__ void dv_request(const VerifyParams& p, VerifySmem& s,
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(DV_THREADS) draft_verify_kernel(const VerifyParams p) {
+template <typename T, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) draft_verify_kernel(const VerifyParams p) {
   pdl_enter();
   __shared__ VerifySmem s;
   const int b = blockIdx.x / DV_CL, rank = static_cast<int>(cluster_ctarank());
@@ -333,16 +377,21 @@ __global__ void __launch_bounds__(DV_THREADS) draft_verify_kernel(const VerifyPa
   const bool rejected = row < r1 - 1;
   const int kind = !rejected ? DV_P : p.q ? DV_REST : DV_REST_LOOKUP;
   const int draft = rejected ? p.tokens[row + 1] : -1;
-  const T* prow = static_cast<const T*>(p.p) + row * p.ldp;
-  const T* qrow = kind == DV_REST ? static_cast<const T*>(p.q) + row * p.ldq : nullptr;
+  DvRow<T> w;
+  w.p = static_cast<const T*>(p.p) + row * p.ldp;
+  w.q = kind == DV_REST ? static_cast<const T*>(p.q) + row * p.ldq : nullptr;
+  w.V = p.V;
+  w.draft = draft;
   constexpr int E = 16 / sizeof(T);
-  // 16-byte vectors where both rows start at the same place of one (a whole row
-  // of an odd vocabulary starts anywhere); element by element where they do not
-  const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(prow) & 15u) / sizeof(T));
-  if (!qrow || mis == static_cast<int>((reinterpret_cast<uintptr_t>(qrow) & 15u) / sizeof(T)))
-    dv_request<T, E>(p, s, b, rank, prow, qrow, mis, kind, draft, accepted);
-  else
-    dv_request<T, 1>(p, s, b, rank, prow, qrow, 0, kind, draft, accepted);
+  // 16-byte vectors where both rows start at the same place of one (a row of an
+  // odd vocabulary starts anywhere); element by element where they do not
+  w.mis = static_cast<int>((reinterpret_cast<uintptr_t>(w.p) & 15u) / sizeof(T));
+  if (!w.q || w.mis == static_cast<int>((reinterpret_cast<uintptr_t>(w.q) & 15u) / sizeof(T))) {
+    dv_request<T, E, WARPS>(p, s, b, rank, w, kind, accepted);
+  } else {
+    w.mis = 0;
+    dv_request<T, 1, WARPS>(p, s, b, rank, w, kind, accepted);
+  }
 }
 
 }  // namespace
@@ -360,16 +409,17 @@ kl_status draft_verify(const kl_verify_cfg& c, const void* p, int64_t ldp, const
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(c.B * DV_CL);
-  cfg.blockDim = dim3(DV_THREADS);
+  const bool few = c.B * DV_CL <= num_sms();
+  cfg.blockDim = dim3(32 * (few ? DV_WARPS_FEW : DV_WARPS_MANY));
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   const double es = static_cast<double>(dtype_size(c.dtype));
   ProfScope ps("draft_verify", st, 0.0, static_cast<double>(c.B) * c.V * es * (q ? 2 : 1));
   if (c.dtype == KL_F32)
-    KL_CUDA(cudaLaunchKernelEx(&cfg, draft_verify_kernel<float>, v));
+    KL_CUDA(cudaLaunchKernelEx(&cfg, few ? draft_verify_kernel<float, DV_WARPS_FEW> : draft_verify_kernel<float, DV_WARPS_MANY>, v));
   else
-    KL_CUDA(cudaLaunchKernelEx(&cfg, draft_verify_kernel<__nv_bfloat16>, v));
+    KL_CUDA(cudaLaunchKernelEx(&cfg, few ? draft_verify_kernel<__nv_bfloat16, DV_WARPS_FEW> : draft_verify_kernel<__nv_bfloat16, DV_WARPS_MANY>, v));
   return KL_OK;
 }
 
