@@ -189,10 +189,18 @@ def version() -> str:
     return load().kl_version().decode()
 
 
+_torch = None
+
+
 def _stream(stream) -> int:
+    global _torch
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _torch is None:
+            import torch
+            torch.cuda.current_stream()      # initialises CUDA, or says why it cannot
+            _torch = torch
+        # the handle alone: building torch's Stream object around it takes ~3 us a call
+        return _torch._C._cuda_getCurrentRawStream(_torch.cuda.current_device())
     return int(getattr(stream, "cuda_stream", stream))
 
 

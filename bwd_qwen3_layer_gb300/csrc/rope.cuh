@@ -23,11 +23,19 @@ struct RopeFreq {
   uint64_t turn[ROPE_MAX_HALF];   // plane i's rate, turns per position, in units of 2^-64 turn
 };
 
-inline RopeFreq rope_freq(int d, float base) {
-  RopeFreq f;
-  for (int i = 0; i < ROPE_MAX_HALF; ++i) {
-    const double rate = i < d / 2 ? pow(static_cast<double>(base), -2.0 * i / d) / 6.283185307179586 : 0.0;
-    f.turn[i] = static_cast<uint64_t>(ldexp(rate, 64));   // rate < 1/(2 pi): fits in 64 bits
+// The rates of a (d, base), formed once per host thread and kept until another
+// pair is asked for: 64 pow() calls took ~3 us of a small launch's host time.
+inline const RopeFreq& rope_freq(int d, float base) {
+  static thread_local RopeFreq f;
+  static thread_local int last_d = 0;
+  static thread_local float last_base = 0.f;
+  if (d != last_d || base != last_base) {
+    for (int i = 0; i < ROPE_MAX_HALF; ++i) {
+      const double rate = i < d / 2 ? pow(static_cast<double>(base), -2.0 * i / d) / 6.283185307179586 : 0.0;
+      f.turn[i] = static_cast<uint64_t>(ldexp(rate, 64));   // rate < 1/(2 pi): fits in 64 bits
+    }
+    last_d = d;
+    last_base = base;
   }
   return f;
 }
