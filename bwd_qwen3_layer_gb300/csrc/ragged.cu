@@ -237,10 +237,13 @@ __global__ void __launch_bounds__(RP_THREADS) ragged_plan_kernel(const PlanParam
 // ---------------------------------------------------------------------------
 // norm, rotation and cache write
 // ---------------------------------------------------------------------------
-constexpr int RQ_THREADS = 256;
+// 128 threads with five heads each in flight, six CTAs per SM: 63 us for 8189 rows
+// of 64 / 8 heads (5.3 TB/s); 256 with three and four 75, 320 with two and three 76.
+// Bulk copies through shared memory by persistent CTAs took 64.5.
+constexpr int RQ_THREADS = 128;
 constexpr int RQ_D = 128;
 constexpr int RQ_LANES = 8;        // threads per head: 8 planes (16 elements) each
-constexpr int RQ_MAX = 3;          // heads a thread has in flight
+constexpr int RQ_MAX = 5;          // heads a thread has in flight
 
 struct QkvParams {
   const __nv_bfloat16* q_pre;
@@ -269,11 +272,62 @@ __device__ __forceinline__ uint4 rq_pack(const float (&f)[8]) {
   return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
-// Thread l of a head's eight holds planes 8 l .. 8 l + 7: elements 8 l .. and
-// 64 + 8 l .. (planes (i, i + 64)), or 16 l .. 16 l + 15 (planes (2i, 2i + 1)).
-// Heads in the order q, k, v; each element is read and written by one thread,
-// so q_out may be q_pre.
-__global__ void __launch_bounds__(RQ_THREADS, 4) ragged_qkv_kernel(const __grid_constant__ QkvParams p) {
+// One head's eighth: thread l of a head's eight holds planes 8 l .. 8 l + 7, that
+// is elements 8 l .. and 64 + 8 l .. (planes (i, i + 64)), or 16 l .. 16 l + 15
+// (planes (2i, 2i + 1)): offsets ia and ib. xa, xb: its elements, normed (gva,
+// gvb: its gains) and turned by the row's (cos, sin). Called by whole
+// warps; `turn` is off for values, which stay as they are.
+__device__ __forceinline__ void rq_turn(uint4& xa, uint4& xb, const uint4& gva, const uint4& gvb, bool norm, bool turn, int inter,
+                                        int ia, float eps, const float2* cs) {
+  float a[8], b[8];
+  rq_unpack(xa, a);
+  rq_unpack(xb, b);
+  if (norm) {                                       // the same for all threads: the shuffles are convergent
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
+#pragma unroll
+    for (int o = RQ_LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (turn) {
+      const float r = rsqrtf(ss / static_cast<float>(RQ_D) + eps);   // two ulp; the result is rounded to bf16
+      float ga[8], gb[8];
+      rq_unpack(gva, ga);
+      rq_unpack(gvb, gb);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        a[e] = a[e] * r * ga[e];
+        b[e] = b[e] * r * gb[e];
+      }
+    }
+  }
+  if (!turn) return;
+  const int l8 = inter ? ia >> 1 : ia;              // 8 l
+  if (inter) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 c0 = cs[l8 + e], c1 = cs[l8 + 4 + e];
+      const float x0 = a[2 * e], y0 = a[2 * e + 1], x1 = b[2 * e], y1 = b[2 * e + 1];
+      a[2 * e] = x0 * c0.x - y0 * c0.y;
+      a[2 * e + 1] = x0 * c0.y + y0 * c0.x;
+      b[2 * e] = x1 * c1.x - y1 * c1.y;
+      b[2 * e + 1] = x1 * c1.y + y1 * c1.x;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float2 c = cs[l8 + e];
+      const float x = a[e], z = b[e];
+      a[e] = x * c.x - z * c.y;
+      b[e] = x * c.y + z * c.x;
+    }
+  }
+  xa = rq_pack(a);
+  xb = rq_pack(b);
+}
+
+// One CTA per row. Heads in the order q, k, v; each element is read and written by
+// one thread, so q_out may be q_pre.
+__global__ void __launch_bounds__(RQ_THREADS, 6) ragged_qkv_kernel(const __grid_constant__ QkvParams p) {
   pdl_enter();
   __shared__ float2 cs[RQ_D / 2];
   const int row = blockIdx.x;
@@ -286,6 +340,10 @@ __global__ void __launch_bounds__(RQ_THREADS, 4) ragged_qkv_kernel(const __grid_
            : h < p.Hq + p.Hkv ? p.k_pre + (static_cast<int64_t>(row) * p.Hkv + (h - p.Hq)) * RQ_D
                               : p.v + (static_cast<int64_t>(row) * p.Hkv + (h - p.Hq - p.Hkv)) * RQ_D;
   };
+  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+  const bool norm = p.gq != nullptr;
+  const uint4 gqa = norm ? *reinterpret_cast<const uint4*>(p.gq + ia) : none, gqb = norm ? *reinterpret_cast<const uint4*>(p.gq + ib) : none;
+  const uint4 gka = norm ? *reinterpret_cast<const uint4*>(p.gk + ia) : none, gkb = norm ? *reinterpret_cast<const uint4*>(p.gk + ib) : none;
   // a row past the last request is read too (the tensors have it), not written
   const int rows = p.cu[p.B], pos = p.pos[row];
   int slot = p.slots[row];
@@ -318,58 +376,13 @@ __global__ void __launch_bounds__(RQ_THREADS, 4) ragged_qkv_kernel(const __grid_
     for (int j = 0; j < RQ_MAX; ++j) {
       const int h = base + j * STEP + h0;
       const bool turn = h < p.Hq + p.Hkv;
-      float a[8], b[8];
-      rq_unpack(xa[j], a);
-      rq_unpack(xb[j], b);
-      if (p.gq) {                                   // the same for all threads: the shuffles are convergent
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
-#pragma unroll
-        for (int o = RQ_LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (turn) {
-          const __nv_bfloat16* g = h < p.Hq ? p.gq : p.gk;
-          const float r = 1.0f / sqrtf(ss / static_cast<float>(RQ_D) + p.eps);
-          float ga[8], gb[8];
-          rq_unpack(*reinterpret_cast<const uint4*>(g + ia), ga);
-          rq_unpack(*reinterpret_cast<const uint4*>(g + ib), gb);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            a[e] = a[e] * r * ga[e];
-            b[e] = b[e] * r * gb[e];
-          }
-        }
-      }
+      rq_turn(xa[j], xb[j], h < p.Hq ? gqa : gka, h < p.Hq ? gqb : gkb, norm, turn, p.inter, ia, p.eps, cs);
       if (h >= heads || (h >= p.Hq && slot < 0)) continue;
       __nv_bfloat16* y = h < p.Hq ? p.q_out + (static_cast<int64_t>(row) * p.Hq + h) * RQ_D
                          : turn ? p.k_pool + (static_cast<int64_t>(slot) * p.Hkv + (h - p.Hq)) * RQ_D
                                 : p.v_pool + (static_cast<int64_t>(slot) * p.Hkv + (h - p.Hq - p.Hkv)) * RQ_D;
-      if (!turn) {
-        *reinterpret_cast<uint4*>(y + ia) = xa[j];
-        *reinterpret_cast<uint4*>(y + ib) = xb[j];
-        continue;
-      }
-      if (p.inter) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 c0 = cs[8 * l + e], c1 = cs[8 * l + 4 + e];
-          const float x0 = a[2 * e], y0 = a[2 * e + 1], x1 = b[2 * e], y1 = b[2 * e + 1];
-          a[2 * e] = x0 * c0.x - y0 * c0.y;
-          a[2 * e + 1] = x0 * c0.y + y0 * c0.x;
-          b[2 * e] = x1 * c1.x - y1 * c1.y;
-          b[2 * e + 1] = x1 * c1.y + y1 * c1.x;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 c = cs[8 * l + e];
-          const float x = a[e], z = b[e];
-          a[e] = x * c.x - z * c.y;
-          b[e] = x * c.y + z * c.x;
-        }
-      }
-      *reinterpret_cast<uint4*>(y + ia) = rq_pack(a);
-      *reinterpret_cast<uint4*>(y + ib) = rq_pack(b);
+      *reinterpret_cast<uint4*>(y + ia) = xa[j];
+      *reinterpret_cast<uint4*>(y + ib) = xb[j];
     }
   }
 }

@@ -246,6 +246,11 @@ def test_attention_without_rows(kl):
     (12, 4, 5, [(3, 7), (2, 190)], True, True, True),
     (7, 7, 24, [(9, 23)], False, True, False),
     (128, 1, 8, [(2, 5)], True, False, True),
+    # more rows than the GPU holds at once, more heads than a CTA holds at once
+    (8, 1, 16, [(700, 3), (0, 1), (33, 64)], False, False, True),
+    (10, 2, 16, [(1, 9), (900, 0), (310, 70000)], True, True, False),
+    (40, 40, 32, [(650, 20)], True, False, False),
+    (100, 100, 64, [(620, 1)], True, False, False),
 ])
 def test_qkv_matches_oracle(kl, Hq, Hkv, bs, reqs, norm, inter, inplace):
     rng = np.random.default_rng(8)
