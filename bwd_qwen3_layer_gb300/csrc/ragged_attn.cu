@@ -66,8 +66,12 @@ constexpr uint32_t RA_OFF_BAR = RA_OFF_V + RA_NST * RA_TILE;
 constexpr size_t RA_SMEM = 1024 + RA_OFF_BAR + 2048;
 // Tensor memory: S of two steps, P of two steps (bf16 pairs), O: all 512 columns.
 constexpr uint32_t RA_TM_P = 256, RA_TM_O = 384;
-constexpr int RA_ITEM_UNITS = 1;              // units an item's start and end count for
-constexpr int RA_MIN_UNITS = 3;               // units per CTA at least
+// Units that an item's start and end count for: its first scores and its epilogue
+// take about as long as two key tiles. At least one such item per CTA: with one
+// unit and three per CTA, short requests shared CTAs while others idled (one of
+// 100 tokens: 12.4 us, now 9.2; the mixed batch of 20 is the same).
+constexpr int RA_ITEM_UNITS = 2;
+constexpr int RA_MIN_UNITS = RA_ITEM_UNITS + 1;
 constexpr float RA_LOG2E = 1.4426950408889634f;
 constexpr float RA_LN2 = 0.6931471805599453f;
 
@@ -163,6 +167,12 @@ __device__ __forceinline__ void ra_tma_4d(uint32_t dst, const void* tmap, int x,
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
+}
+// 32 bytes to a 32-byte aligned address
+__device__ __forceinline__ void ra_st32(void* dst, const uint32_t (&x)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+               "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
 }
 __device__ __forceinline__ void ra_cp16(uint32_t dst, const void* src, bool valid) {
   const int sz = valid ? 16 : 0;   // zero-fill
@@ -322,7 +332,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
 
-  if (threadIdx.x == 0) {
+  if (warp == 3 && lane == 0) {      // not the first warps: they have the first requests to scan
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     for (int s = 0; s < RA_NST; ++s) {
@@ -347,6 +357,9 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     tmem_relinquish();
   }
 
+  if (lane == 0 && warp >= 5 && (TMA || warp == 5))
+    tma_prefetch_desc(warp == 5 ? &p.tmQ : warp == 6 ? &p.tmK : &p.tmV);
+
   // ---- this CTA's run: prefix sums of the requests' units, then the item at unit cta * P ----
   {
     const int per = (p.B + RA_THREADS - 1) / RA_THREADS;
@@ -366,12 +379,12 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     }
     if (lane == 31) wsum[warp] = incl;
     __syncthreads();
-    if (lane == 0 && warp >= 5 && (TMA || warp == 5))
-      tma_prefetch_desc(warp == 5 ? &p.tmQ : warp == 6 ? &p.tmK : &p.tmV);
     long long before = 0, W = 0;
+#pragma unroll
     for (int w = 0; w < RA_WARPS; ++w) {
-      if (w < warp) before += wsum[w];
-      W += wsum[w];
+      const long long v = wsum[w];
+      if (w < warp) before += v;
+      W += v;
     }
     const long long P = max(ra_div(W + ctas - 1, ctas), static_cast<long long>(RA_MIN_UNITS));
     const long long u0 = cta * P;
@@ -492,6 +505,16 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     };
     for (int k = 0; ok && find(k); ++k) {
       const RaPiece w = piece(k);
+      int row[4];
+      auto lookup = [&](int j) {
+        if (TMA) {
+          row[0] = lane < nbox ? pool_row(w.b, j * RA_BKV + lane * p.box, w.L) : no_row;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) row[i] = pool_row(w.b, j * RA_BKV + i * 32 + lane, w.L);
+        }
+      };
+      lookup(w.ta);
       if (is_k) {
         // Q: the buffer is free once the previous piece's last S product is done
         if (!ra_wait_copy(q_empty, (issued_q & 1) ^ 1u, p.err, abort_flag)) { ok = false; break; }
@@ -503,16 +526,6 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
         __syncwarp();
         ++issued_q;
       }
-      int row[4];
-      auto lookup = [&](int j) {
-        if (TMA) {
-          row[0] = lane < nbox ? pool_row(w.b, j * RA_BKV + lane * p.box, w.L) : no_row;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) row[i] = pool_row(w.b, j * RA_BKV + i * 32 + lane, w.L);
-        }
-      };
-      lookup(w.ta);
       for (int j = w.ta; j < w.tb; ++j) {
         if (!ra_wait_copy(empty0 + 8 * s, ph, p.err, abort_flag)) { ok = false; break; }
         const uint32_t dst = ring + s * RA_TILE;
@@ -789,15 +802,16 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
           tmem_ld_wait();
           if (!mine) continue;
           if (whole) {
+            // whole 32-byte sectors: rows lie apart, and an SM writes ~0.7 sectors a
+            // cycle whether they are full or not (16-byte stores took twice as long)
             __nv_bfloat16* orow_p = p.o + orow * RA_D + h * 32;
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint4 x;
-              x.x = pack_bf16x2(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv);
-              x.y = pack_bf16x2(__uint_as_float(v[e + 2]) * inv, __uint_as_float(v[e + 3]) * inv);
-              x.z = pack_bf16x2(__uint_as_float(v[e + 4]) * inv, __uint_as_float(v[e + 5]) * inv);
-              x.w = pack_bf16x2(__uint_as_float(v[e + 6]) * inv, __uint_as_float(v[e + 7]) * inv);
-              *reinterpret_cast<uint4*>(orow_p + e) = x;
+            for (int e = 0; e < 32; e += 16) {
+              uint32_t x[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                x[i] = pack_bf16x2(__uint_as_float(v[e + 2 * i]) * inv, __uint_as_float(v[e + 2 * i + 1]) * inv);
+              ra_st32(orow_p + e, x);
             }
           } else {
             float* po = p.part_o + (pslot * RA_D + h * 32) * RA_BQ + r * 4;      // lanes side by side
