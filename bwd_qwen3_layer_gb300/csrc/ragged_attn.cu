@@ -21,7 +21,7 @@
 // results repeat bit for bit. The workspace holds two pieces per CTA and does
 // not depend on the lengths.
 //
-// Roles (8 warps): warp 0 looks up the pages and copies Q and the keys, warp 1
+// Roles (8 warps): warp 0 looks up the pages and copies the keys, warp 1 Q and
 // the values, warp 2 issues the score products, warp 3 the P V products, warps
 // 4..7 are the softmax (thread = query row = TMEM lane). A step's chain is
 // scores -> softmax -> P V. S and P have two buffers each: S_(n+2) waits only for
@@ -52,7 +52,7 @@ namespace {
 constexpr int RA_D = 128;        // head dim
 constexpr int RA_BQ = 128;       // rows of a query tile
 constexpr int RA_BKV = 128;      // keys per tile
-constexpr int RA_WARPS = 8;      // K copies, V copies, score products, P V products, four of softmax
+constexpr int RA_WARPS = 8;      // K copies, Q and V copies, score products, P V products, four of softmax
 constexpr int RA_THREADS = 32 * RA_WARPS;
 // A key or value tile (32 KB) is 16 groups of 8 keys, each group two swizzled
 // blocks of 8 rows x 64 columns (1 KB): a page of 8 m tokens is then one TMA box
@@ -196,7 +196,14 @@ __device__ __forceinline__ bool ra_wait_copy(uint32_t bar, uint32_t parity, uint
   return true;
 }
 
-__device__ __forceinline__ RaReq ra_req(const RaParams& p, int b) {
+// What the walk reads of the parameters, handed over by value: a reference to
+// kernel parameters makes every access of a called function a slow generic load.
+struct RaLens {
+  const int32_t* cu;
+  const int32_t* ctx;
+  int B, T, Hkv, TQ;
+};
+__device__ __forceinline__ RaReq ra_req(const RaLens& p, int b) {
   RaReq q;
   q.r0 = min(max(p.cu[b], 0), p.T);
   q.n = min(max(p.cu[b + 1], q.r0), p.T) - q.r0;
@@ -228,6 +235,7 @@ __device__ __noinline__ long long ra_units_before(int ctx, int TQ, long long m) 
 }
 __device__ __forceinline__ long long ra_head_units(const RaReq& q, int TQ) {
   if (q.n <= 0) return 0;
+  if (q.n <= TQ) return (q.ctx + q.n - 1) / RA_BKV + 1 + RA_ITEM_UNITS;
   const int QT = (q.n + TQ - 1) / TQ;
   return ra_units_before(q.ctx, TQ, QT - 1) + ra_tiles(q, TQ, QT - 1) + RA_ITEM_UNITS;
 }
@@ -258,7 +266,7 @@ struct RaWalk {
 };
 // The next piece with at least one key tile into c. Called by one lane; one copy
 // of the code for all roles (a CTA's start is bound by instruction fetches).
-__device__ __noinline__ void ra_next(const RaParams& p, RaWalk& w, RaPiece& c) {
+__device__ __noinline__ void ra_next(const RaLens p, RaWalk& w, RaPiece& c) {
   c.tb = 0;
   while (w.left > 0) {
     const int tiles = ra_tiles(w.q, p.TQ, w.qt);
@@ -325,12 +333,13 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
   RaStart* start = reinterpret_cast<RaStart*>(smem + RA_OFF_BAR + 208);
   long long* wsum = reinterpret_cast<long long*>(smem + RA_OFF_BAR + 256);   // the warps' unit sums, then this CTA's units
 
-  RaWalk* walks = reinterpret_cast<RaWalk*>(smem + RA_OFF_BAR + 336);        // [8]
-  RaPiece* pieces = reinterpret_cast<RaPiece*>(smem + RA_OFF_BAR + 912);     // [8][2]
-  static_assert(RA_WARPS * sizeof(RaWalk) <= 576 && RA_WARPS * 2 * sizeof(RaPiece) <= 1136, "shared-memory layout");
+  RaWalk* walks = reinterpret_cast<RaWalk*>(smem + RA_OFF_BAR + 336);        // the finder's, then one per warp
+  RaPiece* pieces = reinterpret_cast<RaPiece*>(smem + RA_OFF_BAR + 848);     // the first one, then two per warp
+  static_assert((RA_WARPS + 1) * sizeof(RaWalk) <= 512 && (RA_WARPS * 2 + 1) * sizeof(RaPiece) <= 1200, "shared-memory layout");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
+  const RaLens lens = {p.cu, p.ctx, p.B, p.T, p.Hkv, p.TQ};
 
   if (warp == 3 && lane == 0) {      // not the first warps: they have the first requests to scan
     mbar_init(q_full, 1);
@@ -367,7 +376,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     long long mine = 0, units = 0;
     RaReq q = {0, 0, 0};
     for (int b = b0; b < b1; ++b) {
-      q = ra_req(p, b);
+      q = ra_req(lens, b);
       units = ra_head_units(q, p.TQ);
       mine += units * p.Hkv;
     }
@@ -388,17 +397,16 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     }
     const long long P = max(ra_div(W + ctas - 1, ctas), static_cast<long long>(RA_MIN_UNITS));
     const long long u0 = cta * P;
-    if (threadIdx.x == 0) wsum[RA_WARPS] = max(0LL, min(P, W - u0));     // units of this CTA
     if (threadIdx.x == 0 && u0 >= W) {
-      start->b = -1;
       start->pieces = 0;
+      pieces[0].tb = 0;
     }
     long long lo = before + incl - mine;      // units before this thread's requests
     if (mine > 0 && u0 >= lo && u0 < lo + mine) {
       int b = b0;
       if (per > 1) {                          // with one request a thread q and units are its own still
         for (;; ++b) {
-          q = ra_req(p, b);
+          q = ra_req(lens, b);
           units = ra_head_units(q, p.TQ);
           if (u0 < lo + units * p.Hkv) break;
           lo += units * p.Hkv;
@@ -406,7 +414,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
       }
       const int g = static_cast<int>(ra_div(u0 - lo, units));
       const long long y = u0 - lo - g * units;
-      int m0 = 0, m1 = (q.n + p.TQ - 1) / p.TQ;      // the query tile: units_before(m0) <= y < units_before(m1)
+      int m0 = 0, m1 = q.n <= p.TQ ? 1 : (q.n + p.TQ - 1) / p.TQ;   // the query tile: units_before(m0) <= y < units_before(m1)
       while (m1 - m0 > 1) {
         const int m = (m0 + m1) >> 1;
         if (ra_units_before(q.ctx, p.TQ, m) <= y) m0 = m; else m1 = m;
@@ -424,6 +432,16 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
       start->rows = min(p.TQ, q.n - m0 * p.TQ) * p.G;
       start->row0 = q.r0 + m0 * p.TQ;
       start->first_slot = off - P >= 0 ? 0 : 1;
+      // the walk to the first piece, for every role at once
+      RaWalk& w = walks[0];
+      w.b = b;
+      w.g = g;
+      w.qt = m0;
+      w.idx = 0;
+      w.q = q;
+      w.off = off;
+      w.left = min(P, W - u0);
+      ra_next(lens, w, pieces[0]);
     }
   }
   tc_fence_before();
@@ -431,32 +449,26 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const uint32_t tmP = tmem + RA_TM_P, tmO = tmem + RA_TM_O;
-  const RaStart st = *start;
-  const long long units = wsum[RA_WARPS];
-  if (threadIdx.x == 0) p.starts[cta] = st;
+  if (threadIdx.x < sizeof(RaStart) / 4)
+    reinterpret_cast<int*>(p.starts + cta)[threadIdx.x] = reinterpret_cast<const int*>(start)[threadIdx.x];
   const int GT = p.G * p.TQ;            // rows of a full query tile
 
-  RaWalk& walk = walks[warp];
-  if (lane == 0) {
-    walk.b = st.b;
-    walk.g = st.g;
-    walk.qt = st.qt;
-    walk.idx = 0;
-    walk.q = st.q;
-    walk.off = st.off;
-    walk.left = units;
-  }
-  auto piece = [&](int k) -> RaPiece& { return pieces[warp * 2 + (k & 1)]; };
+  // Piece 0 is shared (pieces[0]); from there each warp walks for itself.
+  RaWalk& walk = walks[warp + 1];
+  if (lane < sizeof(RaWalk) / 4) reinterpret_cast<int*>(&walk)[lane] = reinterpret_cast<const int*>(&walks[0])[lane];
+  auto piece = [&](int k) -> RaPiece& { return pieces[k ? 1 + warp * 2 + (k & 1) : 0]; };
   // piece k of this CTA into its place; false if there is none
   auto find = [&](int k) -> bool {
-    __syncwarp();                       // every lane is done with piece k - 2
-    if (lane == 0) ra_next(p, walk, piece(k));
-    __syncwarp();
+    if (k > 0) {
+      __syncwarp();                     // every lane is done with piece k - 2
+      if (lane == 0) ra_next(lens, walk, piece(k));
+      __syncwarp();
+    }
     return piece(k).tb > 0;
   };
 
   if (warp < 2) {
-    // ------- copies (warp 0: Q and K, warp 1: V; lane = page box of a tile) -------
+    // ------- copies (warp 0: K, warp 1: Q and V; lane = page box of a tile) -------
     const bool is_k = warp == 0;
     const bool el = elect_one();
     const CUtensorMap* tm = is_k ? &p.tmK : &p.tmV;
@@ -515,7 +527,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
         }
       };
       lookup(w.ta);
-      if (is_k) {
+      if (!is_k) {
         // Q: the buffer is free once the previous piece's last S product is done
         if (!ra_wait_copy(q_empty, (issued_q & 1) ^ 1u, p.err, abort_flag)) { ok = false; break; }
         if (el) {

@@ -495,3 +495,112 @@ def test_a_captured_serving_loop(kl):
                 want, _, _ = O.ragged_attention(got_q[x], K[b][:, None], VV[b][:, None], pages.T, [0, n[b]], [ctx[b]])
                 assert_rel(_host(o)[x], want, TOL_BF16, f"step {step} request {b}")
                 ctx[b] += int(want_acc[b]) + 1    # the rejected drafts' rows are fed again
+
+
+def test_attention_of_many_requests(kl):
+    """More requests than a CTA has threads, most of them idle."""
+    Hq, Hkv, bs = 8, 2, 8
+    rng = np.random.default_rng(41)
+    reqs = [(int(a), int(c)) for a, c in zip(rng.choice([0, 0, 0, 1, 3], 1500), rng.integers(0, 200, 1500))]
+    rng, n, ctx, table, maxb, nb, kp, vp, cu, T = _step(42, reqs, Hkv, bs)
+    q = _bf(rng, T, Hq, D)
+    rc = kl.RaggedCfg(len(reqs), T, bs, maxb, nb)
+    qd, kd, vd, td, cd, xd = _dev(q), _dev(kp), _dev(vp), _i(table), _i(cu), _i(ctx)
+    ws = torch.empty(kl.kl_ragged_attention_ws_bytes(rc, Hq, Hkv, D), dtype=torch.uint8, device="cuda")
+    o = torch.empty_like(qd)
+    kl.kl_ragged_attention(rc, Hq, Hkv, D, kl.KL_BF16, qd.data_ptr(), kd.data_ptr(), vd.data_ptr(), td.data_ptr(), cd.data_ptr(), xd.data_ptr(), o.data_ptr(), 0,
+                           ws.data_ptr(), ws.numel())
+    assert kl.kl_device_status() == 0
+    want, _, A = O.ragged_attention(q, kp, vp, table, cu, ctx)
+    assert (np.abs(_host(o) - want) <= (2.0 ** -8 + 2.0 ** -9 + 2e-4) * A + 2.0 ** -8 * np.abs(want)).all()
+
+
+def test_two_streams_at_once(kl):
+    """The same operators on two streams at the same time, a workspace each: the bits of one after the other."""
+    Hq, Hkv, bs = 64, 8, 16
+    sets = []
+    for seed, reqs in ((51, [(1, 3000), (40, 100), (7, 0)]), (52, [(300, 700), (1, 5)])):
+        rng, n, ctx, table, maxb, nb, kp, vp, cu, T = _step(seed, reqs, Hkv, bs)
+        rc = kl.RaggedCfg(len(reqs), T, bs, maxb, nb)
+        t = dict(q=_dev(_bf(rng, T, Hq, D)), k=_dev(kp), v=_dev(vp), t=_i(table), c=_i(cu), x=_i(ctx),
+                 ws=torch.empty(kl.kl_ragged_attention_ws_bytes(rc, Hq, Hkv, D), dtype=torch.uint8, device="cuda"))
+        t["outs"] = [torch.empty_like(t["q"]) for _ in range(21)]
+        sets.append((rc, t, torch.cuda.Stream()))
+
+    def call(rc, t, o, st):
+        kl.kl_ragged_attention(rc, Hq, Hkv, D, kl.KL_BF16, t["q"].data_ptr(), t["k"].data_ptr(), t["v"].data_ptr(), t["t"].data_ptr(), t["c"].data_ptr(), t["x"].data_ptr(),
+                               o.data_ptr(), 0, t["ws"].data_ptr(), t["ws"].numel(), st)
+
+    for rc, t, st in sets:
+        call(rc, t, t["outs"][0], None)
+    torch.cuda.synchronize()
+    for i in range(1, 21):
+        for rc, t, st in sets:
+            call(rc, t, t["outs"][i], st)
+    assert kl.kl_device_status(sets[0][2]) == 0 and kl.kl_device_status(sets[1][2]) == 0
+    for rc, t, st in sets:
+        assert all(torch.equal(o, t["outs"][0]) for o in t["outs"][1:])
+
+
+def test_offsets_past_32_bits(kl):
+    """Pools of more than 2^31 elements and probability rows past 2^31: what lies at their ends is found."""
+    Hq, Hkv, bs, nb = 64, 8, 16, 140000                       # 2.3e9 elements a pool
+    kp, vp = (torch.empty(nb, bs, Hkv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    rng = np.random.default_rng(61)
+    n, ctx = 3, 90
+    table = np.array([[nb - 1, nb - 7, 5, nb - 3, 0, nb - 2]])
+    pos = np.arange(ctx + n)
+    slots = table[0][pos // bs] * bs + pos % bs
+    T = n + ctx
+    q, k, v = _bf(rng, T, Hq, D), _bf(rng, T, Hkv, D), _bf(rng, T, Hkv, D)
+    rc = kl.RaggedCfg(1, T, bs, table.shape[1], nb)
+    qd, kd, vd, cu, pd, sd = _dev(q), _dev(k), _dev(v), _i([0, T]), _i(np.zeros(T)), _i(slots)
+    kl.kl_ragged_qkv_rope(rc, Hq, Hkv, D, kl.KL_BF16, qd.data_ptr(), kd.data_ptr(), vd.data_ptr(), 0, 0, 1e-6, 1e6, 0, cu.data_ptr(), pd.data_ptr(), sd.data_ptr(),
+                          qd.data_ptr(), kp.data_ptr(), vp.data_ptr())      # position zero: no rotation
+    sl = torch.as_tensor(slots, device="cuda")
+    assert torch.equal(kp.view(-1, Hkv, D)[sl], kd) and torch.equal(vp.view(-1, Hkv, D)[sl], vd)
+    o = torch.empty(n, Hq, D, dtype=torch.bfloat16, device="cuda")
+    rc2 = kl.RaggedCfg(1, n, bs, table.shape[1], nb)
+    ws = torch.empty(kl.kl_ragged_attention_ws_bytes(rc2, Hq, Hkv, D), dtype=torch.uint8, device="cuda")
+    qn, td, c2, xd = qd[ctx:].contiguous(), _i(table), _i([0, n]), _i([ctx])
+    kl.kl_ragged_attention(rc2, Hq, Hkv, D, kl.KL_BF16, qn.data_ptr(), kp.data_ptr(), vp.data_ptr(), td.data_ptr(), c2.data_ptr(), xd.data_ptr(), o.data_ptr(), 0, ws.data_ptr(),
+                           ws.numel())
+    assert kl.kl_device_status() == 0
+    want, _, A = O.ragged_attention(q[ctx:], k[:, None], v[:, None], np.arange(T)[None], [0, n], [ctx])
+    assert (np.abs(_host(o) - want) <= (2.0 ** -8 + 2.0 ** -9 + 2e-4) * A + 2.0 ** -8 * np.abs(want)).all()
+    del kp, vp
+    T, V = 15000, 151936                                      # 2.3e9 probabilities
+    p = torch.empty(T, V, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(62)
+    p[T - 2:] = torch.softmax(torch.randn(2, V, generator=g, device="cuda"), 1)
+    p[0] = torch.softmax(torch.randn(V, generator=g, device="cuda"), 0)
+    p[0, 7] = 0.0
+    tokens = np.full(T, 7)
+    tokens[T - 1] = 11
+    ua, us = np.zeros(T, np.float32), np.array([0.37, 0.61], np.float32)
+    acc, nxt = _verify(kl, p, None, tokens, [0, T - 2, T], ua, us)   # request 0's first draft has probability zero
+    rows = _host(p[[0, T - 2, T - 1]])
+    want = O.draft_verify(rows, None, [7, 7, 11], [0, 1, 3], [0.0, 0.0, 0.0], us)
+    w0 = np.searchsorted(np.cumsum(rows[0]), float(us[0]) * rows[0].sum(), side="right")   # p without the draft, whose weight is zero
+    assert list(acc) == [0, want[0][1]] and list(nxt) == [w0, want[1][1]]
+
+
+def test_a_copy_of_the_rows_in_the_wrong_places_is_left_alone(kl):
+    """cu_rows that run past the tensors or backwards: brought into range, nothing outside is touched."""
+    Hq, Hkv, bs = 8, 1, 16
+    rng, n, ctx, table, maxb, nb, kp, vp, cu, T = _step(71, [(4, 20), (3, 10)], Hkv, bs)
+    q = _dev(_bf(rng, T, Hq, D))
+    rc = kl.RaggedCfg(2, T, bs, maxb, nb)
+    guard = torch.full((T + 8, Hq, D), 5.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(kl.kl_ragged_attention_ws_bytes(rc, Hq, Hkv, D), dtype=torch.uint8, device="cuda")
+    kd, vd, td, xd = _dev(np.nan_to_num(kp)), _dev(np.nan_to_num(vp)), _i(np.clip(table, 0, nb - 1)), _i([20, 10])
+    for bad in ([0, 4, 100], [-3, 4, 7], [4, 2, 7]):
+        cd = _i(bad)
+        kl.kl_ragged_attention(rc, Hq, Hkv, D, kl.KL_BF16, q.data_ptr(), kd.data_ptr(), vd.data_ptr(), td.data_ptr(), cd.data_ptr(), xd.data_ptr(), guard[4:].data_ptr(), 0,
+                               ws.data_ptr(), ws.numel())
+        torch.cuda.synchronize()
+        assert (guard[:4] == 5.0).all() and (guard[4 + T:] == 5.0).all()
+    try:
+        kl.kl_device_status()          # positions past the table may have been reported
+    except kl.KLError as e:
+        assert e.status == kl.KL_ERR_DEVICE
