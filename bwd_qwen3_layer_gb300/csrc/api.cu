@@ -868,6 +868,8 @@ kl_status kl_ragged_attention(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, 
   KL_TRY(check_arrays({table, cu_rows, ctx}, "ragged_attention"));
   if (reinterpret_cast<uintptr_t>(lse) & 3u)
     return set_error(KL_ERR_INVALID_ARG, "ragged_attention: lse not 4-byte aligned");
+  if (reinterpret_cast<uintptr_t>(o) & 31u)
+    return set_error(KL_ERR_INVALID_ARG, "ragged_attention: o not 32-byte aligned (it is written in whole sectors)");
   return ragged_attention(*rc, Hq, Hkv, q, k_pool, v_pool, table, cu_rows, ctx, o, lse, ws, ws_bytes,
                           static_cast<cudaStream_t>(stream));
 }

@@ -253,7 +253,6 @@ struct RaPiece {
   int pos0, L;             // position of its first token; keys of the request
   int ta, tb;              // key tiles; tb = 0: there is no such piece
   int flags;               // 1: all of the item's tiles; 2: the piece goes to slot 1
-  int pad;
 };
 // The walk over a CTA's run. Every role's warp walks for itself, in shared
 // memory: the softmax warps' registers are full of scores, and every one more
@@ -266,15 +265,17 @@ struct RaWalk {
 };
 // The next piece with at least one key tile into c. Called by one lane; one copy
 // of the code for all roles (a CTA's start is bound by instruction fetches).
-__device__ __noinline__ void ra_next(const RaLens p, RaWalk& w, RaPiece& c) {
+__device__ __noinline__ void ra_next(const RaLens p, RaWalk& walk, RaPiece& piece) {
+  RaWalk w = walk;         // in registers: one read, one write each
+  RaPiece c;
   c.tb = 0;
   while (w.left > 0) {
     const int tiles = ra_tiles(w.q, p.TQ, w.qt);
-    const long long len = tiles + RA_ITEM_UNITS;
-    const long long take = min(w.left, len - w.off), e = w.off + take;
+    const int len = tiles + RA_ITEM_UNITS, off = static_cast<int>(w.off);
+    const int e = static_cast<int>(min(w.left, static_cast<long long>(len - off))) + off;
     const int first = w.qt * p.TQ;
-    c.ta = static_cast<int>(max(w.off - RA_ITEM_UNITS, 0LL));
-    c.tb = static_cast<int>(max(e - RA_ITEM_UNITS, 0LL));
+    c.ta = max(off - RA_ITEM_UNITS, 0);
+    c.tb = max(e - RA_ITEM_UNITS, 0);
     c.b = w.b;
     c.g = w.g;
     c.row0 = w.q.r0 + first;
@@ -282,7 +283,7 @@ __device__ __noinline__ void ra_next(const RaLens p, RaWalk& w, RaPiece& c) {
     c.pos0 = w.q.ctx + first;
     c.L = w.q.ctx + w.q.n;
     c.flags = (c.ta == 0 && c.tb == tiles ? 1 : 0) | (w.idx > 0 ? 2 : 0);
-    w.left -= take;
+    w.left -= e - off;
     ++w.idx;
     if (w.left > 0) {      // the item ends here: on to the next
       w.off = 0;
@@ -302,9 +303,11 @@ __device__ __noinline__ void ra_next(const RaLens p, RaWalk& w, RaPiece& c) {
         }
       }
     }
-    if (c.tb > c.ta) return;
+    if (c.tb > c.ta) break;
     c.tb = 0;
   }
+  walk = w;
+  piece = c;
 }
 
 template <bool TMA>
@@ -855,72 +858,78 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
   }
 }
 
-// CTA (c - 1, y): the item that CTA c's run start cuts (if that is the item's
-// first cut with key tiles on both sides), rows 32 y .. 32 y + 31, a lane per row
-// and a warp per 16 columns:
+// CTA c - 1: the item that CTA c's run start cuts, if that is the item's first cut
+// with key tiles on both sides. A lane per row, a warp per 16 columns of 32 rows:
 //   O = sum_s O_s 2^(m_s - M) / sum_s l_s 2^(m_s - M).
 // Pieces lie in CTA order: CTA c - 1's (its last item), then c, c + 1, ... (each
-// one's first).
-constexpr int RC_THREADS = 256;
+// one's first). Bound by latency: the cut, then the pieces, five at a time; one
+// CTA per SM, so that those without a cut are gone at once.
+constexpr int RC_THREADS = 512;
 __global__ void __launch_bounds__(RC_THREADS) ragged_combine_kernel(const __grid_constant__ RaParams p) {
   pdl_enter();
   const int c = blockIdx.x + 1;
   const RaStart st = p.starts[c];
-  const int lane = threadIdx.x & 31, col = (threadIdx.x >> 5) * 16;
-  const int rows = st.rows - static_cast<int>(blockIdx.y) * 32;
-  if (rows <= 0 || st.pieces == 0) return;
-  // few rows (decoding): the lanes that have none take a share of the pieces
-  const int R = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
-  const int r = blockIdx.y * 32 + (lane & (R - 1));
+  if (st.pieces == 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = (warp & 7) * 16;
   auto slot = [&](int s) { return static_cast<int64_t>(c - 1 + s) * 2 + (s == 0 ? st.first_slot : 0); };
-  // running max over the pieces, as within a piece
-  float M = -INFINITY, l = 0.f, a[16];
+  for (int row0 = (warp >> 3) * 32; row0 < st.rows; row0 += RC_THREADS / 8) {
+    const int rows = st.rows - row0;
+    // few rows (decoding): the lanes that have none take a share of the pieces
+    const int R = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+    const int r = row0 + (lane & (R - 1));
+    // running max over the pieces, as within a piece
+    float M = -INFINITY, l = 0.f, a[16];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) a[e] = 0.f;
-  auto add = [&](float m2, float l2, const float (&v)[16]) {
-    if (!(m2 > -INFINITY)) return;                 // a piece whose keys this row does not see
-    const float m_new = fmaxf(M, m2), f0 = exp2f(M - m_new), f = exp2f(m2 - m_new);
-    M = m_new;
-    l = fmaf(l2, f, l * f0);
+    for (int e = 0; e < 16; ++e) a[e] = 0.f;
+    auto add = [&](float m2, float l2, const float (&v)[16]) {
+      if (!(m2 > -INFINITY)) return;               // a piece whose keys this row does not see
+      const float m_new = fmaxf(M, m2), f0 = exp2f(M - m_new), f = exp2f(m2 - m_new);
+      M = m_new;
+      l = fmaf(l2, f, l * f0);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) a[e] = fmaf(v[e], f, a[e] * f0);
-  };
-  if (r < st.rows) {
-#pragma unroll 4
-    for (int s = lane / R; s < st.pieces; s += 32 / R) {
-      const int64_t at = slot(s);
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (at * RA_BQ + r) * 2);
-      const float* po = p.part_o + (at * RA_D + col) * RA_BQ + r * 4;
+      for (int e = 0; e < 16; ++e) a[e] = fmaf(v[e], f, a[e] * f0);
+    };
+    if (r < st.rows) {
+      constexpr int U = 5;                         // pieces whose reads are under way together
+      for (int s0 = lane / R; s0 < st.pieces; s0 += U * (32 / R)) {
+        float2 ml[U];
+        float v[U][16];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int s = s0 + u * (32 / R);
+          ml[u] = make_float2(-INFINITY, 0.f);
+          if (s < st.pieces) {
+            const int64_t at = slot(s);
+            ml[u] = *reinterpret_cast<const float2*>(p.part_ml + (at * RA_BQ + r) * 2);
+            const float* po = p.part_o + (at * RA_D + col) * RA_BQ + r * 4;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 x = *reinterpret_cast<const float4*>(po + e * 4 * RA_BQ);
+              v[u][4 * e] = x.x; v[u][4 * e + 1] = x.y; v[u][4 * e + 2] = x.z; v[u][4 * e + 3] = x.w;
+            }
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) add(ml[u].x, ml[u].y, v[u]);
+      }
+    }
+    for (int o = 16; o >= R; o >>= 1) {
+      const float m2 = __shfl_down_sync(0xffffffffu, M, o), l2 = __shfl_down_sync(0xffffffffu, l, o);
       float v[16];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float4 x = *reinterpret_cast<const float4*>(po + e * 4 * RA_BQ);
-        v[4 * e] = x.x; v[4 * e + 1] = x.y; v[4 * e + 2] = x.z; v[4 * e + 3] = x.w;
-      }
-      add(ml.x, ml.y, v);
+      for (int e = 0; e < 16; ++e) v[e] = __shfl_down_sync(0xffffffffu, a[e], o);
+      if (lane < o) add(m2, l2, v);
     }
-  }
-  for (int o = 16; o >= R; o >>= 1) {
-    const float m2 = __shfl_down_sync(0xffffffffu, M, o), l2 = __shfl_down_sync(0xffffffffu, l, o);
-    float v[16];
+    if (lane >= R || r >= st.rows) continue;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int tok = r / p.G;
+    const int64_t orow = static_cast<int64_t>(st.row0 + tok) * p.Hq + st.g * p.G + (r - tok * p.G);
+    uint32_t x[8];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = __shfl_down_sync(0xffffffffu, a[e], o);
-    if (lane < o) add(m2, l2, v);
+    for (int i = 0; i < 8; ++i) x[i] = pack_bf16x2(a[2 * i] * inv, a[2 * i + 1] * inv);
+    ra_st32(p.o + orow * RA_D + col, x);
+    if (p.lse && col == 0) p.lse[orow] = (M + log2f(l)) * RA_LN2;
   }
-  if (lane >= R || r >= st.rows) return;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const int tok = r / p.G;
-  const int64_t orow = static_cast<int64_t>(st.row0 + tok) * p.Hq + st.g * p.G + (r - tok * p.G);
-#pragma unroll
-  for (int e = 0; e < 16; e += 8) {
-    uint4 x;
-    x.x = pack_bf16x2(a[e] * inv, a[e + 1] * inv);
-    x.y = pack_bf16x2(a[e + 2] * inv, a[e + 3] * inv);
-    x.z = pack_bf16x2(a[e + 4] * inv, a[e + 5] * inv);
-    x.w = pack_bf16x2(a[e + 6] * inv, a[e + 7] * inv);
-    *reinterpret_cast<uint4*>(p.o + orow * RA_D + col + e) = x;
-  }
-  if (p.lse && col == 0) p.lse[orow] = (M + log2f(l)) * RA_LN2;
 }
 
 kl_status ra_map(CUtensorMap* m, int rank, const void* ptr, const cuuint64_t* dims, const cuuint64_t* strides,
@@ -1022,7 +1031,7 @@ kl_status ragged_attention(const kl_ragged_cfg& rc, int Hq, int Hkv, const void*
   KL_CUDA(cudaGetLastError());
   if (ctas > 1) {
     ProfScope ps("ragged_combine", st, 0.0, 4.0 * ctas * RA_D);
-    launch_pdl(ragged_combine_kernel, dim3(ctas - 1, RA_BQ / 32), RC_THREADS, 0, st, p);
+    launch_pdl(ragged_combine_kernel, ctas - 1, RC_THREADS, 0, st, p);
     KL_CUDA(cudaGetLastError());
   }
   return KL_OK;

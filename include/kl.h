@@ -533,7 +533,7 @@ KL_API kl_status kl_ragged_qkv_rope(const kl_ragged_cfg* rc, int32_t Hq, int32_t
  * its table row, or whose table entry lies outside the pool, reads as a zero key
  * and value and is reported (KL_DEVERR_PAGE). The workspace (256-byte aligned)
  * does not depend on the lengths; steps that may run at the same time need one
- * each. o and lse must not overlap the inputs. */
+ * each. o (32-byte aligned) and lse must not overlap the inputs. */
 KL_API size_t kl_ragged_attention_ws_bytes(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d);
 KL_API kl_status kl_ragged_attention(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
                                      const void* q, const void* k_pool, const void* v_pool, const int32_t* table,

@@ -161,6 +161,8 @@ def test_attention_refusals(lib):
         assert call(**{n: 0x1008}) == K.KL_ERR_INVALID_ARG
     for n in ("table", "cu", "ctx"):
         assert call(**{n: None}) == K.KL_ERR_INVALID_ARG
+    assert call(o=0x7010) == K.KL_ERR_INVALID_ARG                           # written in 32-byte sectors
+    assert "32-byte" in K.last_error()
     assert call(ws=None) == K.KL_ERR_NO_MEMORY
     assert call(ws=0x10080) == K.KL_ERR_NO_MEMORY
     assert call(nb=1024) == K.KL_ERR_NO_MEMORY
