@@ -24,6 +24,10 @@ Cases (T = 2048 tokens, hidden 5120, 64/8 heads of 128, intermediate 25600):
   down_few_rows the decode step's down projection: 64 rows x 25600 against
                 5120 x 25600 weights (262 MB) plus the residual, through
                 kl_gemm_ex with its scratch (the few-rows kernel)
+  ragged_decode attention of a ragged step: the paged_attn case
+  ragged_chunk  attention of 4096 new tokens over 12288 cached ones
+  ragged_qkv    norm, rotation and cache write of 8192 new tokens
+  draft_verify  64 requests of four drafts, 151936 classes, fp32
 """
 from __future__ import annotations
 
@@ -151,6 +155,49 @@ def main():
         def run():
             K.kl_paged_attention(pc, HQ, HKV, D, bf, q.data_ptr(), kp.data_ptr(), vp.data_ptr(), table.data_ptr(),
                                  ctx_t.data_ptr(), o.data_ptr(), 0, ws.data_ptr(), nb)
+    elif a.case in ("ragged_decode", "ragged_chunk", "ragged_qkv"):
+        B, ctx, n, bs = {"ragged_decode": (64, 4096, 1, 16), "ragged_chunk": (1, 12288, 4096, 16),
+                         "ragged_qkv": (8, 0, 1024, 16)}[a.case]
+        max_blocks = (ctx + n + bs - 1) // bs
+        n_blocks, R = B * max_blocks, B * n
+        kp, vp = _rand((n_blocks, bs, HKV * D)), _rand((n_blocks, bs, HKV * D))
+        table = torch.randperm(n_blocks, device="cuda").to(torch.int32).reshape(B, max_blocks)
+        ctx_t = torch.full((B,), ctx, dtype=torch.int32, device="cuda")
+        cu = torch.arange(B + 1, dtype=torch.int32, device="cuda") * n
+        q, o = _rand((R, HQ * D)), torch.empty(R, HQ * D, dtype=torch.bfloat16, device="cuda")
+        rc = K.RaggedCfg(B, R, bs, max_blocks, n_blocks)
+        if a.case == "ragged_qkv":
+            k, v, g = _rand((R, HKV * D)), _rand((R, HKV * D)), _rand((D,))
+            pos = (torch.arange(R, device="cuda") % n).to(torch.int32)
+            req = torch.arange(R, device="cuda") // n
+            slots = (table[req, (pos // bs).long()] * bs + pos % bs).to(torch.int32)
+
+            def run():
+                K.kl_ragged_qkv_rope(rc, HQ, HKV, D, bf, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                     g.data_ptr(), 1e-6, 1e6, 0, cu.data_ptr(), pos.data_ptr(), slots.data_ptr(),
+                                     o.data_ptr(), kp.data_ptr(), vp.data_ptr())
+        else:
+            nb = K.kl_ragged_attention_ws_bytes(rc, HQ, HKV, D)
+            ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+
+            def run():
+                K.kl_ragged_attention(rc, HQ, HKV, D, bf, q.data_ptr(), kp.data_ptr(), vp.data_ptr(),
+                                      table.data_ptr(), cu.data_ptr(), ctx_t.data_ptr(), o.data_ptr(), 0,
+                                      ws.data_ptr(), nb)
+    elif a.case == "draft_verify":
+        B, drafts, V = 64, 4, 151936
+        R = B * (drafts + 1)
+        p = torch.softmax(_rand((R, V), 2.5, torch.float32), 1)
+        qd = torch.softmax(torch.log(p) + _rand((R, V), 0.7, torch.float32), 1)
+        cu = torch.arange(B + 1, dtype=torch.int32, device="cuda") * (drafts + 1)
+        tok = torch.cat([torch.zeros(1, device="cuda"), torch.multinomial(qd, 1)[:-1, 0]]).to(torch.int32)
+        ua, us = torch.rand(R, device="cuda"), torch.rand(B, device="cuda")
+        acc, nxt = (torch.empty(B, dtype=torch.int32, device="cuda") for _ in range(2))
+        vc = K.VerifyCfg(B, R, V, K.KL_F32)
+
+        def run():
+            K.kl_draft_verify(vc, p.data_ptr(), V, qd.data_ptr(), V, tok.data_ptr(), cu.data_ptr(), ua.data_ptr(),
+                              us.data_ptr(), acc.data_ptr(), nxt.data_ptr())
     elif a.case == "down_few_rows":
         M, N, Kd = 64, H, I
         A = _rand((M, Kd))

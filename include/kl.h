@@ -475,7 +475,7 @@ KL_API kl_status kl_layer_forward_paged(const kl_layer_cfg* cfg, const kl_paged_
  * step's tensors are ragged: row cu_rows[b] + i is request b's new token i, at
  * position ctx[b] + i (ctx below zero counts as zero). cu_rows [B+1] int32 on
  * the device, starting at 0 and not decreasing; rows from cu_rows[B] on are
- * neither read nor written. Pools and tables are those of kl_paged_cfg. bf16,
+ * not written and reach no result. Pools and tables are those of kl_paged_cfg. bf16,
  * head dim 128, Hq / Hkv <= 128; pool rows (n_blocks * block_size * Hkv) below
  * 2^31; T at most 2^24, max_blocks * block_size at most 2^30. int32 and fp32 arrays of these entry points need only
  * 4-byte alignment (they may be pieces of one buffer). */
@@ -531,9 +531,10 @@ KL_API kl_status kl_ragged_qkv_rope(const kl_ragged_cfg* rc, int32_t Hq, int32_t
  * head floor(h * Hkv / Hq). q, o [T, Hq*d]; lse [T, Hq] fp32 (natural log) or
  * NULL. Slots behind a request's last token may hold anything. A position past
  * its table row, or whose table entry lies outside the pool, reads as a zero key
- * and value and is reported (KL_DEVERR_PAGE). The workspace (256-byte aligned)
- * does not depend on the lengths; steps that may run at the same time need one
- * each. o (32-byte aligned) and lse must not overlap the inputs. */
+ * and value and is reported (KL_DEVERR_PAGE). The workspace (256-byte aligned,
+ * for the current device's SM count) does not depend on the lengths; steps that
+ * may run at the same time need one each. A NaN or an infinity at a position
+ * that a row does not see can reach it when other rows of its tile do see it. o (32-byte aligned) and lse must not overlap the inputs. */
 KL_API size_t kl_ragged_attention_ws_bytes(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d);
 KL_API kl_status kl_ragged_attention(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
                                      const void* q, const void* k_pool, const void* v_pool, const int32_t* table,
