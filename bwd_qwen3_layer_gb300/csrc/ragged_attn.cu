@@ -264,7 +264,7 @@ struct RaWalk {
   long long off, left;     // unit inside the item, units left of the run
 };
 // The next piece with at least one key tile into c. Called by one lane; one copy
-// of the code for all roles (a CTA's start is bound by instruction fetches).
+// of the code for all roles.
 __device__ __noinline__ void ra_next(const RaLens p, RaWalk& walk, RaPiece& piece) {
   RaWalk w = walk;         // in registers: one read, one write each
   RaPiece c;

@@ -15,11 +15,11 @@
 //
 // An index must not depend on how a sum is split, so sums are held far beyond
 // the weights' own precision: p - q as an error-free pair of floats (two-sum,
-// Knuth), accumulated per thread and over a warp in pairs (about 48 bits), and
-// from there by single warps in fp64 (an SM adds two doubles a clock: fp64 sums
-// in every thread took most of the time, 82 us for 64 requests of 151936 classes
-// against the reads' 11.5). The acceptance test is exact: the product of two
-// floats fits a double.
+// Knuth), sums, prefix sums and comparisons in such pairs (about 48 bits). fp64
+// is slow on this part (an addition takes 63 cycles, an SM starts two a cycle):
+// with every thread's sums in it 64 requests of 151936 classes took 82 us, with
+// the warps' prefix sums alone 26, without it 17.6. The acceptance test is exact:
+// the product of two floats fits a double.
 #include "internal.h"
 #include "kl_common.cuh"
 
@@ -27,9 +27,10 @@ namespace kl {
 namespace {
 
 constexpr int DV_CL = 8;           // CTAs (one cluster) per request
-// Warps per CTA: 8 where the requests' CTAs fill the GPU (all of 64 requests'
-// are resident then: 23 us for 64 x 151936; with 16 warps they take two rounds, 30), 16 where
-// every CTA has an SM to itself (one request: 12.0 us; with 32 warps 13.4).
+// Warps per CTA: 8 where the requests' CTAs fill the GPU (four fit on an SM, so
+// all of 64 requests' are resident: 23 us for 64 x 151936 where 16 warps, in two
+// rounds, took 30), 16 where every CTA has an SM to itself (one request: 12.0 us
+// where 32 warps took 13.4; both pairs measured with fp64 prefix sums).
 constexpr int DV_WARPS_MANY = 8, DV_WARPS_FEW = 16;
 
 struct VerifyParams {
@@ -79,7 +80,7 @@ __device__ __forceinline__ void dv_load(const T* row, int64_t i, int V, float (&
   }
 }
 
-// A running sum as an unevaluated pair: hi + lo.
+// A number as an unevaluated pair of floats, hi + lo (about 48 bits).
 struct Pair {
   float hi, lo;
   __device__ __forceinline__ void add(float x) {
@@ -87,15 +88,40 @@ struct Pair {
     lo += (hi - (s - b)) + (x - b);
     hi = s;
   }
-  __device__ __forceinline__ double value() const { return static_cast<double>(hi) + static_cast<double>(lo); }
 };
+__device__ __forceinline__ Pair dv_norm(Pair v) {   // |lo| at most half a step of hi
+  const float s = v.hi + v.lo;
+  return {s, v.lo - (s - v.hi)};
+}
+__device__ __forceinline__ Pair dv_plus(Pair a, Pair b) {
+  a.add(b.hi);
+  a.lo += b.lo;
+  return dv_norm(a);
+}
+// a > b for normed pairs: where the leading parts are close their difference is
+// exact, and where they are not it decides.
+__device__ __forceinline__ bool dv_above(Pair a, Pair b) { return (a.hi - b.hi) + (a.lo - b.lo) > 0.f; }
+__device__ __forceinline__ Pair dv_times(float u, Pair a) {
+  const float p = __fmul_rn(u, a.hi);
+  return dv_norm({p, fmaf(u, a.hi, -p) + u * a.lo});
+}
+__device__ __forceinline__ Pair dv_shfl(Pair v, int lane) {
+  return {__shfl_sync(0xffffffffu, v.hi, lane), __shfl_sync(0xffffffffu, v.lo, lane)};
+}
 // The sum of the warp's 32 pairs, in every lane.
 __device__ __forceinline__ Pair dv_warp_sum(Pair v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float hi = __shfl_xor_sync(0xffffffffu, v.hi, o), lo = __shfl_xor_sync(0xffffffffu, v.lo, o);
-    v.add(hi);
-    v.lo += lo;
+  for (int o = 16; o > 0; o >>= 1)
+    v = dv_plus(v, {__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
+  return v;
+}
+// Inclusive prefix sums over the first N lanes of a warp (N a power of two).
+template <int N>
+__device__ __forceinline__ Pair dv_warp_scan(Pair v, int lane) {
+#pragma unroll
+  for (int o = 1; o < N; o <<= 1) {
+    const Pair x = {__shfl_up_sync(0xffffffffu, v.hi, o), __shfl_up_sync(0xffffffffu, v.lo, o)};
+    if (lane >= o) v = dv_plus(x, v);
   }
   return v;
 }
@@ -117,43 +143,35 @@ __device__ __forceinline__ void dv_weight(int kind, float p, float q, int64_t co
   if (!(w > 0.f)) w = we = 0.f;
 }
 
-__device__ __forceinline__ double dv_warp_scan(double v, int lane) {   // inclusive
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double x = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += x;
-  }
-  return v;
-}
 // The two halves of a cluster-wide barrier: shared memory of another CTA may be
 // written once that CTA runs, so every CTA arrives at its start and waits just
 // before its first such write.
 __device__ __forceinline__ void dv_cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
 __device__ __forceinline__ void dv_cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-__device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v) {
-  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
+__device__ __forceinline__ void st_cluster_pair(uint32_t addr, Pair v) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.hi), "f"(v.lo) : "memory");
 }
 
-// One warp: lane i < n holds the sum of part i. The part whose cumulative sum
-// crosses x: the first i with before + sum_{j <= i} s_j > x; if rounding leaves
-// none, the last one with a positive sum; -1 if there is none. `before` becomes
-// the sum in front of it.
-__device__ __forceinline__ int dv_cross(double s, int lane, double x, double& before) {
-  const double incl = before + dv_warp_scan(s, lane);
-  const unsigned some = __ballot_sync(0xffffffffu, s > 0.0);
-  const unsigned over = __ballot_sync(0xffffffffu, s > 0.0 && incl > x);
+// One warp: lane i holds the sum s of part i (zero where there is none) and the sum
+// incl of the parts up to it. The part whose cumulative sum crosses x: the first i with
+// before + incl_i > x; if rounding leaves none, the last one with a positive sum;
+// -1 if there is none. `before` becomes the sum in front of it.
+__device__ __forceinline__ int dv_cross(Pair s, Pair incl, int lane, Pair x, Pair& before) {
+  const Pair up = dv_plus(before, incl);
+  const unsigned some = __ballot_sync(0xffffffffu, s.hi > 0.f);
+  const unsigned over = __ballot_sync(0xffffffffu, s.hi > 0.f && dv_above(up, x));
   if (!some) return -1;
   const int i = over ? __ffs(over) - 1 : 31 - __clz(some);
-  before = __shfl_sync(0xffffffffu, incl - s, i);
+  if (i > 0) before = dv_plus(before, dv_shfl(incl, i - 1));
   return i;
 }
 
 // What the first warp tells the others: the part to look into (below 0: none),
 // the sum in front of it and the value to cross.
 struct VerifySmem {
-  double slots[2][DV_CL];        // the CTAs' sums, written by each of them (one array per attempt)
-  double parts[32];              // the warps' sums
-  double before, x;
+  Pair slots[2][DV_CL];          // the CTAs' sums, written by each of them (one array per attempt)
+  Pair parts[32];                // the warps' sums
+  Pair before, x;
   int part, accepted, kind;
 };
 
@@ -230,24 +248,26 @@ __device__ __forceinline__ void dv_request(const VerifyParams& p, VerifySmem& s,
 
   for (int attempt = 0; attempt < 2; ++attempt) {
     const Pair sum = dv_sum<T, E>(row, kind, w0, w1);
-    if (lane == 0) s.parts[warp] = sum.value();
+    if (lane == 0) s.parts[warp] = sum;
     if (attempt == 0) dv_cluster_wait();
     __syncthreads();
-    double mine = 0.0;
+    Pair mine = {0.f, 0.f}, upto = mine;
     if (warp == 0) {
-      mine = lane < WARPS ? s.parts[lane] : 0.0;
-      const double cta = __shfl_sync(0xffffffffu, dv_warp_scan(mine, lane), 31);
-      if (lane < DV_CL) st_cluster_f64(mapa_shared(smem_u32(&s.slots[attempt][rank]), lane), cta);
+      if (lane < WARPS) mine = s.parts[lane];
+      upto = dv_warp_scan<WARPS>(mine, lane);
+      const Pair cta = dv_shfl(upto, WARPS - 1);
+      if (lane < DV_CL) st_cluster_pair(mapa_shared(smem_u32(&s.slots[attempt][rank]), lane), cta);
     }
     cluster_sync_all();
     if (warp == 0) {
-      const double part = lane < DV_CL ? s.slots[attempt][lane] : 0.0;
-      const double total = __shfl_sync(0xffffffffu, dv_warp_scan(part, lane), 31);
-      const double x = static_cast<double>(u) * total;
-      double before = 0.0;
+      Pair part = {0.f, 0.f}, before = part;
+      if (lane < DV_CL) part = s.slots[attempt][lane];
+      const Pair incl = dv_warp_scan<DV_CL>(part, lane);
+      const Pair total = dv_shfl(incl, DV_CL - 1);
+      const Pair x = dv_times(u, total);
       int next = kind;
-      int owner = total > 0.0 && total < INFINITY ? dv_cross(part, lane, x, before) : -1;
-      if (owner < 0 && attempt == 0 && kind != DV_P && !(total > 0.0)) {
+      int owner = total.hi > 0.f && total.hi < INFINITY ? dv_cross(part, incl, lane, x, before) : -1;
+      if (owner < 0 && attempt == 0 && kind != DV_P && !(total.hi > 0.f)) {
         next = -1;                                   // nothing left of p - q anywhere: p itself
       } else if (owner < 0) {
         if (rank == 0 && lane == 0) {
@@ -255,7 +275,7 @@ __device__ __forceinline__ void dv_request(const VerifyParams& p, VerifySmem& s,
           p.next[b] = -1;
         }
       } else if (owner == rank) {
-        owner = max(0, dv_cross(mine, lane, x, before));
+        owner = max(0, dv_cross(mine, upto, lane, x, before));
         if (lane == 0) {
           s.before = before;
           s.x = x;
@@ -279,12 +299,13 @@ __device__ __forceinline__ void dv_request(const VerifyParams& p, VerifySmem& s,
     const int s0 = min(c1, c0 + ow * per_warp), s1 = min(c1, s0 + per_warp);
     const int piece = (s1 - s0 + WARPS - 1) / WARPS;
     const int p0 = min(s1, s0 + warp * piece), p1 = min(s1, p0 + piece);
-    const Pair part = dv_sum<T, E>(row, kind, p0, p1);
-    if (lane == 0) s.parts[warp] = part.value();
+    const Pair again = dv_sum<T, E>(row, kind, p0, p1);
+    if (lane == 0) s.parts[warp] = again;
     __syncthreads();
-    const double x = s.x;
-    double before = s.before;
-    const int pw = max(0, dv_cross(lane < WARPS ? s.parts[lane] : 0.0, lane, x, before));
+    const Pair x = s.x;
+    Pair before = s.before;
+    const Pair stretch = lane < WARPS ? s.parts[lane] : Pair{0.f, 0.f};
+    const int pw = max(0, dv_cross(stretch, dv_warp_scan<WARPS>(stretch, lane), lane, x, before));
     if (warp != pw) return;
     // this warp's piece in order, 32 vectors at a time
     int64_t found = -1, last = -1;
@@ -292,7 +313,7 @@ __device__ __forceinline__ void dv_request(const VerifyParams& p, VerifySmem& s,
       const int j = j0 + lane;
       const int64_t col = static_cast<int64_t>(j) * E - row.mis;
       float w[E], we[E];
-      Pair sum = {0.f, 0.f};
+      Pair own = {0.f, 0.f};
 #pragma unroll
       for (int e = 0; e < E; ++e) w[e] = we[e] = 0.f;
       if (j < p1) {
@@ -302,26 +323,26 @@ __device__ __forceinline__ void dv_request(const VerifyParams& p, VerifySmem& s,
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           dv_weight(kind, fp[e], fq[e], col + e, row.draft, w[e], we[e]);
-          sum.add(w[e]);
-          sum.lo += we[e];
+          own.add(w[e]);
+          own.lo += we[e];
         }
       }
-      const double mine2 = sum.value();
-      const double incl = before + dv_warp_scan(mine2, lane);
-      double at = incl - mine2;
+      const Pair incl = dv_warp_scan<32>(dv_norm(own), lane);
+      Pair at = {__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
+      at = lane ? dv_plus(before, at) : before;      // everything in front of this lane's vector
       int64_t hit = -1, pos = -1;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        at += static_cast<double>(w[e]) + static_cast<double>(we[e]);
+        at = dv_plus(at, {w[e], we[e]});
         if (w[e] > 0.f) {
           pos = col + e;
-          if (hit < 0 && at > x) hit = col + e;
+          if (hit < 0 && dv_above(at, x)) hit = col + e;
         }
       }
       const unsigned hits = __ballot_sync(0xffffffffu, hit >= 0), any = __ballot_sync(0xffffffffu, pos >= 0);
       if (hits) found = __shfl_sync(0xffffffffu, hit, __ffs(hits) - 1);
       if (any) last = __shfl_sync(0xffffffffu, pos, 31 - __clz(any));
-      before = __shfl_sync(0xffffffffu, incl, 31);
+      before = dv_plus(before, dv_shfl(incl, 31));
     }
     if (lane == 0) {
       p.acc[b] = accepted;
@@ -332,7 +353,7 @@ __device__ __forceinline__ void dv_request(const VerifyParams& p, VerifySmem& s,
 }
 
 template <typename T, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS) draft_verify_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(32 * WARPS, WARPS == DV_WARPS_MANY ? 4 : 1) draft_verify_kernel(const VerifyParams p) {
   pdl_enter();
   __shared__ VerifySmem s;
   const int b = blockIdx.x / DV_CL, rank = static_cast<int>(cluster_ctarank());
