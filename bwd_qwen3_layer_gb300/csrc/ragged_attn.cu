@@ -12,8 +12,8 @@
 // tensor-core time that the loads hide) and prompts (bound by the tensor cores).
 //
 // Work split. Lengths are on the device only, so the grid is one CTA per SM and
-// every CTA finds its own work: the items' key tiles of 128 (plus one unit for
-// an item's start and end) laid end to end are W units, and CTA c takes units
+// every CTA finds its own work: the items' key tiles of 128 (plus two units
+// for an item's start and end) laid end to end are W units, and CTA c takes units
 // [c P, c P + P), P = ceil(W / CTAs). Every CTA thus streams the same number of
 // key tiles whatever the lengths are. A CTA's first and last item may be cut; it
 // leaves such a piece unnormalised (fp32 O, running max and sum per row) in the
