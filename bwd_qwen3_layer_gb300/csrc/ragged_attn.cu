@@ -82,15 +82,18 @@ struct RaReq {
   int r0, n, ctx;
 };
 
-// Where a CTA's run of units starts: an item and the unit inside it. The cut
-// that the run's start makes, for the joining kernel: pieces of the item, its
-// rows, the first one's row of the step; pieces 0: nothing to join here.
-struct RaStart {
-  int b, g, qt;
-  int pieces, rows, row0;
-  int first_slot;   // of the CTA before: 0 if this item was its first
+// Where a CTA's run of units starts: the unit inside an item.
+struct RaFound {
+  int any;          // 0: no units left for this CTA
+  int g, qt;
   RaReq q;
-  long long off;    // unit within the item
+  long long off;
+};
+// The cut that a run's start makes, for the joining kernel: the item's pieces (0:
+// nothing to join here), its rows, the first one's row of the step.
+struct RaCut {
+  int pieces, rows, row0, g;
+  int first_slot;   // of the CTA before: 0 if this item was its first
 };
 
 struct RaParams {
@@ -104,7 +107,7 @@ struct RaParams {
   float* lse;            // [T, Hq] or null
   float* part_o;         // [CTA][2][32][128][4] unnormalised pieces: 4 columns of the 128 rows together
   float* part_ml;        // [CTA][2][128][2] (max in log2 units, sum)
-  RaStart* starts;       // [CTA]
+  RaCut* cuts;           // [CTA]
   int B, T, Hq, Hkv, G, TQ;
   int bs, max_blocks, n_blocks;
   int box;               // rows per TMA box
@@ -263,11 +266,8 @@ struct RaWalk {
   RaReq q;
   long long off, left;     // unit inside the item, units left of the run
 };
-// The next piece with at least one key tile into c. Called by one lane; one copy
-// of the code for all roles.
-__device__ __noinline__ void ra_next(const RaLens p, RaWalk& walk, RaPiece& piece) {
-  RaWalk w = walk;         // in registers: one read, one write each
-  RaPiece c;
+// The next piece with at least one key tile into c.
+__device__ __forceinline__ void ra_step(const RaLens& p, RaWalk& w, RaPiece& c) {
   c.tb = 0;
   while (w.left > 0) {
     const int tiles = ra_tiles(w.q, p.TQ, w.qt);
@@ -306,13 +306,23 @@ __device__ __noinline__ void ra_next(const RaLens p, RaWalk& walk, RaPiece& piec
     if (c.tb > c.ta) break;
     c.tb = 0;
   }
-  walk = w;
+}
+// The same for a walk in shared memory, called by one lane: one copy of the code
+// for all roles.
+__device__ __noinline__ void ra_next(const RaLens p, const RaWalk& from, RaWalk& to, RaPiece& piece) {
+  if (from.left <= 0) {
+    piece.tb = 0;
+    return;
+  }
+  RaWalk w = from;         // in registers: one read, one write each
+  RaPiece c;
+  ra_step(p, w, c);
+  to = w;
   piece = c;
 }
 
 template <bool TMA>
 __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid_constant__ RaParams p) {
-  pdl_enter();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -333,7 +343,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
   const uint32_t drain_pv = bar + 184;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + RA_OFF_BAR + 192);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + RA_OFF_BAR + 196);
-  RaStart* start = reinterpret_cast<RaStart*>(smem + RA_OFF_BAR + 208);
+  RaFound* found = reinterpret_cast<RaFound*>(smem + RA_OFF_BAR + 208);
   long long* wsum = reinterpret_cast<long long*>(smem + RA_OFF_BAR + 256);   // the warps' unit sums, then this CTA's units
 
   RaWalk* walks = reinterpret_cast<RaWalk*>(smem + RA_OFF_BAR + 336);        // the finder's, then one per warp
@@ -372,7 +382,13 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
   if (lane == 0 && warp >= 5 && (TMA || warp == 5))
     tma_prefetch_desc(warp == 5 ? &p.tmQ : warp == 6 ? &p.tmK : &p.tmV);
 
+  // What is above reads nothing that an earlier kernel writes and runs while the last
+  // one ends: this CTA's shared memory takes a whole SM, so nothing else is on it that
+  // could want its tensor memory (every decoding case 0.2 us less).
+  pdl_enter();
+
   // ---- this CTA's run: prefix sums of the requests' units, then the item at unit cta * P ----
+  long long P;
   {
     const int per = (p.B + RA_THREADS - 1) / RA_THREADS;
     const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
@@ -398,10 +414,10 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
       if (w < warp) before += v;
       W += v;
     }
-    const long long P = max(ra_div(W + ctas - 1, ctas), static_cast<long long>(RA_MIN_UNITS));
+    P = max(ra_div(W + ctas - 1, ctas), static_cast<long long>(RA_MIN_UNITS));
     const long long u0 = cta * P;
     if (threadIdx.x == 0 && u0 >= W) {
-      start->pieces = 0;
+      found->any = 0;
       pieces[0].tb = 0;
     }
     long long lo = before + incl - mine;      // units before this thread's requests
@@ -423,28 +439,13 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
         if (ra_units_before(q.ctx, p.TQ, m) <= y) m0 = m; else m1 = m;
       }
       const long long off = y - (m0 ? ra_units_before(q.ctx, p.TQ, m0) : 0);
-      start->b = b;
-      start->g = g;
-      start->qt = m0;
-      start->q = q;
-      start->off = off;
-      // the first cut of its item with key tiles on both sides joins the pieces
-      const long long len = ra_tiles(q, p.TQ, m0) + RA_ITEM_UNITS;
-      const bool joins = off > RA_ITEM_UNITS && off - P <= RA_ITEM_UNITS;
-      start->pieces = joins ? 1 + static_cast<int>(ra_div(len - off + P - 1, P)) : 0;
-      start->rows = min(p.TQ, q.n - m0 * p.TQ) * p.G;
-      start->row0 = q.r0 + m0 * p.TQ;
-      start->first_slot = off - P >= 0 ? 0 : 1;
       // the walk to the first piece, for every role at once
-      RaWalk& w = walks[0];
-      w.b = b;
-      w.g = g;
-      w.qt = m0;
-      w.idx = 0;
-      w.q = q;
-      w.off = off;
-      w.left = min(P, W - u0);
-      ra_next(lens, w, pieces[0]);
+      RaWalk w = {b, g, m0, 0, q, off, min(P, W - u0)};
+      RaPiece c;
+      ra_step(lens, w, c);
+      pieces[0] = c;
+      walks[0] = w;
+      *found = {1, g, m0, q, off};
     }
   }
   tc_fence_before();
@@ -452,19 +453,15 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const uint32_t tmP = tmem + RA_TM_P, tmO = tmem + RA_TM_O;
-  if (threadIdx.x < sizeof(RaStart) / 4)
-    reinterpret_cast<int*>(p.starts + cta)[threadIdx.x] = reinterpret_cast<const int*>(start)[threadIdx.x];
   const int GT = p.G * p.TQ;            // rows of a full query tile
 
   // Piece 0 is shared (pieces[0]); from there each warp walks for itself.
-  RaWalk& walk = walks[warp + 1];
-  if (lane < sizeof(RaWalk) / 4) reinterpret_cast<int*>(&walk)[lane] = reinterpret_cast<const int*>(&walks[0])[lane];
   auto piece = [&](int k) -> RaPiece& { return pieces[k ? 1 + warp * 2 + (k & 1) : 0]; };
   // piece k of this CTA into its place; false if there is none
   auto find = [&](int k) -> bool {
     if (k > 0) {
       __syncwarp();                     // every lane is done with piece k - 2
-      if (lane == 0) ra_next(lens, walk, piece(k));
+      if (lane == 0) ra_next(lens, walks[k == 1 ? 0 : warp + 1], walks[warp + 1], piece(k));
       __syncwarp();
     }
     return piece(k).tb > 0;
@@ -478,22 +475,18 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     const __nv_bfloat16* pool = is_k ? p.kp : p.vp;
     const uint32_t ring = sb + (is_k ? RA_OFF_K : RA_OFF_V);
     const uint32_t full0 = is_k ? k_full(0) : v_full(0), empty0 = is_k ? k_empty(0) : v_empty(0);
-    const int nbox = RA_BKV / p.box;
+    const int nbox = RA_BKV / p.box, per = 32 / nbox, my = lane / nbox;   // boxes of a tile, tiles of a look-up, this lane's
     const int no_row = p.n_blocks * p.bs;         // past the pool's last row: filled with zeros
     int issued_q = 0, issued = 0, s = 0, as = 0;  // s: the ring's stage; as: the next one to announce
     uint32_t ph = 1;                              // parity that an empty stage's wait passes with
     bool ok = true;
-    // the pool row of position pos, or no_row
-    auto pool_row = [&](int b, int pos, int L) {
-      if (pos >= L) return no_row;
-      const int lb = pos / p.bs;
-      const int blk = lb < p.max_blocks ? p.table[static_cast<int64_t>(b) * p.max_blocks + lb] : -1;
-      if (blk < 0 || blk >= p.n_blocks) {
-        record_error(p.err, KL_DEVERR_PAGE);
-        return no_row;
-      }
-      return blk * p.bs + (pos - lb * p.bs);
+    // the pool row of a position at `at` of its page blk, or no_row
+    auto pool_row = [&](int blk, int at) {
+      if (blk >= 0 && blk < p.n_blocks) return blk * p.bs + at;
+      record_error(p.err, KL_DEVERR_PAGE);
+      return no_row;
     };
+    auto page = [&](int b, int lb) { return lb < p.max_blocks ? p.table[static_cast<int64_t>(b) * p.max_blocks + lb] : -1; };
     // cp.async: the rows of one tile; row[k] of lane l is the pool row of key 32 k + l
     auto gather = [&](uint32_t dst, int g, const int (&row)[4]) {
       const int ch = lane & 15;
@@ -520,16 +513,25 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     };
     for (int k = 0; ok && find(k); ++k) {
       const RaPiece w = piece(k);
-      int row[4];
+      // TMA: one look at the table serves `per` tiles, a lane per box, and the
+      // next tiles' pages are asked for before these are copied: a read of the table
+      // takes 600 to 3000 cycles, which every tile of a run's start waited for.
+      // cp.async: a lane for four of a tile's keys.
+      int row[4], blk = 0, at = 0;
+      const int keys = min(w.L, w.tb * RA_BKV);
+      auto ask = [&](int j) {
+        const int pos = j * RA_BKV + lane * p.box, lb = pos / p.bs;
+        at = pos < keys ? pos - lb * p.bs : -1;
+        if (at >= 0) blk = page(w.b, lb);
+      };
       auto lookup = [&](int j) {
-        if (TMA) {
-          row[0] = lane < nbox ? pool_row(w.b, j * RA_BKV + lane * p.box, w.L) : no_row;
-        } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) row[i] = pool_row(w.b, j * RA_BKV + i * 32 + lane, w.L);
+        for (int i = 0; i < 4; ++i) {
+          const int pos = j * RA_BKV + i * 32 + lane, lb = pos / p.bs;
+          row[i] = pos < keys ? pool_row(page(w.b, lb), pos - lb * p.bs) : no_row;
         }
       };
-      lookup(w.ta);
+      if (TMA) ask(w.ta); else lookup(w.ta);
       if (!is_k) {
         // Q: the buffer is free once the previous piece's last S product is done
         if (!ra_wait_copy(q_empty, (issued_q & 1) ^ 1u, p.err, abort_flag)) { ok = false; break; }
@@ -542,12 +544,17 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
         ++issued_q;
       }
       for (int j = w.ta; j < w.tb; ++j) {
+        const int nth = (j - w.ta) & (per - 1);
+        if (TMA && nth == 0) {
+          row[0] = at >= 0 ? pool_row(blk, at) : no_row;
+          if (j + per < w.tb) ask(j + per);
+        }
         if (!ra_wait_copy(empty0 + 8 * s, ph, p.err, abort_flag)) { ok = false; break; }
         const uint32_t dst = ring + s * RA_TILE;
         if (TMA) {
           if (el) mbar_arrive_expect_tx(full0 + 8 * s, RA_TILE);
           __syncwarp();
-          if (lane < nbox) ra_tma_4d(dst + lane * p.box * 256, tm, 0, 0, 2 * w.g, row[0] >> 3, full0 + 8 * s);
+          if (my == nth) ra_tma_4d(dst + (lane & (nbox - 1)) * p.box * 256, tm, 0, 0, 2 * w.g, row[0] >> 3, full0 + 8 * s);
           __syncwarp();
         } else {
           gather(dst, w.g, row);
@@ -558,7 +565,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
           s = 0;
           ph ^= 1u;
         }
-        if (j + 1 < w.tb) lookup(j + 1);
+        if (!TMA && j + 1 < w.tb) lookup(j + 1);
       }
       // the piece's last tile: its products free Q, which the next piece waits for
       if (!TMA && ok) announce(std::integral_constant<int, 0>());
@@ -665,6 +672,22 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
       fence_async_shared();
       return true;
     };
+    // the cut at this CTA's start, by a warp that has nothing to do yet
+    if (threadIdx.x == RA_THREADS - 1) {
+      RaCut cut = {0, 0, 0, 0, 0};
+      if (found->any) {
+        const RaFound f = *found;
+        // the first cut of its item with key tiles on both sides joins the pieces
+        const long long len = ra_tiles(f.q, p.TQ, f.qt) + RA_ITEM_UNITS;
+        if (f.off > RA_ITEM_UNITS && f.off - P <= RA_ITEM_UNITS) cut.pieces = 1 + static_cast<int>(ra_div(len - f.off + P - 1, P));
+        cut.rows = min(p.TQ, f.q.n - f.qt * p.TQ) * p.G;
+        cut.row0 = f.q.r0 + f.qt * p.TQ;
+        cut.g = f.g;
+        cut.first_slot = f.off - P >= 0 ? 0 : 1;
+      }
+      p.cuts[cta] = cut;
+    }
+    __syncwarp();
     bool ok = true;
     const float scale = p.scale_log2;
     int n = 0;
@@ -858,42 +881,48 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
   }
 }
 
-// CTA c - 1: the item that CTA c's run start cuts, if that is the item's first cut
-// with key tiles on both sides. A lane per row, a warp per 16 columns of 32 rows:
+// Four CTAs per cut: the item that CTA c's run start cuts, if that is the item's
+// first cut with key tiles on both sides, 32 columns each. A lane per row, a warp
+// per 8 columns of 32 rows:
 //   O = sum_s O_s 2^(m_s - M) / sum_s l_s 2^(m_s - M).
 // Pieces lie in CTA order: CTA c - 1's (its last item), then c, c + 1, ... (each
-// one's first). Bound by latency: the cut, then the pieces, five at a time; one
-// CTA per SM, so that those without a cut are gone at once.
-constexpr int RC_THREADS = 512;
-__global__ void __launch_bounds__(RC_THREADS) ragged_combine_kernel(const __grid_constant__ RaParams p) {
+// one's first). Bound by latency: the cut, then the pieces, five at a time (a
+// request of 32768 keys has 19 per head, 77 KB: more than one SM fetches at once).
+// Small CTAs, since most have no cut and only cost their start: 4 of 128 threads a
+// cut; 4 of 256 lost 0.1 to 0.4 us on all but prompts of 200 rows (32.3 against
+// 34.1), 1 of 256 was as fast without cuts but 72 against 63 us on the mixed batch.
+constexpr int RC_THREADS = 128, RC_SPLIT = 4, RC_COLS = 8;
+static_assert(RA_D / RC_SPLIT / RC_COLS == RC_THREADS / 32, "a warp per 8 of a CTA's columns");
+__global__ void __launch_bounds__(RC_THREADS, 5) ragged_combine_kernel(const __grid_constant__ RaParams p) {
   pdl_enter();
-  const int c = blockIdx.x + 1;
-  const RaStart st = p.starts[c];
+  const int c = blockIdx.x / RC_SPLIT + 1;
+  const RaCut st = p.cuts[c];
   if (st.pieces == 0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = (warp & 7) * 16;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = (blockIdx.x % RC_SPLIT) * (RA_D / RC_SPLIT) + warp * RC_COLS;
   auto slot = [&](int s) { return static_cast<int64_t>(c - 1 + s) * 2 + (s == 0 ? st.first_slot : 0); };
-  for (int row0 = (warp >> 3) * 32; row0 < st.rows; row0 += RC_THREADS / 8) {
+  for (int row0 = 0; row0 < st.rows; row0 += 32) {
     const int rows = st.rows - row0;
     // few rows (decoding): the lanes that have none take a share of the pieces
     const int R = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
     const int r = row0 + (lane & (R - 1));
     // running max over the pieces, as within a piece
-    float M = -INFINITY, l = 0.f, a[16];
+    float M = -INFINITY, l = 0.f, a[RC_COLS];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) a[e] = 0.f;
-    auto add = [&](float m2, float l2, const float (&v)[16]) {
+    for (int e = 0; e < RC_COLS; ++e) a[e] = 0.f;
+    auto add = [&](float m2, float l2, const float (&v)[RC_COLS]) {
       if (!(m2 > -INFINITY)) return;               // a piece whose keys this row does not see
       const float m_new = fmaxf(M, m2), f0 = exp2f(M - m_new), f = exp2f(m2 - m_new);
       M = m_new;
       l = fmaf(l2, f, l * f0);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) a[e] = fmaf(v[e], f, a[e] * f0);
+      for (int e = 0; e < RC_COLS; ++e) a[e] = fmaf(v[e], f, a[e] * f0);
     };
     if (r < st.rows) {
       constexpr int U = 5;                         // pieces whose reads are under way together
       for (int s0 = lane / R; s0 < st.pieces; s0 += U * (32 / R)) {
         float2 ml[U];
-        float v[U][16];
+        float v[U][RC_COLS];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int s = s0 + u * (32 / R);
@@ -903,7 +932,7 @@ __global__ void __launch_bounds__(RC_THREADS) ragged_combine_kernel(const __grid
             ml[u] = *reinterpret_cast<const float2*>(p.part_ml + (at * RA_BQ + r) * 2);
             const float* po = p.part_o + (at * RA_D + col) * RA_BQ + r * 4;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < RC_COLS / 4; ++e) {
               const float4 x = *reinterpret_cast<const float4*>(po + e * 4 * RA_BQ);
               v[u][4 * e] = x.x; v[u][4 * e + 1] = x.y; v[u][4 * e + 2] = x.z; v[u][4 * e + 3] = x.w;
             }
@@ -915,19 +944,18 @@ __global__ void __launch_bounds__(RC_THREADS) ragged_combine_kernel(const __grid
     }
     for (int o = 16; o >= R; o >>= 1) {
       const float m2 = __shfl_down_sync(0xffffffffu, M, o), l2 = __shfl_down_sync(0xffffffffu, l, o);
-      float v[16];
+      float v[RC_COLS];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = __shfl_down_sync(0xffffffffu, a[e], o);
+      for (int e = 0; e < RC_COLS; ++e) v[e] = __shfl_down_sync(0xffffffffu, a[e], o);
       if (lane < o) add(m2, l2, v);
     }
     if (lane >= R || r >= st.rows) continue;
     const float inv = l > 0.f ? 1.f / l : 0.f;
     const int tok = r / p.G;
     const int64_t orow = static_cast<int64_t>(st.row0 + tok) * p.Hq + st.g * p.G + (r - tok * p.G);
-    uint32_t x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = pack_bf16x2(a[2 * i] * inv, a[2 * i + 1] * inv);
-    ra_st32(p.o + orow * RA_D + col, x);
+    *reinterpret_cast<uint4*>(p.o + orow * RA_D + col) =
+        make_uint4(pack_bf16x2(a[0] * inv, a[1] * inv), pack_bf16x2(a[2] * inv, a[3] * inv),
+                   pack_bf16x2(a[4] * inv, a[5] * inv), pack_bf16x2(a[6] * inv, a[7] * inv));
     if (p.lse && col == 0) p.lse[orow] = (M + log2f(l)) * RA_LN2;
   }
 }
@@ -945,14 +973,14 @@ kl_status ra_map(CUtensorMap* m, int rank, const void* ptr, const cuuint64_t* di
 }
 
 struct RaWs {
-  size_t o, ml, starts, total;
+  size_t o, ml, cuts, total;
 };
 RaWs ra_ws(int ctas) {
   RaWs w;
   w.o = 0;
   w.ml = w.o + static_cast<size_t>(ctas) * 2 * RA_BQ * RA_D * 4;
-  w.starts = w.ml + align_up(static_cast<size_t>(ctas) * 2 * RA_BQ * 2 * 4, 256);
-  w.total = w.starts + align_up(static_cast<size_t>(ctas) * sizeof(RaStart), 256);
+  w.cuts = w.ml + align_up(static_cast<size_t>(ctas) * 2 * RA_BQ * 2 * 4, 256);
+  w.total = w.cuts + align_up(static_cast<size_t>(ctas) * sizeof(RaCut), 256);
   return w;
 }
 
@@ -1000,7 +1028,7 @@ kl_status ragged_attention(const kl_ragged_cfg& rc, int Hq, int Hkv, const void*
   uint8_t* wb = static_cast<uint8_t*>(ws);
   p.part_o = reinterpret_cast<float*>(wb + lay.o);
   p.part_ml = reinterpret_cast<float*>(wb + lay.ml);
-  p.starts = reinterpret_cast<RaStart*>(wb + lay.starts);
+  p.cuts = reinterpret_cast<RaCut*>(wb + lay.cuts);
   p.B = rc.B;
   p.T = rc.T;
   p.Hq = Hq;
@@ -1031,7 +1059,7 @@ kl_status ragged_attention(const kl_ragged_cfg& rc, int Hq, int Hkv, const void*
   KL_CUDA(cudaGetLastError());
   if (ctas > 1) {
     ProfScope ps("ragged_combine", st, 0.0, 4.0 * ctas * RA_D);
-    launch_pdl(ragged_combine_kernel, ctas - 1, RC_THREADS, 0, st, p);
+    launch_pdl(ragged_combine_kernel, (ctas - 1) * RC_SPLIT, RC_THREADS, 0, st, p);
     KL_CUDA(cudaGetLastError());
   }
   return KL_OK;
