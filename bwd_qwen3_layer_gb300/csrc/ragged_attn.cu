@@ -110,7 +110,7 @@ struct RaParams {
   RaCut* cuts;           // [CTA]
   int B, T, Hq, Hkv, G, TQ;
   int bs, max_blocks, n_blocks;
-  int box;               // rows per TMA box
+  int box_log;           // log2 of the rows per TMA box (8 .. 128)
   float scale_log2;
   uint32_t* err;
 };
@@ -475,7 +475,8 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     const __nv_bfloat16* pool = is_k ? p.kp : p.vp;
     const uint32_t ring = sb + (is_k ? RA_OFF_K : RA_OFF_V);
     const uint32_t full0 = is_k ? k_full(0) : v_full(0), empty0 = is_k ? k_empty(0) : v_empty(0);
-    const int nbox = RA_BKV / p.box, per = 32 / nbox, my = lane / nbox;   // boxes of a tile, tiles of a look-up, this lane's
+    // rows of a box, boxes of a tile, tiles of a look-up, this lane's one
+    const int box = 1 << p.box_log, nbox = RA_BKV >> p.box_log, per = box >> 2, my = lane >> (7 - p.box_log);
     const int no_row = p.n_blocks * p.bs;         // past the pool's last row: filled with zeros
     int issued_q = 0, issued = 0, s = 0, as = 0;  // s: the ring's stage; as: the next one to announce
     uint32_t ph = 1;                              // parity that an empty stage's wait passes with
@@ -520,7 +521,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
       int row[4], blk = 0, at = 0;
       const int keys = min(w.L, w.tb * RA_BKV);
       auto ask = [&](int j) {
-        const int pos = j * RA_BKV + lane * p.box, lb = pos / p.bs;
+        const int pos = j * RA_BKV + lane * box, lb = pos / p.bs;
         at = pos < keys ? pos - lb * p.bs : -1;
         if (at >= 0) blk = page(w.b, lb);
       };
@@ -554,7 +555,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
         if (TMA) {
           if (el) mbar_arrive_expect_tx(full0 + 8 * s, RA_TILE);
           __syncwarp();
-          if (my == nth) ra_tma_4d(dst + (lane & (nbox - 1)) * p.box * 256, tm, 0, 0, 2 * w.g, row[0] >> 3, full0 + 8 * s);
+          if (my == nth) ra_tma_4d(dst + (lane & (nbox - 1)) * box * 256, tm, 0, 0, 2 * w.g, row[0] >> 3, full0 + 8 * s);
           __syncwarp();
         } else {
           gather(dst, w.g, row);
@@ -1000,8 +1001,8 @@ kl_status ragged_attention(const kl_ragged_cfg& rc, int Hq, int Hkv, const void*
   p.G = Hq / Hkv;
   p.TQ = RA_BQ / p.G;
   const bool tma = rc.block_size % 8 == 0;
-  p.box = 128;
-  while (tma && rc.block_size % p.box) p.box >>= 1;    // gcd(block_size, 128)
+  p.box_log = 7;
+  while (tma && rc.block_size & ((1 << p.box_log) - 1)) --p.box_log;    // gcd(block_size, 128)
   {
     const cuuint64_t dq[3] = {RA_D, static_cast<cuuint64_t>(Hq), static_cast<cuuint64_t>(rc.T)};
     const cuuint64_t sq[2] = {RA_D * 2, static_cast<cuuint64_t>(Hq) * RA_D * 2};
@@ -1014,7 +1015,7 @@ kl_status ragged_attention(const kl_ragged_cfg& rc, int Hq, int Hkv, const void*
     const cuuint64_t dk[4] = {64, 8, static_cast<cuuint64_t>(Hkv) * 2,
                               static_cast<cuuint64_t>(rc.n_blocks) * rc.block_size / 8};
     const cuuint64_t sk[3] = {pitch, 128, 8 * pitch};
-    const cuuint32_t bk[4] = {64, 8, 2, static_cast<cuuint32_t>(p.box / 8)};
+    const cuuint32_t bk[4] = {64, 8, 2, 1u << (p.box_log - 3)};
     KL_TRY(ra_map(&p.tmK, 4, kp, dk, sk, bk));
     KL_TRY(ra_map(&p.tmV, 4, vp, dk, sk, bk));
   }
