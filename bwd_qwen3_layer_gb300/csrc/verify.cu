@@ -6,12 +6,12 @@
 //   C_i = sum_{j <= i} w_j > u sum_j w_j.
 //
 // Only one row of p (and q) per request is read whole: V x 4 B each, bound by
-// HBM for many requests and by latency for one. A cluster of eight CTAs takes
-// one request: each finds the row itself (at most a few gathers), sums its
-// eighth of the weights, the eight sums meet in distributed shared memory, and
-// the CTA in whose range the cumulative sum crosses u x total looks for the
-// place: its warps' sums name a stretch of about a thousand weights, which the
-// CTA sums once more (from L2), one vector per lane.
+// HBM for many requests and by latency for one. A cluster of 8 or 16 CTAs takes
+// one request: each finds the row itself (at most a few gathers), sums its share
+// of the weights, the sums meet in distributed shared memory, and the CTA in whose
+// range the cumulative sum crosses u x total looks for the place: its warps' sums
+// name a stretch of about a thousand weights, which the CTA sums once more (from
+// L2), one vector per lane.
 //
 // An index must not depend on how a sum is split, so sums are held far beyond
 // the weights' own precision: p - q as an error-free pair of floats (two-sum,
@@ -26,12 +26,16 @@
 namespace kl {
 namespace {
 
-constexpr int DV_CL = 8;           // CTAs (one cluster) per request
-// Warps per CTA: 8 where the requests' CTAs fill the GPU (four fit on an SM, so
-// all of 64 requests' are resident: 23 us for 64 x 151936 where 16 warps, in two
-// rounds, took 30), 16 where every CTA has an SM to itself (one request: 12.0 us
-// where 32 warps took 13.4; both pairs measured with fp64 prefix sums).
+// CTAs per request (one cluster) and warps per CTA, by how many clusters are
+// resident together (V = 151936, p and q in fp32):
+//   up to 7 requests   16 CTAs of 16 warps, an SM each: 7.1 us; eight of them 8.1;
+//                      from 8 requests on they take two rounds (8: 11.3)
+//   up to 14           8 of 16 warps: 8.3 to 8.6 us, 8 of 8 warps 9.8 to 11.3;
+//                      16 requests take two rounds (12.5)
+//   more               8 of 8 warps, four CTAs per SM: 16 requests 11.1 us, 64 17.0
+constexpr int DV_CL = 8, DV_CL_FEW = 16;
 constexpr int DV_WARPS_MANY = 8, DV_WARPS_FEW = 16;
+constexpr int DV_FEW = 7, DV_SOME = 14;
 
 struct VerifyParams {
   const void* p;
@@ -169,7 +173,7 @@ __device__ __forceinline__ int dv_cross(Pair s, Pair incl, int lane, Pair x, Pai
 // What the first warp tells the others: the part to look into (below 0: none),
 // the sum in front of it and the value to cross.
 struct VerifySmem {
-  Pair slots[2][DV_CL];          // the CTAs' sums, written by each of them (one array per attempt)
+  Pair slots[2][DV_CL_FEW];          // the CTAs' sums, written by each of them (one array per attempt)
   Pair parts[32];                // the warps' sums
   Pair before, x;
   int part, accepted, kind;
@@ -234,13 +238,13 @@ __device__ __forceinline__ Pair dv_sum(const DvRow<T>& r, int kind, int j0, int 
   return dv_sum_kind<T, E, DV_P>(r, j0, j1);
 }
 
-template <typename T, int E, int WARPS>
+template <typename T, int E, int WARPS, int CL>
 __device__ __forceinline__ void dv_request(const VerifyParams& p, VerifySmem& s, int b, int rank, const DvRow<T>& row, int kind,
                                            int accepted) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // columns in vectors of E: vector j holds columns E j - mis ..
   const int nv = static_cast<int>((static_cast<int64_t>(p.V) + row.mis + E - 1) / E);
-  const int per_cta = (nv + DV_CL - 1) / DV_CL;
+  const int per_cta = (nv + CL - 1) / CL;
   const int per_warp = (per_cta + WARPS - 1) / WARPS;
   const int c0 = min(nv, rank * per_cta), c1 = min(nv, c0 + per_cta);
   const int w0 = min(c1, c0 + warp * per_warp), w1 = min(c1, w0 + per_warp);
@@ -256,14 +260,14 @@ __device__ __forceinline__ void dv_request(const VerifyParams& p, VerifySmem& s,
       if (lane < WARPS) mine = s.parts[lane];
       upto = dv_warp_scan<WARPS>(mine, lane);
       const Pair cta = dv_shfl(upto, WARPS - 1);
-      if (lane < DV_CL) st_cluster_pair(mapa_shared(smem_u32(&s.slots[attempt][rank]), lane), cta);
+      if (lane < CL) st_cluster_pair(mapa_shared(smem_u32(&s.slots[attempt][rank]), lane), cta);
     }
     cluster_sync_all();
     if (warp == 0) {
       Pair part = {0.f, 0.f}, before = part;
-      if (lane < DV_CL) part = s.slots[attempt][lane];
-      const Pair incl = dv_warp_scan<DV_CL>(part, lane);
-      const Pair total = dv_shfl(incl, DV_CL - 1);
+      if (lane < CL) part = s.slots[attempt][lane];
+      const Pair incl = dv_warp_scan<CL>(part, lane);
+      const Pair total = dv_shfl(incl, CL - 1);
       const Pair x = dv_times(u, total);
       int next = kind;
       int owner = total.hi > 0.f && total.hi < INFINITY ? dv_cross(part, incl, lane, x, before) : -1;
@@ -352,11 +356,11 @@ __device__ __forceinline__ void dv_request(const VerifyParams& p, VerifySmem& s,
   }
 }
 
-template <typename T, int WARPS>
+template <typename T, int WARPS, int CL>
 __global__ void __launch_bounds__(32 * WARPS, WARPS == DV_WARPS_MANY ? 4 : 1) draft_verify_kernel(const VerifyParams p) {
   pdl_enter();
   __shared__ VerifySmem s;
-  const int b = blockIdx.x / DV_CL, rank = static_cast<int>(cluster_ctarank());
+  const int b = blockIdx.x / CL, rank = static_cast<int>(cluster_ctarank());
   const int r0 = min(max(p.cu[b], 0), p.T), r1 = min(max(p.cu[b + 1], r0), p.T);
   if (r1 <= r0) {                       // the whole cluster leaves here
     if (rank == 0 && threadIdx.x == 0) {
@@ -408,10 +412,10 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == DV_WARPS_MANY ? 4 : 1) dr
   // odd vocabulary starts anywhere); element by element where they do not
   w.mis = static_cast<int>((reinterpret_cast<uintptr_t>(w.p) & 15u) / sizeof(T));
   if (!w.q || w.mis == static_cast<int>((reinterpret_cast<uintptr_t>(w.q) & 15u) / sizeof(T))) {
-    dv_request<T, E, WARPS>(p, s, b, rank, w, kind, accepted);
+    dv_request<T, E, WARPS, CL>(p, s, b, rank, w, kind, accepted);
   } else {
     w.mis = 0;
-    dv_request<T, 1, WARPS>(p, s, b, rank, w, kind, accepted);
+    dv_request<T, 1, WARPS, CL>(p, s, b, rank, w, kind, accepted);
   }
 }
 
@@ -421,26 +425,34 @@ kl_status draft_verify(const kl_verify_cfg& c, const void* p, int64_t ldp, const
                        const int32_t* tokens, const int32_t* cu, const float* ua, const float* us, int32_t* acc,
                        int32_t* next, cudaStream_t st) {
   VerifyParams v = {p, q, ldp, ldq, tokens, cu, ua, us, acc, next, c.B, c.T, c.V, device_error_word()};
+  using Kernel = void (*)(VerifyParams);
+  const bool f32 = c.dtype == KL_F32, few = c.B <= DV_FEW, some = c.B <= DV_SOME;
+  Kernel k;
+  if (few)
+    k = f32 ? Kernel(draft_verify_kernel<float, DV_WARPS_FEW, DV_CL_FEW>) : Kernel(draft_verify_kernel<__nv_bfloat16, DV_WARPS_FEW, DV_CL_FEW>);
+  else if (some)
+    k = f32 ? Kernel(draft_verify_kernel<float, DV_WARPS_FEW, DV_CL>) : Kernel(draft_verify_kernel<__nv_bfloat16, DV_WARPS_FEW, DV_CL>);
+  else
+    k = f32 ? Kernel(draft_verify_kernel<float, DV_WARPS_MANY, DV_CL>) : Kernel(draft_verify_kernel<__nv_bfloat16, DV_WARPS_MANY, DV_CL>);
+  const int cl = few ? DV_CL_FEW : DV_CL;
+  // 16 CTAs are above the portable size; set at every call, as the device may differ
+  if (few) KL_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = DV_CL;
+  attr[1].val.clusterDim.x = cl;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(c.B * DV_CL);
-  const bool few = c.B * DV_CL <= num_sms();
-  cfg.blockDim = dim3(32 * (few ? DV_WARPS_FEW : DV_WARPS_MANY));
+  cfg.gridDim = dim3(c.B * cl);
+  cfg.blockDim = dim3(32 * (some ? DV_WARPS_FEW : DV_WARPS_MANY));
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   const double es = static_cast<double>(dtype_size(c.dtype));
   ProfScope ps("draft_verify", st, 0.0, static_cast<double>(c.B) * c.V * es * (q ? 2 : 1));
-  if (c.dtype == KL_F32)
-    KL_CUDA(cudaLaunchKernelEx(&cfg, few ? draft_verify_kernel<float, DV_WARPS_FEW> : draft_verify_kernel<float, DV_WARPS_MANY>, v));
-  else
-    KL_CUDA(cudaLaunchKernelEx(&cfg, few ? draft_verify_kernel<__nv_bfloat16, DV_WARPS_FEW> : draft_verify_kernel<__nv_bfloat16, DV_WARPS_MANY>, v));
+  KL_CUDA(cudaLaunchKernelEx(&cfg, k, v));
   return KL_OK;
 }
 

@@ -393,6 +393,36 @@ def test_verify_corners(kl):
     assert "0x2" in str(e.value)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_verify_answers_do_not_depend_on_the_batch(kl, dtype):
+    """Three requests alone, and repeated in batches up to 7, 14 and more (each served by another split of the row)."""
+    V, g = 5001, torch.Generator(device="cuda").manual_seed(8)
+    p = torch.softmax(2 * torch.randn(9, V, generator=g, device="cuda"), 1).to(dtype)
+    q = torch.softmax(2 * torch.randn(9, V, generator=g, device="cuda"), 1).to(dtype)
+    tokens = np.concatenate([[0], torch.multinomial(q.float(), 1, generator=g)[:-1, 0].cpu().numpy()])
+    rng = np.random.default_rng(8)
+    ua, us = rng.random(9).astype(np.float32), rng.random(3).astype(np.float32)
+    want = O.draft_verify(_host(p), _host(q), tokens, [0, 4, 5, 9], ua, us)
+    for times in (1, 2, 4, 5, 7):
+        B = 3 * times
+        cu = np.concatenate([[0], (9 * np.arange(times)[:, None] + [4, 5, 9]).reshape(-1)])
+        got = _verify(kl, p.repeat(times, 1), q.repeat(times, 1), np.tile(tokens, times), cu, np.tile(ua, times), np.tile(us, times))
+        assert len(got[0]) == B
+        np.testing.assert_array_equal(got[0], np.tile(want[0], times))
+        np.testing.assert_array_equal(got[1], np.tile(want[1], times))
+    assert kl.kl_device_status() == 0
+
+
+@pytest.mark.parametrize("B", [3, 9, 20])
+def test_verify_a_sum_that_meets_its_mark(kl, B):
+    """4096 equal weights and u = k / 4096: the sum of k weights is exactly u times the total, which the token after it exceeds first."""
+    p = torch.full((B, 4096), 2.0 ** -12, device="cuda")
+    k = np.linspace(0, 4095, B).astype(np.int64)
+    got = _verify(kl, p, None, np.zeros(B, np.int64), np.arange(B + 1), np.zeros(B, np.float32), (k / 4096).astype(np.float32))
+    np.testing.assert_array_equal(got[1], k)
+    assert kl.kl_device_status() == 0
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
