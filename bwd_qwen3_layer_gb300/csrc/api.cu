@@ -883,8 +883,8 @@ kl_status kl_draft_verify(const kl_verify_cfg* c, const void* p, int64_t ldp, co
                      c->V, static_cast<long long>(ldp), static_cast<long long>(ldq));
   if (c->dtype != KL_F32 && c->dtype != KL_BF16)
     return set_error(KL_ERR_INVALID_ARG, "draft_verify: bad dtype %d", c->dtype);
-  if (c->B > (1 << 24) || c->T > (1 << 24))
-    return set_error(KL_ERR_UNSUPPORTED, "draft_verify: too many requests or rows (%d, %d)", c->B, c->T);
+  if (c->B > (1 << 24) || c->T > (1 << 24) || c->V > (1 << 30))
+    return set_error(KL_ERR_UNSUPPORTED, "draft_verify: too many requests, rows or classes (%d, %d, %d)", c->B, c->T, c->V);
   KL_TRY(check_ptrs({p}, "draft_verify p"));
   if (q) KL_TRY(check_ptrs({q}, "draft_verify q"));
   KL_TRY(check_arrays({tokens, cu_rows, u_accept, u_sample, n_accepted, next_token}, "draft_verify"));

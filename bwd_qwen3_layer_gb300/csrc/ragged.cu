@@ -395,7 +395,8 @@ kl_status ragged_check(const kl_ragged_cfg* rc) {
   if (rc->B < 1 || rc->T < 1 || rc->block_size < 1 || rc->max_blocks < 1 || rc->n_blocks < 1)
     return set_error(KL_ERR_INVALID_ARG, "ragged: bad sizes (B %d, T %d, block %d, table %d, pool %d)", rc->B, rc->T,
                      rc->block_size, rc->max_blocks, rc->n_blocks);
-  if (rc->T > (1 << 24)) return set_error(KL_ERR_UNSUPPORTED, "ragged: too many rows (%d)", rc->T);
+  if (rc->T > (1 << 24) || rc->B > (1 << 24))
+    return set_error(KL_ERR_UNSUPPORTED, "ragged: too many rows or requests (%d, %d)", rc->T, rc->B);
   const double rows = static_cast<double>(rc->n_blocks) * rc->block_size;
   if (rows >= 2147483647.0)
     return set_error(KL_ERR_UNSUPPORTED, "ragged: pool rows (%.0f) beyond 32-bit indexing", rows);

@@ -475,10 +475,11 @@ KL_API kl_status kl_layer_forward_paged(const kl_layer_cfg* cfg, const kl_paged_
  * step's tensors are ragged: row cu_rows[b] + i is request b's new token i, at
  * position ctx[b] + i (ctx below zero counts as zero). cu_rows [B+1] int32 on
  * the device, starting at 0 and not decreasing; rows from cu_rows[B] on are
- * not written and reach no result. Pools and tables are those of kl_paged_cfg. bf16,
- * head dim 128, Hq / Hkv <= 128; pool rows (n_blocks * block_size * Hkv) below
- * 2^31; T at most 2^24, max_blocks * block_size at most 2^30. int32 and fp32 arrays of these entry points need only
- * 4-byte alignment (they may be pieces of one buffer). */
+ * not written and reach no result. Pools and tables are those of kl_paged_cfg.
+ * bf16, head dim 128, Hq / Hkv <= 128; pool rows (n_blocks * block_size * Hkv)
+ * below 2^31; B and T at most 2^24, max_blocks * block_size at most 2^30. int32
+ * and fp32 arrays of these entry points need only 4-byte alignment (they may be
+ * pieces of one buffer). */
 typedef struct kl_ragged_cfg {
   int32_t B;           /* requests in the step                               */
   int32_t T;           /* rows of the step's tensors (room for all requests) */
@@ -517,9 +518,9 @@ KL_API kl_status kl_ragged_plan(const kl_ragged_cfg* rc, const int32_t* n_new, c
  * gamma_k [d] (both NULL: no norm), then the rotation at position pos[row] with
  * planes (i, i + d/2) or, rope_interleaved, (2i, 2i + 1). q goes to q_out (may
  * be q_pre), k and the unchanged v to slot slots[row] of the pools, all in one
- * launch. q_pre, q_out [T, Hq*d], k_pre, v [T, Hkv*d]; rope_base at least 1. A row whose slot is below
- * zero leaves the pools alone; a slot past the pool is skipped and reported
- * (KL_DEVERR_PAGE). Two rows must not have the same slot. */
+ * launch. q_pre, q_out [T, Hq*d], k_pre, v [T, Hkv*d]; rope_base at least 1. A
+ * row whose slot is below zero leaves the pools alone; a slot past the pool is
+ * skipped and reported (KL_DEVERR_PAGE). Two rows must not have the same slot. */
 KL_API kl_status kl_ragged_qkv_rope(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
                                     const void* q_pre, const void* k_pre, const void* v, const void* gamma_q,
                                     const void* gamma_k, float eps, float rope_base, int32_t rope_interleaved,
@@ -534,7 +535,8 @@ KL_API kl_status kl_ragged_qkv_rope(const kl_ragged_cfg* rc, int32_t Hq, int32_t
  * and value and is reported (KL_DEVERR_PAGE). The workspace (256-byte aligned,
  * for the current device's SM count) does not depend on the lengths; steps that
  * may run at the same time need one each. A NaN or an infinity at a position
- * that a row does not see can reach it when other rows of its tile do see it. o (32-byte aligned) and lse must not overlap the inputs. */
+ * that a row does not see can reach it when other rows of its tile do see it.
+ * o (32-byte aligned) and lse must not overlap the inputs. */
 KL_API size_t kl_ragged_attention_ws_bytes(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d);
 KL_API kl_status kl_ragged_attention(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
                                      const void* q, const void* k_pool, const void* v_pool, const int32_t* table,
@@ -555,9 +557,10 @@ KL_API kl_status kl_ragged_attention(const kl_ragged_cfg* rc, int32_t Hq, int32_
  * rejection (p alone if that is zero everywhere) and p when every draft was
  * accepted or none was given: next_token[b] is the smallest index whose
  * cumulative weight exceeds u_sample[b] times the sum. Probabilities need not
- * sum to one; a weight that is NaN counts as zero; -1 where no weight is positive or their sum
- * is not finite. A request without rows gets 0 and -1. A draft outside [0, V)
- * is not accepted and reported (KL_DEVERR_TARGET).
+ * sum to one; a weight that is NaN counts as zero; -1 where no weight is
+ * positive or their sum is not finite in fp32. A request without rows gets 0 and
+ * -1. A draft outside [0, V) is not accepted and reported (KL_DEVERR_TARGET).
+ * B and T at most 2^24, V at most 2^30.
  * Products and sums are held to 48 bits or more. All on the device, p and q of
  * type dtype (fp32 or bf16). One launch, no workspace. */
 typedef struct kl_verify_cfg {

@@ -184,6 +184,14 @@ def test_verify_refusals(lib):
         assert call(**{n: 0x1001}) == K.KL_ERR_INVALID_ARG
 
 
+def test_sizes_past_32_bit_counting_are_refused(lib):
+    """Loops over requests and classes step by up to 32768 in 32 bits."""
+    p = [0x1000] * 10
+    assert lib.kl_ragged_plan(ctypes.byref(_rc(B=(1 << 24) + 1)), *p, None) == K.KL_ERR_UNSUPPORTED
+    v = K.VerifyCfg(1, 1, (1 << 30) + 1, K.KL_BF16)
+    assert lib.kl_draft_verify(ctypes.byref(v), 0x1000, 1 << 31, None, 0, *p[:6], None) == K.KL_ERR_UNSUPPORTED
+
+
 def test_layer_refusals(lib):
     def cfg(**kw):
         base = dict(B=1, S=64, H=256, Hq=4, Hkv=2, d=128, I=512, eps=1e-6, rope_base=1e6, dtype=K.KL_BF16)
