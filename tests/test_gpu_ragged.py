@@ -223,6 +223,49 @@ def test_attention_reports_pages_outside_the_pool(kl, bs):
     assert (np.abs(_host(o) - want) <= tol).all()
 
 
+def test_attention_does_not_depend_on_the_block_size(kl):
+    """Runs of some fifty key tiles a CTA: the same cache in pages of 8 to 256 tokens and of sizes that are gathered row by row gives the same bits."""
+    Hq, Hkv, reqs = 64, 8, [(1, 39990), (3, 40001), (1, 37777)]
+    g = torch.Generator(device="cuda").manual_seed(9)
+    q = torch.randn(5, Hq, D, generator=g, device="cuda").bfloat16()
+    kv = [[torch.randn(a + c, Hkv, D, generator=g, device="cuda").bfloat16() for a, c in reqs] for _ in range(2)]
+    cu, ctx = _i([0, 1, 4, 5]), _i([c for _, c in reqs])
+    first = None
+    for bs in (16, 8, 32, 40, 128, 256, 20, 1):
+        per = [-(-(a + c) // bs) for a, c in reqs]
+        maxb, nb = max(per) + 1, sum(per) + 2
+        order = torch.randperm(nb, generator=g, device="cuda")
+        table = torch.full((3, maxb), nb + 9, device="cuda")
+        pools = [torch.full((nb * bs, Hkv, D), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        at = 0
+        for b, (a, c) in enumerate(reqs):
+            table[b, :per[b]] = order[at:at + per[b]]
+            at += per[b]
+            pos = torch.arange(a + c, device="cuda")
+            for pool, x in zip(pools, kv):
+                pool[table[b, pos // bs] * bs + pos % bs] = x[b]
+        td = table.to(torch.int32)
+        rc = kl.RaggedCfg(3, 5, bs, maxb, nb)
+        ws = torch.empty(kl.kl_ragged_attention_ws_bytes(rc, Hq, Hkv, D), dtype=torch.uint8, device="cuda")
+        o = torch.empty_like(q)
+        kl.kl_ragged_attention(rc, Hq, Hkv, D, kl.KL_BF16, q.data_ptr(), pools[0].data_ptr(), pools[1].data_ptr(), td.data_ptr(), cu.data_ptr(), ctx.data_ptr(), o.data_ptr(),
+                               0, ws.data_ptr(), ws.numel())
+        assert kl.kl_device_status() == 0
+        if first is None:
+            first = o
+        assert torch.equal(o, first), bs
+    for b, (a, c) in enumerate(reqs):
+        r0 = int(cu[b])
+        for i in range(a):
+            k, v = (x[b][:c + i + 1].double() for x in kv)
+            qi = q[r0 + i].double().reshape(Hkv, Hq // Hkv, D)
+            w = torch.softmax(torch.einsum("hgd,khd->hgk", qi, k) / D ** 0.5, -1)
+            want, A = (torch.einsum("hgk,khd->hgd", w, x).reshape(Hq, D) for x in (v, v.abs()))
+            # as in test_attention_matches_oracle, with running sums of up to 2^16 keys
+            tol = (2.0 ** -8 + 2.0 ** -8 + 2e-4) * A + 2.0 ** -8 * want.abs()
+            assert ((first[r0 + i].double() - want).abs() <= tol).all(), (b, i)
+
+
 def test_attention_without_rows(kl):
     rc = kl.RaggedCfg(3, 4, 16, 2, 4)
     q = torch.randn(4, 8, D, device="cuda").bfloat16()
