@@ -12,8 +12,8 @@
 // tensor-core time that the loads hide) and prompts (bound by the tensor cores).
 //
 // Work split. Lengths are on the device only, so the grid is one CTA per SM and
-// every CTA finds its own work: the items' key tiles of 128 (plus two units
-// for an item's start and end) laid end to end are W units, and CTA c takes units
+// every CTA finds its own work: the items' key tiles of 128 (plus four
+// units for an item's start and end) laid end to end are W units, and CTA c takes units
 // [c P, c P + P), P = ceil(W / CTAs). Every CTA thus streams the same number of
 // key tiles whatever the lengths are. A CTA's first and last item may be cut; it
 // leaves such a piece unnormalised (fp32 O, running max and sum per row) in the
@@ -66,12 +66,12 @@ constexpr uint32_t RA_OFF_BAR = RA_OFF_V + RA_NST * RA_TILE;
 constexpr size_t RA_SMEM = 1024 + RA_OFF_BAR + 2048;
 // Tensor memory: S of two steps, P of two steps (bf16 pairs), O: all 512 columns.
 constexpr uint32_t RA_TM_P = 256, RA_TM_O = 384;
-// Units that an item's start and end count for: its first scores and its epilogue
-// take about as long as two key tiles. At least one such item per CTA: with one
-// unit and three per CTA, short requests shared CTAs while others idled (one of
-// 100 tokens: 12.4 us, now 9.2; the mixed batch of 20 is the same).
-constexpr int RA_ITEM_UNITS = 2;
-constexpr int RA_MIN_UNITS = RA_ITEM_UNITS + 1;
+// Units that an item's start and end count for: its first scores, the last product
+// and the epilogue take about four key tiles' time. Mixed batch of 20: with two,
+// CTAs with two pieces ended at 51 us and those with eight at 61, 63 us in all;
+// with four 60.4. A run may be as short as one unit: one request of 500 keys takes 8.8
+// us, 11.2 with runs of at least five (100 keys: 8.3 and 7.9).
+constexpr int RA_ITEM_UNITS = 4;
 constexpr float RA_LOG2E = 1.4426950408889634f;
 constexpr float RA_LN2 = 0.6931471805599453f;
 
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
       if (w < warp) before += v;
       W += v;
     }
-    P = max(ra_div(W + ctas - 1, ctas), static_cast<long long>(RA_MIN_UNITS));
+    P = max(ra_div(W + ctas - 1, ctas), 1LL);
     const long long u0 = cta * P;
     if (threadIdx.x == 0 && u0 >= W) {
       found->any = 0;
