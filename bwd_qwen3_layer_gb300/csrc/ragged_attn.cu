@@ -789,7 +789,8 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
       ++n;
       return true;
     };
-    for (int k = 0; ok && find(k); ++k) {
+    bool more = find(0);
+    for (int k = 0; ok && more; ++k) {
       int left, whole;                             // tiles left; those that every row sees whole
       bool busy;
       {
@@ -823,7 +824,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
         }
       }
       if (!ok) break;
-      // the piece's last P V product, step n - 1's
+      more = find(k + 1);                          // while the piece's last P V product, step n - 1's, runs
       if (!mbar_wait_warp(p_done((n - 1) & 1), ((n - 1) >> 1) & 1, p.err, abort_flag)) { ok = false; break; }
       tc_fence_after();
       if (busy) {
