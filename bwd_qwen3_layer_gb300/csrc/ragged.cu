@@ -8,7 +8,8 @@
 //                       of the rows, of the new table entries and, after a cluster
 //                       barrier, when nobody reads the list any more, of the
 //                       blocks given back; the first CTA updates the counts.
-//                       Bound by latency: three dependent reads and a scan.
+//                       Bound by latency: three dependent reads and a scan
+//                       (64 decoding requests 4.9 us, 700 of 40 tokens 8.7).
 //   ragged_qkv_kernel   one CTA per row: all its q, k and v heads, 16 bytes a
 //                       thread and plane half, the row's 64 (cos, sin) pairs
 //                       formed once in shared memory while the heads are on

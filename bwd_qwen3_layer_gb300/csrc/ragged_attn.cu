@@ -37,6 +37,13 @@
 // sizes gather row by row with 16-byte cp.async. Slots behind a context's end
 // may hold anything (NaN too): their scores are masked, and the last tile's
 // value rows behind the end are zeroed before the product reads them.
+//
+// Measured (64 / 8 heads, pages of 16): 64 requests of ~4096 keys 168-172 us, 0.92
+// to 0.95 of the HBM copy rate; one of 32768 keys 30; 4096 rows over 12288 keys 1161 us in a
+// burst, 0.86 of the burst tensor rate: a step is ~1440 cycles, of which the
+// products take 1024 and shared memory's 160 KB (products' reads, copies' writes)
+// 1250. Two warpgroups of softmax in turn (168 registers) gained 3 % there and
+// lost 4 to 14 % everywhere else.
 #include <cudaTypedefs.h>
 #include <math.h>
 #include <string.h>
