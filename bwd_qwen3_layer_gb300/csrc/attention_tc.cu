@@ -124,9 +124,9 @@ __global__ void __launch_bounds__(THREADS, 1) fa_fwd_tc_kernel(const __grid_cons
   auto v_empty = [&](int s) { return bar + 56 + 8 * s; };
   auto s_full = [&](int s) { return bar + 72 + 8 * s; };
   auto s_free = [&](int s) { return bar + 88 + 8 * s; };
-  const uint32_t p_full = bar + 104;
-  const uint32_t p_free = bar + 112;
-  const uint32_t q_tm = bar + 120;     // Q copied into tensor memory
+  auto p_full = [&](int s) { return bar + 104 + 8 * s; };   // by step parity, see the persistent form
+  const uint32_t p_free = bar + 120;
+  const uint32_t q_tm = bar + 128;     // Q copied into tensor memory
   const uint32_t drain = bar + 152;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + OFF_BAR + 160);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_BAR + 164);
@@ -149,8 +149,8 @@ __global__ void __launch_bounds__(THREADS, 1) fa_fwd_tc_kernel(const __grid_cons
       mbar_init(v_empty(s), 1);
       mbar_init(s_full(s), 1);
       mbar_init(s_free(s), 4);
+      mbar_init(p_full(s), 4);
     }
-    mbar_init(p_full, 4);
     mbar_init(p_free, 1);
     mbar_init(q_tm, 4);
     mbar_init(drain, 1);
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_fwd_tc_kernel(const __grid_cons
     auto issue_pv = [&](int j) -> bool {
       const int s = j & 1;
       const uint32_t ph = (j >> 1) & 1;
-      if (!mbar_wait_warp(p_full, j & 1, p.err, abort_flag)) return false;
+      if (!mbar_wait_warp(p_full(s), ph, p.err, abort_flag)) return false;
       if (!mbar_wait_warp(v_full(s), ph, p.err, abort_flag)) return false;
       tc_fence_after();
       if (el) {
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_fwd_tc_kernel(const __grid_cons
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
+      if (lane == 0) mbar_arrive(p_full(s));
     }
     // O / l and lse once the last P V product is done. p_free completes once per
     // P V product, and the last scores' completion shows only the product two
@@ -416,10 +416,14 @@ __global__ void __launch_bounds__(THREADS, 1) fa_fwd_tc_persist_kernel(const __g
   auto v_empty = [&](int s) { return bar + 56 + 8 * s; };
   auto s_full = [&](int s) { return bar + 72 + 8 * s; };
   auto s_free = [&](int s) { return bar + 88 + 8 * s; };
-  const uint32_t p_full = bar + 104;
-  const uint32_t p_free = bar + 112;
-  const uint32_t q_empty = bar + 120;
-  auto o_empty = [&](int s) { return bar + 128 + 8 * s; };
+  // P of the steps of one parity each. S_(g+1) is issued before P_g is waited for, so
+  // a warp can be a step ahead of another: on one barrier its two arrivals would
+  // complete step g's phase for the other, whose P is not written yet. With two, its
+  // next arrival on the same barrier needs S_(g+2), issued only after P_g V_g.
+  auto p_full = [&](int s) { return bar + 104 + 8 * s; };
+  const uint32_t p_free = bar + 120;
+  const uint32_t q_empty = bar + 128;
+  auto o_empty = [&](int s) { return bar + 136 + 8 * s; };
   const uint32_t drain = bar + 152;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + OFF_BAR + 160);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_BAR + 164);
@@ -439,8 +443,8 @@ __global__ void __launch_bounds__(THREADS, 1) fa_fwd_tc_persist_kernel(const __g
       mbar_init(s_full(s), 1);
       mbar_init(s_free(s), 4);
       mbar_init(o_empty(s), 4);
+      mbar_init(p_full(s), 4);
     }
-    mbar_init(p_full, 4);
     mbar_init(p_free, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_fwd_tc_persist_kernel(const __g
     auto issue_pv = [&](int gp, int ob, bool first) -> bool {
       const int s = gp & 1;
       const uint32_t ph = (gp >> 1) & 1;
-      if (!mbar_wait_warp(p_full, gp & 1, p.err, abort_flag)) return false;
+      if (!mbar_wait_warp(p_full(s), ph, p.err, abort_flag)) return false;
       if (!mbar_wait_warp(v_full(s), ph, p.err, abort_flag)) return false;
       tc_fence_after();
       if (el) {
@@ -661,7 +665,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_fwd_tc_persist_kernel(const __g
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full);
+        if (lane == 0) mbar_arrive(p_full(s));
       }
       if (!ok) break;
       // O / l and lse once the item's last P V product (step g - 1) is done. p_free
