@@ -383,6 +383,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_fwd_tc_kernel(const __grid_cons
             *reinterpret_cast<uint4*>(orow + c * 32 + e) = w;
           }
         }
+        __syncwarp();                            // the next load is a whole warp's
       }
       if (qrow < p.S) p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.S + qrow] = (m + log2f(l)) * LN2_F;
     } else {
@@ -694,6 +695,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_fwd_tc_persist_kernel(const __g
             *reinterpret_cast<uint4*>(orow + c * 32 + e) = w;
           }
         }
+        __syncwarp();                            // the next load is a whole warp's
       }
       tc_fence_before();
       __syncwarp();
@@ -1237,6 +1239,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) fa_bwd_dkdv_tc_kernel(const __
         tmem_ld_cols<32>(tmem_row + c, lo);
         tmem_ld_cols<32>(tmem_row + 64 + c, hi);
         if (orow) dkdv_store_row<32>(orow, c, lo, hi, is_k, p.scale, cs);
+        __syncwarp();                            // the next load is a whole warp's
       }
     }
   } else {
@@ -1569,6 +1572,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) fa_bwd_dq_tc_kernel(const __gr
                 make_float4(__uint_as_float(v[e]) * p.scale, __uint_as_float(v[e + 1]) * p.scale,
                             __uint_as_float(v[e + 2]) * p.scale, __uint_as_float(v[e + 3]) * p.scale);
         }
+        __syncwarp();                            // the next load is a whole warp's
       }
     } else {
       *abort_flag = 1;

@@ -913,6 +913,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) gemm_bf16_tcp_kernel(const __
           } else if (row < pr.M) {
             store_swiglu(pr, row, col0, vg, vu);
           }
+          __syncwarp();   // the next load is a whole warp's
         }
       } else if (pr.epi == GEMM_EPI_ROPE) {
         // two heads of 128 columns; plane i pairs column i with i + 64 of its head
@@ -941,6 +942,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) gemm_bf16_tcp_kernel(const __
             } else if (row < pr.M) {
               store_rope(pr, row, colA, va, vb, cs + 32 * c);
             }
+            __syncwarp();   // the next load is a whole warp's
           }
         }
       } else {
@@ -996,6 +998,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) gemm_bf16_tcp_kernel(const __
               dot = 0.f;
             }
           }
+          __syncwarp();   // the next load is a whole warp's
         }
       }
       tc_fence_before();

@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(SK_THREADS, 1) gemm_skinny_kernel(const __grid
               pu[q4 * SK_BN] = make_float4(uu[4 * q4], uu[4 * q4 + 1], uu[4 * q4 + 2], uu[4 * q4 + 3]);
           }
         }
+        __syncwarp();   // the next load is a whole warp's
       }
       tc_fence_before();
       __syncwarp();
@@ -407,6 +408,7 @@ __global__ void __launch_bounds__(SK_THREADS, 1) gemm_skinny_kernel(const __grid
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem_base, tmem_cols);
   }

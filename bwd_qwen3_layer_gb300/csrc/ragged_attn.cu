@@ -847,8 +847,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
           uint32_t v[32];
           tmem_ld_32x32b_x32(oadr + h * 32, v);
           tmem_ld_wait();
-          if (!mine) continue;
-          if (whole) {
+          if (mine && whole) {
             // whole 32-byte sectors: rows lie apart, and an SM writes ~0.7 sectors a
             // cycle whether they are full or not (16-byte stores took twice as long)
             __nv_bfloat16* orow_p = p.o + orow * RA_D + h * 32;
@@ -860,12 +859,13 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
                 x[i] = pack_bf16x2(__uint_as_float(v[e + 2 * i]) * inv, __uint_as_float(v[e + 2 * i + 1]) * inv);
               ra_st32(orow_p + e, x);
             }
-          } else {
+          } else if (mine) {
             float* po = p.part_o + (pslot * RA_D + h * 32) * RA_BQ + r * 4;      // lanes side by side
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
               *reinterpret_cast<uint4*>(po + e * RA_BQ) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
           }
+          __syncwarp();                            // the next load is a whole warp's
         }
         if (mine) {
           if (whole) {
