@@ -920,7 +920,9 @@ __global__ void __launch_bounds__(RC_THREADS, 5) ragged_combine_kernel(const __g
 #pragma unroll
     for (int e = 0; e < RC_COLS; ++e) a[e] = 0.f;
     auto add = [&](float m2, float l2, const float (&v)[RC_COLS]) {
-      if (!(m2 > -INFINITY)) return;               // a piece whose keys this row does not see
+      // A piece whose keys this row does not see has the sum 0. Not the maximum: that of
+      // scores which are all NaN is -inf too (max drops NaN), and their sum is NaN.
+      if (l2 == 0.f) return;
       const float m_new = fmaxf(M, m2), f0 = exp2f(M - m_new), f = exp2f(m2 - m_new);
       M = m_new;
       l = fmaf(l2, f, l * f0);

@@ -1,0 +1,57 @@
+"""NaN in queries, keys and values of the paged cache: where a row sees one its result is NaN, whether one CTA held the
+row's keys or several did."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_ragged import D, _bf, _dev, _i, _step
+
+pytestmark = pytest.mark.gpu
+
+
+def _attention(kl, Hq, Hkv, bs, shape, q, kp, vp, table, cu, ctx):
+    maxb, nb = shape
+    rc = kl.RaggedCfg(len(ctx), q.shape[0], bs, maxb, nb)
+    ws = torch.empty(kl.kl_ragged_attention_ws_bytes(rc, Hq, Hkv, D), dtype=torch.uint8, device="cuda")
+    o, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device="cuda")
+    kl.kl_ragged_attention(rc, Hq, Hkv, D, kl.KL_BF16, q.data_ptr(), kp.data_ptr(), vp.data_ptr(), table.data_ptr(), cu.data_ptr(), ctx.data_ptr(),
+                           o.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel())
+    assert kl.kl_device_status() == 0
+    return o, lse
+
+
+def _case(seed, reqs, Hq, Hkv, bs):
+    rng, n, ctx, table, maxb, nb, kp, vp, cu, T = _step(seed, reqs, Hkv, bs)
+    slot = lambda b, p: (int(table[b, p // bs]), p % bs)  # noqa: E731
+    return (maxb, nb), _dev(_bf(rng, T, Hq, D)), _dev(kp), _dev(vp), _i(table), _i(cu), _i(ctx), slot
+
+
+@pytest.mark.parametrize("Hq,Hkv,reqs,row", [
+    (8, 1, [(1, 20000)], 0),                       # cut into many pieces
+    (64, 8, [(3, 3000), (1, 500)], 2),
+    (8, 2, [(1, 20)] * 400, 77),                   # items held whole
+])
+def test_a_query_of_nan_gives_nan(kl, Hq, Hkv, reqs, row):
+    shape, q, kp, vp, table, cu, ctx, _ = _case(1, reqs, Hq, Hkv, 16)
+    want, want_lse = _attention(kl, Hq, Hkv, 16, shape, q, kp, vp, table, cu, ctx)
+    assert torch.isfinite(want).all() and torch.isfinite(want_lse).all()
+    q[row, 1, 5] = float("nan")
+    o, lse = _attention(kl, Hq, Hkv, 16, shape, q, kp, vp, table, cu, ctx)
+    assert torch.isnan(o[row, 1]).all() and torch.isnan(lse[row, 1])
+    want[row, 1], want_lse[row, 1] = o[row, 1], lse[row, 1]
+    keep = torch.ones_like(lse, dtype=torch.bool)
+    keep[row, 1] = False
+    assert torch.equal(o[keep], want[keep]) and torch.equal(lse[keep], want_lse[keep])
+
+
+@pytest.mark.parametrize("bs", [16, 5])
+@pytest.mark.parametrize("cached", [128 * 160, 128 * 2, 0])
+def test_a_key_of_nan_gives_nan(kl, cached, bs):
+    """The request's own key, alone in its last key tile (for the longest: alone in a piece)."""
+    Hq, Hkv = 8, 1
+    shape, q, kp, vp, table, cu, ctx, slot = _case(2, [(1, cached), (1, 40)], Hq, Hkv, bs)
+    want, _ = _attention(kl, Hq, Hkv, bs, shape, q, kp, vp, table, cu, ctx)
+    kp[slot(0, cached)][0, 3] = float("nan")
+    o, lse = _attention(kl, Hq, Hkv, bs, shape, q, kp, vp, table, cu, ctx)
+    assert torch.isnan(o[0]).all() and torch.isnan(lse[0]).all()
+    assert torch.equal(o[1], want[1])
