@@ -261,8 +261,10 @@ __global__ void __launch_bounds__(PA_THREADS, 2) paged_attn_kernel(const __grid_
       Lt[h] = 0.f;
 #pragma unroll
       for (int w = 0; w < PA_WARPS; ++w) {
-        const float mw = mlbuf[(w * PA_MR + rr) * 2];
-        if (mw > -INFINITY) Lt[h] += mlbuf[(w * PA_MR + rr) * 2 + 1] * exp2f(mw - M[h]);
+        // a warp whose keys the row does not see has the sum 0; one whose scores are
+        // all NaN has the maximum -inf too (max drops NaN), and its sum is NaN
+        const float mw = mlbuf[(w * PA_MR + rr) * 2], lw = mlbuf[(w * PA_MR + rr) * 2 + 1];
+        if (lw != 0.f) Lt[h] += lw * exp2f(mw - M[h]);
       }
       f[h] = mrow[h] > -INFINITY ? exp2f(mrow[h] - M[h]) : 0.f;
     }
@@ -408,19 +410,17 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
   float M = -INFINITY;
   for (int s = 0; s < np; ++s) M = fmaxf(M, p.part_ml[(base + s * PA_MR) * 2]);
   float Lsum = 0.f, a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-  if (M > -INFINITY) {
-    for (int s = 0; s < np; ++s) {
-      const int64_t pc = base + s * PA_MR;
-      const float ms = p.part_ml[pc * 2];
-      if (!(ms > -INFINITY)) continue;
-      const float f = exp2f(ms - M);
-      Lsum += p.part_ml[pc * 2 + 1] * f;
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + pc * PA_D + lane * 4);
-      a0 = fmaf(v.x, f, a0);
-      a1 = fmaf(v.y, f, a1);
-      a2 = fmaf(v.z, f, a2);
-      a3 = fmaf(v.w, f, a3);
-    }
+  for (int s = 0; s < np; ++s) {
+    const int64_t pc = base + s * PA_MR;
+    const float ms = p.part_ml[pc * 2], ls = p.part_ml[pc * 2 + 1];
+    if (ls == 0.f) continue;                       // no key of this piece is visible (as in finish: by the sum)
+    const float f = exp2f(ms - M);
+    Lsum += ls * f;
+    const float4 v = *reinterpret_cast<const float4*>(p.part_o + pc * PA_D + lane * 4);
+    a0 = fmaf(v.x, f, a0);
+    a1 = fmaf(v.y, f, a1);
+    a2 = fmaf(v.z, f, a2);
+    a3 = fmaf(v.w, f, a3);
   }
   const float inv = Lsum > 0.f ? 1.f / Lsum : 0.f;
   const int it = r / p.G, head = g * p.G + (r - it * p.G);

@@ -55,3 +55,40 @@ def test_a_key_of_nan_gives_nan(kl, cached, bs):
     o, lse = _attention(kl, Hq, Hkv, bs, shape, q, kp, vp, table, cu, ctx)
     assert torch.isnan(o[0]).all() and torch.isnan(lse[0]).all()
     assert torch.equal(o[1], want[1])
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,n_new,ctx", [
+    (1, 64, 8, 1, 2000),          # context split over CTAs
+    (40, 64, 8, 1, 700),          # some items whole, some cut
+    (64, 8, 1, 1, 40),
+    (3, 12, 4, 3, 190),
+])
+def test_a_query_or_key_of_nan_in_the_uniform_step(kl, B, Hq, Hkv, n_new, ctx):
+    bs = 16
+    shape, q, kp, vp, table, cu, ctxd, slot = _case(5, [(n_new, ctx)] * B, Hq, Hkv, bs)
+    kp, vp = torch.nan_to_num(kp), torch.nan_to_num(vp)
+    table = table.clamp(max=shape[1] - 1)
+    pc = kl.PagedCfg(B, n_new, bs, *shape)
+    ws = torch.empty(max(256, kl.kl_paged_attention_ws_bytes(pc, Hq, Hkv, D)), dtype=torch.uint8, device="cuda")
+
+    def call():
+        o, lse = torch.zeros_like(q), torch.zeros(B, Hq, n_new, device="cuda")
+        kl.kl_paged_attention(pc, Hq, Hkv, D, kl.KL_BF16, q.data_ptr(), kp.data_ptr(), vp.data_ptr(), table.data_ptr(), ctxd.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                              ws.data_ptr(), ws.numel())
+        assert kl.kl_device_status() == 0
+        return o.view(B, n_new, Hq, D), lse
+
+    want, want_lse = call()
+    for b in range(0, B, 7):                       # every seventh sequence has a NaN query in head 1 of its last token
+        q.view(B, n_new, Hq, D)[b, -1, 1, 5] = float("nan")
+    o, lse = call()
+    keep = torch.ones(B, n_new, Hq, dtype=torch.bool, device="cuda")
+    keep[::7, -1, 1] = False
+    assert torch.isnan(o[~keep]).all() and torch.isnan(lse.transpose(1, 2)[~keep]).all()
+    assert torch.equal(o[keep], want[keep]) and torch.equal(lse.transpose(1, 2)[keep], want_lse.transpose(1, 2)[keep])
+    # a NaN in the last key: every head of its kv head in the last token
+    q.copy_(torch.nan_to_num(q))
+    kp[slot(B - 1, ctx + n_new - 1)][0, 3] = float("nan")
+    o, lse = call()
+    G = Hq // Hkv
+    assert torch.isnan(o[B - 1, -1, :G]).all() and torch.isnan(lse[B - 1, :G, -1]).all()
