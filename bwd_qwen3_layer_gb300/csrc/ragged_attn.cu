@@ -34,9 +34,9 @@
 // box = gcd(block_size, 128) rows, each found through the table; a box past the
 // context, past its table row or whose table entry lies outside the pool starts
 // past the tensor's last row and is filled with zeros by the copy. Other block
-// sizes gather row by row with 16-byte cp.async. Slots behind a context's end
-// may hold anything (NaN too): their scores are masked, and the last tile's
-// value rows behind the end are zeroed before the product reads them.
+// sizes gather row by row with 16-byte cp.async. Slots behind the last position
+// that a query tile sees may hold anything (NaN too): their scores are masked,
+// and the last tile's value rows behind it are zeroed before the product reads them.
 //
 // Measured (64 / 8 heads, pages of 16): 64 requests of ~4096 keys 168-172 us, 0.92
 // to 0.95 of the HBM copy rate; one of 32768 keys 30; 4096 rows over 12288 keys 1161 us in a
@@ -260,7 +260,7 @@ __device__ __noinline__ long long ra_div(long long a, long long b) {
 struct RaPiece {
   int b, g;                // request, kv head
   int row0, toks;          // the tile's first row of the step, its tokens
-  int pos0, L;             // position of its first token; keys of the request
+  int pos0, L;             // position of its first token; keys that its last one sees
   int ta, tb;              // key tiles; tb = 0: there is no such piece
   int flags;               // 1: all of the item's tiles; 2: the piece goes to slot 1
 };
@@ -288,7 +288,7 @@ __device__ __forceinline__ void ra_step(const RaLens& p, RaWalk& w, RaPiece& c) 
     c.row0 = w.q.r0 + first;
     c.toks = min(p.TQ, w.q.n - first);
     c.pos0 = w.q.ctx + first;
-    c.L = w.q.ctx + w.q.n;
+    c.L = c.pos0 + c.toks;
     c.flags = (c.ta == 0 && c.tb == tiles ? 1 : 0) | (w.idx > 0 ? 2 : 0);
     w.left -= e - off;
     ++w.idx;
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     const int r = quarter * 32 + lane;           // row within the tile = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t oadr = tmO + lane_off, padr = tmP + lane_off;
-    // The tile that holds the context's end: its value rows behind it become zero
+    // The tile that holds the last key the query tile sees: its value rows behind it become zero
     // (each of the four warps its 32).
     auto clear_tail = [&](int end, int n) -> bool {
       if (end >= RA_BKV) return true;
@@ -700,7 +700,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
     const float scale = p.scale_log2;
     int n = 0;
     float m = -INFINITY, l = 0.f;                  // the row's running max (log2 units) and sum
-    int lim = 0, end = 0;                          // the row's last key and the context's end, from the tile's first key
+    int lim = 0, end = 0;                          // the row's last key and the end of the query tile's, from the tile's first key
     // One step of a warp with rows. CUT: some row of the tile ends inside its keys.
     // The whole tiles before have a body of their own, without what that takes
     // (tests and masks cost them ~180 cycles a step).

@@ -534,8 +534,11 @@ KL_API kl_status kl_ragged_qkv_rope(const kl_ragged_cfg* rc, int32_t Hq, int32_t
  * its table row, or whose table entry lies outside the pool, reads as a zero key
  * and value and is reported (KL_DEVERR_PAGE). The workspace (256-byte aligned,
  * for the current device's SM count) does not depend on the lengths; steps that
- * may run at the same time need one each. A NaN or an infinity at a position
- * that a row does not see can reach it when other rows of its tile do see it.
+ * may run at the same time need one each. A NaN or an infinity in a value at a
+ * position that a row does not see reaches it only when a later row of its query
+ * tile sees it (tiles of floor(128 / (Hq / Hkv)) consecutive new tokens of a
+ * request, from its first on). A NaN in a query, or in a key that a row sees,
+ * makes the row's o and lse NaN.
  * o (32-byte aligned) and lse must not overlap the inputs. */
 KL_API size_t kl_ragged_attention_ws_bytes(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d);
 KL_API kl_status kl_ragged_attention(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,

@@ -1,5 +1,5 @@
 """NaN in queries, keys and values of the paged cache: where a row sees one its result is NaN, whether one CTA held the
-row's keys or several did."""
+row's keys or several did, and a later token's does not reach the query tiles that do not see it."""
 import numpy as np
 import pytest
 import torch
@@ -55,6 +55,36 @@ def test_a_key_of_nan_gives_nan(kl, cached, bs):
     o, lse = _attention(kl, Hq, Hkv, bs, shape, q, kp, vp, table, cu, ctx)
     assert torch.isnan(o[0]).all() and torch.isnan(lse[0]).all()
     assert torch.equal(o[1], want[1])
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("bs", [16, 5, 128])
+@pytest.mark.parametrize("Hq,Hkv,n,cached,at", [(64, 8, 200, 0, 100), (64, 8, 200, 77, 150), (8, 8, 300, 0, 250), (4, 1, 130, 1000, 40)])
+def test_a_later_value_stays_with_the_query_tiles_that_see_it(kl, Hq, Hkv, n, cached, at, bs, value):
+    """Query tiles are 128 / (Hq / Hkv) tokens. Tiles that end before the new token `at` keep their bits; the tokens from it
+    on get what the formula gives."""
+    shape, q, kp, vp, table, cu, ctx, slot = _case(3, [(n, cached), (1, 40)], Hq, Hkv, bs)
+    want, _ = _attention(kl, Hq, Hkv, bs, shape, q, kp, vp, table, cu, ctx)
+    vp[slot(0, cached + at)][0, 3] = value
+    o, _ = _attention(kl, Hq, Hkv, bs, shape, q, kp, vp, table, cu, ctx)
+    G = Hq // Hkv
+    before = at // (128 // G) * (128 // G)
+    assert torch.equal(o[:before], want[:before])
+    assert torch.equal(o[n], want[n])
+    assert not torch.isfinite(o[at:n, :G, 3]).any()
+    others = torch.arange(D, device="cuda") != 3
+    assert torch.equal(o[at:][..., others], want[at:][..., others])
+
+
+@pytest.mark.parametrize("bs", [16, 5])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_a_later_key_reaches_no_earlier_token(kl, bs, value):
+    Hq, Hkv, n, at = 64, 8, 200, 100
+    shape, q, kp, vp, table, cu, ctx, slot = _case(4, [(n, 30)], Hq, Hkv, bs)
+    want, _ = _attention(kl, Hq, Hkv, bs, shape, q, kp, vp, table, cu, ctx)
+    kp[slot(0, 30 + at)][:, 3] = value
+    o, _ = _attention(kl, Hq, Hkv, bs, shape, q, kp, vp, table, cu, ctx)
+    assert torch.equal(o[:at], want[:at])
 
 
 @pytest.mark.parametrize("B,Hq,Hkv,n_new,ctx", [
