@@ -15,11 +15,16 @@
 //
 // An index must not depend on how a sum is split, so sums are held far beyond
 // the weights' own precision: p - q as an error-free pair of floats (two-sum,
-// Knuth), sums, prefix sums and comparisons in such pairs (about 48 bits). fp64
+// Knuth), sums, prefix sums and comparisons in such pairs, a lane's running sum in
+// three floats. The error of a sum, relative to it, whatever V is: a lane's 4 to 32
+// elements are added as a tree of at most 5 levels, whose roundings (each at most
+// 2^-24 of itself) come to 30 x 2^-48 at most; joining such groups loses below
+// 2^-60 of them; the joins of lanes, warps and CTAs are 16 additions of pairs, 2^-46
+// each. Below 2^-41 in all, some 2^-47 as a rule. fp64
 // is slow on this part (an addition takes 63 cycles, an SM starts two a cycle):
 // with every thread's sums in it 64 requests of 151936 classes took 82 us, with
-// the warps' prefix sums alone 26, without it 17.6. The acceptance test is exact:
-// the product of two floats fits a double.
+// the warps' prefix sums alone 26, without it 19 (rows in L2; 21.4 where they are
+// not). The acceptance test is exact: the product of two floats fits a double.
 #include "internal.h"
 #include "kl_common.cuh"
 
@@ -27,12 +32,17 @@ namespace kl {
 namespace {
 
 // CTAs per request (one cluster) and warps per CTA, by how many clusters are
-// resident together (V = 151936, p and q in fp32):
-//   up to 7 requests   16 CTAs of 16 warps, an SM each: 7.1 us; eight of them 8.1;
-//                      from 8 requests on they take two rounds (8: 11.3)
-//   up to 14           8 of 16 warps: 8.3 to 8.6 us, 8 of 8 warps 9.8 to 11.3;
-//                      16 requests take two rounds (12.5)
-//   more               8 of 8 warps, four CTAs per SM: 16 requests 11.1 us, 64 17.0
+// resident together (V = 151936, p and q in fp32 and in L2; rows that are not in it
+// after the stroke):
+//   up to 7 requests   16 CTAs of 16 warps, an SM each: one 7.1 us / 6.9, seven 7.3 /
+//                      9.2; eight CTAs for one 8.1; from 8 requests on they take two
+//                      rounds (8: 11.3)
+//   up to 14           8 of 16 warps: 8.5 to 8.6 us / 10.8 to 11.3, 8 of 8 warps 9.8
+//                      to 11.3; 16 requests take two rounds (12.5)
+//   more               8 of 8 warps, four CTAs per SM: 16 requests 11.1 us / 14.8, 64
+//                      19.2 / 21.4, 128 34 / 35.5
+// With 5000 classes all splits lie close: 5.8 to 6.3 us for 1 to 16 requests in fp32
+// (6.5 to 6.9 in bf16), 7.2 for 64.
 constexpr int DV_CL = 8, DV_CL_FEW = 16;
 constexpr int DV_WARPS_MANY = 8, DV_WARPS_FEW = 16;
 constexpr int DV_FEW = 7, DV_SOME = 14;
@@ -87,21 +97,49 @@ __device__ __forceinline__ void dv_load(const T* row, int64_t i, int V, float (&
 // A number as an unevaluated pair of floats, hi + lo (about 48 bits).
 struct Pair {
   float hi, lo;
-  __device__ __forceinline__ void add(float x) {
-    const float s = hi + x, b = s - hi;
-    lo += (hi - (s - b)) + (x - b);
-    hi = s;
-  }
 };
+// a + b, and its rounding error
+__device__ __forceinline__ Pair dv_two_sum(float a, float b) {
+  const float s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
 __device__ __forceinline__ Pair dv_norm(Pair v) {   // |lo| at most half a step of hi
   const float s = v.hi + v.lo;
   return {s, v.lo - (s - v.hi)};
 }
-__device__ __forceinline__ Pair dv_plus(Pair a, Pair b) {
-  a.add(b.hi);
-  a.lo += b.lo;
-  return dv_norm(a);
+__device__ __forceinline__ Pair dv_join(Pair a, Pair b) {   // not normed
+  const Pair s = dv_two_sum(a.hi, b.hi);
+  return {s.hi, s.lo + (a.lo + b.lo)};
 }
+__device__ __forceinline__ Pair dv_plus(Pair a, Pair b) { return dv_norm(dv_join(a, b)); }
+// The sum of N pairs (N a power of two) as a tree: an error that is added up one by
+// one grows with the square of their number, one of a tree with that of its levels.
+template <int N>
+__device__ __forceinline__ Pair dv_tree(const Pair (&v)[N]) {
+  if constexpr (N == 1) {
+    return v[0];
+  } else {
+    Pair half[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) half[i] = dv_join(v[2 * i], v[2 * i + 1]);
+    return dv_tree<N / 2>(half);
+  }
+}
+// A running sum of pairs: the errors' sum has an error term of its own, so that its
+// precision does not depend on how many are added.
+struct Sum {
+  float hi = 0.f, lo = 0.f, rest = 0.f;
+  __device__ __forceinline__ void add(Pair v) {
+    const Pair a = dv_two_sum(hi, v.hi), b = dv_two_sum(lo, a.lo), c = dv_two_sum(b.hi, v.lo);
+    hi = a.hi;
+    lo = c.hi;
+    rest += b.lo + c.lo;
+  }
+  __device__ __forceinline__ Pair value() const {
+    const Pair s = dv_norm({hi, lo});
+    return dv_norm({s.hi, s.lo + rest});
+  }
+};
 // a > b for normed pairs: where the leading parts are close their difference is
 // exact, and where they are not it decides.
 __device__ __forceinline__ bool dv_above(Pair a, Pair b) { return (a.hi - b.hi) + (a.lo - b.lo) > 0.f; }
@@ -188,14 +226,11 @@ struct DvRow {
 };
 
 template <typename T, int E, int KIND>
-__device__ __forceinline__ void dv_add(const DvRow<T>& r, int64_t col, const float (&fp)[E], const float (&fq)[E], Pair& sum) {
+__device__ __forceinline__ Pair dv_vector(const DvRow<T>& r, int64_t col, const float (&fp)[E], const float (&fq)[E]) {
+  Pair v[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    float w, we;
-    dv_weight(KIND, fp[e], fq[e], col + e, r.draft, w, we);
-    sum.add(w);
-    if (KIND == DV_REST) sum.lo += we;
-  }
+  for (int e = 0; e < E; ++e) dv_weight(KIND, fp[e], fq[e], col + e, r.draft, v[e].hi, v[e].lo);
+  return dv_tree<E>(v);
 }
 
 // Sum of the warp's vectors j0 .. j1 - 1, lane by lane: the whole ones four at a
@@ -206,13 +241,13 @@ __device__ __forceinline__ Pair dv_sum_kind(const DvRow<T>& r, int j0, int j1) {
   const int lane = threadIdx.x & 31;
   const int lo = max(j0, r.mis ? 1 : 0);
   const int hi = min(j1, static_cast<int>((static_cast<int64_t>(r.V) + r.mis) / E));
-  Pair sum = {0.f, 0.f};
+  Sum sum;
   auto one = [&](int j) {
     const int64_t col = static_cast<int64_t>(j) * E - r.mis;
     float fp[E], fq[E] = {};
     dv_load<T, E>(r.p, col, r.V, fp);
     if (KIND == DV_REST) dv_load<T, E>(r.q, col, r.V, fq);
-    dv_add<T, E, KIND>(r, col, fp, fq, sum);
+    sum.add(dv_vector<T, E, KIND>(r, col, fp, fq));
   };
   int j = lo + lane;
   for (; j + 32 * (U - 1) < hi; j += 32 * U) {
@@ -223,13 +258,15 @@ __device__ __forceinline__ Pair dv_sum_kind(const DvRow<T>& r, int j0, int j1) {
       dv_load_whole<T, E>(r.p + col, fp[u]);
       if (KIND == DV_REST) dv_load_whole<T, E>(r.q + col, fq[u]);
     }
+    Pair v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) dv_add<T, E, KIND>(r, static_cast<int64_t>(j + 32 * u) * E - r.mis, fp[u], fq[u], sum);
+    for (int u = 0; u < U; ++u) v[u] = dv_vector<T, E, KIND>(r, static_cast<int64_t>(j + 32 * u) * E - r.mis, fp[u], fq[u]);
+    sum.add(dv_tree<U>(v));
   }
   for (; j < hi; j += 32) one(j);
   if (lane == 0 && j0 < lo && j0 < j1) one(j0);
   if (lane == 31 && j1 > hi && j1 - 1 >= lo) one(j1 - 1);
-  return dv_warp_sum(sum);
+  return dv_warp_sum(sum.value());
 }
 template <typename T, int E>
 __device__ __forceinline__ Pair dv_sum(const DvRow<T>& r, int kind, int j0, int j1) {
@@ -307,38 +344,35 @@ __device__ __forceinline__ void dv_request(const VerifyParams& p, VerifySmem& s,
     if (lane == 0) s.parts[warp] = again;
     __syncthreads();
     const Pair x = s.x;
-    Pair before = s.before;
+    Pair front = s.before;
     const Pair stretch = lane < WARPS ? s.parts[lane] : Pair{0.f, 0.f};
-    const int pw = max(0, dv_cross(stretch, dv_warp_scan<WARPS>(stretch, lane), lane, x, before));
+    const int pw = max(0, dv_cross(stretch, dv_warp_scan<WARPS>(stretch, lane), lane, x, front));
     if (warp != pw) return;
     // this warp's piece in order, 32 vectors at a time
     int64_t found = -1, last = -1;
+    Sum upto_here;
+    upto_here.add(front);
     for (int j0 = p0; j0 < p1 && found < 0; j0 += 32) {
       const int j = j0 + lane;
       const int64_t col = static_cast<int64_t>(j) * E - row.mis;
-      float w[E], we[E];
-      Pair own = {0.f, 0.f};
+      Pair w[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) w[e] = we[e] = 0.f;
+      for (int e = 0; e < E; ++e) w[e] = {0.f, 0.f};
       if (j < p1) {
         float fp[E], fq[E] = {};
         dv_load<T, E>(row.p, col, p.V, fp);
         if (kind == DV_REST) dv_load<T, E>(row.q, col, p.V, fq);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          dv_weight(kind, fp[e], fq[e], col + e, row.draft, w[e], we[e]);
-          own.add(w[e]);
-          own.lo += we[e];
-        }
+        for (int e = 0; e < E; ++e) dv_weight(kind, fp[e], fq[e], col + e, row.draft, w[e].hi, w[e].lo);
       }
-      const Pair incl = dv_warp_scan<32>(dv_norm(own), lane);
+      const Pair incl = dv_warp_scan<32>(dv_norm(dv_tree<E>(w)), lane), before = upto_here.value();
       Pair at = {__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
       at = lane ? dv_plus(before, at) : before;      // everything in front of this lane's vector
       int64_t hit = -1, pos = -1;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        at = dv_plus(at, {w[e], we[e]});
-        if (w[e] > 0.f) {
+        at = dv_plus(at, w[e]);
+        if (w[e].hi > 0.f) {
           pos = col + e;
           if (hit < 0 && dv_above(at, x)) hit = col + e;
         }
@@ -346,7 +380,7 @@ __device__ __forceinline__ void dv_request(const VerifyParams& p, VerifySmem& s,
       const unsigned hits = __ballot_sync(0xffffffffu, hit >= 0), any = __ballot_sync(0xffffffffu, pos >= 0);
       if (hits) found = __shfl_sync(0xffffffffu, hit, __ffs(hits) - 1);
       if (any) last = __shfl_sync(0xffffffffu, pos, 31 - __clz(any));
-      before = dv_plus(before, dv_shfl(incl, 31));
+      upto_here.add(dv_shfl(incl, 31));
     }
     if (lane == 0) {
       p.acc[b] = accepted;

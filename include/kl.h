@@ -564,8 +564,10 @@ KL_API kl_status kl_ragged_attention(const kl_ragged_cfg* rc, int32_t Hq, int32_
  * positive or their sum is not finite in fp32. A request without rows gets 0 and
  * -1. A draft outside [0, V) is not accepted and reported (KL_DEVERR_TARGET).
  * B and T at most 2^24, V at most 2^30.
- * Products and sums are held to 48 bits or more. All on the device, p and q of
- * type dtype (fp32 or bf16). One launch, no workspace. */
+ * The acceptance test is exact; sums, their products with u_sample and the
+ * comparisons between them are off by less than 2^-41 of the sum, whatever V and
+ * the batch are. All on the device, p and q of type dtype (fp32 or bf16). One
+ * launch, no workspace. */
 typedef struct kl_verify_cfg {
   int32_t B;        /* requests                                              */
   int32_t T;        /* rows of p, q, tokens and u_accept                     */
