@@ -510,7 +510,15 @@ typedef struct kl_ragged_cfg {
  * entries become -1 and the blocks it lacks count in *missing. Then the blocks
  * of ended requests are appended to the list, in request order and table order.
  * Rows beyond T are dropped (KL_DEVERR_ROWS); a position past its table row
- * has slot -1 (KL_DEVERR_PAGE). */
+ * has slot -1 (KL_DEVERR_PAGE).
+ * A pool that runs short is no error of this call and leaves a consistent state:
+ * a request that could not have its blocks is asked for again, with the same ctx
+ * and tokens, once blocks have come back. Its rows are in this step all the same:
+ * kl_ragged_attention (and the layer) reads the blocks that are not there as zero
+ * keys and values and reports KL_DEVERR_PAGE, which after a step with *missing
+ * above zero says no more than that. Results of such a request's rows from its
+ * first slot of -1 on mean nothing; its rows before and the other requests are
+ * right. */
 KL_API kl_status kl_ragged_plan(const kl_ragged_cfg* rc, const int32_t* n_new, const int32_t* ctx, int32_t* table,
                                 int32_t* held, int32_t* free_list, int32_t* n_free, int32_t* cu_rows, int32_t* pos,
                                 int32_t* slots, int32_t* missing, void* stream);
