@@ -189,18 +189,23 @@ def version() -> str:
     return load().kl_version().decode()
 
 
-_torch = None
+_current_stream = None
 
 
 def _stream(stream) -> int:
-    global _torch
+    global _current_stream
     if stream is None:
-        if _torch is None:
+        if _current_stream is None:
             import torch
             torch.cuda.current_stream()      # initialises CUDA, or says why it cannot
-            _torch = torch
-        # the handle alone: building torch's Stream object around it takes ~3 us a call
-        return _torch._C._cuda_getCurrentRawStream(_torch.cuda.current_device())
+            # the handle alone: building torch's Stream object around it takes ~3 us a call. The function that gives
+            # it is not a public one; where a torch lacks it, the object it is.
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            if raw is None:
+                _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+            else:
+                _current_stream = lambda: raw(torch.cuda.current_device())  # noqa: E731
+        return _current_stream()
     return int(getattr(stream, "cuda_stream", stream))
 
 
