@@ -38,11 +38,12 @@
 // that a query tile sees may hold anything (NaN too): their scores are masked,
 // and the last tile's value rows behind it are zeroed before the product reads them.
 //
-// Measured (64 / 8 heads, pages of 16): 64 requests of ~4096 keys 168-172 us, 0.92
-// to 0.95 of the HBM copy rate; one of 32768 keys 30; 4096 rows over 12288 keys 1161 us in a
-// burst, 0.86 of the burst tensor rate: a step is ~1440 cycles, of which the
-// products take 1024 and shared memory's 160 KB (products' reads, copies' writes)
-// 1250. Two warpgroups of softmax in turn (168 registers) gained 3 % there and
+// Measured (64 / 8 heads, pages of 16): 64 requests of ~4096 keys 164-172 us, 0.92
+// to 0.97 of the HBM copy rate; one of 32768 keys 30; 4096 rows over 12288 keys 1161-1180 us
+// in a burst, 0.85 of the burst tensor rate, 1290-1344 back to back under the power cap. Pages
+// of five, which go row by row: 321, 50 and 4053 us. The chunk's step is ~1440 cycles, of
+// which the products take 1024 and shared memory's 160 KB (products' reads, copies'
+// writes) 1250. Two warpgroups of softmax in turn (168 registers) gained 3 % there and
 // lost 4 to 14 % everywhere else.
 #include <cudaTypedefs.h>
 #include <math.h>

@@ -447,7 +447,9 @@ KL_API size_t kl_paged_attention_ws_bytes(const kl_paged_cfg* pc, int32_t Hq, in
  * the new tokens' keys and values must already be written. Query i of
  * sequence b sees keys at positions <= ctx[b] + i; scale 1/sqrt(d); query
  * head h reads kv head floor(h * Hkv / Hq). o [B*n_new, Hq*d] device; lse
- * [B, Hq, n_new] fp32 device (natural log) or NULL. */
+ * [B, Hq, n_new] fp32 device (natural log) or NULL. A NaN in a query, or in a
+ * key that a row sees, makes the row's o and lse NaN; one (or an infinity) in a
+ * new token's value can reach the earlier new tokens of its sequence. */
 KL_API kl_status kl_paged_attention(const kl_paged_cfg* pc, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
                                     const void* q, const void* k_pool, const void* v_pool,
                                     const int32_t* table, const int32_t* ctx, void* o, float* lse,
@@ -526,7 +528,8 @@ KL_API kl_status kl_ragged_plan(const kl_ragged_cfg* rc, const int32_t* n_new, c
  * gamma_k [d] (both NULL: no norm), then the rotation at position pos[row] with
  * planes (i, i + d/2) or, rope_interleaved, (2i, 2i + 1). q goes to q_out (may
  * be q_pre), k and the unchanged v to slot slots[row] of the pools, all in one
- * launch. q_pre, q_out [T, Hq*d], k_pre, v [T, Hkv*d]; rope_base at least 1. A
+ * launch. (All T rows of q_pre, k_pre and v are read, whatever they hold: room for
+ * many more rows than a step has costs their traffic.) q_pre, q_out [T, Hq*d], k_pre, v [T, Hkv*d]; rope_base at least 1. A
  * row whose slot is below zero leaves the pools alone; a slot past the pool is
  * skipped and reported (KL_DEVERR_PAGE). Two rows must not have the same slot. */
 KL_API kl_status kl_ragged_qkv_rope(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
