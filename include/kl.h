@@ -529,9 +529,10 @@ KL_API kl_status kl_ragged_plan(const kl_ragged_cfg* rc, const int32_t* n_new, c
  * planes (i, i + d/2) or, rope_interleaved, (2i, 2i + 1). q goes to q_out (may
  * be q_pre), k and the unchanged v to slot slots[row] of the pools, all in one
  * launch. (All T rows of q_pre, k_pre and v are read, whatever they hold: room for
- * many more rows than a step has costs their traffic.) q_pre, q_out [T, Hq*d], k_pre, v [T, Hkv*d]; rope_base at least 1. A
- * row whose slot is below zero leaves the pools alone; a slot past the pool is
- * skipped and reported (KL_DEVERR_PAGE). Two rows must not have the same slot. */
+ * many more rows than a step has costs their traffic.) q_pre, q_out [T, Hq*d],
+ * k_pre, v [T, Hkv*d]; rope_base at least 1. A row whose slot is below zero
+ * leaves the pools alone; a slot past the pool is skipped and reported
+ * (KL_DEVERR_PAGE). Two rows must not have the same slot. */
 KL_API kl_status kl_ragged_qkv_rope(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
                                     const void* q_pre, const void* k_pre, const void* v, const void* gamma_q,
                                     const void* gamma_k, float eps, float rope_base, int32_t rope_interleaved,
@@ -576,8 +577,8 @@ KL_API kl_status kl_ragged_attention(const kl_ragged_cfg* rc, int32_t Hq, int32_
  * -1. A draft outside [0, V) is not accepted and reported (KL_DEVERR_TARGET).
  * B and T at most 2^24, V at most 2^30.
  * The acceptance test is exact; sums, their products with u_sample and the
- * comparisons between them are off by less than 2^-41 of the sum, whatever V and
- * the batch are. All on the device, p and q of type dtype (fp32 or bf16). One
+ * comparisons between them are off by less than 2^-41 of the sum (of one above
+ * 2^-100), whatever V and the batch are. All on the device, p and q of type dtype (fp32 or bf16). One
  * launch, no workspace. */
 typedef struct kl_verify_cfg {
   int32_t B;        /* requests                                              */
