@@ -129,7 +129,7 @@ def _pool(shape, gen):
 
 def _scale(largest):
     m, e = torch.frexp(largest)
-    return torch.ldexp(torch.ones_like(largest), torch.where(m <= 0.875, e - 9, e - 8).clamp(min=-64))
+    return torch.ldexp(torch.ones_like(largest), torch.where(m <= 0.875, e - 9, e - 8).where(m > 0, -64).clamp(min=-64))
 
 
 def prepare(case, seed):
@@ -415,7 +415,7 @@ def _exact_append(s):
             page, place = divmod(slots[r], bs)
             for h in range(Hkv):
                 m, e = math.frexp(max(row[h] for row in largest[r:r + n]))
-                want = 2.0 ** max(-64, e - 9 if m <= 0.875 else e - 8)
+                want = 2.0 ** max(-64, -64 if m == 0 else e - 9 if m <= 0.875 else e - 8)
                 if place and scales[page][h] < want:
                     pool[page, :place, h] = _nearest8(pool[page, :place, h] * scales[page][h] / want)
                 scales[page][h] = max(want, scales[page][h]) if place else want
