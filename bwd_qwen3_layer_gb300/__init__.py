@@ -139,6 +139,14 @@ _SIGNATURES = {
     "kl_draft_verify": (ctypes.c_int, [_P(VerifyCfg), _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "kl_layer_forward_ragged_ws_bytes": (_sz, [_P(LayerCfg), _P(RaggedCfg)]),
     "kl_layer_forward_ragged": (ctypes.c_int, [_P(LayerCfg), _P(RaggedCfg), _P(LayerWeights)] + [_vp] * 10 + [_sz, _vp]),
+    "kl_ragged_qkv_rope8": (ctypes.c_int, [_P(RaggedCfg), _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _f32, _f32,
+                                           _i32] + [_vp] * 9),
+    "kl_ragged_attention8_ws_bytes": (_sz, [_P(RaggedCfg), _i32, _i32, _i32]),
+    "kl_ragged_attention8": (ctypes.c_int, [_P(RaggedCfg), _i32, _i32, _i32, _i32] + [_vp] * 11 + [_sz, _vp]),
+    "kl_layer_forward_ragged8_ws_bytes": (_sz, [_P(LayerCfg), _P(RaggedCfg)]),
+    "kl_layer_forward_ragged8": (ctypes.c_int, [_P(LayerCfg), _P(RaggedCfg), _P(LayerWeights)] + [_vp] * 12 + [_sz, _vp]),
+    "kl_token_logprobs": (ctypes.c_int, [_i32, _i32, _i32, _vp, _i64, _vp, _i32] + [_vp] * 6),
+    "kl_token_logprobs_bwd": (ctypes.c_int, [_i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i64, _vp]),
     "kl_profile_enable": (ctypes.c_int, [_i32]),
     "kl_profile_read": (_i32, [_vp, _i32]),
     "kl_launch_count": (ctypes.c_uint64, []),
@@ -391,6 +399,50 @@ def kl_layer_forward_ragged(cfg: LayerCfg, rc: RaggedCfg, w: LayerWeights, X, Y,
                             pos, slots, ws, ws_bytes, stream=None) -> None:
     check(load().kl_layer_forward_ragged(ctypes.byref(cfg), ctypes.byref(rc), ctypes.byref(w), X, Y, k_pool, v_pool,
                                          table, cu_rows, ctx, pos, slots, ws, ws_bytes, _stream(stream)))
+
+
+def kl_ragged_qkv_rope8(rc: RaggedCfg, Hq, Hkv, d, dtype, q_pre, k_pre, v, gamma_q, gamma_k, eps, rope_base,
+                        rope_interleaved, cu_rows, pos, slots, q_out, k_pool, v_pool, k_scale, v_scale,
+                        stream=None) -> None:
+    check(load().kl_ragged_qkv_rope8(ctypes.byref(rc), Hq, Hkv, d, dtype, q_pre, k_pre, v, gamma_q, gamma_k, eps,
+                                     rope_base, rope_interleaved, cu_rows, pos, slots, q_out, k_pool, v_pool, k_scale,
+                                     v_scale, _stream(stream)))
+
+
+def kl_ragged_attention8_ws_bytes(rc: RaggedCfg, Hq, Hkv, d) -> int:
+    return load().kl_ragged_attention8_ws_bytes(ctypes.byref(rc), Hq, Hkv, d)
+
+
+def kl_ragged_attention8(rc: RaggedCfg, Hq, Hkv, d, dtype, q, k_pool, v_pool, k_scale, v_scale, table, cu_rows, ctx, o,
+                         lse, ws, ws_bytes, stream=None) -> None:
+    check(load().kl_ragged_attention8(ctypes.byref(rc), Hq, Hkv, d, dtype, q, k_pool, v_pool, k_scale, v_scale, table,
+                                      cu_rows, ctx, o, lse, ws, ws_bytes, _stream(stream)))
+
+
+def kl_layer_forward_ragged8_ws_bytes(cfg: LayerCfg, rc: RaggedCfg) -> int:
+    return load().kl_layer_forward_ragged8_ws_bytes(ctypes.byref(cfg), ctypes.byref(rc))
+
+
+def kl_layer_forward_ragged8(cfg: LayerCfg, rc: RaggedCfg, w: LayerWeights, X, Y, k_pool, v_pool, k_scale, v_scale,
+                             table, cu_rows, ctx, pos, slots, ws, ws_bytes, stream=None) -> None:
+    check(load().kl_layer_forward_ragged8(ctypes.byref(cfg), ctypes.byref(rc), ctypes.byref(w), X, Y, k_pool, v_pool,
+                                          k_scale, v_scale, table, cu_rows, ctx, pos, slots, ws, ws_bytes,
+                                          _stream(stream)))
+
+
+KL_LOGPROBS_MAX_TOP = 32
+
+
+def kl_token_logprobs(N, V, dtype, z, ldz, tokens, n_top, logprob, entropy, norm, top_id, top_logprob,
+                      stream=None) -> None:
+    check(load().kl_token_logprobs(N, V, dtype, z, ldz, tokens, n_top, logprob, entropy, norm, top_id, top_logprob,
+                                   _stream(stream)))
+
+
+def kl_token_logprobs_bwd(N, V, dtype, z, ldz, tokens, norm, entropy, d_logprob, d_entropy, dz_dtype, dz, lddz,
+                          stream=None) -> None:
+    check(load().kl_token_logprobs_bwd(N, V, dtype, z, ldz, tokens, norm, entropy, d_logprob, d_entropy, dz_dtype, dz,
+                                       lddz, _stream(stream)))
 
 
 def kl_device_status(stream=None) -> int:

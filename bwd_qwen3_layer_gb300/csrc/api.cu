@@ -835,21 +835,32 @@ kl_status kl_ragged_plan(const kl_ragged_cfg* rc, const int32_t* n_new, const in
                      static_cast<cudaStream_t>(stream));
 }
 
+// What kl_ragged_qkv_rope and its 8-bit form check.
+static kl_status qkv_rope_check(const char* what, const char* gains, const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d,
+                                int32_t dtype, const void* q_pre, const void* k_pre, const void* v, const void* gamma_q,
+                                const void* gamma_k, float eps, float rope_base, int32_t rope_interleaved,
+                                const int32_t* cu_rows, const int32_t* pos, const int32_t* slots, const void* q_out,
+                                const void* k_pool, const void* v_pool) {
+  KL_TRY(ragged_heads_check(rc, Hq, Hkv, d, dtype));
+  KL_TRY(check_ptrs({q_pre, k_pre, v, q_out, k_pool, v_pool}, what));
+  KL_TRY(check_arrays({cu_rows, pos, slots}, what));
+  if (!gamma_q != !gamma_k) return set_error(KL_ERR_INVALID_ARG, "%s: one of gamma_q, gamma_k is null", what);
+  if (gamma_q) KL_TRY(check_ptrs({gamma_q, gamma_k}, gains));
+  // rates below 1 / (2 pi) turns per position fit the fixed-point angle
+  if (!(rope_base >= 1.f) || !(rope_base < INFINITY) || !(eps >= 0.f) || !(eps < INFINITY) ||
+      (rope_interleaved != 0 && rope_interleaved != 1))
+    return set_error(KL_ERR_INVALID_ARG, "%s: base %g, eps %g, interleaved %d", what, rope_base, eps,
+                     rope_interleaved);
+  return KL_OK;
+}
+
 kl_status kl_ragged_qkv_rope(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
                              const void* q_pre, const void* k_pre, const void* v, const void* gamma_q,
                              const void* gamma_k, float eps, float rope_base, int32_t rope_interleaved,
                              const int32_t* cu_rows, const int32_t* pos, const int32_t* slots, void* q_out,
                              void* k_pool, void* v_pool, void* stream) {
-  KL_TRY(ragged_heads_check(rc, Hq, Hkv, d, dtype));
-  KL_TRY(check_ptrs({q_pre, k_pre, v, q_out, k_pool, v_pool}, "ragged_qkv_rope"));
-  KL_TRY(check_arrays({cu_rows, pos, slots}, "ragged_qkv_rope"));
-  if (!gamma_q != !gamma_k) return set_error(KL_ERR_INVALID_ARG, "ragged_qkv_rope: one of gamma_q, gamma_k is null");
-  if (gamma_q) KL_TRY(check_ptrs({gamma_q, gamma_k}, "ragged_qkv_rope gains"));
-  // rates below 1 / (2 pi) turns per position fit the fixed-point angle
-  if (!(rope_base >= 1.f) || !(rope_base < INFINITY) || !(eps >= 0.f) || !(eps < INFINITY) ||
-      (rope_interleaved != 0 && rope_interleaved != 1))
-    return set_error(KL_ERR_INVALID_ARG, "ragged_qkv_rope: base %g, eps %g, interleaved %d", rope_base, eps,
-                     rope_interleaved);
+  KL_TRY(qkv_rope_check("ragged_qkv_rope", "ragged_qkv_rope gains", rc, Hq, Hkv, d, dtype, q_pre, k_pre, v, gamma_q, gamma_k, eps, rope_base,
+                        rope_interleaved, cu_rows, pos, slots, q_out, k_pool, v_pool));
   return ragged_qkv_rope(*rc, Hq, Hkv, q_pre, k_pre, v, gamma_q, gamma_k, eps, rope_base, rope_interleaved, cu_rows,
                          pos, slots, q_out, k_pool, v_pool, static_cast<cudaStream_t>(stream));
 }
@@ -859,17 +870,25 @@ size_t kl_ragged_attention_ws_bytes(const kl_ragged_cfg* rc, int32_t Hq, int32_t
   return ragged_attention_ws();
 }
 
+static kl_status ragged_attention_check(const char* what, const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d,
+                                        int32_t dtype, const void* q, const void* k_pool, const void* v_pool,
+                                        const int32_t* table, const int32_t* cu_rows, const int32_t* ctx, const void* o,
+                                        const float* lse) {
+  KL_TRY(ragged_heads_check(rc, Hq, Hkv, d, dtype));
+  KL_TRY(check_ptrs({q, k_pool, v_pool, o}, what));
+  KL_TRY(check_arrays({table, cu_rows, ctx}, what));
+  if (reinterpret_cast<uintptr_t>(lse) & 3u)
+    return set_error(KL_ERR_INVALID_ARG, "%s: lse not 4-byte aligned", what);
+  if (reinterpret_cast<uintptr_t>(o) & 31u)
+    return set_error(KL_ERR_INVALID_ARG, "%s: o not 32-byte aligned (it is written in whole sectors)", what);
+  return KL_OK;
+}
+
 kl_status kl_ragged_attention(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
                               const void* q, const void* k_pool, const void* v_pool, const int32_t* table,
                               const int32_t* cu_rows, const int32_t* ctx, void* o, float* lse, void* ws,
                               size_t ws_bytes, void* stream) {
-  KL_TRY(ragged_heads_check(rc, Hq, Hkv, d, dtype));
-  KL_TRY(check_ptrs({q, k_pool, v_pool, o}, "ragged_attention"));
-  KL_TRY(check_arrays({table, cu_rows, ctx}, "ragged_attention"));
-  if (reinterpret_cast<uintptr_t>(lse) & 3u)
-    return set_error(KL_ERR_INVALID_ARG, "ragged_attention: lse not 4-byte aligned");
-  if (reinterpret_cast<uintptr_t>(o) & 31u)
-    return set_error(KL_ERR_INVALID_ARG, "ragged_attention: o not 32-byte aligned (it is written in whole sectors)");
+  KL_TRY(ragged_attention_check("ragged_attention", rc, Hq, Hkv, d, dtype, q, k_pool, v_pool, table, cu_rows, ctx, o, lse));
   return ragged_attention(*rc, Hq, Hkv, q, k_pool, v_pool, table, cu_rows, ctx, o, lse, ws, ws_bytes,
                           static_cast<cudaStream_t>(stream));
 }
@@ -903,41 +922,154 @@ static kl_status ragged_layer_check(const kl_layer_cfg* cfg, const kl_ragged_cfg
   return KL_OK;
 }
 
-size_t kl_layer_forward_ragged_ws_bytes(const kl_layer_cfg* cfg, const kl_ragged_cfg* rc) {
+static size_t ragged_layer_ws(const kl_layer_cfg* cfg, const kl_ragged_cfg* rc, size_t att) {
   Dims D;
   if (ragged_layer_check(cfg, rc, &D) != KL_OK) return 0;
   Carver c(nullptr);
   PagedWs w;
-  carve_paged(D, ragged_attention_ws(), c, &w);
+  carve_paged(D, att, c, &w);
   return c.off;
+}
+
+// The layer over either cache: bf16 pools, or with ks and vs pools of 8-bit codes.
+static kl_status ragged_layer(const char* what, const kl_layer_cfg* cfg, const kl_ragged_cfg* rc,
+                              const kl_layer_weights* w, const void* X, void* Y, void* k_pool, void* v_pool, float* ks,
+                              float* vs, const int32_t* table, const int32_t* cu_rows, const int32_t* ctx,
+                              const int32_t* pos, const int32_t* slots, void* ws, size_t ws_bytes, void* stream) {
+  Dims D;
+  KL_TRY(ragged_layer_check(cfg, rc, &D));
+  if (!w) return set_error(KL_ERR_INVALID_ARG, "%s: null weights", what);
+  KL_TRY(check_ptrs({w->gamma1, w->wq, w->wk, w->wv, w->wo, w->gamma2, w->wg, w->wu, w->wd},
+                    ks ? "layer_forward_ragged8 weights" : "layer_forward_ragged weights"));
+  if (D.qk_norm)
+    KL_TRY(check_ptrs({w->gamma_q, w->gamma_k},
+                      ks ? "layer_forward_ragged8 q/k norm gains" : "layer_forward_ragged q/k norm gains"));
+  KL_TRY(check_ptrs({X, Y, k_pool, v_pool}, ks ? "layer_forward_ragged8 buffers" : "layer_forward_ragged buffers"));
+  KL_TRY(check_arrays({table, cu_rows, ctx, pos, slots}, what));
+  const size_t att = ks ? ragged_attention8_ws() : ragged_attention_ws();
+  const size_t need = ragged_layer_ws(cfg, rc, att);
+  if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return set_error(KL_ERR_NO_MEMORY, "%s: workspace too small or not 256-byte aligned", what);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Carver c(ws);
+  PagedWs b;
+  carve_paged(D, att, c, &b);
+  KL_TRY(paged_qkv(D, w, X, cfg->eps, b, st));
+  const void* gq = D.qk_norm ? w->gamma_q : nullptr;
+  const void* gk = D.qk_norm ? w->gamma_k : nullptr;
+  if (ks) {
+    KL_TRY(ragged_qkv_rope8(*rc, D.Hq, D.Hkv, b.q_pre, b.k_pre, b.v, gq, gk, cfg->eps, cfg->rope_base, D.inter, cu_rows,
+                            pos, slots, b.q, k_pool, v_pool, ks, vs, st));
+    KL_TRY(ragged_attention8(*rc, D.Hq, D.Hkv, b.q, k_pool, v_pool, ks, vs, table, cu_rows, ctx, b.o, nullptr, b.att,
+                             b.att_bytes, st));
+  } else {
+    KL_TRY(ragged_qkv_rope(*rc, D.Hq, D.Hkv, b.q_pre, b.k_pre, b.v, gq, gk, cfg->eps, cfg->rope_base, D.inter, cu_rows,
+                           pos, slots, b.q, k_pool, v_pool, st));
+    KL_TRY(ragged_attention(*rc, D.Hq, D.Hkv, b.q, k_pool, v_pool, table, cu_rows, ctx, b.o, nullptr, b.att, b.att_bytes,
+                            st));
+  }
+  return paged_out_mlp(D, w, X, Y, cfg->eps, b, st);
+}
+
+size_t kl_layer_forward_ragged_ws_bytes(const kl_layer_cfg* cfg, const kl_ragged_cfg* rc) {
+  return ragged_layer_ws(cfg, rc, ragged_attention_ws());
 }
 
 kl_status kl_layer_forward_ragged(const kl_layer_cfg* cfg, const kl_ragged_cfg* rc, const kl_layer_weights* w,
                                   const void* X, void* Y, void* k_pool, void* v_pool, const int32_t* table,
                                   const int32_t* cu_rows, const int32_t* ctx, const int32_t* pos, const int32_t* slots,
                                   void* ws, size_t ws_bytes, void* stream) {
-  Dims D;
-  KL_TRY(ragged_layer_check(cfg, rc, &D));
-  if (!w) return set_error(KL_ERR_INVALID_ARG, "layer_forward_ragged: null weights");
-  KL_TRY(check_ptrs({w->gamma1, w->wq, w->wk, w->wv, w->wo, w->gamma2, w->wg, w->wu, w->wd},
-                    "layer_forward_ragged weights"));
-  if (D.qk_norm) KL_TRY(check_ptrs({w->gamma_q, w->gamma_k}, "layer_forward_ragged q/k norm gains"));
-  KL_TRY(check_ptrs({X, Y, k_pool, v_pool}, "layer_forward_ragged buffers"));
-  KL_TRY(check_arrays({table, cu_rows, ctx, pos, slots}, "layer_forward_ragged"));
-  const size_t need = kl_layer_forward_ragged_ws_bytes(cfg, rc);
-  if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u))
-    return set_error(KL_ERR_NO_MEMORY, "layer_forward_ragged: workspace too small or not 256-byte aligned");
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  Carver c(ws);
-  PagedWs b;
-  carve_paged(D, ragged_attention_ws(), c, &b);
-  KL_TRY(paged_qkv(D, w, X, cfg->eps, b, st));
-  KL_TRY(ragged_qkv_rope(*rc, D.Hq, D.Hkv, b.q_pre, b.k_pre, b.v, D.qk_norm ? w->gamma_q : nullptr,
-                         D.qk_norm ? w->gamma_k : nullptr, cfg->eps, cfg->rope_base, D.inter, cu_rows, pos, slots, b.q,
-                         k_pool, v_pool, st));
-  KL_TRY(ragged_attention(*rc, D.Hq, D.Hkv, b.q, k_pool, v_pool, table, cu_rows, ctx, b.o, nullptr, b.att, b.att_bytes,
-                          st));
-  return paged_out_mlp(D, w, X, Y, cfg->eps, b, st);
+  return ragged_layer("layer_forward_ragged", cfg, rc, w, X, Y, k_pool, v_pool, nullptr, nullptr, table, cu_rows, ctx,
+                      pos, slots, ws, ws_bytes, stream);
+}
+
+kl_status kl_ragged_qkv_rope8(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
+                              const void* q_pre, const void* k_pre, const void* v, const void* gamma_q,
+                              const void* gamma_k, float eps, float rope_base, int32_t rope_interleaved,
+                              const int32_t* cu_rows, const int32_t* pos, const int32_t* slots, void* q_out,
+                              void* k_pool, void* v_pool, float* k_scale, float* v_scale, void* stream) {
+  KL_TRY(qkv_rope_check("ragged_qkv_rope8", "ragged_qkv_rope8 gains", rc, Hq, Hkv, d, dtype, q_pre, k_pre, v, gamma_q, gamma_k, eps, rope_base,
+                        rope_interleaved, cu_rows, pos, slots, q_out, k_pool, v_pool));
+  KL_TRY(check_arrays({k_scale, v_scale}, "ragged_qkv_rope8 scales"));
+  return ragged_qkv_rope8(*rc, Hq, Hkv, q_pre, k_pre, v, gamma_q, gamma_k, eps, rope_base, rope_interleaved, cu_rows,
+                          pos, slots, q_out, k_pool, v_pool, k_scale, v_scale, static_cast<cudaStream_t>(stream));
+}
+
+size_t kl_ragged_attention8_ws_bytes(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d) {
+  if (ragged_heads_check(rc, Hq, Hkv, d, KL_BF16) != KL_OK) return 0;
+  return ragged_attention8_ws();
+}
+
+kl_status kl_ragged_attention8(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
+                               const void* q, const void* k_pool, const void* v_pool, const float* k_scale,
+                               const float* v_scale, const int32_t* table, const int32_t* cu_rows, const int32_t* ctx,
+                               void* o, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  KL_TRY(ragged_attention_check("ragged_attention8", rc, Hq, Hkv, d, dtype, q, k_pool, v_pool, table, cu_rows, ctx, o,
+                                lse));
+  KL_TRY(check_arrays({k_scale, v_scale}, "ragged_attention8 scales"));
+  return ragged_attention8(*rc, Hq, Hkv, q, k_pool, v_pool, k_scale, v_scale, table, cu_rows, ctx, o, lse, ws, ws_bytes,
+                           static_cast<cudaStream_t>(stream));
+}
+
+size_t kl_layer_forward_ragged8_ws_bytes(const kl_layer_cfg* cfg, const kl_ragged_cfg* rc) {
+  return ragged_layer_ws(cfg, rc, ragged_attention8_ws());
+}
+
+kl_status kl_layer_forward_ragged8(const kl_layer_cfg* cfg, const kl_ragged_cfg* rc, const kl_layer_weights* w,
+                                   const void* X, void* Y, void* k_pool, void* v_pool, float* k_scale, float* v_scale,
+                                   const int32_t* table, const int32_t* cu_rows, const int32_t* ctx, const int32_t* pos,
+                                   const int32_t* slots, void* ws, size_t ws_bytes, void* stream) {
+  KL_TRY(check_arrays({k_scale, v_scale}, "layer_forward_ragged8 scales"));
+  return ragged_layer("layer_forward_ragged8", cfg, rc, w, X, Y, k_pool, v_pool, k_scale, v_scale, table, cu_rows, ctx,
+                      pos, slots, ws, ws_bytes, stream);
+}
+
+static kl_status logprobs_check(const char* what, int32_t N, int32_t V, int32_t dtype, const void* z, int64_t ldz,
+                                const int32_t* tokens) {
+  if (N < 1 || V < 1 || ldz < V)
+    return set_error(KL_ERR_INVALID_ARG, "%s: bad sizes (N %d, V %d, row stride %lld)", what, N, V,
+                     static_cast<long long>(ldz));
+  if (dtype != KL_F32 && dtype != KL_BF16) return set_error(KL_ERR_INVALID_ARG, "%s: bad dtype %d", what, dtype);
+  if (N > (1 << 24) || V > (1 << 30)) return set_error(KL_ERR_UNSUPPORTED, "%s: too many rows or classes (%d, %d)", what, N, V);
+  KL_TRY(check_ptrs({z}, what));
+  return check_arrays({tokens}, what);
+}
+
+kl_status kl_token_logprobs(int32_t N, int32_t V, int32_t dtype, const void* z, int64_t ldz, const int32_t* tokens,
+                            int32_t n_top, float* logprob, float* entropy, float* norm, int32_t* top_id,
+                            float* top_logprob, void* stream) {
+  KL_TRY(logprobs_check("token_logprobs", N, V, dtype, z, ldz, tokens));
+  if (n_top < 0 || n_top > KL_LOGPROBS_MAX_TOP)
+    return set_error(KL_ERR_INVALID_ARG, "token_logprobs: %d alternatives (0 to %d)", n_top, KL_LOGPROBS_MAX_TOP);
+  KL_TRY(check_arrays({logprob}, "token_logprobs"));
+  if (entropy) KL_TRY(check_arrays({entropy}, "token_logprobs entropy"));
+  if (norm) KL_TRY(check_arrays({norm}, "token_logprobs norm"));
+  if (n_top) KL_TRY(check_arrays({top_id, top_logprob}, "token_logprobs alternatives"));
+  return token_logprobs(N, V, dtype, z, ldz, tokens, n_top, logprob, entropy, norm, top_id, top_logprob,
+                        static_cast<cudaStream_t>(stream));
+}
+
+kl_status kl_token_logprobs_bwd(int32_t N, int32_t V, int32_t dtype, const void* z, int64_t ldz, const int32_t* tokens,
+                                const float* norm, const float* entropy, const float* d_logprob,
+                                const float* d_entropy, int32_t dz_dtype, void* dz, int64_t lddz, void* stream) {
+  KL_TRY(logprobs_check("token_logprobs_bwd", N, V, dtype, z, ldz, tokens));
+  if (dz_dtype != KL_F32 && dz_dtype != KL_BF16)
+    return set_error(KL_ERR_INVALID_ARG, "token_logprobs_bwd: bad gradient dtype %d", dz_dtype);
+  if (lddz < V) return set_error(KL_ERR_INVALID_ARG, "token_logprobs_bwd: row stride %lld below V", static_cast<long long>(lddz));
+  KL_TRY(check_ptrs({dz}, "token_logprobs_bwd dz"));
+  KL_TRY(check_arrays({norm}, "token_logprobs_bwd norm"));
+  if (d_logprob) KL_TRY(check_arrays({d_logprob}, "token_logprobs_bwd d_logprob"));
+  if (d_entropy) KL_TRY(check_arrays({d_entropy, entropy}, "token_logprobs_bwd entropy"));
+  {
+    // in place each element is read before it is written by the same thread; any other overlap is not
+    const uintptr_t z0 = reinterpret_cast<uintptr_t>(z), d0 = reinterpret_cast<uintptr_t>(dz);
+    const uintptr_t zn = (static_cast<uintptr_t>(N - 1) * ldz + V) * dtype_size(dtype);
+    const uintptr_t dn = (static_cast<uintptr_t>(N - 1) * lddz + V) * dtype_size(dz_dtype);
+    if (z0 < d0 + dn && d0 < z0 + zn && !(z0 == d0 && dtype == dz_dtype && ldz == lddz))
+      return set_error(KL_ERR_INVALID_ARG, "token_logprobs_bwd: dz overlaps the logits");
+  }
+  return token_logprobs_bwd(N, V, dtype, z, ldz, tokens, norm, entropy, d_logprob, d_entropy, dz_dtype, dz, lddz,
+                            static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

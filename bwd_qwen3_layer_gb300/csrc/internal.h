@@ -171,6 +171,22 @@ size_t ragged_attention_ws();
 kl_status ragged_attention(const kl_ragged_cfg& rc, int Hq, int Hkv, const void* q, const void* kp, const void* vp,
                            const int32_t* table, const int32_t* cu, const int32_t* ctx, void* o, float* lse, void* ws,
                            size_t ws_bytes, cudaStream_t st);
+// ragged8.cu, ragged_attn8.cu: the same over pools of e4m3 codes with a scale per block and head
+kl_status ragged_qkv_rope8(const kl_ragged_cfg& rc, int Hq, int Hkv, const void* q_pre, const void* k_pre, const void* v,
+                           const void* gq, const void* gk, float eps, float base, int inter, const int32_t* cu,
+                           const int32_t* pos, const int32_t* slots, void* q_out, void* kp, void* vp, float* ks,
+                           float* vs, cudaStream_t st);
+size_t ragged_attention8_ws();
+kl_status ragged_attention8(const kl_ragged_cfg& rc, int Hq, int Hkv, const void* q, const void* kp, const void* vp,
+                            const float* ks, const float* vs, const int32_t* table, const int32_t* cu,
+                            const int32_t* ctx, void* o, float* lse, void* ws, size_t ws_bytes, cudaStream_t st);
+// logprobs.cu: log probabilities of given tokens and their gradient
+kl_status token_logprobs(int N, int V, int dtype, const void* z, int64_t ldz, const int32_t* tokens, int n_top,
+                         float* logprob, float* entropy, float* norm, int32_t* top_id, float* top_logprob,
+                         cudaStream_t st);
+kl_status token_logprobs_bwd(int N, int V, int dtype, const void* z, int64_t ldz, const int32_t* tokens,
+                             const float* norm, const float* entropy, const float* dlp, const float* dent, int dz_dtype,
+                             void* dz, int64_t lddz, cudaStream_t st);
 // verify.cu: drafted tokens against the target's probabilities
 kl_status draft_verify(const kl_verify_cfg& c, const void* p, int64_t ldp, const void* q, int64_t ldq,
                        const int32_t* tokens, const int32_t* cu, const float* ua, const float* us, int32_t* acc,

@@ -600,6 +600,94 @@ KL_API kl_status kl_layer_forward_ragged(const kl_layer_cfg* cfg, const kl_ragge
                                          const int32_t* cu_rows, const int32_t* ctx, const int32_t* pos,
                                          const int32_t* slots, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* The ragged step over a cache held in 8 bits: the pages' paged-KV paragraph */
+/* with half the bytes, which is what a decoding step is bound by            */
+/* ------------------------------------------------------------------------ */
+
+/* A pool is [n_blocks][block_size][Hkv * d] bytes of e4m3 codes (4 exponent and
+ * 3 mantissa bits, largest value 448, code 0x7f NaN); beside it lies
+ * [n_blocks][Hkv] fp32, a scale for each block and head: a slot's element is
+ * scale * code. Tables, rows and limits are those of kl_ragged_cfg; pools are
+ * 16-byte aligned, scales 4-byte.
+ *
+ * kl_ragged_qkv_rope8: kl_ragged_qkv_rope with the new keys (normed, rotated)
+ * and values into such pools, rounded once from fp32. The new rows of a block
+ * (in one step they must be consecutive rows and slots, as kl_ragged_plan leaves
+ * them, and a block belongs to one request) are written together. With a their largest
+ * size in a head, w = 2^e is the least power of two, e at least -64, with
+ * a / w <= 448. A block whose first new slot is its slot 0 gets the scale w and
+ * forgets its earlier one, which need not be initialised; any other gets the larger
+ * of its scale and w, and when that grows the codes of the slots before the first
+ * new one are rounded again at the new scale (exact, the scales being powers of two,
+ * but for codes that reach the subnormal range, off by half of 2^-9 scale at most).
+ * Slots behind the new ones keep their codes and mean nothing. A code is the
+ * nearest to value / scale, halves to the even one; an infinity or a NaN is held
+ * as NaN and does not count for a. Scales are written by this call alone, or are
+ * positive powers of two. q_out may be q_pre; nothing else overlaps. */
+KL_API kl_status kl_ragged_qkv_rope8(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
+                                     const void* q_pre, const void* k_pre, const void* v, const void* gamma_q,
+                                     const void* gamma_k, float eps, float rope_base, int32_t rope_interleaved,
+                                     const int32_t* cu_rows, const int32_t* pos, const int32_t* slots, void* q_out,
+                                     void* k_pool, void* v_pool, float* k_scale, float* v_scale, void* stream);
+/* kl_ragged_attention over such pools; q and o stay bf16 (dtype). Any positive,
+ * finite, normal scale is taken. A block that is read as zero (see there) has no
+ * scale. A NaN in a query, in a key that a row sees or in the scale of a block
+ * that it sees makes the row's o and lse NaN, as an infinity in a query does; a
+ * NaN in a value reaches rows as there. */
+KL_API size_t kl_ragged_attention8_ws_bytes(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d);
+KL_API kl_status kl_ragged_attention8(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
+                                      const void* q, const void* k_pool, const void* v_pool, const float* k_scale,
+                                      const float* v_scale, const int32_t* table, const int32_t* cu_rows,
+                                      const int32_t* ctx, void* o, float* lse, void* ws, size_t ws_bytes, void* stream);
+/* kl_layer_forward_ragged over such pools: the same arguments with the scales. */
+KL_API size_t kl_layer_forward_ragged8_ws_bytes(const kl_layer_cfg* cfg, const kl_ragged_cfg* rc);
+KL_API kl_status kl_layer_forward_ragged8(const kl_layer_cfg* cfg, const kl_ragged_cfg* rc, const kl_layer_weights* w,
+                                          const void* X, void* Y, void* k_pool, void* v_pool, float* k_scale,
+                                          float* v_scale, const int32_t* table, const int32_t* cu_rows,
+                                          const int32_t* ctx, const int32_t* pos, const int32_t* slots, void* ws,
+                                          size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Log probabilities of given tokens: what a server answers with and what a   */
+/* policy gradient trains on. The lm-head loss without its mean, its gradient */
+/* with a weight for each row                                                */
+/* ------------------------------------------------------------------------ */
+
+/* Row n of z [N, V] (dtype fp32 or bf16, row stride ldz elements) holds logits;
+ * m is its largest, s = sum exp(z - m), p = exp(z - m) / s.
+ *   logprob [N]  z[t] - m - log s at the token t = tokens[n]; 0 where t = -1 (the
+ *                row has none); any other t outside [0, V) gets 0 and is reported
+ *                (KL_DEVERR_TARGET)
+ *   entropy [N]  -sum p log p, a class with p = 0 counting nothing
+ *   norm [N, 2]  (m, log s): kept apart, so that large logits lose nothing
+ *   top_id, top_logprob [N, n_top]  the n_top (0 to KL_LOGPROBS_MAX_TOP) most
+ *                likely classes and their log probabilities, in falling order, the
+ *                lower index first where logits are equal (0 and -0 are); -1 and
+ *                -infinity where no class with a logit above -infinity is left
+ * fp32 and int32; entropy and norm may be NULL, so may the two top arrays when
+ * n_top is 0. A row without any logit above -infinity has logprob -infinity (or 0,
+ * without a token), entropy 0 and norm (-infinity, -infinity). A NaN or +infinity
+ * in a row makes the row's numbers NaN (but m and the 0 of a row without a token),
+ * and its top classes mean nothing.
+ * N at most 2^24, V at most 2^30. One launch, no workspace; the same bits from run to run. */
+#define KL_LOGPROBS_MAX_TOP 32
+KL_API kl_status kl_token_logprobs(int32_t N, int32_t V, int32_t dtype, const void* z, int64_t ldz,
+                                   const int32_t* tokens, int32_t n_top, float* logprob, float* entropy, float* norm,
+                                   int32_t* top_id, float* top_logprob, void* stream);
+/* The gradient of sum_n d_logprob[n] logprob[n] + d_entropy[n] entropy[n]:
+ *   dz_j = d_logprob (1[j = t] - p_j) - d_entropy p_j (log p_j + entropy),
+ * from the forward's norm and entropy. d_logprob or d_entropy may be NULL (zero;
+ * entropy is read with d_entropy only). Rows without a token get nothing from d_logprob
+ * (a token outside [0, V) but for -1 is reported), rows without any logit above
+ * -infinity zeros, as every class with p = 0. dz [N, V] (dz_dtype fp32 or bf16, row
+ * stride lddz) is overwritten; it may be z itself (same type and stride), else it
+ * must not overlap z. */
+KL_API kl_status kl_token_logprobs_bwd(int32_t N, int32_t V, int32_t dtype, const void* z, int64_t ldz,
+                                       const int32_t* tokens, const float* norm, const float* entropy,
+                                       const float* d_logprob, const float* d_entropy, int32_t dz_dtype, void* dz,
+                                       int64_t lddz, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

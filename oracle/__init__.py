@@ -59,3 +59,12 @@ from .paged import (  # noqa: F401,E402
     rope_at,
 )
 from .ragged import draft_verify, ragged_attention, ragged_plan  # noqa: F401,E402
+from .cache8 import (  # noqa: F401,E402
+    cache8_append,
+    dequantised,
+    e4m3_half_step,
+    e4m3_round,
+    e4m3_values,
+    scale_for,
+)
+from .logprobs import token_logprobs, token_logprobs_bwd  # noqa: F401,E402
