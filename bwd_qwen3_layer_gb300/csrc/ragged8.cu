@@ -17,6 +17,7 @@
 // take a row's queries each.
 #include <float.h>
 
+#include "e4m3.cuh"
 #include "ragged_rope.cuh"
 
 namespace kl {
@@ -46,23 +47,6 @@ struct Rope8Params {
   RopeFreq f;
 };
 
-// Four floats of at most 448 in size as e4m3 (nearest, halves to even; NaN stays NaN).
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-  return static_cast<uint32_t>(lo) | static_cast<uint32_t>(hi) << 16;
-}
-// Four e4m3 codes as floats.
-__device__ __forceinline__ float4 e4m3x4_to_f(uint32_t v) {
-  uint32_t lo, hi;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"(static_cast<uint16_t>(v)));
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"(static_cast<uint16_t>(v >> 16)));
-  float4 r;
-  asm("{.reg .f16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}" : "=f"(r.x), "=f"(r.y) : "r"(lo));
-  asm("{.reg .f16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}" : "=f"(r.z), "=f"(r.w) : "r"(hi));
-  return r;
-}
 // The least power of two w >= 2^-64 with a / w <= 448 = 1.75 * 2^8, for finite a >= 0.
 __device__ __forceinline__ float scale_for(float a) {
   const uint32_t bits = __float_as_uint(a);

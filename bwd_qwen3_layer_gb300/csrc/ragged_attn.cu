@@ -45,21 +45,15 @@
 // which the products take 1024 and shared memory's 160 KB (products' reads, copies'
 // writes) 1250. Two warpgroups of softmax in turn (168 registers) gained 3 % there and
 // lost 4 to 14 % everywhere else.
-#include <cudaTypedefs.h>
-#include <math.h>
 #include <string.h>
 
 #include <type_traits>
 
-#include "internal.h"
-#include "kl_common.cuh"
+#include "ragged_walk.cuh"
 
 namespace kl {
 namespace {
 
-constexpr int RA_D = 128;        // head dim
-constexpr int RA_BQ = 128;       // rows of a query tile
-constexpr int RA_BKV = 128;      // keys per tile
 constexpr int RA_WARPS = 8;      // K copies, Q and V copies, score products, P V products, four of softmax
 constexpr int RA_THREADS = 32 * RA_WARPS;
 // A key or value tile (32 KB) is 16 groups of 8 keys, each group two swizzled
@@ -74,36 +68,6 @@ constexpr uint32_t RA_OFF_BAR = RA_OFF_V + RA_NST * RA_TILE;
 constexpr size_t RA_SMEM = 1024 + RA_OFF_BAR + 2048;
 // Tensor memory: S of two steps, P of two steps (bf16 pairs), O: all 512 columns.
 constexpr uint32_t RA_TM_P = 256, RA_TM_O = 384;
-// Units that an item's start and end count for: its first scores, the last product
-// and the epilogue take about four key tiles' time. Mixed batch of 20: with two,
-// CTAs with two pieces ended at 51 us and those with eight at 61, 63 us in all;
-// with four 60.4. A run may be as short as one unit: one request of 500 keys takes 8.8
-// us, 11.2 with runs of at least five (100 keys: 8.3 and 7.9).
-constexpr int RA_ITEM_UNITS = 4;
-constexpr float RA_LOG2E = 1.4426950408889634f;
-constexpr float RA_LN2 = 0.6931471805599453f;
-
-// One request's rows and context, every value brought into range (no table row
-// is as long as RA_MAX_CTX, so a context beyond it is past its table anyway).
-constexpr int RA_MAX_CTX = 1 << 30;
-struct RaReq {
-  int r0, n, ctx;
-};
-
-// Where a CTA's run of units starts: the unit inside an item.
-struct RaFound {
-  int any;          // 0: no units left for this CTA
-  int g, qt;
-  RaReq q;
-  long long off;
-};
-// The cut that a run's start makes, for the joining kernel: the item's pieces (0:
-// nothing to join here), its rows, the first one's row of the step.
-struct RaCut {
-  int pieces, rows, row0, g;
-  int first_slot;   // of the CTA before: 0 if this item was its first
-};
-
 struct RaParams {
   CUtensorMap tmQ, tmK, tmV;
   const __nv_bfloat16* kp;
@@ -111,11 +75,7 @@ struct RaParams {
   const int32_t* table;
   const int32_t* cu;
   const int32_t* ctx;
-  __nv_bfloat16* o;
-  float* lse;            // [T, Hq] or null
-  float* part_o;         // [CTA][2][32][128][4] unnormalised pieces: 4 columns of the 128 rows together
-  float* part_ml;        // [CTA][2][128][2] (max in log2 units, sum)
-  RaCut* cuts;           // [CTA]
+  RaJoin j;              // o, lse and the pieces of cut items
   int B, T, Hq, Hkv, G, TQ;
   int bs, max_blocks, n_blocks;
   int box_log;           // log2 of the rows per TMA box (8 .. 128)
@@ -123,38 +83,9 @@ struct RaParams {
   uint32_t* err;
 };
 
-__device__ __forceinline__ float ra_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // Q, K-major (two 64-column swizzle blocks of 128 rows), k-step kk of 16 columns
 __device__ __forceinline__ uint64_t ra_desc_q(uint32_t base, int kk) {
   return smem_desc_sw128(base + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024);
-}
-// Pairs of floats in one 64-bit register: one instruction for two elements.
-__device__ __forceinline__ uint64_t ra_pair(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-__device__ __forceinline__ void ra_unpair(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t ra_fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t ra_add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ float ra_max3(float a, uint32_t b, uint32_t c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
-  return d;
 }
 // K, K-major, in groups of 8 keys 2 KB apart
 __device__ __forceinline__ uint64_t ra_desc_k(uint32_t base, int kk) {
@@ -165,170 +96,6 @@ __device__ __forceinline__ uint64_t ra_desc_k(uint32_t base, int kk) {
 __device__ __forceinline__ uint64_t ra_desc_v(uint32_t base, int kk) {
   return smem_desc_sw128(base + kk * 4096, 1024, 2048);
 }
-__device__ __forceinline__ void ra_tma_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void ra_tma_4d(uint32_t dst, const void* tmap, int x, int y, int z, int w, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-      : "memory");
-}
-// 32 bytes to a 32-byte aligned address
-__device__ __forceinline__ void ra_st32(void* dst, const uint32_t (&x)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]),
-               "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-               : "memory");
-}
-__device__ __forceinline__ void ra_cp16(uint32_t dst, const void* src, bool valid) {
-  const int sz = valid ? 16 : 0;   // zero-fill
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(sz) : "memory");
-}
-
-// mbar_wait_warp for a copy warp, which is a ring ahead of the products: between
-// probes it sleeps, so that its issue slots go to the softmax warp beside it.
-__device__ __forceinline__ bool ra_wait_copy(uint32_t bar, uint32_t parity, uint32_t* err, volatile int* abort_flag) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 0; !__all_sync(0xffffffffu, mbar_test_wait(bar, parity)); ++i) {
-    __nanosleep(100);
-    if ((i & 63u) == 63u) {
-      const uint64_t t = global_timer_ns();
-      if (i == 63u) t0 = t;
-      const bool late = t - t0 > KL_WAIT_LIMIT_NS;
-      if (late) record_error(err, KL_DEVERR_TIMEOUT);
-      if (__any_sync(0xffffffffu, late || *abort_flag)) return false;
-    }
-  }
-  return true;
-}
-
-// What the walk reads of the parameters, handed over by value: a reference to
-// kernel parameters makes every access of a called function a slow generic load.
-struct RaLens {
-  const int32_t* cu;
-  const int32_t* ctx;
-  int B, T, Hkv, TQ;
-};
-__device__ __forceinline__ RaReq ra_req(const RaLens& p, int b) {
-  RaReq q;
-  q.r0 = min(max(p.cu[b], 0), p.T);
-  q.n = min(max(p.cu[b + 1], q.r0), p.T) - q.r0;
-  q.ctx = min(max(p.ctx[b], 0), RA_MAX_CTX);
-  return q;
-}
-// Key tiles of query tile qt (its last token's limit decides).
-__device__ __forceinline__ int ra_tiles(const RaReq& q, int TQ, int qt) {
-  return (q.ctx + min(q.n, (qt + 1) * TQ) - 1) / RA_BKV + 1;
-}
-// Units of query tiles 0 .. m-1, all but the request's last one:
-//   sum_{k=1}^{m} (floor((ctx - 1 + k TQ) / 128) + 1 + RA_ITEM_UNITS).
-// The quotients repeat with period 128 / gcd(TQ, 128) up to a constant step, so
-// whole periods are summed in closed form.
-__device__ __noinline__ long long ra_units_before(int ctx, int TQ, long long m) {
-  const int sh = __ffs(TQ) - 1;                   // gcd(TQ, 128) = 2^sh, TQ <= 128
-  const int period = RA_BKV >> sh, step = TQ >> sh;
-  const long long a = static_cast<long long>(ctx) - 1;
-  const long long c = m >> (7 - sh);
-  const int r = static_cast<int>(m & (period - 1));
-  long long full = 0, part = 0;
-  for (int k = 1; k <= (c ? period : r); ++k) {
-    const long long v = (a + static_cast<long long>(k) * TQ) >> 7;
-    full += v;
-    if (k <= r) part += v;
-  }
-  return m * (1 + RA_ITEM_UNITS) + (c ? c * full + static_cast<long long>(period) * step * (c * (c - 1) / 2) : 0) +
-         part + static_cast<long long>(r) * step * c;
-}
-__device__ __forceinline__ long long ra_head_units(const RaReq& q, int TQ) {
-  if (q.n <= 0) return 0;
-  if (q.n <= TQ) return (q.ctx + q.n - 1) / RA_BKV + 1 + RA_ITEM_UNITS;
-  const int QT = (q.n + TQ - 1) / TQ;
-  return ra_units_before(q.ctx, TQ, QT - 1) + ra_tiles(q, TQ, QT - 1) + RA_ITEM_UNITS;
-}
-
-// Quotient of non-negative numbers; most fit 32 bits, whose division is several times faster.
-__device__ __noinline__ long long ra_div(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
-
-// One piece of a CTA's run: the query tile and the range of its key tiles.
-struct RaPiece {
-  int b, g;                // request, kv head
-  int row0, toks;          // the tile's first row of the step, its tokens
-  int pos0, L;             // position of its first token; keys that its last one sees
-  int ta, tb;              // key tiles; tb = 0: there is no such piece
-  int flags;               // 1: all of the item's tiles; 2: the piece goes to slot 1
-};
-// The walk over a CTA's run. Every role's warp walks for itself, in shared
-// memory: the softmax warps' registers are full of scores, and every one more
-// costs their steps (with the walk in registers they spilled).
-struct RaWalk {
-  int b, g, qt;            // request (its lengths: q), kv head, query tile
-  int idx;                 // items met so far: the first one's pieces take slot 0, a later one's slot 1
-  RaReq q;
-  long long off, left;     // unit inside the item, units left of the run
-};
-// The next piece with at least one key tile into c.
-__device__ __forceinline__ void ra_step(const RaLens& p, RaWalk& w, RaPiece& c) {
-  c.tb = 0;
-  while (w.left > 0) {
-    const int tiles = ra_tiles(w.q, p.TQ, w.qt);
-    const int len = tiles + RA_ITEM_UNITS, off = static_cast<int>(w.off);
-    const int e = static_cast<int>(min(w.left, static_cast<long long>(len - off))) + off;
-    const int first = w.qt * p.TQ;
-    c.ta = max(off - RA_ITEM_UNITS, 0);
-    c.tb = max(e - RA_ITEM_UNITS, 0);
-    c.b = w.b;
-    c.g = w.g;
-    c.row0 = w.q.r0 + first;
-    c.toks = min(p.TQ, w.q.n - first);
-    c.pos0 = w.q.ctx + first;
-    c.L = c.pos0 + c.toks;
-    c.flags = (c.ta == 0 && c.tb == tiles ? 1 : 0) | (w.idx > 0 ? 2 : 0);
-    w.left -= e - off;
-    ++w.idx;
-    if (w.left > 0) {      // the item ends here: on to the next
-      w.off = 0;
-      if (first + p.TQ < w.q.n) {
-        ++w.qt;
-      } else {
-        w.qt = 0;
-        if (++w.g == p.Hkv) {
-          w.g = 0;
-          do {
-            if (++w.b >= p.B) {      // cannot happen: the run lies inside the W units
-              w.left = 0;
-              break;
-            }
-            w.q = ra_req(p, w.b);
-          } while (w.q.n <= 0);
-        }
-      }
-    }
-    if (c.tb > c.ta) break;
-    c.tb = 0;
-  }
-}
-// The same for a walk in shared memory, called by one lane: one copy of the code
-// for all roles.
-__device__ __noinline__ void ra_next(const RaLens p, const RaWalk& from, RaWalk& to, RaPiece& piece) {
-  if (from.left <= 0) {
-    piece.tb = 0;
-    return;
-  }
-  RaWalk w = from;         // in registers: one read, one write each
-  RaPiece c;
-  ra_step(p, w, c);
-  to = w;
-  piece = c;
-}
-
 template <bool TMA>
 __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid_constant__ RaParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -396,66 +163,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
   pdl_enter();
 
   // ---- this CTA's run: prefix sums of the requests' units, then the item at unit cta * P ----
-  long long P;
-  {
-    const int per = (p.B + RA_THREADS - 1) / RA_THREADS;
-    const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
-    long long mine = 0, units = 0;
-    RaReq q = {0, 0, 0};
-    for (int b = b0; b < b1; ++b) {
-      q = ra_req(lens, b);
-      units = ra_head_units(q, p.TQ);
-      mine += units * p.Hkv;
-    }
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 31) wsum[warp] = incl;
-    __syncthreads();
-    long long before = 0, W = 0;
-#pragma unroll
-    for (int w = 0; w < RA_WARPS; ++w) {
-      const long long v = wsum[w];
-      if (w < warp) before += v;
-      W += v;
-    }
-    P = max(ra_div(W + ctas - 1, ctas), 1LL);
-    const long long u0 = cta * P;
-    if (threadIdx.x == 0 && u0 >= W) {
-      found->any = 0;
-      pieces[0].tb = 0;
-    }
-    long long lo = before + incl - mine;      // units before this thread's requests
-    if (mine > 0 && u0 >= lo && u0 < lo + mine) {
-      int b = b0;
-      if (per > 1) {                          // with one request a thread q and units are its own still
-        for (;; ++b) {
-          q = ra_req(lens, b);
-          units = ra_head_units(q, p.TQ);
-          if (u0 < lo + units * p.Hkv) break;
-          lo += units * p.Hkv;
-        }
-      }
-      const int g = static_cast<int>(ra_div(u0 - lo, units));
-      const long long y = u0 - lo - g * units;
-      int m0 = 0, m1 = q.n <= p.TQ ? 1 : (q.n + p.TQ - 1) / p.TQ;   // the query tile: units_before(m0) <= y < units_before(m1)
-      while (m1 - m0 > 1) {
-        const int m = (m0 + m1) >> 1;
-        if (ra_units_before(q.ctx, p.TQ, m) <= y) m0 = m; else m1 = m;
-      }
-      const long long off = y - (m0 ? ra_units_before(q.ctx, p.TQ, m0) : 0);
-      // the walk to the first piece, for every role at once
-      RaWalk w = {b, g, m0, 0, q, off, min(P, W - u0)};
-      RaPiece c;
-      ra_step(lens, w, c);
-      pieces[0] = c;
-      walks[0] = w;
-      *found = {1, g, m0, q, off};
-    }
-  }
+  const long long P = ra_find_run<RA_WARPS>(lens, cta, ctas, wsum, found, &pieces[0], &walks[0]);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -694,7 +402,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
         cut.g = f.g;
         cut.first_slot = f.off - P >= 0 ? 0 : 1;
       }
-      p.cuts[cta] = cut;
+      p.j.cuts[cta] = cut;
     }
     __syncwarp();
     bool ok = true;
@@ -851,7 +559,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
           if (mine && whole) {
             // whole 32-byte sectors: rows lie apart, and an SM writes ~0.7 sectors a
             // cycle whether they are full or not (16-byte stores took twice as long)
-            __nv_bfloat16* orow_p = p.o + orow * RA_D + h * 32;
+            __nv_bfloat16* orow_p = p.j.o + orow * RA_D + h * 32;
 #pragma unroll
             for (int e = 0; e < 32; e += 16) {
               uint32_t x[8];
@@ -861,7 +569,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
               ra_st32(orow_p + e, x);
             }
           } else if (mine) {
-            float* po = p.part_o + (pslot * RA_D + h * 32) * RA_BQ + r * 4;      // lanes side by side
+            float* po = p.j.part_o + (pslot * RA_D + h * 32) * RA_BQ + r * 4;      // lanes side by side
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
               *reinterpret_cast<uint4*>(po + e * RA_BQ) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
@@ -870,9 +578,9 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
         }
         if (mine) {
           if (whole) {
-            if (p.lse) p.lse[orow] = (m + log2f(l)) * RA_LN2;
+            if (p.j.lse) p.j.lse[orow] = (m + log2f(l)) * RA_LN2;
           } else {
-            *reinterpret_cast<float2*>(p.part_ml + (pslot * RA_BQ + r) * 2) = make_float2(m, l);
+            *reinterpret_cast<float2*>(p.j.part_ml + (pslot * RA_BQ + r) * 2) = make_float2(m, l);
           }
         }
       }
@@ -903,7 +611,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
 // 34.1), 1 of 256 was as fast without cuts but 72 against 63 us on the mixed batch.
 constexpr int RC_THREADS = 128, RC_SPLIT = 4, RC_COLS = 8;
 static_assert(RA_D / RC_SPLIT / RC_COLS == RC_THREADS / 32, "a warp per 8 of a CTA's columns");
-__global__ void __launch_bounds__(RC_THREADS, 5) ragged_combine_kernel(const __grid_constant__ RaParams p) {
+__global__ void __launch_bounds__(RC_THREADS, 5) ragged_combine_kernel(const __grid_constant__ RaJoin p) {
   pdl_enter();
   const int c = blockIdx.x / RC_SPLIT + 1;
   const RaCut st = p.cuts[c];
@@ -972,30 +680,6 @@ __global__ void __launch_bounds__(RC_THREADS, 5) ragged_combine_kernel(const __g
   }
 }
 
-kl_status ra_map(CUtensorMap* m, int rank, const void* ptr, const cuuint64_t* dims, const cuuint64_t* strides,
-                 const cuuint32_t* box) {
-  auto fn = tensor_map_encoder();
-  if (!fn) return set_error(KL_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return set_error(KL_ERR_INVALID_ARG, "ragged attention: tensor map encode failed (%d)", (int)r);
-  return KL_OK;
-}
-
-struct RaWs {
-  size_t o, ml, cuts, total;
-};
-RaWs ra_ws(int ctas) {
-  RaWs w;
-  w.o = 0;
-  w.ml = w.o + static_cast<size_t>(ctas) * 2 * RA_BQ * RA_D * 4;
-  w.cuts = w.ml + align_up(static_cast<size_t>(ctas) * 2 * RA_BQ * 2 * 4, 256);
-  w.total = w.cuts + align_up(static_cast<size_t>(ctas) * sizeof(RaCut), 256);
-  return w;
-}
-
 }  // namespace
 
 size_t ragged_attention_ws() { return ra_ws(num_sms()).total; }
@@ -1009,7 +693,7 @@ kl_status ragged_attention(const kl_ragged_cfg& rc, int Hq, int Hkv, const void*
     return set_error(KL_ERR_NO_MEMORY, "ragged attention: workspace too small or not 256-byte aligned");
   RaParams p;
   memset(&p, 0, sizeof(p));
-  p.G = Hq / Hkv;
+  p.G = p.j.G = Hq / Hkv;
   p.TQ = RA_BQ / p.G;
   const bool tma = rc.block_size % 8 == 0;
   p.box_log = 7;
@@ -1018,7 +702,7 @@ kl_status ragged_attention(const kl_ragged_cfg& rc, int Hq, int Hkv, const void*
     const cuuint64_t dq[3] = {RA_D, static_cast<cuuint64_t>(Hq), static_cast<cuuint64_t>(rc.T)};
     const cuuint64_t sq[2] = {RA_D * 2, static_cast<cuuint64_t>(Hq) * RA_D * 2};
     const cuuint32_t bq[3] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(p.TQ)};
-    KL_TRY(ra_map(&p.tmQ, 3, q, dq, sq, bq));
+    KL_TRY(ra_map(&p.tmQ, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dq, sq, bq));
   }
   if (tma) {
     // (64 columns, 8 rows, column blocks, groups of 8 rows)
@@ -1027,23 +711,23 @@ kl_status ragged_attention(const kl_ragged_cfg& rc, int Hq, int Hkv, const void*
                               static_cast<cuuint64_t>(rc.n_blocks) * rc.block_size / 8};
     const cuuint64_t sk[3] = {pitch, 128, 8 * pitch};
     const cuuint32_t bk[4] = {64, 8, 2, 1u << (p.box_log - 3)};
-    KL_TRY(ra_map(&p.tmK, 4, kp, dk, sk, bk));
-    KL_TRY(ra_map(&p.tmV, 4, vp, dk, sk, bk));
+    KL_TRY(ra_map(&p.tmK, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, kp, dk, sk, bk));
+    KL_TRY(ra_map(&p.tmV, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, vp, dk, sk, bk));
   }
   p.kp = static_cast<const __nv_bfloat16*>(kp);
   p.vp = static_cast<const __nv_bfloat16*>(vp);
   p.table = table;
   p.cu = cu;
   p.ctx = ctx;
-  p.o = static_cast<__nv_bfloat16*>(o);
-  p.lse = lse;
+  p.j.o = static_cast<__nv_bfloat16*>(o);
+  p.j.lse = lse;
   uint8_t* wb = static_cast<uint8_t*>(ws);
-  p.part_o = reinterpret_cast<float*>(wb + lay.o);
-  p.part_ml = reinterpret_cast<float*>(wb + lay.ml);
-  p.cuts = reinterpret_cast<RaCut*>(wb + lay.cuts);
+  p.j.part_o = reinterpret_cast<float*>(wb + lay.o);
+  p.j.part_ml = reinterpret_cast<float*>(wb + lay.ml);
+  p.j.cuts = reinterpret_cast<RaCut*>(wb + lay.cuts);
   p.B = rc.B;
   p.T = rc.T;
-  p.Hq = Hq;
+  p.Hq = p.j.Hq = Hq;
   p.Hkv = Hkv;
   p.bs = rc.block_size;
   p.max_blocks = rc.max_blocks;
@@ -1069,9 +753,13 @@ kl_status ragged_attention(const kl_ragged_cfg& rc, int Hq, int Hkv, const void*
       launch_pdl(ragged_attn_kernel<false>, ctas, RA_THREADS, RA_SMEM, st, p);
   }
   KL_CUDA(cudaGetLastError());
+  return ragged_join(p.j, ctas, st);
+}
+
+kl_status ragged_join(const RaJoin& j, int ctas, cudaStream_t st) {
   if (ctas > 1) {
     ProfScope ps("ragged_combine", st, 0.0, 4.0 * ctas * RA_D);
-    launch_pdl(ragged_combine_kernel, (ctas - 1) * RC_SPLIT, RC_THREADS, 0, st, p);
+    launch_pdl(ragged_combine_kernel, (ctas - 1) * RC_SPLIT, RC_THREADS, 0, st, j);
     KL_CUDA(cudaGetLastError());
   }
   return KL_OK;
