@@ -24,8 +24,11 @@
 //
 // Roles (8 warps): warp 0 copies the keys, warp 1 the values and looks up the scales,
 // warp 2 issues the score products and, between two of them, splits the next piece's
-// queries, warp 3 issues the P V products, warps 4..7 are the softmax (thread = query row
-// = TMEM lane; idle at first, they split the first piece's queries). Barriers, stages and buffers as in the bf16
+// queries, warp 3 issues the P V products, warps 4..11 are the softmax (thread = query row
+// = TMEM lane and half of the tile's keys; idle at first, they split the first piece's
+// queries). Two warps share an SM quarter's instruction issue, which one could not fill:
+// with four softmax warps a step took 2900 cycles. They tell each other their row maxima.
+// Barriers, stages and buffers as in the bf16
 // kernel. A key tile of 16 KB is 16 groups of 8 keys x 128 bytes (one swizzle atom each);
 // with block_size a multiple of 8 it is 128 / box TMA boxes, box = gcd(block_size, 128),
 // and a scale serves whole groups; other block sizes go row by row with 16-byte cp.async
@@ -40,7 +43,7 @@
 namespace kl {
 namespace {
 
-constexpr int A8_WARPS = 8;
+constexpr int A8_WARPS = 12;
 constexpr int A8_THREADS = 32 * A8_WARPS;
 constexpr uint32_t A8_TILE = 128 * 128;       // a tile of keys, of values, of one part of the queries
 constexpr int A8_NST = 4;                     // stages of the K and of the V ring
@@ -49,8 +52,9 @@ constexpr uint32_t A8_OFF_Q = 0;              // two pieces' queries, high and l
 constexpr uint32_t A8_OFF_K = A8_OFF_Q + 4 * A8_TILE;
 constexpr uint32_t A8_OFF_V = A8_OFF_K + A8_NST * A8_TILE;
 constexpr uint32_t A8_OFF_BAR = A8_OFF_V + A8_NST * A8_TILE;
-constexpr uint32_t A8_OFF_QS = A8_OFF_BAR + 2048;           // the rows' factors, of four pieces
-constexpr uint32_t A8_OFF_SC = A8_OFF_QS + 4 * RA_BQ * 4;   // the ring of scales
+constexpr uint32_t A8_OFF_QS = A8_OFF_BAR + 2560;           // the rows' factors, of four pieces
+constexpr uint32_t A8_OFF_X = A8_OFF_QS + 4 * RA_BQ * 4;    // what the halves of a row tell each other
+constexpr uint32_t A8_OFF_SC = A8_OFF_X + 4 * RA_BQ * 4;    // the ring of scales
 constexpr size_t a8_smem(bool tma) { return 1024 + A8_OFF_SC + A8_SCR * 3 * (tma ? 16 : 128) * 4; }
 // Tensor memory: S of two steps, P of two steps (high and low parts), O: all 512 columns.
 constexpr uint32_t A8_TM_P = 256, A8_TM_O = 384;
@@ -117,13 +121,14 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
   auto p_done = [&](int s) { return bar + 224 + 8 * s; };   // O += P_n V_n computed
   auto sc_full = [&](int n) { return bar + 240 + 8 * (n & (A8_SCR - 1)); };    // the tile's scales written
   const uint32_t drain = bar + 272, drain_pv = bar + 280, q_first = bar + 288;   // the first piece's queries
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + A8_OFF_BAR + 304);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + A8_OFF_BAR + 308);
-  RaFound* found = reinterpret_cast<RaFound*>(smem + A8_OFF_BAR + 320);
-  long long* wsum = reinterpret_cast<long long*>(smem + A8_OFF_BAR + 384);
-  RaWalk* walks = reinterpret_cast<RaWalk*>(smem + A8_OFF_BAR + 448);        // the finder's, then one per warp
-  RaPiece* pieces = reinterpret_cast<RaPiece*>(smem + A8_OFF_BAR + 960);    // the first one, then two per warp
-  static_assert(sizeof(RaFound) <= 64 && A8_WARPS * 8 <= 64 && (A8_WARPS + 1) * sizeof(RaWalk) <= 512 && (A8_WARPS * 2 + 1) * sizeof(RaPiece) <= 1088,
+  auto told = [&](int q, int x) { return bar + 296 + 16 * q + 8 * (x & 1); };   // both halves of quarter q's rows have spoken
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + A8_OFF_BAR + 360);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + A8_OFF_BAR + 364);
+  RaFound* found = reinterpret_cast<RaFound*>(smem + A8_OFF_BAR + 368);
+  long long* wsum = reinterpret_cast<long long*>(smem + A8_OFF_BAR + 432);
+  RaWalk* walks = reinterpret_cast<RaWalk*>(smem + A8_OFF_BAR + 528);        // the finder's, then one per warp
+  RaPiece* pieces = reinterpret_cast<RaPiece*>(smem + A8_OFF_BAR + 1152);    // the first one, then two per warp
+  static_assert(sizeof(RaFound) <= 64 && A8_WARPS * 8 <= 96 && (A8_WARPS + 1) * sizeof(RaWalk) <= 624 && (A8_WARPS * 2 + 1) * sizeof(RaPiece) <= 1408,
                 "shared-memory layout");
   float* qscale = reinterpret_cast<float*>(smem + A8_OFF_QS);
   constexpr int GRP = TMA ? 8 : 1;               // keys that share a scale
@@ -136,7 +141,8 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
 
   if (warp == 3 && lane == 0) {
     for (int k = 0; k < 4; ++k) mbar_init(q_full(k), 1);
-    mbar_init(q_first, 4);
+    mbar_init(q_first, 8);
+    for (int k = 0; k < 8; ++k) mbar_init(told(k >> 1, k), 2);
     for (int k = 0; k < 2; ++k) mbar_init(q_empty(k), 1);
     for (int s = 0; s < A8_NST; ++s) {
       mbar_init(k_full(s), TMA ? 1 : 32);
@@ -146,8 +152,8 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(s_full(s), 1);
-      mbar_init(s_free(s), 4);
-      mbar_init(p_full(s), 4);
+      mbar_init(s_free(s), 8);
+      mbar_init(p_full(s), 8);
       mbar_init(p_done(s), 1);
     }
     for (int n = 0; n < A8_SCR; ++n) mbar_init(sc_full(n), 1);
@@ -470,29 +476,31 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
     mbar_wait(drain_pv, 0, p.err);
   } else {
     // ---------------- softmax / correction / epilogue ----------------
-    const int quarter = warp & 3;
+    const int quarter = warp & 3, half = (warp >> 2) - 1;
     const int r = quarter * 32 + lane;           // row within the tile = TMEM lane
+    constexpr int KEYS = RA_BKV / 2;             // keys 64 half .. 64 half + 63 of each tile
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t oadr = tmO + lane_off, padr = tmP + lane_off;
+    const uint32_t oadr = tmO + lane_off + half * 64, padr = tmP + lane_off + half * 16;
+    float* said = reinterpret_cast<float*>(smem + A8_OFF_X);    // [exchange % 2][half][row]
     // The tile that holds the last key the query tile sees: its value rows behind it become zero
-    // (each of the four warps its 32).
+    // (each of the eight warps half of its 32).
     auto clear_tail = [&](int end, int n) -> bool {
       if (end >= RA_BKV) return true;
       const int vs = n % A8_NST;
       if (!mbar_wait_warp(v_full(vs), (n / A8_NST) & 1, p.err, abort_flag)) return false;
       if (r >= end) {
-        const uint32_t va = sb + A8_OFF_V + vs * A8_TILE + r * 128;
+        const uint32_t va = sb + A8_OFF_V + vs * A8_TILE + r * 128 + half * 64;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) st_shared_v4(va + c * 16, 0u, 0u, 0u, 0u);
+        for (int c = 0; c < 4; ++c) st_shared_v4(va + c * 16, 0u, 0u, 0u, 0u);
       }
       fence_async_shared();
       return true;
     };
     bool more = find(0);
     if (more) {
-      // the first piece's queries, each warp its 32 rows
+      // the first piece's queries, each warp 16 rows
       const RaPiece& c = piece(0);
-      const int r0 = quarter * 32, rows = min(c.toks * p.G, r0 + 32);
+      const int r0 = quarter * 32 + half * 16, all = c.toks * p.G, rows = min(all, r0 + 16);
       for (int at = r0; at < rows; at += 8) {
         uint4 x[4];
 #pragma unroll
@@ -500,13 +508,13 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
 #pragma unroll
         for (int u = 0; u < 4; ++u) split_q(x[u], 0, rows, at + 2 * u);
       }
-      if (r >= rows) qscale[r] = 0.f;              // no row: no factor
+      if (half == 0 && r >= all) qscale[r] = 0.f;  // no row: no factor
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_first);
     }
     // the cut at this CTA's start, by a warp that has little to do yet
-    if (warp == 7 && lane == 31) {
+    if (warp == 11 && lane == 31) {
       RaCut cut = {0, 0, 0, 0, 0};
       if (found->any) {
         const RaFound f = *found;
@@ -522,10 +530,21 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
     }
     __syncwarp();
     bool ok = true;
-    int n = 0;
-    float m = -INFINITY, l = 0.f;                  // the row's running max of t (log2 units) and sum of P' / b
+    int n = 0, x = 0;                              // steps and exchanges so far
+    float m = -INFINITY, l = 0.f;                  // the row's running max of t (log2 units), this half's sum of P' / b
     float rs = 0.f;                                // the row's factor: score in log2 units = S * rs * a
-    int lim = 0, end = 0;                          // the row's last key and the end of the query tile's, from the tile's first key
+    int lim = 0, end = 0;                          // the row's last key, from this half's first; the end of the query tile's, from the tile's
+    // v to the other half of the row, the other half's into v
+    auto exchange = [&](float& v) -> bool {
+      float* at = said + (x & 1) * 2 * RA_BQ + r;
+      at[half * RA_BQ] = v;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(told(quarter, x));
+      if (!mbar_wait_warp(told(quarter, x), (x >> 1) & 1, p.err, abort_flag)) return false;
+      v = at[(half ^ 1) * RA_BQ];
+      ++x;
+      return true;
+    };
     // One step of a warp with rows. CUT: some row of the tile ends inside its keys.
     auto step = [&](auto cut, bool first) -> bool {
       constexpr bool CUT = decltype(cut)::value;
@@ -533,17 +552,35 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       if (CUT && TMA && !clear_tail(end, n)) return false;
       if (!mbar_wait_warp(s_full(s), (n >> 1) & 1, p.err, abort_flag)) return false;
       tc_fence_after();
-      const uint32_t sadr = tmem + lane_off + s * 128;
-      uint32_t sv[RA_BKV];
+      const uint32_t sadr = tmem + lane_off + s * 128 + half * KEYS;
+      uint32_t sv[KEYS];
       tmem_ld_32x32b_x32(sadr, *reinterpret_cast<uint32_t(*)[32]>(sv));
       tmem_ld_32x32b_x32(sadr + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
-      tmem_ld_32x32b_x32(sadr + 64, *reinterpret_cast<uint32_t(*)[32]>(sv + 64));
-      tmem_ld_32x32b_x32(sadr + 96, *reinterpret_cast<uint32_t(*)[32]>(sv + 96));
       // P's columns are free once the product of step n - 2 is done: probed here,
       // where the probe's latency costs nothing, and most likely it is
       const uint32_t done_ph = ((n >> 1) & 1) ^ 1u;
       const bool p_ready = n < 2 || mbar_test_wait(p_done(s), done_ph);
       const bool sc_ok = mbar_wait_warp(sc_full(n), (n / A8_SCR) & 1, p.err, abort_flag);
+      // this half's scales; what takes S of a group to the score (with keys cut off never zero, so
+      // that their -inf stays)
+      constexpr int HG = KEYS / GRP;
+      const uint32_t sca = sc0 + (n & (A8_SCR - 1)) * 3 * NG * 4 + half * HG * 4;
+      auto factor = [&](float a) { return CUT ? a8_max_nan(rs * a, 1.17549435e-38f) : rs * a; };
+      float f[TMA ? HG : 1], lb[TMA ? HG : 1];
+      if (TMA && sc_ok) {
+#pragma unroll
+        for (int g = 0; g < HG; g += 4) {
+          const float4 a4 = a8_ld4(sca + g * 4), l4 = a8_ld4(sca + (NG + g) * 4);
+          f[g % (TMA ? HG : 1)] = factor(a4.x);
+          f[(g + 1) % (TMA ? HG : 1)] = factor(a4.y);
+          f[(g + 2) % (TMA ? HG : 1)] = factor(a4.z);
+          f[(g + 3) % (TMA ? HG : 1)] = factor(a4.w);
+          lb[g % (TMA ? HG : 1)] = l4.x;
+          lb[(g + 1) % (TMA ? HG : 1)] = l4.y;
+          lb[(g + 2) % (TMA ? HG : 1)] = l4.z;
+          lb[(g + 3) % (TMA ? HG : 1)] = l4.w;
+        }
+      }
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
@@ -551,42 +588,40 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       if (lane == 0) mbar_arrive(s_free(s));       // S[s] may be overwritten from here on
       if (CUT) {                                   // keys 0 .. lim are kept
 #pragma unroll
-        for (int e = 0; e < RA_BKV; ++e)
+        for (int e = 0; e < KEYS; ++e)
           if (e > lim) sv[e] = __float_as_uint(-INFINITY);
       }
-      const uint32_t sca = sc0 + (n & (A8_SCR - 1)) * 3 * NG * 4;
-      // what takes S of group g to the score: never zero, so that -inf stays
-      auto factor = [&](float a) { return a8_max_nan(rs * a, 1.17549435e-38f); };
       float mx = -INFINITY;
       if (TMA) {
+        float t[8];
 #pragma unroll
-        for (int g = 0; g < NG; g += 4) {
-          const float4 a = a8_ld4(sca + g * 4), lb = a8_ld4(sca + (NG + g) * 4);
-          float t[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const uint32_t* x = sv + ((g + u) * GRP) % RA_BKV;
-            float y = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1 % GRP]));
-            y = ra_max3(y, x[2 % GRP], x[3 % GRP]);
-            y = ra_max3(y, x[4 % GRP], x[5 % GRP]);
-            y = ra_max3(y, x[6 % GRP], x[7 % GRP]);
-            t[u] = fmaf(y, factor(u == 0 ? a.x : u == 1 ? a.y : u == 2 ? a.z : a.w), u == 0 ? lb.x : u == 1 ? lb.y : u == 2 ? lb.z : lb.w);
-          }
-          mx = ra_max3(mx, __float_as_uint(t[0]), __float_as_uint(t[1]));
-          mx = ra_max3(mx, __float_as_uint(t[2]), __float_as_uint(t[3]));
+        for (int g = 0; g < 8; ++g) {
+          const uint32_t* y = sv + g * 8;
+          float v = fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
+          v = ra_max3(v, y[2], y[3]);
+          v = ra_max3(v, y[4], y[5]);
+          v = ra_max3(v, y[6], y[7]);
+          t[g] = fmaf(v, f[g % (TMA ? HG : 1)], lb[g % (TMA ? HG : 1)]);
         }
+#pragma unroll
+        for (int g = 0; g < 8; g += 2) mx = ra_max3(mx, __float_as_uint(t[g]), __float_as_uint(t[g + 1]));
       } else {
         // t itself, in place of S
 #pragma unroll
-        for (int e = 0; e < RA_BKV; e += 4) {
-          const float4 a = a8_ld4(sca + e * 4), lb = a8_ld4(sca + (RA_BKV + e) * 4);
-          float t[4] = {fmaf(__uint_as_float(sv[e]), factor(a.x), lb.x), fmaf(__uint_as_float(sv[e + 1]), factor(a.y), lb.y),
-                        fmaf(__uint_as_float(sv[e + 2]), factor(a.z), lb.z), fmaf(__uint_as_float(sv[e + 3]), factor(a.w), lb.w)};
+        for (int e = 0; e < KEYS; e += 4) {
+          const float4 a4 = a8_ld4(sca + e * 4), l4 = a8_ld4(sca + (NG + e) * 4);
+          float t[4] = {fmaf(__uint_as_float(sv[e]), factor(a4.x), l4.x), fmaf(__uint_as_float(sv[e + 1]), factor(a4.y), l4.y),
+                        fmaf(__uint_as_float(sv[e + 2]), factor(a4.z), l4.z), fmaf(__uint_as_float(sv[e + 3]), factor(a4.w), l4.w)};
           mx = ra_max3(mx, __float_as_uint(t[0]), __float_as_uint(t[1]));
           mx = ra_max3(mx, __float_as_uint(t[2]), __float_as_uint(t[3]));
 #pragma unroll
           for (int u = 0; u < 4; ++u) sv[e + u] = __float_as_uint(t[u]);
         }
+      }
+      {
+        float other = mx;
+        if (!exchange(other)) return false;
+        mx = fmaxf(mx, other);
       }
       // A row of a later piece's tile can be fully masked (its token ends before these
       // keys): mx = -inf, and m stays -inf.
@@ -600,7 +635,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
           if (!mbar_wait_warp(p_done(s ^ 1), ((n - 1) >> 1) & 1, p.err, abort_flag)) return false;
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
+          for (int c = 0; c < 4; ++c) {            // this half's columns of O
             uint32_t v[16];
             tmem_ld_32x32b_x16(oadr + c * 16, v);
             tmem_ld_wait();
@@ -612,63 +647,56 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       }
       const float neg = m > -INFINITY ? A8_LIFT - m : 0.f;
       uint64_t r0 = 0, r1 = 0;
-      if (!__all_sync(0xffffffffu, p_ready) && !mbar_wait_warp(p_done(s), done_ph, p.err, abort_flag)) return false;
-      tc_fence_after();
+      uint32_t ph[16], pl[16];
+      // four weights: their sum's halves, both parts
+      auto weights = [&](int w, uint64_t x0, uint64_t x1, uint64_t& y0, uint64_t& y1) {
+        float p0, p1, p2, p3;
+        ra_unpair(x0, p0, p1);
+        ra_unpair(x1, p2, p3);
+        const uint32_t u0 = __float_as_uint(ra_ex2(p0)), u1 = __float_as_uint(ra_ex2(p1)), u2 = __float_as_uint(ra_ex2(p2)), u3 = __float_as_uint(ra_ex2(p3));
+        y0 = ra_pair(u0, u1);
+        y1 = ra_pair(u2, u3);
+        // four bits kept, the rest rounded to four
+        constexpr uint32_t KEEP = 0xfff00000u;
+        ph[w] = e4m3x4(__uint_as_float(u0 & KEEP), __uint_as_float(u1 & KEEP), __uint_as_float(u2 & KEEP), __uint_as_float(u3 & KEEP));
+        float d0, d1, d2, d3;
+        ra_unpair(a8_sub2(y0, ra_pair(u0 & KEEP, u1 & KEEP)), d0, d1);
+        ra_unpair(a8_sub2(y1, ra_pair(u2 & KEEP, u3 & KEEP)), d2, d3);
+        pl[w] = e4m3x4(d0, d1, d2, d3);
+      };
+      if (TMA) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t ph[16], pl[16];
-        // four weights: their sum's halves, both parts
-        auto weights = [&](int w, uint64_t x0, uint64_t x1, uint64_t& y0, uint64_t& y1) {
-          float p0, p1, p2, p3;
-          ra_unpair(x0, p0, p1);
-          ra_unpair(x1, p2, p3);
-          const uint32_t u0 = __float_as_uint(ra_ex2(p0)), u1 = __float_as_uint(ra_ex2(p1)), u2 = __float_as_uint(ra_ex2(p2)), u3 = __float_as_uint(ra_ex2(p3));
-          y0 = ra_pair(u0, u1);
-          y1 = ra_pair(u2, u3);
-          // four bits kept, the rest rounded to four
-          constexpr uint32_t KEEP = 0xfff00000u;
-          ph[w] = e4m3x4(__uint_as_float(u0 & KEEP), __uint_as_float(u1 & KEEP), __uint_as_float(u2 & KEEP), __uint_as_float(u3 & KEEP));
-          float d0, d1, d2, d3;
-          ra_unpair(a8_sub2(y0, ra_pair(u0 & KEEP, u1 & KEEP)), d0, d1);
-          ra_unpair(a8_sub2(y1, ra_pair(u2 & KEEP, u3 & KEEP)), d2, d3);
-          pl[w] = e4m3x4(d0, d1, d2, d3);
-        };
-        if (TMA) {
-#pragma unroll
-          for (int g = half * (NG / 2); g < (half + 1) * (NG / 2); g += 4) {
-            const float4 a = a8_ld4(sca + g * 4), lb = a8_ld4(sca + (NG + g) * 4), ib = a8_ld4(sca + (2 * NG + g) * 4);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const uint32_t* x = sv + ((g + u) * GRP) % RA_BKV;
-              const uint32_t f = __float_as_uint(factor(u == 0 ? a.x : u == 1 ? a.y : u == 2 ? a.z : a.w));
-              const uint32_t c = __float_as_uint((u == 0 ? lb.x : u == 1 ? lb.y : u == 2 ? lb.z : lb.w) + neg);
-              const uint32_t iv = __float_as_uint(u == 0 ? ib.x : u == 1 ? ib.y : u == 2 ? ib.z : ib.w);
-              const uint64_t f2 = ra_pair(f, f), c2 = ra_pair(c, c), iv2 = ra_pair(iv, iv);
-              uint64_t y0, y1, y2, y3;
-              weights(2 * (g + u) % 16, ra_fma2(ra_pair(x[0], x[1 % GRP]), f2, c2), ra_fma2(ra_pair(x[2 % GRP], x[3 % GRP]), f2, c2), y0, y1);
-              weights((2 * (g + u) + 1) % 16, ra_fma2(ra_pair(x[4 % GRP], x[5 % GRP]), f2, c2), ra_fma2(ra_pair(x[6 % GRP], x[7 % GRP]), f2, c2), y2, y3);
-              r0 = ra_fma2(ra_add2(y0, y1), iv2, r0);
-              r1 = ra_fma2(ra_add2(y2, y3), iv2, r1);
-            }
-          }
-        } else {
-          const uint64_t neg2 = ra_pair(__float_as_uint(neg), __float_as_uint(neg));
-#pragma unroll
-          for (int e = half * 64; e < half * 64 + 64; e += 4) {
-            const float4 ib = a8_ld4(sca + (2 * RA_BKV + e) * 4);
-            uint64_t y0, y1;
-            weights(e / 4 % 16, ra_add2(ra_pair(sv[e], sv[e + 1]), neg2), ra_add2(ra_pair(sv[e + 2], sv[e + 3]), neg2), y0, y1);
-            r0 = ra_fma2(y0, ra_pair(__float_as_uint(ib.x), __float_as_uint(ib.y)), r0);
-            r1 = ra_fma2(y1, ra_pair(__float_as_uint(ib.z), __float_as_uint(ib.w)), r1);
-          }
+        for (int g = 0; g < 8; ++g) {
+          const uint32_t* v = sv + g * 8;
+          float ib;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ib) : "r"(sca + (2 * NG + g) * 4));
+          const uint32_t fu = __float_as_uint(f[g % (TMA ? HG : 1)]), cu = __float_as_uint(lb[g % (TMA ? HG : 1)] + neg), iu = __float_as_uint(ib);
+          const uint64_t f2 = ra_pair(fu, fu), c2 = ra_pair(cu, cu), iv2 = ra_pair(iu, iu);
+          uint64_t y0, y1, y2, y3;
+          weights(2 * g, ra_fma2(ra_pair(v[0], v[1]), f2, c2), ra_fma2(ra_pair(v[2], v[3]), f2, c2), y0, y1);
+          weights(2 * g + 1, ra_fma2(ra_pair(v[4], v[5]), f2, c2), ra_fma2(ra_pair(v[6], v[7]), f2, c2), y2, y3);
+          r0 = ra_fma2(ra_add2(y0, y1), iv2, r0);
+          r1 = ra_fma2(ra_add2(y2, y3), iv2, r1);
         }
-        tmem_st_32x32b_x16(padr + s * 64 + half * 16, ph);
-        tmem_st_32x32b_x16(padr + s * 64 + 32 + half * 16, pl);
+      } else {
+        const uint64_t neg2 = ra_pair(__float_as_uint(neg), __float_as_uint(neg));
+#pragma unroll
+        for (int e = 0; e < KEYS; e += 4) {
+          const float4 ib = a8_ld4(sca + (2 * NG + e) * 4);
+          uint64_t y0, y1;
+          weights(e / 4, ra_add2(ra_pair(sv[e], sv[e + 1]), neg2), ra_add2(ra_pair(sv[e + 2], sv[e + 3]), neg2), y0, y1);
+          r0 = ra_fma2(y0, ra_pair(__float_as_uint(ib.x), __float_as_uint(ib.y)), r0);
+          r1 = ra_fma2(y1, ra_pair(__float_as_uint(ib.z), __float_as_uint(ib.w)), r1);
+        }
       }
       float a0, a1, a2, a3;
       ra_unpair(r0, a0, a1);
       ra_unpair(r1, a2, a3);
       l += (a0 + a1) + (a2 + a3);
+      if (!__all_sync(0xffffffffu, p_ready) && !mbar_wait_warp(p_done(s), done_ph, p.err, abort_flag)) return false;
+      tc_fence_after();
+      tmem_st_32x32b_x16(padr + s * 64, ph);
+      tmem_st_32x32b_x16(padr + s * 64 + 32, pl);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -686,13 +714,13 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
         left = c.tb - c.ta;
         const int over = c.pos0 - c.ta * RA_BKV;   // the tile's first row's last key
         whole = min(left, (over + 1) >> 7);        // below zero: none
-        lim = over + min(r / p.G, c.toks - 1);     // padding rows: the last real row's limit
+        lim = over + min(r / p.G, c.toks - 1) - half * KEYS;     // padding rows: the last real row's limit
         end = c.L - c.ta * RA_BKV;
         busy = quarter * 32 < c.toks * p.G;        // some row of this warp is real
       }
       m = -INFINITY;
       l = 0.f;
-      if (k > 0 && !mbar_wait_warp(q_full(k), ((k - (k & 3 ? 0 : 4)) >> 2) & 1, p.err, abort_flag)) { ok = false; break; }
+      if (!mbar_wait_warp(k ? q_full(k) : q_first, k ? ((k - (k & 3 ? 0 : 4)) >> 2) & 1 : 0, p.err, abort_flag)) { ok = false; break; }
       rs = qscale[(k & 3) * RA_BQ + r];
       if (busy) {
         bool first = true;
@@ -718,6 +746,11 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       if (!mbar_wait_warp(p_done((n - 1) & 1), ((n - 1) >> 1) & 1, p.err, abort_flag)) { ok = false; break; }
       tc_fence_after();
       if (busy) {
+        {
+          float other = l;
+          if (!exchange(other)) { ok = false; break; }
+          l = half == 0 ? l + other : other + l;   // the same sum in both halves
+        }
         const RaPiece& c = piece(k);
         const bool whole = c.flags & 1;
         const int tok = r / p.G;
@@ -726,29 +759,29 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
         const int64_t pslot = static_cast<int64_t>(cta) * 2 + (c.flags >> 1);
         const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
+        for (int h = 0; h < 2; ++h) {
           uint32_t v[32];
           tmem_ld_32x32b_x32(oadr + h * 32, v);
           tmem_ld_wait();
           if (mine && whole) {
-            __nv_bfloat16* orow_p = p.j.o + orow * RA_D + h * 32;
+            __nv_bfloat16* orow_p = p.j.o + orow * RA_D + half * 64 + h * 32;
 #pragma unroll
             for (int e = 0; e < 32; e += 16) {
-              uint32_t x[8];
+              uint32_t y[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                x[i] = pack_bf16x2(__uint_as_float(v[e + 2 * i]) * inv, __uint_as_float(v[e + 2 * i + 1]) * inv);
-              ra_st32(orow_p + e, x);
+                y[i] = pack_bf16x2(__uint_as_float(v[e + 2 * i]) * inv, __uint_as_float(v[e + 2 * i + 1]) * inv);
+              ra_st32(orow_p + e, y);
             }
           } else if (mine) {
-            float* po = p.j.part_o + (pslot * RA_D + h * 32) * RA_BQ + r * 4;      // lanes side by side
+            float* po = p.j.part_o + (pslot * RA_D + half * 64 + h * 32) * RA_BQ + r * 4;      // lanes side by side
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
               *reinterpret_cast<uint4*>(po + e * RA_BQ) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
           }
           __syncwarp();                            // the next load is a whole warp's
         }
-        if (mine) {
+        if (mine && half == 0) {
           if (whole) {
             if (p.j.lse) p.j.lse[orow] = (m - A8_LIFT + log2f(l)) * RA_LN2;
           } else {
