@@ -13,21 +13,39 @@
 // cutting, the rest rounded to 4, off by 2^-8 at most as a bf16 weight is.
 //
 // Scales. t_j = s_j a_j + log2 b_j is what the running maximum m is taken of, and P'_j =
-// 2^(t_j - m + 6) = 2^(6 - m) p_j b_j goes into the product with the values' codes: its
-// range does not depend on how the pages' scales differ. The row's sum adds P'_j / b_j.
-// m is raised when t exceeds it by more than 2.5, so P' stays below 2^8.5 < 448. A
-// weight below 2^-12 of the row's largest is off by 2^-16 of that one at most.
+// 2^(t_j - m + 4) = 2^(4 - m) p_j b_j goes into the product with the values' codes: its
+// range does not depend on how the pages' scales differ. The row's sum adds P'_j / b_j. m
+// is raised when t exceeds it by more than 4.7 in some row of a warp, so P' stays below
+// 2^8.7 < 448 (and then to the maximum of every row: O's columns are read and written once
+// for all). Codes below 2^-6 lose bits, each part by 2^-10 at most: a weight is off by 2^-13 of the row's
+// largest at most, where that is more than its own 2^-8. (Raised at 2.5, with P' up to 2^6,
+// a chunk's steps waited for the product before them a third of the time.)
 //
 // Work split, walk and join are those of the bf16 kernel (ragged_walk.cuh): query tiles
 // of floor(128 / G) tokens x G heads, runs of key tiles of 128 keys, one CTA per SM,
 // pieces of cut items joined in CTA order: results repeat bit for bit.
 //
-// Roles (8 warps): warp 0 copies the keys, warp 1 the values and looks up the scales,
-// warp 2 issues the score products and, between two of them, splits the next piece's
-// queries, warp 3 issues the P V products, warps 4..11 are the softmax (thread = query row
-// = TMEM lane and half of the tile's keys; idle at first, they split the first piece's
-// queries). Two warps share an SM quarter's instruction issue, which one could not fill:
-// with four softmax warps a step took 2900 cycles. They tell each other their row maxima.
+// Roles (12 warps): warp 0 copies the keys and, between two tiles, splits the next
+// piece's queries, warp 1 copies the values and looks up the scales, warp 2 issues the
+// score products, warp 3 the P V products. Warps 4..7 are the softmax of the even steps,
+// 8..11 of the odd ones (thread = query row = TMEM lane): a step's chain of waits, loads,
+// maxima, 128 exponentials and splits a row is longer than two steps' products, so two are
+// under way. The running maximum passes from one group to the other through shared memory;
+// O has one scale. The softmax warps, idle at first, split the first piece's queries.
+// Scores stay in tensor memory and are read twice, for the maximum and for the weights, 32
+// columns at a time, so that a step's code is a few small loops: unrolled over 128 keys (30
+// KB a step, 170 KB in all) the instruction fetch took longer than the work, 3800 cycles a
+// step. P takes the columns of S that have been read; three such buffers keep the score
+// products two steps ahead.
+//
+// Few rows. A piece of at most 16 rows (decoding) would leave seven of eight TMEM lanes
+// and all but one softmax warp idle, and its products, which read 128 rows of both parts
+// whatever they hold, would take more of shared memory's time than the copies. Both
+// parts of its queries are rows of one tile instead, row r's at lanes r and 16 + r of
+// each quarter of the lanes: half the products, and each quarter's warp, which takes 32 of
+// the tile's keys (a lane 16), adds the parts. Weights likewise, in shared memory, from
+// where the P V product reads them: lanes r and 16 + r of O are added at the end.
+//
 // Barriers, stages and buffers as in the bf16
 // kernel. A key tile of 16 KB is 16 groups of 8 keys x 128 bytes (one swizzle atom each);
 // with block_size a multiple of 8 it is 128 / box TMA boxes, box = gcd(block_size, 128),
@@ -48,18 +66,24 @@ constexpr int A8_THREADS = 32 * A8_WARPS;
 constexpr uint32_t A8_TILE = 128 * 128;       // a tile of keys, of values, of one part of the queries
 constexpr int A8_NST = 4;                     // stages of the K and of the V ring
 constexpr int A8_SCR = 4;                     // tiles in the ring of scales
+constexpr int A8_SB = 3;                      // steps whose scores and weights are in tensor memory
+constexpr int A8_FEW = 16;                    // rows of a piece that has both parts in one tile
+constexpr uint32_t A8_FEW_TILE = 2 * A8_FEW * 128;          // 32 rows: a quarter of the lanes
 constexpr uint32_t A8_OFF_Q = 0;              // two pieces' queries, high and low parts
-constexpr uint32_t A8_OFF_K = A8_OFF_Q + 4 * A8_TILE;
+constexpr uint32_t A8_OFF_P = A8_OFF_Q + 4 * A8_TILE;       // weights of few rows, three steps (the product reads 128
+                                              // rows: what lies behind gives rows that nobody reads)
+constexpr uint32_t A8_OFF_K = A8_OFF_P + A8_SB * A8_FEW_TILE;
 constexpr uint32_t A8_OFF_V = A8_OFF_K + A8_NST * A8_TILE;
 constexpr uint32_t A8_OFF_BAR = A8_OFF_V + A8_NST * A8_TILE;
 constexpr uint32_t A8_OFF_QS = A8_OFF_BAR + 2560;           // the rows' factors, of four pieces
-constexpr uint32_t A8_OFF_X = A8_OFF_QS + 4 * RA_BQ * 4;    // what the halves of a row tell each other
-constexpr uint32_t A8_OFF_SC = A8_OFF_X + 4 * RA_BQ * 4;    // the ring of scales
+constexpr uint32_t A8_OFF_MX = A8_OFF_QS + 4 * RA_BQ * 4;   // the rows' maxima, of four steps
+constexpr uint32_t A8_OFF_L = A8_OFF_MX + 4 * RA_BQ * 4;    // the groups' sums, of two pieces
+constexpr uint32_t A8_OFF_SC = A8_OFF_L + 4 * RA_BQ * 4;    // the ring of scales
 constexpr size_t a8_smem(bool tma) { return 1024 + A8_OFF_SC + A8_SCR * 3 * (tma ? 16 : 128) * 4; }
-// Tensor memory: S of two steps, P of two steps (high and low parts), O: all 512 columns.
-constexpr uint32_t A8_TM_P = 256, A8_TM_O = 384;
-constexpr float A8_LIFT = 6.0f;               // P' of the running maximum is 2^6 ...
-constexpr float A8_LAG = 2.5f;                // ... to 2^8.5
+// Tensor memory: S of three steps, whose columns P takes as they are read, and O: all 512 columns.
+constexpr uint32_t A8_TM_O = 384;
+constexpr float A8_LIFT = 4.0f;               // P' of the running maximum is 2^4 ...
+constexpr float A8_LAG = 4.7f;                // ... to 2^8.7
 
 struct A8Params {
   CUtensorMap tmK, tmV;
@@ -73,6 +97,7 @@ struct A8Params {
   const int32_t* ctx;
   RaJoin j;              // o, lse and the pieces of cut items
   int B, T, Hq, Hkv, G, TQ;
+  int inv_g;             // ceil(2^16 / G): r / G = r inv_g >> 16 for r < 128
   int bs, max_blocks, n_blocks;
   int box_log;           // log2 of the rows per TMA box (8 .. 128)
   float scale_log2;
@@ -84,9 +109,23 @@ __device__ __forceinline__ uint64_t a8_desc_k(uint32_t base, int kk) { return sm
 // Values as the MN-major B operand: n = head dim, 128 bytes; k-step kk of 32 keys = four groups
 __device__ __forceinline__ uint64_t a8_desc_v(uint32_t base, int kk) { return smem_desc_sw128(base + kk * 4096, 1024, 1024); }
 
-__device__ __forceinline__ uint64_t a8_sub2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+// Pairs of f16 in one register, and four of them as e4m3.
+__device__ __forceinline__ uint32_t a8_f16x2(uint32_t lo, uint32_t hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
+  return d;
+}
+__device__ __forceinline__ uint32_t a8_sub_h(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t a8_e4m3x4_h(uint32_t a, uint32_t b) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(b));
+  uint32_t d;
+  asm("mov.b32 %0, {%1, %2};" : "=r"(d) : "h"(lo), "h"(hi));
   return d;
 }
 // max that a NaN survives
@@ -99,6 +138,32 @@ __device__ __forceinline__ float4 a8_ld4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
   return v;
+}
+
+// 32 lanes x 8 consecutive 32-bit columns from registers into TMEM
+__device__ __forceinline__ void a8_tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// mbar_wait_warp in few instructions (there are twenty of them in the kernel): the limit counts probes,
+// each of which may sleep for up to a microsecond or so.
+__device__ __forceinline__ bool a8_wait(uint32_t bar, uint32_t parity, uint32_t* err, volatile int* abort_flag) {
+  for (uint32_t i = 0; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++i) {
+    if ((i & 63u) != 63u) continue;
+    if (i > 1u << 21) record_error(err, KL_DEVERR_TIMEOUT);
+    if (__any_sync(0xffffffffu, i > 1u << 21 || *abort_flag)) return false;
+  }
+  return true;
+}
+
+template <int N>
+__device__ __forceinline__ void a8_ldv(uint32_t addr, float (&v)[4]) {
+  if (N == 4)
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(addr));
+  else
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "r"(addr));
 }
 
 template <bool TMA>
@@ -115,20 +180,24 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
   auto k_empty = [&](int s) { return bar + 80 + 8 * s; };
   auto v_full = [&](int s) { return bar + 112 + 8 * s; };
   auto v_empty = [&](int s) { return bar + 144 + 8 * s; };
-  auto s_full = [&](int s) { return bar + 176 + 8 * s; };   // S_n computed
-  auto s_free = [&](int s) { return bar + 192 + 8 * s; };   // S_n read
-  auto p_full = [&](int s) { return bar + 208 + 8 * s; };   // P_n written (and V_n's tail cleared)
-  auto p_done = [&](int s) { return bar + 224 + 8 * s; };   // O += P_n V_n computed
-  auto sc_full = [&](int n) { return bar + 240 + 8 * (n & (A8_SCR - 1)); };    // the tile's scales written
-  const uint32_t drain = bar + 272, drain_pv = bar + 280, q_first = bar + 288;   // the first piece's queries
-  auto told = [&](int q, int x) { return bar + 296 + 16 * q + 8 * (x & 1); };   // both halves of quarter q's rows have spoken
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + A8_OFF_BAR + 360);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + A8_OFF_BAR + 364);
-  RaFound* found = reinterpret_cast<RaFound*>(smem + A8_OFF_BAR + 368);
-  long long* wsum = reinterpret_cast<long long*>(smem + A8_OFF_BAR + 432);
-  RaWalk* walks = reinterpret_cast<RaWalk*>(smem + A8_OFF_BAR + 528);        // the finder's, then one per warp
-  RaPiece* pieces = reinterpret_cast<RaPiece*>(smem + A8_OFF_BAR + 1152);    // the first one, then two per warp
-  static_assert(sizeof(RaFound) <= 64 && A8_WARPS * 8 <= 96 && (A8_WARPS + 1) * sizeof(RaWalk) <= 624 && (A8_WARPS * 2 + 1) * sizeof(RaPiece) <= 1408,
+  auto s_full = [&](int n) { return bar + 176 + 8 * (n % A8_SB); };   // S_n computed
+  auto p_full = [&](int n) { return bar + 200 + 8 * (n % A8_SB); };   // P_n written (and V_n's tail cleared)
+  auto p_done = [&](int n) { return bar + 224 + 8 * (n % A8_SB); };   // O += P_n V_n computed
+  auto phase = [&](int n) -> uint32_t { return (n / A8_SB) & 1; };    // their parity for step n
+  auto sc_full = [&](int n) { return bar + 248 + 8 * (n & (A8_SCR - 1)); };    // the tile's scales written
+  const uint32_t drain = bar + 280, drain_pv = bar + 288;
+  const uint32_t q_first = bar + 296;                              // the first piece's queries
+  auto told = [&](int q, int t) { return bar + 304 + 32 * q + 8 * (t & 3); };   // the step's maxima of quarter q's rows
+  auto told_few = [&](int t) { return bar + 432 + 8 * (t & 3); };  // those of all quarters
+  const uint32_t sums = bar + 464;                                 // a piece's sums of both groups
+  const uint32_t o_free = bar + 472;                               // a piece's O has been read
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + A8_OFF_BAR + 480);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + A8_OFF_BAR + 484);
+  RaFound* found = reinterpret_cast<RaFound*>(smem + A8_OFF_BAR + 488);
+  long long* wsum = reinterpret_cast<long long*>(smem + A8_OFF_BAR + 552);
+  RaWalk* walks = reinterpret_cast<RaWalk*>(smem + A8_OFF_BAR + 648);        // the finder's, then one per warp
+  RaPiece* pieces = reinterpret_cast<RaPiece*>(smem + A8_OFF_BAR + 1272);    // the first one, then two per warp
+  static_assert(sizeof(RaFound) <= 64 && A8_WARPS * 8 <= 96 && (A8_WARPS + 1) * sizeof(RaWalk) <= 624 && (A8_WARPS * 2 + 1) * sizeof(RaPiece) <= 1288,
                 "shared-memory layout");
   float* qscale = reinterpret_cast<float*>(smem + A8_OFF_QS);
   constexpr int GRP = TMA ? 8 : 1;               // keys that share a scale
@@ -142,7 +211,10 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
   if (warp == 3 && lane == 0) {
     for (int k = 0; k < 4; ++k) mbar_init(q_full(k), 1);
     mbar_init(q_first, 8);
-    for (int k = 0; k < 8; ++k) mbar_init(told(k >> 1, k), 2);
+    for (int k = 0; k < 16; ++k) mbar_init(told(k >> 2, k), 1);
+    for (int k = 0; k < 4; ++k) mbar_init(told_few(k), 4);
+    mbar_init(sums, 8);
+    mbar_init(o_free, 8);
     for (int k = 0; k < 2; ++k) mbar_init(q_empty(k), 1);
     for (int s = 0; s < A8_NST; ++s) {
       mbar_init(k_full(s), TMA ? 1 : 32);
@@ -150,11 +222,10 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       mbar_init(v_full(s), TMA ? 1 : 32);
       mbar_init(v_empty(s), 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(s_full(s), 1);
-      mbar_init(s_free(s), 8);
-      mbar_init(p_full(s), 8);
-      mbar_init(p_done(s), 1);
+    for (int n = 0; n < A8_SB; ++n) {
+      mbar_init(s_full(n), 1);
+      mbar_init(p_full(n), 4);
+      mbar_init(p_done(n), 1);
     }
     for (int n = 0; n < A8_SCR; ++n) mbar_init(sc_full(n), 1);
     mbar_init(drain, 1);
@@ -175,7 +246,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const uint32_t tmP = tmem + A8_TM_P, tmO = tmem + A8_TM_O;
+  const uint32_t tmO = tmem + A8_TM_O;
 
   // Piece 0 is shared (pieces[0]); from there each warp walks for itself.
   auto piece = [&](int k) -> RaPiece& { return pieces[k ? 1 + warp * 2 + (k & 1) : 0]; };
@@ -189,40 +260,59 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
     return piece(k).tb > 0;
   };
   auto page = [&](int b, int lb) { return lb < p.max_blocks ? p.table[static_cast<int64_t>(b) * p.max_blocks + lb] : -1; };
-  // Queries, two rows at a time, 16 lanes each: row r0 + (lane >> 4) of a piece with `rows` of them ...
-  auto load_q = [&](const RaPiece& c, int rows, int r0) {
-    const int r = r0 + (lane >> 4), tok = r / p.G;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (r < rows)
-      x = *reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(c.row0 + tok) * p.Hq + c.g * p.G + (r - tok * p.G)) * RA_D + (lane & 15) * 8);
-    return x;
+  // the parity that piece k's queries' barrier is waited for with (q_full(0) serves from piece 4 on)
+  auto q_phase = [&](int k) -> uint32_t { return k ? ((k - (k & 3 ? 0 : 4)) >> 2) & 1 : 0; };
+  auto token_of = [&](int r) { return (r * p.inv_g) >> 16; };
+  // Queries, four rows at a time, 8 lanes of 16 elements each: row r0 + (lane >> 3) of a piece with `rows` ...
+  auto load_q = [&](const RaPiece& c, int rows, int r0, uint4 (&x)[2]) {
+    const int r = r0 + (lane >> 3), tok = token_of(r);
+    if (r >= rows) return;
+    const uint4* src = reinterpret_cast<const uint4*>(
+        p.q + (static_cast<int64_t>(c.row0 + tok) * p.Hq + c.g * p.G + (r - tok * p.G)) * RA_D + (lane & 7) * 16);
+    x[0] = src[0];
+    x[1] = src[1];
   };
-  // ... split into its two parts, and its factor, into piece k's places.
-  auto split_q = [&](const uint4& x, int k, int rows, int r0) {
-    const int r = r0 + (lane >> 4), j = lane & 15;
-    const float2 f0 = unpack_bf16x2(x.x), f1 = unpack_bf16x2(x.y), f2 = unpack_bf16x2(x.z), f3 = unpack_bf16x2(x.w);
-    // the largest size, as bits: an infinity or a NaN is above all numbers
-    auto size = [](float a, float b) { return max(__float_as_uint(a) & 0x7fffffffu, __float_as_uint(b) & 0x7fffffffu); };
-    uint32_t a = max(max(size(f0.x, f0.y), size(f1.x, f1.y)), max(size(f2.x, f2.y), size(f3.x, f3.y)));
+  // ... split into its two parts, and its factor, into piece k's places (few rows: into every quarter's).
+  auto split_q = [&](const uint4 (&x)[2], int k, int rows, int r0) {
+    const int r = r0 + (lane >> 3), j = lane & 7;
+    const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+    // the largest size, as bits (two at a time): an infinity or a NaN is above all numbers
+    uint32_t a2 = 0;
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-    const int e = max(static_cast<int>(a >> 23) - 127, -110);
+    for (int i = 0; i < 8; ++i) a2 = __vmaxu2(a2, w[i] & 0x7fff7fffu);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) a2 = __vmaxu2(a2, __shfl_xor_sync(0xffffffffu, a2, o));
+    const uint32_t a = max(a2 & 0xffffu, a2 >> 16);
+    const int e = max(static_cast<int>(a >> 7) - 127, -110);
     const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - e) << 23), down = __uint_as_float(static_cast<uint32_t>(127 - 7 + e) << 23);
-    auto split = [&](const float2& s, const float2& t, uint32_t& hi4, uint32_t& lo4) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 s = unpack_bf16x2(w[2 * i]), t = unpack_bf16x2(w[2 * i + 1]);
       const float x0 = s.x * up, x1 = s.y * up, x2 = t.x * up, x3 = t.y * up;
-      hi4 = e4m3x4(x0, x1, x2, x3);
-      const float4 h = e4m3x4_to_f(hi4);
-      lo4 = e4m3x4(x0 - h.x, x1 - h.y, x2 - h.z, x3 - h.w);
-    };
-    uint2 h, l;
-    split(f0, f1, h.x, l.x);
-    split(f2, f3, h.y, l.y);
-    if (r < rows) {
-      const uint32_t at = sb + A8_OFF_Q + (k & 1) * 2 * A8_TILE + r * 128 + (((j >> 1) ^ (r & 7)) << 4) + (j & 1) * 8;
-      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(h.x), "r"(h.y) : "memory");
-      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + A8_TILE), "r"(l.x), "r"(l.y) : "memory");
-      if (j == 0) qscale[(k & 3) * RA_BQ + r] = a >= 0x7f800000u ? __int_as_float(0x7fffffff) : down * p.scale_log2;
+      hi[i] = e4m3x4(x0, x1, x2, x3);
+      const float4 h = e4m3x4_to_f(hi[i]);
+      lo[i] = e4m3x4(x0 - h.x, x1 - h.y, x2 - h.z, x3 - h.w);
     }
+    if (r < rows) {
+      const bool few = rows <= A8_FEW;
+      uint32_t at = sb + A8_OFF_Q + (k & 1) * 2 * A8_TILE + r * 128 + ((j ^ (r & 7)) << 4);
+      float* f = qscale + (k & 3) * RA_BQ + r;
+      const float v = a >= 0x7f80u ? __int_as_float(0x7fffffff) : down * p.scale_log2;
+#pragma unroll 1
+      for (int c = 0; c < (few ? 4 : 1); ++c, at += A8_FEW_TILE, f += 32) {
+        st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
+        st_shared_v4(at + (few ? A8_FEW * 128 : A8_TILE), lo[0], lo[1], lo[2], lo[3]);
+        if (j == 0) *f = v;
+        if (j == 1 && few) f[A8_FEW] = v;
+      }
+    }
+  };
+  // no row: no factor (from place `from` on in steps of `by`)
+  auto no_rows = [&](int k, int rows, int from, int by) {
+#pragma unroll 1
+    for (int r = from; r < RA_BQ; r += by)
+      if ((rows <= A8_FEW ? r & (A8_FEW - 1) : r) >= rows) qscale[(k & 3) * RA_BQ + r] = 0.f;
   };
 
   if (warp < 2) {
@@ -298,66 +388,132 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       if (lane == 0) mbar_arrive(sc_full(tile));
       ++tile;
     };
-    for (int k = 0; ok && find(k); ++k) {
+    // Warp 0: the next piece's queries, eight rows at a time once the S products of the piece before this
+    // one are done with the buffer; all of them by this piece's end.
+    int q_at = 0, q_rows = 0;
+    auto split_next = [&](int k, bool must) -> bool {
+      if (q_at == 0 && k > 0) {
+        const uint32_t ph = ((k - 1) >> 1) & 1;
+        if (must ? !a8_wait(q_empty(k + 1), ph, p.err, abort_flag) : !__all_sync(0xffffffffu, mbar_test_wait(q_empty(k + 1), ph))) return !must;
+      }
+      const RaPiece& c = piece(k + 1);
+      uint4 x[2][2] = {};
+      load_q(c, q_rows, q_at, x[0]);
+      load_q(c, q_rows, q_at + 4, x[1]);
+#pragma unroll 1
+      for (int u = 0; u < 2; ++u, q_at += 4) {
+        if (q_at < q_rows) split_q(x[0], k + 1, q_rows, q_at);
+        x[0][0] = x[1][0];
+        x[0][1] = x[1][1];
+      }
+      if (q_at >= q_rows) {
+        no_rows(k + 1, q_rows, lane, 32);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full(k + 1));
+      }
+      return true;
+    };
+    int row[4];
+    // TMA: the batches that have been asked for (up to three): this lane's box's page, place in it (below
+    // zero: none) and kv head; the piece and tile of the next one; whether the first one's scales have been too
+    int blk[3] = {}, at[3] = {}, head[3] = {}, queued = 0, ask_k = 0, ask_j = -1;
+    bool asked = false;
+    auto scales = [&](int i) {
+      a[1] = b[1] = 1.f;                           // a page that is read as zero has none
+      if (at[i] < 0 || blk[i] < 0 || blk[i] >= p.n_blocks) return;
+      const int64_t sc = static_cast<int64_t>(blk[i]) * p.Hkv + head[i];
+      a[1] = p.ks[sc];
+      b[1] = p.vs[sc];
+    };
+    bool have = find(0);
+    for (int k = 0; ok && have; ++k) {
       const RaPiece w = piece(k);
-      // TMA: one look at the table serves `per` tiles, a lane per box, and the next
-      // tiles' pages are asked for before these are copied. cp.async: a lane for four
-      // of a tile's keys.
-      int row[4], blk = 0, at = 0;
-      const int keys = min(w.L, w.tb * RA_BKV);
-      auto ask = [&](int j) {
-        const int pos = j * RA_BKV + lane * box, lb = pos / p.bs;
-        at = pos < keys ? pos - lb * p.bs : -1;
-        if (at >= 0) blk = page(w.b, lb);
-      };
-      auto scales = [&](int i, int blk, bool there) {
-        a[i] = b[i] = 1.f;                         // a page that is read as zero has none
-        if (is_k || !there) return;
-        const int64_t at = static_cast<int64_t>(blk) * p.Hkv + w.g;
-        a[i] = p.ks[at];
-        b[i] = p.vs[at];
-      };
-      auto lookup = [&](int j) {
+      have = find(k + 1);
+      q_at = 0;
+      q_rows = is_k && have ? piece(k + 1).toks * p.G : 0;
+      if (TMA) {
+        // One look at the table serves a batch of `per` tiles, a lane per box. Pages are asked for two
+        // batches ahead (the next piece's too), scales one: a read takes 1000 to 3000 cycles while HBM is busy.
+        for (int j = w.ta; j < w.tb; ++j) {
+          const int nth = (j - w.ta) & (per - 1);
+          if (nth == 0) {
+            while (queued < 3 && (ask_k < k + 1 || (ask_k == k + 1 && have))) {
+              const RaPiece& c = piece(ask_k);
+              if (ask_j < 0) ask_j = c.ta;
+              const int pos = ask_j * RA_BKV + lane * box, lb = pos / p.bs;
+              const int there = pos < min(c.L, c.tb * RA_BKV) ? pos - lb * p.bs : -1;
+              const int pg = there >= 0 ? page(c.b, lb) : 0;
+              if (queued == 0) { at[0] = there; blk[0] = pg; head[0] = c.g; }
+              else if (queued == 1) { at[1] = there; blk[1] = pg; head[1] = c.g; }
+              else { at[2] = there; blk[2] = pg; head[2] = c.g; }
+              ++queued;
+              ask_j += per;
+              if (ask_j >= c.tb) {
+                ask_j = -1;
+                ++ask_k;
+              }
+            }
+            row[0] = at[0] >= 0 ? pool_row(blk[0], at[0]) : no_row;
+            if (!is_k) {
+              if (!asked) scales(0);               // into a[1], b[1]
+              a[0] = a[1];
+              b[0] = b[1];
+              asked = queued > 1;
+              if (asked) scales(1);
+            }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int pos = j * RA_BKV + i * 32 + lane, lb = pos / p.bs;
-          const int pg = pos < keys ? page(w.b, lb) : 0;
-          row[i] = pos < keys ? pool_row(pg, pos - lb * p.bs) : no_row;
-          scales(i, pg, row[i] != no_row);
-        }
-      };
-      if (TMA) ask(w.ta); else lookup(w.ta);
-      for (int j = w.ta; j < w.tb; ++j) {
-        const int nth = (j - w.ta) & (per - 1);
-        if (TMA && nth == 0) {
-          row[0] = at >= 0 ? pool_row(blk, at) : no_row;
-          if (j > w.ta) publish(per - 1);          // the batch before is no longer at hand
-          scales(0, blk, row[0] != no_row);
-          if (j + per < w.tb) ask(j + per);
-        }
-        if (!ra_wait_copy(empty0 + 8 * s, ph, p.err, abort_flag)) { ok = false; break; }
-        const uint32_t dst = ring + s * A8_TILE;
-        if (TMA) {
+            for (int i = 0; i < 2; ++i) { at[i] = at[i + 1]; blk[i] = blk[i + 1]; head[i] = head[i + 1]; }
+            --queued;
+          }
+          if (!ra_wait_copy(empty0 + 8 * s, ph, p.err, abort_flag)) { ok = false; break; }
           if (el) mbar_arrive_expect_tx(full0 + 8 * s, A8_TILE);
           __syncwarp();
-          if (my == nth) ra_tma_3d(dst + (lane & (nbox - 1)) * box * 128, tm, 0, w.g, row[0], full0 + 8 * s);
+          if (my == nth) ra_tma_3d(ring + s * A8_TILE + (lane & (nbox - 1)) * box * 128, tm, 0, w.g, row[0], full0 + 8 * s);
           __syncwarp();
-          if (nth > 0) publish(nth - 1);          // a tile later: the reads have had the time
-        } else {
-          gather(dst, w.g, row);
+          publish(nth);
+          ++issued;
+          if (++s == A8_NST) {
+            s = 0;
+            ph ^= 1u;
+          }
+          if (q_at < q_rows && !split_next(k, false)) { ok = false; break; }
+        }
+      } else {
+        // a lane for four of a tile's keys
+        const int keys = min(w.L, w.tb * RA_BKV);
+        auto lookup = [&](int j) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int pos = j * RA_BKV + i * 32 + lane, lb = pos / p.bs;
+            const int pg = pos < keys ? page(w.b, lb) : 0;
+            row[i] = pos < keys ? pool_row(pg, pos - lb * p.bs) : no_row;
+            a[i] = b[i] = 1.f;                     // a page that is read as zero has none
+            if (!is_k && row[i] != no_row) {
+              const int64_t sc = static_cast<int64_t>(pg) * p.Hkv + w.g;
+              a[i] = p.ks[sc];
+              b[i] = p.vs[sc];
+            }
+          }
+        };
+        lookup(w.ta);
+        for (int j = w.ta; j < w.tb; ++j) {
+          if (!ra_wait_copy(empty0 + 8 * s, ph, p.err, abort_flag)) { ok = false; break; }
+          gather(ring + s * A8_TILE, w.g, row);
           publish(0);
           if (j > w.ta) announce(std::integral_constant<int, 1>());   // the tile before
+          ++issued;
+          if (++s == A8_NST) {
+            s = 0;
+            ph ^= 1u;
+          }
+          if (j + 1 < w.tb) lookup(j + 1);
+          if (q_at < q_rows && !split_next(k, false)) { ok = false; break; }
         }
-        ++issued;
-        if (++s == A8_NST) {
-          s = 0;
-          ph ^= 1u;
-        }
-        if (!TMA && j + 1 < w.tb) lookup(j + 1);
+        // the piece's last tile: its products free Q, which the next piece waits for
+        if (ok) announce(std::integral_constant<int, 0>());
       }
-      if (TMA && ok) publish((w.tb - 1 - w.ta) & (per - 1));
-      // the piece's last tile: its products free Q, which the next piece waits for
-      if (!TMA && ok) announce(std::integral_constant<int, 0>());
+      while (ok && q_at < q_rows) ok = split_next(k, true);
     }
     if (!ok) *abort_flag = 1;
     // copies still in flight must land before exit
@@ -367,54 +523,31 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
   } else if (warp == 2) {
-    // ---------- S_n = hi K_n^T + lo K_n^T into S[n % 2] (whole warp; the elected lane issues) ----------
+    // ---------- S_n = hi K_n^T + lo K_n^T into S[n % 3] (whole warp; the elected lane issues) ----------
     const bool el = elect_one();
     const uint32_t idesc = idesc_e4m3_f32(128, 128, 0, 0);
     int n = 0, ks = 0;                        // step, K stage
     uint32_t kph = 0;
-    bool ok = true, have = find(0);
-    if (have && !mbar_wait_warp(q_first, 0, p.err, abort_flag)) ok = false;
-    for (int k = 0; ok && have; ++k) {
+    bool ok = true;
+    for (int k = 0; ok && find(k); ++k) {
       const int tiles = piece(k).tb - piece(k).ta;
+      const bool few = piece(k).toks * p.G <= A8_FEW;
       const uint32_t qb = sb + A8_OFF_Q + (k & 1) * 2 * A8_TILE;
-      // The next piece's queries are split between this one's products, sixteen rows at a time; the
-      // next sixteen are on their way meanwhile.
-      have = find(k + 1);
-      constexpr int U = 8;
-      uint4 x[U];
-      int at = 0, rows = 0;
-      if (have) rows = piece(k + 1).toks * p.G;
-      auto load = [&]() {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (at + 2 * u < rows) x[u] = load_q(piece(k + 1), rows, at + 2 * u);
-      };
-      auto split = [&]() -> bool {
-        // the buffer is free once the S products of the piece before this one are done
-        if (at == 0 && k > 0 && !mbar_wait_warp(q_empty(k + 1), ((k - 1) >> 1) & 1, p.err, abort_flag)) return false;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (at + 2 * u < rows) split_q(x[u], k + 1, rows, at + 2 * u);
-        at += 2 * U;
-        load();
-        return true;
-      };
-      load();
+      if (!a8_wait(k ? q_full(k) : q_first, q_phase(k), p.err, abort_flag)) { ok = false; break; }
       for (int j = 0; j < tiles; ++j, ++n) {
-        const int s = n & 1;
-        if ((n >= 2 && !mbar_wait_warp(s_free(s), ((n >> 1) & 1) ^ 1u, p.err, abort_flag)) ||
-            !mbar_wait_warp(k_full(ks), kph, p.err, abort_flag)) {
+        // the columns are free once the product of three steps before is done with its P
+        if ((n >= A8_SB && !a8_wait(p_done(n), phase(n) ^ 1u, p.err, abort_flag)) ||
+            !a8_wait(k_full(ks), kph, p.err, abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
         if (el) {
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t kd = a8_desc_k(sb + A8_OFF_K + ks * A8_TILE, kk);
-            umma_e4m3(tmem + s * 128, a8_desc_k(qb, kk), kd, idesc, kk > 0);
-            umma_e4m3(tmem + s * 128, a8_desc_k(qb + A8_TILE, kk), kd, idesc, 1u);
-          }
-          umma_commit(s_full(s));
+          const uint32_t kb = sb + A8_OFF_K + ks * A8_TILE;
+#pragma unroll 1
+          for (int kk = 0; kk < (few ? 4 : 8); ++kk)      // high parts, then low ones
+            umma_e4m3(tmem + n % A8_SB * 128, a8_desc_k(qb + (kk >> 2) * A8_TILE, kk & 3), a8_desc_k(kb, kk & 3), idesc, kk > 0);
+          umma_commit(s_full(n));
           umma_commit(k_empty(ks));
           if (j == tiles - 1) umma_commit(q_empty(k));   // the piece's last use of Q
         }
@@ -423,14 +556,6 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
           ks = 0;
           kph ^= 1u;
         }
-        if (at < rows && !split()) { ok = false; break; }
-      }
-      while (ok && at < rows) ok = split();
-      if (ok && have) {
-        for (int r = rows + lane; r < ((rows + 31) & ~31); r += 32) qscale[((k + 1) & 3) * RA_BQ + r] = 0.f;   // no rows: no factor
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full(k + 1));
       }
     }
     if (!ok) *abort_flag = 1;
@@ -446,21 +571,24 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
     bool ok = true;
     for (int k = 0; ok && find(k); ++k) {
       const int tiles = piece(k).tb - piece(k).ta;
+      const bool few = piece(k).toks * p.G <= A8_FEW;
+      if (k > 0 && !a8_wait(o_free, (k - 1) & 1, p.err, abort_flag)) { ok = false; break; }
       for (int j = 0; j < tiles; ++j, ++n) {
-        const int s = n & 1;
-        if (!mbar_wait_warp(v_full(vs), vph, p.err, abort_flag) ||
-            !mbar_wait_warp(p_full(s), (n >> 1) & 1, p.err, abort_flag)) {
+        if (!a8_wait(v_full(vs), vph, p.err, abort_flag) || !a8_wait(p_full(n), phase(n), p.err, abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
         if (el) {
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t vd = a8_desc_v(sb + A8_OFF_V + vs * A8_TILE, kk);
-            umma_e4m3_ta(tmO, tmP + s * 64 + kk * 8, vd, idesc, (j > 0 || kk > 0) ? 1u : 0u);
-            umma_e4m3_ta(tmO, tmP + s * 64 + 32 + kk * 8, vd, idesc, 1u);
+          const uint32_t vb = sb + A8_OFF_V + vs * A8_TILE, pb = sb + A8_OFF_P + n % A8_SB * A8_FEW_TILE;
+          const uint32_t pt = tmem + n % A8_SB * 128;     // 16 columns for 32 keys: high parts, low parts
+#pragma unroll 1
+          for (int kk = 0; kk < (few ? 4 : 8); ++kk) {
+            const uint32_t acc = j > 0 || kk > 0;
+            if (few) umma_e4m3(tmO, a8_desc_k(pb, kk), a8_desc_v(vb, kk), idesc, acc);
+            else umma_e4m3_ta(tmO, pt + kk * 8, a8_desc_v(vb, kk >> 1), idesc, acc);
           }
-          umma_commit(p_done(s));
+          umma_commit(p_done(n));
           umma_commit(v_empty(vs));
         }
         __syncwarp();
@@ -476,39 +604,38 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
     mbar_wait(drain_pv, 0, p.err);
   } else {
     // ---------------- softmax / correction / epilogue ----------------
-    const int quarter = warp & 3, half = (warp >> 2) - 1;
-    const int r = quarter * 32 + lane;           // row within the tile = TMEM lane
-    constexpr int KEYS = RA_BKV / 2;             // keys 64 half .. 64 half + 63 of each tile
+    const int quarter = warp & 3, grp = (warp >> 2) - 1;         // grp: the parity of its steps
+    const int r = quarter * 32 + lane;           // TMEM lane: the row within the tile, or (few rows) a part of row lane & 15
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t oadr = tmO + lane_off + half * 64, padr = tmP + lane_off + half * 16;
-    float* said = reinterpret_cast<float*>(smem + A8_OFF_X);    // [exchange % 2][half][row]
+    const uint32_t oadr = tmO + lane_off;
+    float* maxima = reinterpret_cast<float*>(smem + A8_OFF_MX);   // [step % 4][row]
+    float* lsum = reinterpret_cast<float*>(smem + A8_OFF_L);      // [piece % 2][group][row]
     // The tile that holds the last key the query tile sees: its value rows behind it become zero
-    // (each of the eight warps half of its 32).
+    // (each of the group's four warps its 32).
     auto clear_tail = [&](int end, int n) -> bool {
       if (end >= RA_BKV) return true;
       const int vs = n % A8_NST;
-      if (!mbar_wait_warp(v_full(vs), (n / A8_NST) & 1, p.err, abort_flag)) return false;
+      if (!a8_wait(v_full(vs), (n / A8_NST) & 1, p.err, abort_flag)) return false;
       if (r >= end) {
-        const uint32_t va = sb + A8_OFF_V + vs * A8_TILE + r * 128 + half * 64;
+        const uint32_t va = sb + A8_OFF_V + vs * A8_TILE + r * 128;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) st_shared_v4(va + c * 16, 0u, 0u, 0u, 0u);
+        for (int c = 0; c < 8; ++c) st_shared_v4(va + c * 16, 0u, 0u, 0u, 0u);
       }
       fence_async_shared();
       return true;
     };
     bool more = find(0);
     if (more) {
-      // the first piece's queries, each warp 16 rows
+      // the first piece's queries, four rows a warp at a time
       const RaPiece& c = piece(0);
-      const int r0 = quarter * 32 + half * 16, all = c.toks * p.G, rows = min(all, r0 + 16);
-      for (int at = r0; at < rows; at += 8) {
-        uint4 x[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = load_q(c, rows, at + 2 * u);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) split_q(x[u], 0, rows, at + 2 * u);
+      const int rows = c.toks * p.G;
+#pragma unroll 1
+      for (int at = (warp - 4) * 4; at < rows; at += 32) {
+        uint4 x[2] = {};
+        load_q(c, rows, at, x);
+        split_q(x, 0, rows, at);
       }
-      if (half == 0 && r >= all) qscale[r] = 0.f;  // no row: no factor
+      no_rows(0, rows, threadIdx.x - 128, 256);
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_first);
@@ -530,241 +657,340 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
     }
     __syncwarp();
     bool ok = true;
-    int n = 0, x = 0;                              // steps and exchanges so far
-    float m = -INFINITY, l = 0.f;                  // the row's running max of t (log2 units), this half's sum of P' / b
+    int n0 = 0;                                    // the piece's first step
+    int t_all = 0, t_few = 0;                      // steps before it whose maxima were told (of this quarter's rows; of few rows)
+    float m = -INFINITY, l = 0.f;                  // the row's running max of t (log2 units) after this group's last step, its sum of P' / b
     float rs = 0.f;                                // the row's factor: score in log2 units = S * rs * a
-    int lim = 0, end = 0;                          // the row's last key, from this half's first; the end of the query tile's, from the tile's
-    // v to the other half of the row, the other half's into v
-    auto exchange = [&](float& v) -> bool {
-      float* at = said + (x & 1) * 2 * RA_BQ + r;
-      at[half * RA_BQ] = v;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(told(quarter, x));
-      if (!mbar_wait_warp(told(quarter, x), (x >> 1) & 1, p.err, abort_flag)) return false;
-      v = at[(half ^ 1) * RA_BQ];
-      ++x;
+    int lim = 0, end = 0;                          // from the piece's first key: the row's last key; the end of the query tile's
+    bool real = false;                             // this lane's row is one of the piece's
+    // The maximum after one more step, which only moves when some row's would by more than A8_LAG (the
+    // final O / l cancels a stale one). All warps that have these rows come to the same answer.
+    auto raised = [&](float m, float mx) { return __any_sync(0xffffffffu, real && mx > m + A8_LAG) ? fmaxf(m, mx) : m; };
+    // the rows' maxima of the piece's step j, told by all who have them
+    auto heard = [&](auto few, int j, float& mx) -> bool {
+      const int t = (decltype(few)::value ? t_few : t_all) + j;
+      if (!a8_wait(decltype(few)::value ? told_few(t) : told(quarter, t), (t >> 2) & 1, p.err, abort_flag)) return false;
+      const float* at = maxima + (t & 3) * RA_BQ;
+      if (decltype(few)::value) {
+        at += lane & 15;
+        mx = fmaxf(fmaxf(fmaxf(at[0], at[16]), fmaxf(at[32], at[48])), fmaxf(fmaxf(at[64], at[80]), fmaxf(at[96], at[112])));
+      } else {
+        mx = at[r];
+      }
       return true;
     };
-    // One step of a warp with rows. CUT: some row of the tile ends inside its keys.
-    auto step = [&](auto cut, bool first) -> bool {
-      constexpr bool CUT = decltype(cut)::value;
-      const int s = n & 1;
-      if (CUT && TMA && !clear_tail(end, n)) return false;
-      if (!mbar_wait_warp(s_full(s), (n >> 1) & 1, p.err, abort_flag)) return false;
-      tc_fence_after();
-      const uint32_t sadr = tmem + lane_off + s * 128 + half * KEYS;
-      uint32_t sv[KEYS];
-      tmem_ld_32x32b_x32(sadr, *reinterpret_cast<uint32_t(*)[32]>(sv));
-      tmem_ld_32x32b_x32(sadr + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
-      // P's columns are free once the product of step n - 2 is done: probed here,
-      // where the probe's latency costs nothing, and most likely it is
-      const uint32_t done_ph = ((n >> 1) & 1) ^ 1u;
-      const bool p_ready = n < 2 || mbar_test_wait(p_done(s), done_ph);
-      const bool sc_ok = mbar_wait_warp(sc_full(n), (n / A8_SCR) & 1, p.err, abort_flag);
-      // this half's scales; what takes S of a group to the score (with keys cut off never zero, so
-      // that their -inf stays)
-      constexpr int HG = KEYS / GRP;
-      const uint32_t sca = sc0 + (n & (A8_SCR - 1)) * 3 * NG * 4 + half * HG * 4;
-      auto factor = [&](float a) { return CUT ? a8_max_nan(rs * a, 1.17549435e-38f) : rs * a; };
-      float f[TMA ? HG : 1], lb[TMA ? HG : 1];
-      if (TMA && sc_ok) {
+    // Four weights' exponents -> their values (pairs), and both parts: as f16, of whose 11 bits four are kept
+    // and the rest is rounded to four. (In fp32 the masks and differences took four instructions more for
+    // four weights, and one warp 11.8 cycles a weight, 7.9 so.)
+    auto weights = [&](uint64_t x0, uint64_t x1, uint64_t& y0, uint64_t& y1, uint32_t& hi, uint32_t& lo) {
+      float p0, p1, p2, p3;
+      ra_unpair(x0, p0, p1);
+      ra_unpair(x1, p2, p3);
+      const uint32_t u0 = __float_as_uint(ra_ex2(p0)), u1 = __float_as_uint(ra_ex2(p1)), u2 = __float_as_uint(ra_ex2(p2)), u3 = __float_as_uint(ra_ex2(p3));
+      y0 = ra_pair(u0, u1);
+      y1 = ra_pair(u2, u3);
+      const uint32_t h0 = a8_f16x2(u0, u1), h1 = a8_f16x2(u2, u3);
+      constexpr uint32_t KEEP = 0xff80ff80u;
+      hi = a8_e4m3x4_h(h0 & KEEP, h1 & KEEP);
+      lo = a8_e4m3x4_h(a8_sub_h(h0, h0 & KEEP), a8_sub_h(h1, h1 & KEEP));
+    };
+    // What takes S to the score, S * factor(a); with keys cut off never zero, so that their -inf stays.
+    float least = 0.f;
+    auto factor = [&](float a) { return a8_max_nan(rs * a, least); };
+    // keys behind `last` of these do not count
+    auto mask = [&](auto& sv, int last) {
+      constexpr int N = sizeof(sv) / 4;
 #pragma unroll
-        for (int g = 0; g < HG; g += 4) {
-          const float4 a4 = a8_ld4(sca + g * 4), l4 = a8_ld4(sca + (NG + g) * 4);
-          f[g % (TMA ? HG : 1)] = factor(a4.x);
-          f[(g + 1) % (TMA ? HG : 1)] = factor(a4.y);
-          f[(g + 2) % (TMA ? HG : 1)] = factor(a4.z);
-          f[(g + 3) % (TMA ? HG : 1)] = factor(a4.w);
-          lb[g % (TMA ? HG : 1)] = l4.x;
-          lb[(g + 1) % (TMA ? HG : 1)] = l4.y;
-          lb[(g + 2) % (TMA ? HG : 1)] = l4.z;
-          lb[(g + 3) % (TMA ? HG : 1)] = l4.w;
-        }
-      }
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (!sc_ok) return false;
-      if (lane == 0) mbar_arrive(s_free(s));       // S[s] may be overwritten from here on
-      if (CUT) {                                   // keys 0 .. lim are kept
-#pragma unroll
-        for (int e = 0; e < KEYS; ++e)
-          if (e > lim) sv[e] = __float_as_uint(-INFINITY);
-      }
+      for (int e = 0; e < N; ++e)
+        if (e > last) sv[e] = __float_as_uint(-INFINITY);
+    };
+    // The maximum of t over N keys, whose scales start at shared address sc (TMA: N / 8 of them, else N).
+    auto max_t = [&](auto& sv, uint32_t sc) {
+      constexpr int N = sizeof(sv) / 4, GV = N < 32 ? 2 : 4;
       float mx = -INFINITY;
       if (TMA) {
-        float t[8];
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          const uint32_t* y = sv + g * 8;
-          float v = fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
-          v = ra_max3(v, y[2], y[3]);
-          v = ra_max3(v, y[4], y[5]);
-          v = ra_max3(v, y[6], y[7]);
-          t[g] = fmaf(v, f[g % (TMA ? HG : 1)], lb[g % (TMA ? HG : 1)]);
+        for (int g = 0; g < N / 8; g += GV) {
+          float a4[4], l4[4], t[4];
+          a8_ldv<GV>(sc + g * 4, a4);
+          a8_ldv<GV>(sc + (NG + g) * 4, l4);
+#pragma unroll
+          for (int u = 0; u < GV; ++u) {
+            const uint32_t* y = sv + (g + u) * 8;
+            float v = fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
+            v = ra_max3(v, y[2], y[3]);
+            v = ra_max3(v, y[4], y[5]);
+            v = ra_max3(v, y[6], y[7]);
+            t[u] = fmaf(v, factor(a4[u]), l4[u]);
+          }
+#pragma unroll
+          for (int u = 0; u < GV; u += 2) mx = ra_max3(mx, __float_as_uint(t[u]), __float_as_uint(t[u + 1]));
         }
-#pragma unroll
-        for (int g = 0; g < 8; g += 2) mx = ra_max3(mx, __float_as_uint(t[g]), __float_as_uint(t[g + 1]));
       } else {
-        // t itself, in place of S
 #pragma unroll
-        for (int e = 0; e < KEYS; e += 4) {
-          const float4 a4 = a8_ld4(sca + e * 4), l4 = a8_ld4(sca + (NG + e) * 4);
-          float t[4] = {fmaf(__uint_as_float(sv[e]), factor(a4.x), l4.x), fmaf(__uint_as_float(sv[e + 1]), factor(a4.y), l4.y),
-                        fmaf(__uint_as_float(sv[e + 2]), factor(a4.z), l4.z), fmaf(__uint_as_float(sv[e + 3]), factor(a4.w), l4.w)};
+        for (int e = 0; e < N; e += 4) {
+          float a4[4], l4[4], t[4];
+          a8_ldv<4>(sc + e * 4, a4);
+          a8_ldv<4>(sc + (NG + e) * 4, l4);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) t[u] = fmaf(__uint_as_float(sv[e + u]), factor(a4[u]), l4[u]);
           mx = ra_max3(mx, __float_as_uint(t[0]), __float_as_uint(t[1]));
           mx = ra_max3(mx, __float_as_uint(t[2]), __float_as_uint(t[3]));
-#pragma unroll
-          for (int u = 0; u < 4; ++u) sv[e + u] = __float_as_uint(t[u]);
         }
       }
-      {
-        float other = mx;
-        if (!exchange(other)) return false;
-        mx = fmaxf(mx, other);
-      }
-      // A row of a later piece's tile can be fully masked (its token ends before these
-      // keys): mx = -inf, and m stays -inf.
-      const bool raise = mx > m + A8_LAG;
-      if (__any_sync(0xffffffffu, raise)) {
-        const float m_new = raise ? mx : m;
-        const float alpha = raise ? ra_ex2(m - m_new) : 1.0f;
-        m = m_new;
-        l *= alpha;
-        if (!first) {
-          if (!mbar_wait_warp(p_done(s ^ 1), ((n - 1) >> 1) & 1, p.err, abort_flag)) return false;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {            // this half's columns of O
-            uint32_t v[16];
-            tmem_ld_32x32b_x16(oadr + c * 16, v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-            tmem_st_32x32b_x16(oadr + c * 16, v);
-          }
-        }
-      }
-      const float neg = m > -INFINITY ? A8_LIFT - m : 0.f;
-      uint64_t r0 = 0, r1 = 0;
-      uint32_t ph[16], pl[16];
-      // four weights: their sum's halves, both parts
-      auto weights = [&](int w, uint64_t x0, uint64_t x1, uint64_t& y0, uint64_t& y1) {
-        float p0, p1, p2, p3;
-        ra_unpair(x0, p0, p1);
-        ra_unpair(x1, p2, p3);
-        const uint32_t u0 = __float_as_uint(ra_ex2(p0)), u1 = __float_as_uint(ra_ex2(p1)), u2 = __float_as_uint(ra_ex2(p2)), u3 = __float_as_uint(ra_ex2(p3));
-        y0 = ra_pair(u0, u1);
-        y1 = ra_pair(u2, u3);
-        // four bits kept, the rest rounded to four
-        constexpr uint32_t KEEP = 0xfff00000u;
-        ph[w] = e4m3x4(__uint_as_float(u0 & KEEP), __uint_as_float(u1 & KEEP), __uint_as_float(u2 & KEEP), __uint_as_float(u3 & KEEP));
-        float d0, d1, d2, d3;
-        ra_unpair(a8_sub2(y0, ra_pair(u0 & KEEP, u1 & KEEP)), d0, d1);
-        ra_unpair(a8_sub2(y1, ra_pair(u2 & KEEP, u3 & KEEP)), d2, d3);
-        pl[w] = e4m3x4(d0, d1, d2, d3);
-      };
+      return mx;
+    };
+    // N keys' weights, four to a word of each part; their sum goes into r0, r1.
+    auto weigh = [&](auto& sv, uint32_t sc, float neg, auto& ph, auto& pl, uint64_t& r0, uint64_t& r1) {
+      constexpr int N = sizeof(sv) / 4, GV = N < 32 ? 2 : 4;
       if (TMA) {
+        float a4[4], l4[4], i4[4];
+        a8_ldv<GV>(sc, a4);
+        a8_ldv<GV>(sc + NG * 4, l4);
+        a8_ldv<GV>(sc + 2 * NG * 4, i4);
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
+        for (int g = 0; g < N / 8; ++g) {
           const uint32_t* v = sv + g * 8;
-          float ib;
-          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ib) : "r"(sca + (2 * NG + g) * 4));
-          const uint32_t fu = __float_as_uint(f[g % (TMA ? HG : 1)]), cu = __float_as_uint(lb[g % (TMA ? HG : 1)] + neg), iu = __float_as_uint(ib);
-          const uint64_t f2 = ra_pair(fu, fu), c2 = ra_pair(cu, cu), iv2 = ra_pair(iu, iu);
+          const uint32_t fu = __float_as_uint(factor(a4[g])), cu = __float_as_uint(l4[g] + neg), iu = __float_as_uint(i4[g]);
+          const uint64_t f2 = ra_pair(fu, fu), c2 = ra_pair(cu, cu), iv = ra_pair(iu, iu);
           uint64_t y0, y1, y2, y3;
-          weights(2 * g, ra_fma2(ra_pair(v[0], v[1]), f2, c2), ra_fma2(ra_pair(v[2], v[3]), f2, c2), y0, y1);
-          weights(2 * g + 1, ra_fma2(ra_pair(v[4], v[5]), f2, c2), ra_fma2(ra_pair(v[6], v[7]), f2, c2), y2, y3);
-          r0 = ra_fma2(ra_add2(y0, y1), iv2, r0);
-          r1 = ra_fma2(ra_add2(y2, y3), iv2, r1);
+          weights(ra_fma2(ra_pair(v[0], v[1]), f2, c2), ra_fma2(ra_pair(v[2], v[3]), f2, c2), y0, y1, ph[2 * g], pl[2 * g]);
+          weights(ra_fma2(ra_pair(v[4], v[5]), f2, c2), ra_fma2(ra_pair(v[6], v[7]), f2, c2), y2, y3, ph[2 * g + 1], pl[2 * g + 1]);
+          r0 = ra_fma2(ra_add2(y0, y1), iv, r0);
+          r1 = ra_fma2(ra_add2(y2, y3), iv, r1);
         }
       } else {
-        const uint64_t neg2 = ra_pair(__float_as_uint(neg), __float_as_uint(neg));
 #pragma unroll
-        for (int e = 0; e < KEYS; e += 4) {
-          const float4 ib = a8_ld4(sca + (2 * NG + e) * 4);
+        for (int e = 0; e < N; e += 4) {
+          float a4[4], l4[4], i4[4];
+          a8_ldv<4>(sc + e * 4, a4);
+          a8_ldv<4>(sc + (NG + e) * 4, l4);
+          a8_ldv<4>(sc + (2 * NG + e) * 4, i4);
+          auto two = [&](float a, float b) { return ra_pair(__float_as_uint(a), __float_as_uint(b)); };
           uint64_t y0, y1;
-          weights(e / 4, ra_add2(ra_pair(sv[e], sv[e + 1]), neg2), ra_add2(ra_pair(sv[e + 2], sv[e + 3]), neg2), y0, y1);
-          r0 = ra_fma2(y0, ra_pair(__float_as_uint(ib.x), __float_as_uint(ib.y)), r0);
-          r1 = ra_fma2(y1, ra_pair(__float_as_uint(ib.z), __float_as_uint(ib.w)), r1);
+          weights(ra_fma2(ra_pair(sv[e], sv[e + 1]), two(factor(a4[0]), factor(a4[1])), two(l4[0] + neg, l4[1] + neg)),
+                  ra_fma2(ra_pair(sv[e + 2], sv[e + 3]), two(factor(a4[2]), factor(a4[3])), two(l4[2] + neg, l4[3] + neg)), y0, y1,
+                  ph[e / 4], pl[e / 4]);
+          r0 = ra_fma2(y0, two(i4[0], i4[1]), r0);
+          r1 = ra_fma2(y1, two(i4[2], i4[3]), r1);
         }
       }
+    };
+    // What lies between a step's maximum and its weights. The maximum after the step before, which the other
+    // group had, comes first; then this step's is told. (In this order: who hears step n knows that step n - 1 was
+    // heard.) A row of a later piece's tile can be fully masked (its token ends before these keys): mx = -inf,
+    // and m stays -inf.
+    auto agree = [&](auto few, int j, float mx) -> bool {
+      constexpr bool FEW = decltype(few)::value;
+      float m1 = m;
+      if (j > 0) {
+        float before;
+        if (!heard(few, j - 1, before)) return false;
+        m1 = raised(m, before);
+      }
+      const int t = (FEW ? t_few : t_all) + j;
+      maxima[(t & 3) * RA_BQ + r] = mx;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(FEW ? told_few(t) : told(quarter, t));
+      if (FEW && !heard(few, j, mx)) return false;
+      const float m2 = raised(m1, mx);
+      if (m2 > m) {
+        l *= ra_ex2(m - m2);
+        m = m2;
+      }
+      if (j > 0 && (!FEW || quarter == 0) && __any_sync(0xffffffffu, m2 > m1)) {
+        // O at the new scale, after the product of the step before (its barrier is at no earlier phase: S_n was
+        // computed after the product of step n - 3)
+        const float alpha = m2 > m1 ? ra_ex2(m1 - m2) : 1.0f;
+        if (!a8_wait(p_done(n0 + j - 1), phase(n0 + j - 1), p.err, abort_flag)) return false;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(oadr + c * 16, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+          tmem_st_32x32b_x16(oadr + c * 16, v);
+        }
+      }
+      return true;
+    };
+    auto sum_up = [&](uint64_t r0, uint64_t r1) {
       float a0, a1, a2, a3;
       ra_unpair(r0, a0, a1);
       ra_unpair(r1, a2, a3);
       l += (a0 + a1) + (a2 + a3);
-      if (!__all_sync(0xffffffffu, p_ready) && !mbar_wait_warp(p_done(s), done_ph, p.err, abort_flag)) return false;
+    };
+    // Step j of the piece by a warp with rows. cut: some row of the tile ends inside its keys.
+    auto step = [&](bool cut, int j) -> bool {
+      const int n = n0 + j;
+      if (cut && TMA && !clear_tail(end - j * RA_BKV, n)) return false;
+      if (!a8_wait(s_full(n), phase(n), p.err, abort_flag) || !a8_wait(sc_full(n), (n / A8_SCR) & 1, p.err, abort_flag)) return false;
       tc_fence_after();
-      tmem_st_32x32b_x16(padr + s * 64, ph);
-      tmem_st_32x32b_x16(padr + s * 64 + 32, pl);
+      const uint32_t sadr = tmem + lane_off + n % A8_SB * 128;
+      const uint32_t sca = sc0 + (n & (A8_SCR - 1)) * 3 * NG * 4;
+      least = cut ? 1.17549435e-38f : 0.f;
+      const int last = lim - j * RA_BKV;           // keys 0 .. last of the tile are kept
+      float mx = -INFINITY;
+      uint32_t sv[32], sw[32];
+      tmem_ld_32x32b_x32(sadr, sv);
+#pragma unroll 1
+      for (int c = 0; c < RA_BKV; c += 64) {       // the next 32 columns are on their way
+        tmem_ld_wait();
+        tmem_ld_32x32b_x32(sadr + c + 32, sw);
+        if (cut) mask(sv, last - c);
+        mx = fmaxf(mx, max_t(sv, sca + c / GRP * 4));
+        tmem_ld_wait();
+        tmem_ld_32x32b_x32(sadr + ((c + 64) & (RA_BKV - 1)), sv);     // the last time: the first ones again
+        if (cut) mask(sw, last - c - 32);
+        mx = fmaxf(mx, max_t(sw, sca + (c + 32) / GRP * 4));
+      }
+      if (!agree(std::false_type(), j, mx)) return false;
+      const float neg = m > -INFINITY ? A8_LIFT - m : 0.f;
+      uint64_t r0 = 0, r1 = 0;
+      uint32_t ph[8], pl[8];
+#pragma unroll 1
+      for (int c = 0; c < RA_BKV; c += 64) {       // P: 16 columns for 32 keys, high and low parts, where S has been read
+        tmem_ld_wait();
+        tmem_ld_32x32b_x32(sadr + c + 32, sw);
+        if (cut) mask(sv, last - c);
+        weigh(sv, sca + c / GRP * 4, neg, ph, pl, r0, r1);
+        a8_tmem_st8(sadr + c / 2, ph);
+        a8_tmem_st8(sadr + c / 2 + 8, pl);
+        tmem_ld_wait();
+        if (c == 0) tmem_ld_32x32b_x32(sadr + 64, sv);
+        if (cut) mask(sw, last - c - 32);
+        weigh(sw, sca + (c + 32) / GRP * 4, neg, ph, pl, r0, r1);
+        a8_tmem_st8(sadr + c / 2 + 16, ph);
+        a8_tmem_st8(sadr + c / 2 + 24, pl);
+      }
+      sum_up(r0, r1);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(s));
-      lim -= RA_BKV;
-      end -= RA_BKV;
-      ++n;
+      if (lane == 0) mbar_arrive(p_full(n));
+      return true;
+    };
+    // The same of a piece of few rows: this warp has 32 keys of the tile, a lane 16 of them.
+    auto step_few = [&](bool cut, int j) -> bool {
+      const int n = n0 + j;
+      if (cut && TMA && !clear_tail(end - j * RA_BKV, n)) return false;
+      if (!a8_wait(s_full(n), phase(n), p.err, abort_flag) || !a8_wait(sc_full(n), (n / A8_SCR) & 1, p.err, abort_flag)) return false;
+      tc_fence_after();
+      const int first = quarter * 32 + (lane & 16);      // this lane's first key of the tile
+      const uint32_t sca = sc0 + ((n & (A8_SCR - 1)) * 3 * NG + first / GRP) * 4;
+      least = cut ? 1.17549435e-38f : 0.f;
+      uint32_t sw[32], sv[16];
+      tmem_ld_32x32b_x32(tmem + lane_off + n % A8_SB * 128 + quarter * 32, sw);
+      tmem_ld_wait();
+      // lanes r and 16 + r: high and low part of row r over 32 keys; each takes 16 and adds the other's part
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const uint32_t keep = lane & 16 ? sw[e + 16] : sw[e], give = lane & 16 ? sw[e] : sw[e + 16];
+        sv[e] = __float_as_uint(__uint_as_float(keep) + __uint_as_float(__shfl_xor_sync(0xffffffffu, give, 16)));
+      }
+      if (cut) mask(sv, lim - j * RA_BKV - first);
+      if (!agree(std::true_type(), j, max_t(sv, sca))) return false;
+      const float neg = m > -INFINITY ? A8_LIFT - m : 0.f;
+      uint64_t r0 = 0, r1 = 0;
+      uint32_t ph[4], pl[4];
+      weigh(sv, sca, neg, ph, pl, r0, r1);
+      // row lane & 15, its low parts 16 rows further on; 16 keys: one 16-byte chunk of its 128 bytes
+      const uint32_t at = sb + A8_OFF_P + n % A8_SB * A8_FEW_TILE + (lane & 15) * 128 + ((2 * quarter + (lane >> 4)) ^ (lane & 7)) * 16;
+      st_shared_v4(at, ph[0], ph[1], ph[2], ph[3]);
+      st_shared_v4(at + A8_FEW * 128, pl[0], pl[1], pl[2], pl[3]);
+      sum_up(r0, r1);
+      fence_async_shared();
+      tmem_st_wait();                              // O's, if the maximum was raised
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full(n));
       return true;
     };
     for (int k = 0; ok && more; ++k) {
-      int left, whole;                             // tiles left; those that every row sees whole
-      bool busy;
+      int left, whole, rows;                       // tiles left; those that every row sees whole; rows
       {
         const RaPiece& c = piece(k);
         left = c.tb - c.ta;
+        rows = c.toks * p.G;
         const int over = c.pos0 - c.ta * RA_BKV;   // the tile's first row's last key
         whole = min(left, (over + 1) >> 7);        // below zero: none
-        lim = over + min(r / p.G, c.toks - 1) - half * KEYS;     // padding rows: the last real row's limit
+        lim = over + min(token_of(rows <= A8_FEW ? lane & 15 : r), c.toks - 1);     // padding rows: the last real row's limit
         end = c.L - c.ta * RA_BKV;
-        busy = quarter * 32 < c.toks * p.G;        // some row of this warp is real
       }
+      const bool few = rows <= A8_FEW;
+      const bool busy = few || quarter * 32 < rows;      // some row of this warp is real
+      real = (few ? lane & (A8_FEW - 1) : r) < rows;
       m = -INFINITY;
       l = 0.f;
-      if (!mbar_wait_warp(k ? q_full(k) : q_first, k ? ((k - (k & 3 ? 0 : 4)) >> 2) & 1 : 0, p.err, abort_flag)) { ok = false; break; }
+      if (!a8_wait(k ? q_full(k) : q_first, q_phase(k), p.err, abort_flag)) { ok = false; break; }
       rs = qscale[(k & 3) * RA_BQ + r];
-      if (busy) {
-        bool first = true;
-        for (int i = 0; ok && i < whole; ++i, first = false) ok = step(std::false_type(), first);
-        for (int i = max(whole, 0); ok && i < left; ++i, first = false) ok = step(std::true_type(), first);
+      int j = (n0 & 1) ^ grp;                      // this group's first step
+      if (few) {
+        for (; ok && j < left; j += 2) ok = step_few(j >= whole, j);
+      } else if (busy) {
+        for (; ok && j < left; j += 2) ok = step(j >= whole, j);
       } else {
-        // no real row: P stays whatever it is, its O rows are never read. The product
-        // of step n - 2 is waited for all the same: this warp must not count for
-        // step n's phase while another still works on step n - 2.
-        for (int i = 0; ok && i < left; ++i, ++n, end -= RA_BKV) {
-          const int s = n & 1;
-          ok = (!TMA || clear_tail(end, n)) && mbar_wait_warp(s_full(s), (n >> 1) & 1, p.err, abort_flag) &&
-               (n < 2 || mbar_wait_warp(p_done(s), ((n >> 1) & 1) ^ 1u, p.err, abort_flag));
+        // no real row: P stays whatever it is, its O rows are never read
+        for (; ok && j < left; j += 2) {
+          const int n = n0 + j;
+          ok = (!TMA || clear_tail(end - j * RA_BKV, n)) && a8_wait(s_full(n), phase(n), p.err, abort_flag);
           __syncwarp();
-          if (ok && lane == 0) {
-            mbar_arrive(s_free(s));
-            mbar_arrive(p_full(s));
-          }
+          if (ok && lane == 0) mbar_arrive(p_full(n));
         }
       }
       if (!ok) break;
-      more = find(k + 1);                          // while the piece's last P V product, step n - 1's, runs
-      if (!mbar_wait_warp(p_done((n - 1) & 1), ((n - 1) >> 1) & 1, p.err, abort_flag)) { ok = false; break; }
-      tc_fence_after();
-      if (busy) {
-        {
-          float other = l;
-          if (!exchange(other)) { ok = false; break; }
-          l = half == 0 ? l + other : other + l;   // the same sum in both halves
+      // the last step's maximum, if the other group had it, and both groups' sums
+      if (busy && j != left + 1) {
+        float mx;
+        if (!(few ? heard(std::true_type(), left - 1, mx) : heard(std::false_type(), left - 1, mx))) { ok = false; break; }
+        const float m2 = raised(m, mx);
+        if (m2 > m) {
+          l *= ra_ex2(m - m2);
+          m = m2;
         }
-        const RaPiece& c = piece(k);
-        const bool whole = c.flags & 1;
-        const int tok = r / p.G;
-        const bool mine = r < c.toks * p.G;
+      }
+      float* sum = lsum + (k & 1) * 2 * RA_BQ;
+      sum[grp * RA_BQ + r] = l;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sums);
+      n0 += left;
+      if (few) t_few += left; else if (busy) t_all += left;
+      const RaPiece c = piece(k);
+      more = find(k + 1);                          // while the piece's last P V product, step n0 - 1's, runs
+      // in this order: once both groups are through, the product of step n0 - 4 is done, and the barrier of
+      // step n0 - 1's at no earlier phase
+      if (!a8_wait(sums, k & 1, p.err, abort_flag) || !a8_wait(p_done(n0 - 1), phase(n0 - 1), p.err, abort_flag)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      if (few ? quarter == 0 : busy) {             // each group half of the columns
+        if (few) {
+          l = 0.f;
+#pragma unroll 1
+          for (int q = 0; q < 16; ++q) l += sum[q * 16 + (lane & 15)];
+        } else {
+          l = sum[r] + sum[RA_BQ + r];
+        }
+        const bool all = c.flags & 1;
+        const int tok = token_of(r);
+        const bool mine = r < rows;
         const int64_t orow = static_cast<int64_t>(c.row0 + tok) * p.Hq + c.g * p.G + (r - tok * p.G);
         const int64_t pslot = static_cast<int64_t>(cta) * 2 + (c.flags >> 1);
-        const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
-#pragma unroll
+        const float inv = all ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           uint32_t v[32];
-          tmem_ld_32x32b_x32(oadr + h * 32, v);
+          tmem_ld_32x32b_x32(oadr + grp * 64 + h * 32, v);
           tmem_ld_wait();
-          if (mine && whole) {
-            __nv_bfloat16* orow_p = p.j.o + orow * RA_D + half * 64 + h * 32;
+          if (few) {                               // the low parts' share
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(__shfl_down_sync(0xffffffffu, v[e], 16)));
+          }
+          if (mine && all) {
+            __nv_bfloat16* orow_p = p.j.o + orow * RA_D + grp * 64 + h * 32;
 #pragma unroll
             for (int e = 0; e < 32; e += 16) {
               uint32_t y[8];
@@ -774,24 +1000,25 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
               ra_st32(orow_p + e, y);
             }
           } else if (mine) {
-            float* po = p.j.part_o + (pslot * RA_D + half * 64 + h * 32) * RA_BQ + r * 4;      // lanes side by side
+            float* po = p.j.part_o + (pslot * RA_D + grp * 64 + h * 32) * RA_BQ + r * 4;      // lanes side by side
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
               *reinterpret_cast<uint4*>(po + e * RA_BQ) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
           }
           __syncwarp();                            // the next load is a whole warp's
         }
-        if (mine && half == 0) {
-          if (whole) {
+        if (mine && grp == 0) {
+          if (all) {
             if (p.j.lse) p.j.lse[orow] = (m - A8_LIFT + log2f(l)) * RA_LN2;
           } else {
             *reinterpret_cast<float2*>(p.j.part_ml + (pslot * RA_BQ + r) * 2) = make_float2(m - A8_LIFT, l);
           }
         }
       }
-      // the next piece's first P V into O follows this warp's next arrival
+      // O is read: the next piece's first P V may write it
       tc_fence_before();
       __syncwarp();
+      if (lane == 0) mbar_arrive(o_free);
     }
     if (!ok) *abort_flag = 1;
   }
@@ -819,6 +1046,7 @@ kl_status ragged_attention8(const kl_ragged_cfg& rc, int Hq, int Hkv, const void
   memset(&p, 0, sizeof(p));
   p.G = p.j.G = Hq / Hkv;
   p.TQ = RA_BQ / p.G;
+  p.inv_g = (65536 + p.G - 1) / p.G;
   const bool tma = rc.block_size % 8 == 0;
   p.box_log = 7;
   while (tma && rc.block_size & ((1 << p.box_log) - 1)) --p.box_log;    // gcd(block_size, 128)

@@ -45,9 +45,10 @@ def _step8(seed, reqs, Hkv, bs, extra_rows=0, any_scale=False):
 def _attention_tol(q, kc, ks, vc, vs, table, cu, ctx, want, A):
     """The bound on |o - oracle| of a weight that is a sum of two e4m3 numbers, elementwise, and the one on lse.
     Queries: two e4m3 pieces hold a bf16 number's 8 bits; below 2^-10 of the row's largest one they are off by 2^-10 at a largest of
-    128 or more: 2^-17 of it. Weights: cut to 4 bits, the rest rounded to 4: 2^-8; below, off by 2^-9 / 2 twice, where the row's largest
-    weight times scale is held as 2^6 or more: 2^-16 of that weight, in units of the scale, twice. fp32 sums as in the bf16 test:
-    2^-24 x 128 x sum |q k| / sqrt(d) of a score and 2^-9 A of the running sums; the result is rounded to bf16, 2^-8 |o|."""
+    128 or more: 2^-17 of it. Weights: f16 (2^-11) cut to 4 bits, the rest, below 2^-3 of the weight's power of two, rounded to
+    4: 2^-8 of it; codes below 2^-6 are off by 2^-10 instead, in both parts, where the row's largest weight times scale is held as
+    2^4 or more: 2^-13 of that weight, in units of the scale. fp32 sums as in the bf16 test: 2^-24 x 128 x sum |q k| / sqrt(d) of a
+    score and 2^-9 A of the running sums; the result is rounded to bf16, 2^-8 |o|."""
     T, Hq, d = q.shape
     bs, Hkv = kc.shape[1], kc.shape[2]
     tol, ltol = np.zeros_like(want), np.zeros((T, Hq))
@@ -68,7 +69,7 @@ def _attention_tol(q, kc, ks, vc, vs, table, cu, ctx, want, A):
                 mag = np.abs(k).sum(1) * kb / np.sqrt(d)
                 dz = 2.0 ** -17 * np.abs(q[r, h]).max() * mag.max() + 2.0 ** -17 * (np.abs(k) @ np.abs(q[r, h]) * kb).max() / np.sqrt(d)
                 ltol[r, h] = dz + 1e-6 * abs(z).max() + L_ * 2.0 ** -24 + 1e-6
-                tol[r, h] = (2.0 ** -8 + 2.0 ** -9 + 2 * dz) * A[r, h] + 2.0 ** -8 * np.abs(want[r, h]) + 2.0 ** -15 * (w * vb).max() * np.abs(v).sum(0)
+                tol[r, h] = (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -9 + 2 * dz) * A[r, h] + 2.0 ** -8 * np.abs(want[r, h]) + 2.0 ** -13 * (w * vb).max() * np.abs(v).sum(0)
     return tol, ltol
 
 
