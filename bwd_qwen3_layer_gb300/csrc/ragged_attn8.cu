@@ -25,9 +25,9 @@
 // of floor(128 / G) tokens x G heads, runs of key tiles of 128 keys, one CTA per SM,
 // pieces of cut items joined in CTA order: results repeat bit for bit.
 //
-// Roles (12 warps): warp 0 copies the keys and, between two tiles, splits the next
-// piece's queries, warp 1 copies the values and looks up the scales, warp 2 issues the
-// score products, warp 3 the P V products. Warps 4..7 are the softmax of the even steps,
+// Roles (12 warps): warp 0 copies the keys, warp 1 the values and looks up the scales; both
+// split the next piece's queries between two tiles. Warp 2 issues the score products, warp 3
+// the P V products. Warps 4..7 are the softmax of the even steps,
 // 8..11 of the odd ones (thread = query row = TMEM lane): a step's chain of waits, loads,
 // maxima, 128 exponentials and splits a row is longer than two steps' products, so two are
 // under way. The running maximum passes from one group to the other through shared memory;
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
   const RaLens lens = {p.cu, p.ctx, p.B, p.T, p.Hkv, p.TQ};
 
   if (warp == 3 && lane == 0) {
-    for (int k = 0; k < 4; ++k) mbar_init(q_full(k), 1);
+    for (int k = 0; k < 4; ++k) mbar_init(q_full(k), 2);
     mbar_init(q_first, 8);
     for (int k = 0; k < 16; ++k) mbar_init(told(k >> 2, k), 1);
     for (int k = 0; k < 4; ++k) mbar_init(told_few(k), 4);
@@ -388,29 +388,25 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       if (lane == 0) mbar_arrive(sc_full(tile));
       ++tile;
     };
-    // Warp 0: the next piece's queries, eight rows at a time once the S products of the piece before this
-    // one are done with the buffer; all of them by this piece's end.
+    // The next piece's queries, four rows at a time, in turn by these two warps, once the S products of the
+    // piece before this one are done with the buffer; all of them by this piece's end.
     int q_at = 0, q_rows = 0;
+    uint4 qx[2] = {};
     auto split_next = [&](int k, bool must) -> bool {
-      if (q_at == 0 && k > 0) {
+      if (q_at < 8 && k > 0) {
         const uint32_t ph = ((k - 1) >> 1) & 1;
         if (must ? !a8_wait(q_empty(k + 1), ph, p.err, abort_flag) : !__all_sync(0xffffffffu, mbar_test_wait(q_empty(k + 1), ph))) return !must;
       }
-      const RaPiece& c = piece(k + 1);
-      uint4 x[2][2] = {};
-      load_q(c, q_rows, q_at, x[0]);
-      load_q(c, q_rows, q_at + 4, x[1]);
-#pragma unroll 1
-      for (int u = 0; u < 2; ++u, q_at += 4) {
-        if (q_at < q_rows) split_q(x[0], k + 1, q_rows, q_at);
-        x[0][0] = x[1][0];
-        x[0][1] = x[1][1];
-      }
-      if (q_at >= q_rows) {
-        no_rows(k + 1, q_rows, lane, 32);
+      if (q_at < q_rows) split_q(qx, k + 1, q_rows, q_at);
+      q_at += 8;
+      if (q_at < q_rows) {
+        load_q(piece(k + 1), q_rows, q_at, qx);    // on their way until the next tile
+      } else {
+        no_rows(k + 1, q_rows, lane + 32 * warp, 64);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full(k + 1));
+        q_rows = 0;
       }
       return true;
     };
@@ -430,8 +426,9 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
     for (int k = 0; ok && have; ++k) {
       const RaPiece w = piece(k);
       have = find(k + 1);
-      q_at = 0;
-      q_rows = is_k && have ? piece(k + 1).toks * p.G : 0;
+      q_at = 4 * warp;
+      q_rows = have ? piece(k + 1).toks * p.G : 0;
+      if (q_at < q_rows) load_q(piece(k + 1), q_rows, q_at, qx);
       if (TMA) {
         // One look at the table serves a batch of `per` tiles, a lane per box. Pages are asked for two
         // batches ahead (the next piece's too), scales one: a read takes 1000 to 3000 cycles while HBM is busy.
@@ -477,7 +474,9 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
             s = 0;
             ph ^= 1u;
           }
-          if (q_at < q_rows && !split_next(k, false)) { ok = false; break; }
+          // as many as the tiles that are left make necessary
+          for (int due = q_rows > 0 ? max(1, (q_rows - q_at + 8 * (w.tb - j) - 1) / (8 * (w.tb - j))) : 0; ok && due > 0 && q_rows > 0; --due) ok = split_next(k, false);
+          if (!ok) break;
         }
       } else {
         // a lane for four of a tile's keys
@@ -508,12 +507,14 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
             ph ^= 1u;
           }
           if (j + 1 < w.tb) lookup(j + 1);
-          if (q_at < q_rows && !split_next(k, false)) { ok = false; break; }
+          // as many as the tiles that are left make necessary
+          for (int due = q_rows > 0 ? max(1, (q_rows - q_at + 8 * (w.tb - j) - 1) / (8 * (w.tb - j))) : 0; ok && due > 0 && q_rows > 0; --due) ok = split_next(k, false);
+          if (!ok) break;
         }
         // the piece's last tile: its products free Q, which the next piece waits for
         if (ok) announce(std::integral_constant<int, 0>());
       }
-      while (ok && q_at < q_rows) ok = split_next(k, true);
+      while (ok && q_rows > 0) ok = split_next(k, true);
     }
     if (!ok) *abort_flag = 1;
     // copies still in flight must land before exit
@@ -1056,8 +1057,9 @@ kl_status ragged_attention8(const kl_ragged_cfg& rc, int Hq, int Hkv, const void
     const cuuint64_t dk[3] = {RA_D, static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(rc.n_blocks) * rc.block_size};
     const cuuint64_t sk[2] = {RA_D, pitch};
     const cuuint32_t bk[3] = {RA_D, 1, 1u << p.box_log};
-    KL_TRY(ra_map(&p.tmK, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, kp, dk, sk, bk));
-    KL_TRY(ra_map(&p.tmV, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, vp, dk, sk, bk));
+    // a row is 128 bytes, its neighbours are other heads': 256-byte fetches would bring those, too
+    KL_TRY(ra_map(&p.tmK, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, kp, dk, sk, bk, CU_TENSOR_MAP_L2_PROMOTION_L2_128B));
+    KL_TRY(ra_map(&p.tmV, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, vp, dk, sk, bk, CU_TENSOR_MAP_L2_PROMOTION_L2_128B));
   }
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.kp = static_cast<const uint8_t*>(kp);

@@ -70,12 +70,12 @@ inline RaWs ra_ws(int ctas) {
 }
 
 inline kl_status ra_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* ptr, const cuuint64_t* dims, const cuuint64_t* strides,
-                 const cuuint32_t* box) {
+                 const cuuint32_t* box, CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
   auto fn = tensor_map_encoder();
   if (!fn) return set_error(KL_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r = fn(m, type, rank, const_cast<void*>(ptr), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promotion,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return set_error(KL_ERR_INVALID_ARG, "ragged attention: tensor map encode failed (%d)", (int)r);
   return KL_OK;
