@@ -25,13 +25,14 @@
 // of floor(128 / G) tokens x G heads, runs of key tiles of 128 keys, one CTA per SM,
 // pieces of cut items joined in CTA order: results repeat bit for bit.
 //
-// Roles (12 warps): warp 0 copies the keys, warp 1 the values and looks up the scales; both
-// split the next piece's queries between two tiles. Warp 2 issues the score products, warp 3
-// the P V products. Warps 4..7 are the softmax of the even steps,
+// Roles (16 warps): warp 0 copies the keys, warp 1 the values, warp 2 issues the score
+// products, warp 3 the P V products. Warps 4..7 are the softmax of the even steps,
 // 8..11 of the odd ones (thread = query row = TMEM lane): a step's chain of waits, loads,
 // maxima, 128 exponentials and splits a row is longer than two steps' products, so two are
 // under way. The running maximum passes from one group to the other through shared memory;
-// O has one scale. The softmax warps, idle at first, split the first piece's queries.
+// O has one scale. Warp 12 looks up the scales, warps 13..15 split the next piece's queries
+// (the first piece's: the softmax warps, idle at first): done by the copy warps in between,
+// both held the copies up (124 us instead of LATER for a decoding batch).
 // Scores stay in tensor memory and are read twice, for the maximum and for the weights, 32
 // columns at a time, so that a step's code is a few small loops: unrolled over 128 keys (30
 // KB a step, 170 KB in all) the instruction fetch took longer than the work, 3800 cycles a
@@ -61,11 +62,13 @@
 namespace kl {
 namespace {
 
-constexpr int A8_WARPS = 12;
+constexpr int A8_WARPS = 16;
 constexpr int A8_THREADS = 32 * A8_WARPS;
 constexpr uint32_t A8_TILE = 128 * 128;       // a tile of keys, of values, of one part of the queries
 constexpr int A8_NST = 4;                     // stages of the K and of the V ring
-constexpr int A8_SCR = 4;                     // tiles in the ring of scales
+constexpr int A8_QR = 8;                      // pieces in the ring of the rows' factors
+constexpr int a8_scr(bool tma) { return tma ? 8 : 4; }      // tiles in the ring of scales
+constexpr int A8_QW = 3;                      // warps that split queries
 constexpr int A8_SB = 3;                      // steps whose scores and weights are in tensor memory
 constexpr int A8_FEW = 16;                    // rows of a piece that has both parts in one tile
 constexpr uint32_t A8_FEW_TILE = 2 * A8_FEW * 128;          // 32 rows: a quarter of the lanes
@@ -75,11 +78,12 @@ constexpr uint32_t A8_OFF_P = A8_OFF_Q + 4 * A8_TILE;       // weights of few ro
 constexpr uint32_t A8_OFF_K = A8_OFF_P + A8_SB * A8_FEW_TILE;
 constexpr uint32_t A8_OFF_V = A8_OFF_K + A8_NST * A8_TILE;
 constexpr uint32_t A8_OFF_BAR = A8_OFF_V + A8_NST * A8_TILE;
-constexpr uint32_t A8_OFF_QS = A8_OFF_BAR + 2560;           // the rows' factors, of four pieces
-constexpr uint32_t A8_OFF_MX = A8_OFF_QS + 4 * RA_BQ * 4;   // the rows' maxima, of four steps
+constexpr uint32_t A8_OFF_QS = A8_OFF_BAR + 3072;           // the rows' factors, of eight pieces
+constexpr uint32_t A8_OFF_MX = A8_OFF_QS + A8_QR * RA_BQ * 4;   // the rows' maxima, of four steps
 constexpr uint32_t A8_OFF_L = A8_OFF_MX + 4 * RA_BQ * 4;    // the groups' sums, of two pieces
 constexpr uint32_t A8_OFF_SC = A8_OFF_L + 4 * RA_BQ * 4;    // the ring of scales
-constexpr size_t a8_smem(bool tma) { return 1024 + A8_OFF_SC + A8_SCR * 3 * (tma ? 16 : 128) * 4; }
+constexpr size_t a8_smem(bool tma) { return 1024 + A8_OFF_SC + a8_scr(tma) * 3 * (tma ? 16 : 128) * 4; }
+static_assert(a8_smem(false) <= 232448, "shared memory");
 // Tensor memory: S of three steps, whose columns P takes as they are read, and O: all 512 columns.
 constexpr uint32_t A8_TM_O = 384;
 constexpr float A8_LIFT = 4.0f;               // P' of the running maximum is 2^4 ...
@@ -173,9 +177,11 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sb = smem_u32(smem);
   const uint32_t bar = sb + A8_OFF_BAR;
-  auto q_full = [&](int k) { return bar + 0 + 8 * (k & 3); };      // piece k's queries: four, so that no
-                                                                   // waiter is two phases behind
-  auto q_empty = [&](int k) { return bar + 32 + 8 * (k & 1); };    // its last S product is done with them
+  constexpr int A8_SCR = a8_scr(TMA);
+  // piece k's queries: eight, since with pieces of one tile the score products run three pieces ahead of
+  // the softmax and the queries two more, and no waiter may be two phases behind
+  auto q_full = [&](int k) { return bar + 576 + 8 * (k & (A8_QR - 1)); };
+  auto q_empty = [&](int k) { return bar + 0 + 8 * (k & 1); };    // its last S product is done with them
   auto k_full = [&](int s) { return bar + 48 + 8 * s; };
   auto k_empty = [&](int s) { return bar + 80 + 8 * s; };
   auto v_full = [&](int s) { return bar + 112 + 8 * s; };
@@ -185,19 +191,21 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
   auto p_done = [&](int n) { return bar + 224 + 8 * (n % A8_SB); };   // O += P_n V_n computed
   auto phase = [&](int n) -> uint32_t { return (n / A8_SB) & 1; };    // their parity for step n
   auto sc_full = [&](int n) { return bar + 248 + 8 * (n & (A8_SCR - 1)); };    // the tile's scales written
-  const uint32_t drain = bar + 280, drain_pv = bar + 288;
-  const uint32_t q_first = bar + 296;                              // the first piece's queries
-  auto told = [&](int q, int t) { return bar + 304 + 32 * q + 8 * (t & 3); };   // the step's maxima of quarter q's rows
-  auto told_few = [&](int t) { return bar + 432 + 8 * (t & 3); };  // those of all quarters
-  const uint32_t sums = bar + 464;                                 // a piece's sums of both groups
-  const uint32_t o_free = bar + 472;                               // a piece's O has been read
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + A8_OFF_BAR + 480);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + A8_OFF_BAR + 484);
-  RaFound* found = reinterpret_cast<RaFound*>(smem + A8_OFF_BAR + 488);
-  long long* wsum = reinterpret_cast<long long*>(smem + A8_OFF_BAR + 552);
-  RaWalk* walks = reinterpret_cast<RaWalk*>(smem + A8_OFF_BAR + 648);        // the finder's, then one per warp
-  RaPiece* pieces = reinterpret_cast<RaPiece*>(smem + A8_OFF_BAR + 1272);    // the first one, then two per warp
-  static_assert(sizeof(RaFound) <= 64 && A8_WARPS * 8 <= 96 && (A8_WARPS + 1) * sizeof(RaWalk) <= 624 && (A8_WARPS * 2 + 1) * sizeof(RaPiece) <= 1288,
+  auto sc_empty = [&](int n) { return bar + 312 + 8 * (n & (A8_SCR - 1)); };   // and read
+  const uint32_t drain = bar + 376, drain_pv = bar + 384;
+  const uint32_t q_first = bar + 392;                              // the first piece's queries
+  auto told = [&](int q, int t) { return bar + 400 + 32 * q + 8 * (t & 3); };   // the step's maxima of quarter q's rows
+  auto told_few = [&](int t) { return bar + 528 + 8 * (t & 3); };  // those of all quarters
+  const uint32_t sums = bar + 560;                                 // a piece's sums of both groups
+  const uint32_t o_free = bar + 568;                               // a piece's O has been read
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + A8_OFF_BAR + 640);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + A8_OFF_BAR + 644);
+  RaFound* found = reinterpret_cast<RaFound*>(smem + A8_OFF_BAR + 648);
+  long long* wsum = reinterpret_cast<long long*>(smem + A8_OFF_BAR + 712);
+  RaWalk* walks = reinterpret_cast<RaWalk*>(smem + A8_OFF_BAR + 840);        // the finder's, then one per warp
+  RaPiece* pieces = reinterpret_cast<RaPiece*>(smem + A8_OFF_BAR + 1656);    // the first one, then two per warp
+  static_assert(sizeof(RaFound) <= 64 && A8_WARPS * 8 <= 128 && (A8_WARPS + 1) * sizeof(RaWalk) <= 816 &&
+                    (A8_WARPS * 2 + 1) * sizeof(RaPiece) <= 1416,
                 "shared-memory layout");
   float* qscale = reinterpret_cast<float*>(smem + A8_OFF_QS);
   constexpr int GRP = TMA ? 8 : 1;               // keys that share a scale
@@ -209,7 +217,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
   const RaLens lens = {p.cu, p.ctx, p.B, p.T, p.Hkv, p.TQ};
 
   if (warp == 3 && lane == 0) {
-    for (int k = 0; k < 4; ++k) mbar_init(q_full(k), 2);
+    for (int k = 0; k < A8_QR; ++k) mbar_init(q_full(k), A8_QW);
     mbar_init(q_first, 8);
     for (int k = 0; k < 16; ++k) mbar_init(told(k >> 2, k), 1);
     for (int k = 0; k < 4; ++k) mbar_init(told_few(k), 4);
@@ -227,7 +235,10 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       mbar_init(p_full(n), 4);
       mbar_init(p_done(n), 1);
     }
-    for (int n = 0; n < A8_SCR; ++n) mbar_init(sc_full(n), 1);
+    for (int n = 0; n < A8_SCR; ++n) {
+      mbar_init(sc_full(n), 1);
+      mbar_init(sc_empty(n), 4);
+    }
     mbar_init(drain, 1);
     mbar_init(drain_pv, 1);
     *abort_flag = 0;
@@ -260,8 +271,8 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
     return piece(k).tb > 0;
   };
   auto page = [&](int b, int lb) { return lb < p.max_blocks ? p.table[static_cast<int64_t>(b) * p.max_blocks + lb] : -1; };
-  // the parity that piece k's queries' barrier is waited for with (q_full(0) serves from piece 4 on)
-  auto q_phase = [&](int k) -> uint32_t { return k ? ((k - (k & 3 ? 0 : 4)) >> 2) & 1 : 0; };
+  // the parity that piece k's queries' barrier is waited for with (q_full(0) serves from piece 8 on)
+  auto q_phase = [&](int k) -> uint32_t { return k ? ((k - (k & (A8_QR - 1) ? 0 : A8_QR)) / A8_QR) & 1 : 0; };
   auto token_of = [&](int r) { return (r * p.inv_g) >> 16; };
   // Queries, four rows at a time, 8 lanes of 16 elements each: row r0 + (lane >> 3) of a piece with `rows` ...
   auto load_q = [&](const RaPiece& c, int rows, int r0, uint4 (&x)[2]) {
@@ -297,7 +308,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
     if (r < rows) {
       const bool few = rows <= A8_FEW;
       uint32_t at = sb + A8_OFF_Q + (k & 1) * 2 * A8_TILE + r * 128 + ((j ^ (r & 7)) << 4);
-      float* f = qscale + (k & 3) * RA_BQ + r;
+      float* f = qscale + (k & (A8_QR - 1)) * RA_BQ + r;
       const float v = a >= 0x7f80u ? __int_as_float(0x7fffffff) : down * p.scale_log2;
 #pragma unroll 1
       for (int c = 0; c < (few ? 4 : 1); ++c, at += A8_FEW_TILE, f += 32) {
@@ -312,7 +323,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
   auto no_rows = [&](int k, int rows, int from, int by) {
 #pragma unroll 1
     for (int r = from; r < RA_BQ; r += by)
-      if ((rows <= A8_FEW ? r & (A8_FEW - 1) : r) >= rows) qscale[(k & 3) * RA_BQ + r] = 0.f;
+      if ((rows <= A8_FEW ? r & (A8_FEW - 1) : r) >= rows) qscale[(k & (A8_QR - 1)) * RA_BQ + r] = 0.f;
   };
 
   if (warp < 2) {
@@ -359,124 +370,38 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       mbar_arrive(full0 + 8 * as);
       as = as == A8_NST - 1 ? 0 : as + 1;
     };
-    // Warp 1: the scales of the next tile in line, from a batch's lanes (TMA; `which` of its tiles) or a
-    // lane's four keys, into the ring. Its entry is free: the copies wait for the product of four tiles before.
-    float a[4] = {1.f, 1.f, 1.f, 1.f}, b[4] = {1.f, 1.f, 1.f, 1.f};
-    int tile = 0;
-    auto publish = [&](int which) {
-      if (is_k) return;
-      float* sc = reinterpret_cast<float*>(smem + A8_OFF_SC) + (tile & (A8_SCR - 1)) * 3 * NG;
-      if (TMA) {
-        if (my == which) {
-          const float lb = log2f(b[0]), ib = 1.f / b[0];
-          const int gs = box >> 3, g0 = (lane & (nbox - 1)) * gs;
-          for (int g = g0; g < g0 + gs; ++g) {
-            sc[g] = a[0];
-            sc[NG + g] = lb;
-            sc[2 * NG + g] = ib;
-          }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sc[(i * 32 + lane) % NG] = a[i];
-          sc[NG + (i * 32 + lane) % NG] = log2f(b[i]);
-          sc[2 * NG + (i * 32 + lane) % NG] = 1.f / b[i];
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(sc_full(tile));
-      ++tile;
-    };
-    // The next piece's queries, four rows at a time, in turn by these two warps, once the S products of the
-    // piece before this one are done with the buffer; all of them by this piece's end.
-    int q_at = 0, q_rows = 0;
-    uint4 qx[2] = {};
-    auto split_next = [&](int k, bool must) -> bool {
-      if (q_at < 8 && k > 0) {
-        const uint32_t ph = ((k - 1) >> 1) & 1;
-        if (must ? !a8_wait(q_empty(k + 1), ph, p.err, abort_flag) : !__all_sync(0xffffffffu, mbar_test_wait(q_empty(k + 1), ph))) return !must;
-      }
-      if (q_at < q_rows) split_q(qx, k + 1, q_rows, q_at);
-      q_at += 8;
-      if (q_at < q_rows) {
-        load_q(piece(k + 1), q_rows, q_at, qx);    // on their way until the next tile
-      } else {
-        no_rows(k + 1, q_rows, lane + 32 * warp, 64);
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full(k + 1));
-        q_rows = 0;
-      }
-      return true;
-    };
     int row[4];
-    // TMA: the batches that have been asked for (up to three): this lane's box's page, place in it (below
-    // zero: none) and kv head; the piece and tile of the next one; whether the first one's scales have been too
-    int blk[3] = {}, at[3] = {}, head[3] = {}, queued = 0, ask_k = 0, ask_j = -1;
-    bool asked = false;
-    auto scales = [&](int i) {
-      a[1] = b[1] = 1.f;                           // a page that is read as zero has none
-      if (at[i] < 0 || blk[i] < 0 || blk[i] >= p.n_blocks) return;
-      const int64_t sc = static_cast<int64_t>(blk[i]) * p.Hkv + head[i];
-      a[1] = p.ks[sc];
-      b[1] = p.vs[sc];
+    int blk = 0, at = -1;                          // TMA: the next batch's page of this lane's box and the place in it
+    auto ask = [&](const RaPiece& c, int j) {
+      const int pos = j * RA_BKV + lane * box, lb = pos / p.bs;
+      at = pos < min(c.L, c.tb * RA_BKV) ? pos - lb * p.bs : -1;
+      if (at >= 0) blk = page(c.b, lb);
     };
     bool have = find(0);
+    if (TMA && have) ask(piece(0), piece(0).ta);
     for (int k = 0; ok && have; ++k) {
       const RaPiece w = piece(k);
       have = find(k + 1);
-      q_at = 4 * warp;
-      q_rows = have ? piece(k + 1).toks * p.G : 0;
-      if (q_at < q_rows) load_q(piece(k + 1), q_rows, q_at, qx);
       if (TMA) {
-        // One look at the table serves a batch of `per` tiles, a lane per box. Pages are asked for two
-        // batches ahead (the next piece's too), scales one: a read takes 1000 to 3000 cycles while HBM is busy.
+        // One look at the table serves a batch of `per` tiles, a lane per box; the next batch's pages (the
+        // next piece's, at the end of this one) are asked for before this one's tiles are copied.
         for (int j = w.ta; j < w.tb; ++j) {
           const int nth = (j - w.ta) & (per - 1);
           if (nth == 0) {
-            while (queued < 3 && (ask_k < k + 1 || (ask_k == k + 1 && have))) {
-              const RaPiece& c = piece(ask_k);
-              if (ask_j < 0) ask_j = c.ta;
-              const int pos = ask_j * RA_BKV + lane * box, lb = pos / p.bs;
-              const int there = pos < min(c.L, c.tb * RA_BKV) ? pos - lb * p.bs : -1;
-              const int pg = there >= 0 ? page(c.b, lb) : 0;
-              if (queued == 0) { at[0] = there; blk[0] = pg; head[0] = c.g; }
-              else if (queued == 1) { at[1] = there; blk[1] = pg; head[1] = c.g; }
-              else { at[2] = there; blk[2] = pg; head[2] = c.g; }
-              ++queued;
-              ask_j += per;
-              if (ask_j >= c.tb) {
-                ask_j = -1;
-                ++ask_k;
-              }
-            }
-            row[0] = at[0] >= 0 ? pool_row(blk[0], at[0]) : no_row;
-            if (!is_k) {
-              if (!asked) scales(0);               // into a[1], b[1]
-              a[0] = a[1];
-              b[0] = b[1];
-              asked = queued > 1;
-              if (asked) scales(1);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) { at[i] = at[i + 1]; blk[i] = blk[i + 1]; head[i] = head[i + 1]; }
-            --queued;
+            row[0] = at >= 0 ? pool_row(blk, at) : no_row;
+            if (j + per < w.tb) ask(w, j + per);
+            else if (have) ask(piece(k + 1), piece(k + 1).ta);
           }
           if (!ra_wait_copy(empty0 + 8 * s, ph, p.err, abort_flag)) { ok = false; break; }
           if (el) mbar_arrive_expect_tx(full0 + 8 * s, A8_TILE);
           __syncwarp();
           if (my == nth) ra_tma_3d(ring + s * A8_TILE + (lane & (nbox - 1)) * box * 128, tm, 0, w.g, row[0], full0 + 8 * s);
           __syncwarp();
-          publish(nth);
           ++issued;
           if (++s == A8_NST) {
             s = 0;
             ph ^= 1u;
           }
-          // as many as the tiles that are left make necessary
-          for (int due = q_rows > 0 ? max(1, (q_rows - q_at + 8 * (w.tb - j) - 1) / (8 * (w.tb - j))) : 0; ok && due > 0 && q_rows > 0; --due) ok = split_next(k, false);
-          if (!ok) break;
         }
       } else {
         // a lane for four of a tile's keys
@@ -485,21 +410,13 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int pos = j * RA_BKV + i * 32 + lane, lb = pos / p.bs;
-            const int pg = pos < keys ? page(w.b, lb) : 0;
-            row[i] = pos < keys ? pool_row(pg, pos - lb * p.bs) : no_row;
-            a[i] = b[i] = 1.f;                     // a page that is read as zero has none
-            if (!is_k && row[i] != no_row) {
-              const int64_t sc = static_cast<int64_t>(pg) * p.Hkv + w.g;
-              a[i] = p.ks[sc];
-              b[i] = p.vs[sc];
-            }
+            row[i] = pos < keys ? pool_row(page(w.b, lb), pos - lb * p.bs) : no_row;
           }
         };
         lookup(w.ta);
         for (int j = w.ta; j < w.tb; ++j) {
           if (!ra_wait_copy(empty0 + 8 * s, ph, p.err, abort_flag)) { ok = false; break; }
           gather(ring + s * A8_TILE, w.g, row);
-          publish(0);
           if (j > w.ta) announce(std::integral_constant<int, 1>());   // the tile before
           ++issued;
           if (++s == A8_NST) {
@@ -507,14 +424,10 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
             ph ^= 1u;
           }
           if (j + 1 < w.tb) lookup(j + 1);
-          // as many as the tiles that are left make necessary
-          for (int due = q_rows > 0 ? max(1, (q_rows - q_at + 8 * (w.tb - j) - 1) / (8 * (w.tb - j))) : 0; ok && due > 0 && q_rows > 0; --due) ok = split_next(k, false);
-          if (!ok) break;
         }
         // the piece's last tile: its products free Q, which the next piece waits for
         if (ok) announce(std::integral_constant<int, 0>());
       }
-      while (ok && q_rows > 0) ok = split_next(k, true);
     }
     if (!ok) *abort_flag = 1;
     // copies still in flight must land before exit
@@ -603,6 +516,120 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
     if (el) umma_commit(drain_pv);
     __syncwarp();
     mbar_wait(drain_pv, 0, p.err);
+  } else if (warp == 12) {
+    // ---------- scales (TMA: lane = page box of a batch of tiles; else a lane for four of a tile's keys) ----------
+    const int box = 1 << p.box_log, nbox = RA_BKV >> p.box_log, my = lane >> (7 - p.box_log);
+    const int per = TMA ? box >> 2 : 1;            // tiles of a look-up
+    constexpr int KS = TMA ? 1 : 4;
+    // Pages are asked for two batches ahead (the next piece's too), scales one: a read takes 1000 to 3000
+    // cycles while HBM is busy. The batches that have been asked for: this lane's pages (below zero: none) and
+    // the kv head; the piece and tile of the next one.
+    int blk[3][KS] = {}, head[3] = {}, queued = 0, ask_k = 0, ask_j = -1, n = 0;
+    float a[2][KS], b[2][KS];                      // this batch's, the next one's
+    bool asked = false;
+    auto scales = [&](int i) {
+#pragma unroll
+      for (int e = 0; e < KS; ++e) {
+        a[1][e] = b[1][e] = 1.f;                   // a page that is read as zero has none
+        if (blk[i][e] < 0 || blk[i][e] >= p.n_blocks) continue;
+        const int64_t sc = static_cast<int64_t>(blk[i][e]) * p.Hkv + head[i];
+        a[1][e] = p.ks[sc];
+        b[1][e] = p.vs[sc];
+      }
+    };
+    bool ok = true, have = find(0);
+    for (int k = 0; ok && have; ++k) {
+      const RaPiece w = piece(k);
+      have = find(k + 1);
+      for (int j = w.ta; j < w.tb; ++j, ++n) {
+        const int nth = (j - w.ta) & (per - 1);
+        if (nth == 0) {
+          while (queued < 3 && (ask_k < k + 1 || (ask_k == k + 1 && have))) {
+            const RaPiece& c = piece(ask_k);
+            if (ask_j < 0) ask_j = c.ta;
+#pragma unroll
+            for (int e = 0; e < KS; ++e) {
+              const int pos = ask_j * RA_BKV + (TMA ? lane * box : e * 32 + lane);
+              const int pg = pos < min(c.L, c.tb * RA_BKV) ? page(c.b, pos / p.bs) : -1;
+#pragma unroll
+              for (int i = 0; i < 3; ++i)
+                if (queued == i) blk[i][e] = pg;
+            }
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+              if (queued == i) head[i] = c.g;
+            ++queued;
+            ask_j += per;
+            if (ask_j >= c.tb) {
+              ask_j = -1;
+              ++ask_k;
+            }
+          }
+          if (!asked) scales(0);
+#pragma unroll
+          for (int e = 0; e < KS; ++e) {
+            a[0][e] = a[1][e];
+            b[0][e] = b[1][e];
+          }
+          asked = queued > 1;
+          if (asked) scales(1);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            head[i] = head[i + 1];
+#pragma unroll
+            for (int e = 0; e < KS; ++e) blk[i][e] = blk[i + 1][e];
+          }
+          --queued;
+        }
+        if (n >= A8_SCR && !ra_wait_copy(sc_empty(n), ((n / A8_SCR) & 1) ^ 1u, p.err, abort_flag)) { ok = false; break; }
+        float* sc = reinterpret_cast<float*>(smem + A8_OFF_SC) + (n & (A8_SCR - 1)) * 3 * NG;
+        if (TMA) {
+          if (my == nth) {
+            const float lb = log2f(b[0][0]), ib = 1.f / b[0][0];
+            const int gs = box >> 3, g0 = (lane & (nbox - 1)) * gs;
+            for (int g = g0; g < g0 + gs; ++g) {
+              sc[g] = a[0][0];
+              sc[NG + g] = lb;
+              sc[2 * NG + g] = ib;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < KS; ++e) {
+            sc[(e * 32 + lane) % NG] = a[0][e];
+            sc[NG + (e * 32 + lane) % NG] = log2f(b[0][e]);
+            sc[2 * NG + (e * 32 + lane) % NG] = 1.f / b[0][e];
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sc_full(n));
+      }
+    }
+    if (!ok) *abort_flag = 1;
+  } else if (warp > 12) {
+    // ---------- queries of the pieces after the first, four rows at a time ----------
+    bool ok = find(0);                             // a CTA without a run has no walk either
+    for (int k = 1; ok && find(k); ++k) {
+      const RaPiece& c = piece(k);
+      const int rows = c.toks * p.G;
+      uint4 x[2] = {}, y[2] = {};
+      int at = 4 * (warp - 13);
+      load_q(c, rows, at, x);
+      // the buffer is free once the S products of the piece before the last are done
+      if (k > 1 && !ra_wait_copy(q_empty(k), ((k - 2) >> 1) & 1, p.err, abort_flag)) { ok = false; break; }
+#pragma unroll 1
+      for (; at < rows; at += 4 * A8_QW) {
+        load_q(c, rows, at + 4 * A8_QW, y);        // the next ones are on their way
+        split_q(x, k, rows, at);
+        x[0] = y[0];
+        x[1] = y[1];
+      }
+      no_rows(k, rows, lane + 32 * (warp - 13), 32 * A8_QW);
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full(k));
+    }
+    if (!ok && piece(0).tb > 0) *abort_flag = 1;
   } else {
     // ---------------- softmax / correction / epilogue ----------------
     const int quarter = warp & 3, grp = (warp >> 2) - 1;         // grp: the parity of its steps
@@ -870,7 +897,10 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(n));
+      if (lane == 0) {
+        mbar_arrive(p_full(n));
+        mbar_arrive(sc_empty(n));
+      }
       return true;
     };
     // The same of a piece of few rows: this warp has 32 keys of the tile, a lane 16 of them.
@@ -906,7 +936,10 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       tmem_st_wait();                              // O's, if the maximum was raised
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(n));
+      if (lane == 0) {
+        mbar_arrive(p_full(n));
+        mbar_arrive(sc_empty(n));
+      }
       return true;
     };
     for (int k = 0; ok && more; ++k) {
@@ -926,7 +959,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       m = -INFINITY;
       l = 0.f;
       if (!a8_wait(k ? q_full(k) : q_first, q_phase(k), p.err, abort_flag)) { ok = false; break; }
-      rs = qscale[(k & 3) * RA_BQ + r];
+      rs = qscale[(k & (A8_QR - 1)) * RA_BQ + r];
       int j = (n0 & 1) ^ grp;                      // this group's first step
       if (few) {
         for (; ok && j < left; j += 2) ok = step_few(j >= whole, j);
@@ -938,7 +971,10 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
           const int n = n0 + j;
           ok = (!TMA || clear_tail(end - j * RA_BKV, n)) && a8_wait(s_full(n), phase(n), p.err, abort_flag);
           __syncwarp();
-          if (ok && lane == 0) mbar_arrive(p_full(n));
+          if (ok && lane == 0) {
+            mbar_arrive(p_full(n));
+            mbar_arrive(sc_empty(n));
+          }
         }
       }
       if (!ok) break;
