@@ -151,14 +151,16 @@ __device__ __forceinline__ void a8_tmem_st8(uint32_t taddr, const uint32_t (&r)[
                : "memory");
 }
 
-// mbar_wait_warp in few instructions (there are twenty of them in the kernel): the limit counts probes,
-// each of which may sleep for up to a microsecond or so.
+// mbar_wait_warp in few instructions (there are thirty of them in the kernel, whose hot loops have to fit
+// the SM's instruction cache). A probe may sleep for a microsecond or so; their number has a limit.
+static __device__ __noinline__ bool a8_give_up(uint32_t probes, uint32_t* err, volatile int* abort_flag) {
+  const bool late = probes > 1u << 21;
+  if (late) record_error(err, KL_DEVERR_TIMEOUT);
+  return __any_sync(0xffffffffu, late || *abort_flag);
+}
 __device__ __forceinline__ bool a8_wait(uint32_t bar, uint32_t parity, uint32_t* err, volatile int* abort_flag) {
-  for (uint32_t i = 0; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++i) {
-    if ((i & 63u) != 63u) continue;
-    if (i > 1u << 21) record_error(err, KL_DEVERR_TIMEOUT);
-    if (__any_sync(0xffffffffu, i > 1u << 21 || *abort_flag)) return false;
-  }
+  for (uint32_t i = 0; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++i)
+    if ((i & 63u) == 63u && a8_give_up(i, err, abort_flag)) return false;
   return true;
 }
 
@@ -392,7 +394,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
             if (j + per < w.tb) ask(w, j + per);
             else if (have) ask(piece(k + 1), piece(k + 1).ta);
           }
-          if (!ra_wait_copy(empty0 + 8 * s, ph, p.err, abort_flag)) { ok = false; break; }
+          if (!a8_wait(empty0 + 8 * s, ph, p.err, abort_flag)) { ok = false; break; }
           if (el) mbar_arrive_expect_tx(full0 + 8 * s, A8_TILE);
           __syncwarp();
           if (my == nth) ra_tma_3d(ring + s * A8_TILE + (lane & (nbox - 1)) * box * 128, tm, 0, w.g, row[0], full0 + 8 * s);
@@ -415,7 +417,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
         };
         lookup(w.ta);
         for (int j = w.ta; j < w.tb; ++j) {
-          if (!ra_wait_copy(empty0 + 8 * s, ph, p.err, abort_flag)) { ok = false; break; }
+          if (!a8_wait(empty0 + 8 * s, ph, p.err, abort_flag)) { ok = false; break; }
           gather(ring + s * A8_TILE, w.g, row);
           if (j > w.ta) announce(std::integral_constant<int, 1>());   // the tile before
           ++issued;
@@ -581,7 +583,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
           }
           --queued;
         }
-        if (n >= A8_SCR && !ra_wait_copy(sc_empty(n), ((n / A8_SCR) & 1) ^ 1u, p.err, abort_flag)) { ok = false; break; }
+        if (n >= A8_SCR && !a8_wait(sc_empty(n), ((n / A8_SCR) & 1) ^ 1u, p.err, abort_flag)) { ok = false; break; }
         float* sc = reinterpret_cast<float*>(smem + A8_OFF_SC) + (n & (A8_SCR - 1)) * 3 * NG;
         if (TMA) {
           if (my == nth) {
@@ -616,7 +618,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       int at = 4 * (warp - 13);
       load_q(c, rows, at, x);
       // the buffer is free once the S products of the piece before the last are done
-      if (k > 1 && !ra_wait_copy(q_empty(k), ((k - 2) >> 1) & 1, p.err, abort_flag)) { ok = false; break; }
+      if (k > 1 && !a8_wait(q_empty(k), ((k - 2) >> 1) & 1, p.err, abort_flag)) { ok = false; break; }
 #pragma unroll 1
       for (; at < rows; at += 4 * A8_QW) {
         load_q(c, rows, at + 4 * A8_QW, y);        // the next ones are on their way
@@ -861,37 +863,27 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       least = cut ? 1.17549435e-38f : 0.f;
       const int last = lim - j * RA_BKV;           // keys 0 .. last of the tile are kept
       float mx = -INFINITY;
-      uint32_t sv[32], sw[32];
+      uint32_t sv[32];
       tmem_ld_32x32b_x32(sadr, sv);
 #pragma unroll 1
-      for (int c = 0; c < RA_BKV; c += 64) {       // the next 32 columns are on their way
+      for (int c = 0; c < RA_BKV; c += 32) {
         tmem_ld_wait();
-        tmem_ld_32x32b_x32(sadr + c + 32, sw);
         if (cut) mask(sv, last - c);
         mx = fmaxf(mx, max_t(sv, sca + c / GRP * 4));
-        tmem_ld_wait();
-        tmem_ld_32x32b_x32(sadr + ((c + 64) & (RA_BKV - 1)), sv);     // the last time: the first ones again
-        if (cut) mask(sw, last - c - 32);
-        mx = fmaxf(mx, max_t(sw, sca + (c + 32) / GRP * 4));
+        tmem_ld_32x32b_x32(sadr + ((c + 32) & (RA_BKV - 1)), sv);     // at the end the first ones again
       }
       if (!agree(std::false_type(), j, mx)) return false;
       const float neg = m > -INFINITY ? A8_LIFT - m : 0.f;
       uint64_t r0 = 0, r1 = 0;
       uint32_t ph[8], pl[8];
 #pragma unroll 1
-      for (int c = 0; c < RA_BKV; c += 64) {       // P: 16 columns for 32 keys, high and low parts, where S has been read
+      for (int c = 0; c < RA_BKV; c += 32) {       // P: 16 columns for 32 keys, high and low parts, where S has been read
         tmem_ld_wait();
-        tmem_ld_32x32b_x32(sadr + c + 32, sw);
         if (cut) mask(sv, last - c);
         weigh(sv, sca + c / GRP * 4, neg, ph, pl, r0, r1);
+        if (c < RA_BKV - 32) tmem_ld_32x32b_x32(sadr + c + 32, sv);
         a8_tmem_st8(sadr + c / 2, ph);
         a8_tmem_st8(sadr + c / 2 + 8, pl);
-        tmem_ld_wait();
-        if (c == 0) tmem_ld_32x32b_x32(sadr + 64, sv);
-        if (cut) mask(sw, last - c - 32);
-        weigh(sw, sca + (c + 32) / GRP * 4, neg, ph, pl, r0, r1);
-        a8_tmem_st8(sadr + c / 2 + 16, ph);
-        a8_tmem_st8(sadr + c / 2 + 24, pl);
       }
       sum_up(r0, r1);
       tmem_st_wait();
