@@ -88,10 +88,11 @@ def test_forward_matches_oracle(kl, N, V, top, kind, dtype):
     r = _forward(kl, zd, td, top)
     assert kl.kl_device_status() == 0
     _check(r, w, V)
-    # rows of any stride and alignment, NaN between them; without entropy and norm: the same bits
+    # rows of any stride and alignment (which says in what groups a row is summed), NaN between them
     for ld in (V + 1, V + 5, (V + 15) // 16 * 16 + 16):
-        r2 = _forward(kl, zd, td, top, ld)
-        assert all(torch.equal(a, b) for a, b in zip(r, r2)), ld
+        _check(_forward(kl, zd, td, top, ld), w, V)
+    # again, and without entropy and norm: the same bits
+    assert all(torch.equal(a, b) for a, b in zip(r, _forward(kl, zd, td, top)))
     r3 = _forward(kl, zd, td, top, parts=False)
     assert torch.equal(r[0], r3[0]) and torch.equal(r[3], r3[3]) and torch.equal(r[4], r3[4]) and (r3[1] == 7.0).all() and (r3[2] == 7.0).all()
     assert kl.kl_device_status() == 0
