@@ -3,21 +3,24 @@
 //   log p_t = x_t - log s,  H = log s - u / s,
 //   dz_j = a (1[j = t] - p_j) - b p_j (log p_j + H).
 //
-// Forward: one read of the logits, bound by HBM (about six instructions a logit, below
-// half of the issue slots at that rate). A cluster of 1 to 16 CTAs takes a row; a thread
-// keeps its own m, s, u over 32-byte vectors of the row, rescaled when its maximum moves;
-// the threads' meet in the warp, the CTA and, through distributed shared memory, the
-// cluster, always in the same order.
+// Forward: one read of the logits, bound by HBM where there are many rows (2045 x 151936
+// bf16: 96 us, 95 % of the copy rate), by the trips behind the pass where there are few
+// (one row with 5 alternatives 6 us, 64 x 151936 fp32 with 20: 15, of which the pass 8;
+// 301 x 32001 with 8: 12). A cluster of up to 8 CTAs takes a row; a thread keeps its own
+// m, s, u over 32-byte vectors of the row, rescaled when its maximum moves; the threads'
+// meet in the warp, the CTA and, through distributed shared memory, the cluster's first
+// CTA, always in the same order. What runs once per row is kept short: fetching unrolled
+// code costs such a launch more than its loops do (wider unrolls there: 6 -> 9 us).
 //
 // Most likely classes. A class is a 64-bit key, the logit in the order of unsigned numbers
 // above the complement of the index: keys are distinct, equal logits go to the lower index.
 // A thread's maximum is known from the pass. The n best threads of a CTA hold the n best
 // classes of its share, and a class worth listing is at least as good as the n-th best
-// thread's maximum (found bit by bit): those threads' vectors (n of 256
-// threads') are read once more, from L2, and what passes, a few more than n as a rule, is
-// put in order by counting who is better. The first CTA orders the cluster's lists in the
-// same way. Should more pass than there is room for (rows of equal logits, rows whose best
-// classes fill few threads' vectors), the CTA looks for its n best one after the other.
+// thread's maximum (found bit by bit): those threads' vectors (n of 256 threads') are read
+// once more, from L2, and what passes, a few more than n as a rule, is put in order by
+// counting who is better. The first CTA orders the cluster's lists in the same way. Should
+// more pass than there is room for (rows of equal logits, rows whose best classes fill few
+// threads' vectors), the CTA looks for its n best one after the other.
 #include <cooperative_groups.h>
 #include <limits.h>
 #include <math.h>
@@ -205,19 +208,22 @@ __device__ __forceinline__ uint64_t lp_fma2(uint64_t a, uint64_t b, uint64_t c) 
 constexpr int LP_CLUSTER = 8;                  // CTAs per row at most
 struct LpShared {
   LpSum warp_sum[LP_WARPS];
-  LpSum sum;                                   // this CTA's
+  LpSum sum[LP_CLUSTER];                       // (first CTA) the CTAs'
   int chosens, count;                          // how many threads and classes may be listed
   uint64_t round[LP_WARPS];
   uint16_t chosen[LP_THREADS];                 // threads that hold classes to list
-  alignas(16) uint64_t top[KL_LOGPROBS_MAX_TOP];   // this CTA's classes in order, 0 behind the last
+  alignas(16) uint64_t top[LP_THREADS];        // (first CTA) the CTAs' classes in order, n each, 0 behind the last
   alignas(16) uint64_t keys[LP_ROOM];
 };
 static_assert(LP_CLUSTER * KL_LOGPROBS_MAX_TOP <= LP_THREADS && LP_THREADS <= LP_ROOM, "a thread per listed class");
 
-// TOP: alternatives are wanted.
+// TOP: alternatives are wanted. Four CTAs on an SM have the registers for the next vectors; without alternatives
+// five do (2045 x 151936 bf16: 96 us with five, 105 with four, 102 with the eight that come of no bound, whose
+// next vectors the compiler does not hold; 64 x 151936 fp32 with 20: 14.8 with four, 17.5 with five, 18.9 with eight).
+constexpr int LP_SLOTS = 4;
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(LP_THREADS) token_logprobs_kernel(const __grid_constant__ LpParams p) {
-  pdl_enter();
+__global__ void __launch_bounds__(LP_THREADS, TOP ? LP_SLOTS : LP_SLOTS + 1) token_logprobs_kernel(const __grid_constant__ LpParams p) {
+  pdl_wait();
   __shared__ LpShared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int CL = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
@@ -225,6 +231,8 @@ __global__ void __launch_bounds__(LP_THREADS) token_logprobs_kernel(const __grid
   const LpRow<T> row(static_cast<const T*>(p.z) + static_cast<int64_t>(n) * p.ldz, p.V);
   constexpr int NV = LpVec<T>::N;
 
+  if (TOP) sh.top[tid] = 0;
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");   // the first CTA runs and its list is empty
   const int step = CL * LP_THREADS, i0 = rank * LP_THREADS + tid;
   const bool ends = rank == CL - 1;            // this CTA has the row's ends too
 
@@ -281,16 +289,18 @@ __global__ void __launch_bounds__(LP_THREADS) token_logprobs_kernel(const __grid
     const float z = Elem<T>::to_f(row.z[row.end(tid)]);
     a = lp_merge(a, {fmaxf(z, -INFINITY), z == -INFINITY ? 0.f : z - z + 1.f, 0.f});
   }
+  pdl_launch_dependents();
   // threads of a warp, warps of the CTA, CTAs of the cluster
   const uint32_t mine = TOP ? lp_order(a.m) : 0;
   a = lp_warp_sum(a);
   if (lane == 0) sh.warp_sum[warp] = a;
-  if (TOP && tid < KL_LOGPROBS_MAX_TOP) sh.top[tid] = 0;
   if (tid == 0) sh.chosens = sh.count = 0;
   __syncthreads();
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+  LpShared& first = *cluster.map_shared_rank(&sh, 0);
   if (warp == LP_WARPS - 1) {
     const LpSum t = lp_warp_sum(lane < LP_WARPS ? sh.warp_sum[lane] : LpSum{-INFINITY, 0.f, 0.f});
-    if (lane == 0) sh.sum = t;
+    if (lane == 0) first.sum[rank] = t;
   }
   if (TOP) {
     // the greatest number that at least n threads' maxima reach, bit by bit; one that just n reach will do
@@ -339,7 +349,7 @@ __global__ void __launch_bounds__(LP_THREADS) token_logprobs_kernel(const __grid
       for (int i = tid; i < count; i += LP_THREADS) {
         const uint64_t key = sh.keys[i];
         const int r = lp_rank(sh.keys, (count + 3) & ~3, key);
-        if (r < p.top) sh.top[r] = key;
+        if (r < p.top) first.top[rank * p.top + r] = key;
       }
     } else {
       // one after the other, each the best behind the one before
@@ -365,14 +375,14 @@ __global__ void __launch_bounds__(LP_THREADS) token_logprobs_kernel(const __grid
         __syncthreads();
         for (int w = 0; w < LP_WARPS; ++w) b = sh.round[w] > b ? sh.round[w] : b;
         before = b;
-        if (tid == 0) sh.top[k] = b;
+        if (tid == 0) first.top[rank * p.top + k] = b;
         if (b == 0) break;
       }
     }
   }
   cluster.sync();
   if (rank == 0) {
-    const LpSum t = lp_warp_sum(lane < CL ? *cluster.map_shared_rank(&sh.sum, lane) : LpSum{-INFINITY, 0.f, 0.f});
+    const LpSum t = lp_warp_sum(lane < CL ? sh.sum[lane] : LpSum{-INFINITY, 0.f, 0.f});
     const bool empty = t.m == -INFINITY && t.s == 0.f;
     const float ls = empty ? -INFINITY : logf(t.s);
     if (tid == 0) {
@@ -389,14 +399,12 @@ __global__ void __launch_bounds__(LP_THREADS) token_logprobs_kernel(const __grid
     if (TOP) {
       // the CTAs' lists in one order, a thread per class
       const int all = CL * p.top;
-      const uint64_t key = tid < all ? cluster.map_shared_rank(sh.top, tid / p.top)[tid % p.top] : 0;
-      __syncthreads();                         // the counts above have been read
-      if (tid < ((all + 3) & ~3)) sh.keys[tid] = key;
+      const uint64_t key = sh.top[tid];
       const int have = __syncthreads_count(key != 0);
       int32_t* id = p.top_id + static_cast<int64_t>(n) * p.top;
       float* out = p.top_lp + static_cast<int64_t>(n) * p.top;
       if (key) {
-        const int r = lp_rank(sh.keys, (all + 3) & ~3, key);
+        const int r = lp_rank(sh.top, (all + 3) & ~3, key);
         if (r < p.top) {
           id[r] = lp_class(key);
           out[r] = lp_logit(key) - t.m - ls;
@@ -408,7 +416,6 @@ __global__ void __launch_bounds__(LP_THREADS) token_logprobs_kernel(const __grid
       }
     }
   }
-  cluster.sync();                              // peers' shared memory has been read
 }
 
 struct LpBwdParams {
@@ -527,11 +534,11 @@ kl_status token_logprobs(int N, int V, int dtype, const void* z, int64_t ldz, co
                          float* logprob, float* entropy, float* norm, int32_t* top_id, float* top_logprob,
                          cudaStream_t st) {
   const LpParams p = {z, ldz, tokens, logprob, entropy, norm, top_id, top_logprob, N, V, n_top, device_error_word()};
-  // CTAs per row: enough for six on each SM, each with a vector for every thread at least
+  // CTAs per row: as many as run at once, each with a vector for every thread at least (301 x 32001: 12 us with
+  // two, 17 with four, of which a part waits; 64 x 151936: 15 with eight, 21 where only three run on an SM)
   const int per = LP_THREADS * 32 / static_cast<int>(dtype_size(dtype));
   int cl = 1;
-  while (cl < LP_CLUSTER && static_cast<int64_t>(N) * cl < 6 * num_sms() && static_cast<int64_t>(cl) * per < V) cl *= 2;
-  if (static_cast<int64_t>(N) * cl > 2147483647LL) cl = 1;
+  while (cl < LP_CLUSTER && 2 * static_cast<int64_t>(N) * cl <= LP_SLOTS * num_sms() && static_cast<int64_t>(cl) * per < V) cl *= 2;
   ProfScope ps("token_logprobs", st, 0.0, static_cast<double>(N) * V * dtype_size(dtype));
   if (dtype == KL_F32)
     return n_top ? launch_cluster(token_logprobs_kernel<float, true>, N * cl, cl, st, p)
