@@ -19,8 +19,11 @@
 // thread's maximum (found bit by bit): those threads' vectors (n of 256 threads') are read
 // once more, from L2, and what passes, a few more than n as a rule, is put in order by
 // counting who is better. The first CTA orders the cluster's lists in the same way. Should
-// more pass than there is room for (rows of equal logits, rows whose best classes fill few
-// threads' vectors), the CTA looks for its n best one after the other.
+// more pass than there is room for, equal logits are the reason (a mask of the type's
+// lowest value, a row of one value): then the better classes are listed alone and of the
+// equal ones the first, found by reading the row from its beginning. If the better ones
+// alone are too many (they fill few threads' vectors), the CTA looks for its n best one
+// after the other.
 #include <cooperative_groups.h>
 #include <limits.h>
 #include <math.h>
@@ -215,7 +218,8 @@ struct LpShared {
   alignas(16) uint64_t top[LP_THREADS];        // (first CTA) the CTAs' classes in order, n each, 0 behind the last
   alignas(16) uint64_t keys[LP_ROOM];
 };
-static_assert(LP_CLUSTER * KL_LOGPROBS_MAX_TOP <= LP_THREADS && LP_THREADS <= LP_ROOM, "a thread per listed class");
+static_assert(LP_CLUSTER * KL_LOGPROBS_MAX_TOP <= LP_THREADS, "a thread per listed class");
+static_assert(LP_THREADS + KL_LOGPROBS_MAX_TOP <= LP_ROOM, "room for the first equal classes");
 
 // TOP: alternatives are wanted. Four CTAs on an SM have the registers for the next vectors; without alternatives
 // five do (2045 x 151936 bf16: 96 us with five, 105 with four, 102 with the eight that come of no bound, whose
@@ -311,38 +315,48 @@ __global__ void __launch_bounds__(LP_THREADS, TOP ? LP_SLOTS : LP_SLOTS + 1) tok
       if (reach >= p.top) lowest |= bit;
       if (reach == p.top) break;
     }
-    const uint64_t last = static_cast<uint64_t>(lowest) << 32;       // 0 if there are fewer: everything passes
-    auto list = [&](float z, int j) {
-      const uint64_t key = lp_key(z, j);
-      if (key == 0 || key < last) return;
-      const int at = atomicAdd(&sh.count, 1);
-      if (at < LP_ROOM) sh.keys[at] = key;
-    };
     if (mine != 0 && mine >= lowest) sh.chosen[atomicAdd(&sh.chosens, 1)] = static_cast<uint16_t>(tid);
-    __syncthreads();
-    // the chosen threads' vectors once more, in quarters, spread over all threads: a trip or two to L2 as a rule
-    constexpr int NQ = NV / 4;
-    const int chosen = sh.chosens, each = (row.vecs + step - 1) / step;
+    const uint32_t above = lowest + (sizeof(T) == 2 ? 1u << 16 : 1u);        // better ones are at least this
+    uint32_t least = lowest;                     // 0 if there are fewer than n: everything passes
+    int count;
 #pragma unroll 1
-    for (int k = tid; k < chosen * each * 4; k += LP_THREADS) {
-      const int vec = k >> 2, i = rank * LP_THREADS + sh.chosen[vec % chosen] + vec / chosen * step;
-      if (i >= row.vecs) continue;
-      const T* q = row.at(i) + (k & 3) * NQ;
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(q));
-      const int j = static_cast<int>(q - row.z);
-      if (sizeof(T) == 4) {
-        list(__uint_as_float(w.x), j);
-        list(__uint_as_float(w.y), j + 1);
-      } else {
-        list(__uint_as_float(w.x << 16), j);
-        list(__uint_as_float(w.x & 0xffff0000u), j + 1);
-        list(__uint_as_float(w.y << 16), j + 2);
-        list(__uint_as_float(w.y & 0xffff0000u), j + 3);
+    for (;;) {
+      const uint64_t last = static_cast<uint64_t>(least) << 32;
+      auto list = [&](float z, int j) {
+        const uint64_t key = lp_key(z, j);
+        if (key == 0 || key < last) return;
+        const int at = atomicAdd(&sh.count, 1);
+        if (at < LP_ROOM) sh.keys[at] = key;
+      };
+      __syncthreads();
+      // the chosen threads' vectors once more, in quarters, spread over all threads: a trip or two to L2 as a rule
+      constexpr int NQ = NV / 4;
+      const int chosen = sh.chosens, each = (row.vecs + step - 1) / step;
+#pragma unroll 1
+      for (int k = tid; k < chosen * each * 4; k += LP_THREADS) {
+        const int vec = k >> 2, i = rank * LP_THREADS + sh.chosen[vec % chosen] + vec / chosen * step;
+        if (i >= row.vecs) continue;
+        const T* q = row.at(i) + (k & 3) * NQ;
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(q));
+        const int j = static_cast<int>(q - row.z);
+        if (sizeof(T) == 4) {
+          list(__uint_as_float(w.x), j);
+          list(__uint_as_float(w.y), j + 1);
+        } else {
+          list(__uint_as_float(w.x << 16), j);
+          list(__uint_as_float(w.x & 0xffff0000u), j + 1);
+          list(__uint_as_float(w.y << 16), j + 2);
+          list(__uint_as_float(w.y & 0xffff0000u), j + 3);
+        }
       }
+      if (ends && tid < row.head + row.tail) list(Elem<T>::to_f(row.z[row.end(tid)]), row.end(tid));
+      __syncthreads();
+      count = sh.count;
+      if (count <= LP_ROOM || least == above) break;
+      least = above;                             // the better ones alone
+      __syncthreads();
+      if (tid == 0) sh.count = 0;
     }
-    if (ends && tid < row.head + row.tail) list(Elem<T>::to_f(row.z[row.end(tid)]), row.end(tid));
-    __syncthreads();
-    const int count = sh.count;
     if (count <= LP_ROOM) {
       if (tid < 4 && count + tid < ((count + 3) & ~3)) sh.keys[count + tid] = 0;
       __syncthreads();
@@ -350,6 +364,35 @@ __global__ void __launch_bounds__(LP_THREADS, TOP ? LP_SLOTS : LP_SLOTS + 1) tok
         const uint64_t key = sh.keys[i];
         const int r = lp_rank(sh.keys, (count + 3) & ~3, key);
         if (r < p.top) first.top[rank * p.top + r] = key;
+      }
+      if (least != lowest && count < p.top) {
+        // and the first of the equal ones, LP_THREADS classes at a time: the ones before the vectors, the CTA's
+        // vectors, the ones behind
+        __syncthreads();                         // the keys have been read
+        if (tid == 0) sh.count = 0;
+        __syncthreads();
+        const int blocks = (row.vecs + LP_THREADS - 1) / LP_THREADS;
+        int found = 0;
+#pragma unroll 1
+        for (int b = ends ? -1 : 0; b <= (ends ? blocks * NV : blocks * NV - 1) && found < p.top - count; ++b) {
+          int j = row.head + b * LP_THREADS + tid, behind = row.head + row.vecs * NV;
+          if (b < 0) j = tid, behind = row.head;
+          else if (b == blocks * NV) j = behind + tid, behind = p.V;
+          else if (b / NV % CL != rank) continue;
+          const uint64_t key = j < behind ? lp_key(Elem<T>::to_f(row.z[j]), j) : 0;
+          const uint32_t o = static_cast<uint32_t>(key >> 32);
+          if (key && o >= lowest && o < above) sh.keys[atomicAdd(&sh.count, 1)] = key;
+          __syncthreads();
+          found = sh.count;                      // below n and a thread each more
+          __syncthreads();
+        }
+        if (tid < 4 && found + tid < ((found + 3) & ~3)) sh.keys[found + tid] = 0;
+        __syncthreads();
+        for (int i = tid; i < found; i += LP_THREADS) {
+          const uint64_t key = sh.keys[i];
+          const int r = count + lp_rank(sh.keys, (found + 3) & ~3, key);
+          if (r < p.top) first.top[rank * p.top + r] = key;
+        }
       }
     } else {
       // one after the other, each the best behind the one before

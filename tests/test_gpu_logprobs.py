@@ -98,6 +98,25 @@ def test_forward_matches_oracle(kl, N, V, top, kind, dtype):
     assert kl.kl_device_status() == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N,V,top,stride", [(1, 151936, 32, None), (3, 151936, 5, None), (4, 30011, 20, 30013), (700, 9001, 32, 9002), (900, 5003, 1, None)])
+def test_alternatives_among_equal_logits(kl, N, V, top, stride, dtype):
+    """More equal logits than a list holds: the alternatives are the better ones and the first of the equal ones, wherever these lie."""
+    rng = np.random.default_rng(V + top)
+    z = np.full((N, V), -3.3e38)
+    for n in range(N):
+        z[n, rng.choice(V, [0, 3, top - 1, top, 40][n % 5], replace=False)] = rng.standard_normal([0, 3, top - 1, top, 40][n % 5])
+        if n % 3 == 1:                              # the equal ones only behind most of the row, but for the row's first class
+            z[n, 1:V * 7 // 8] = -np.inf
+        elif n % 3 == 2:                            # or the row's last
+            z[n, V // 16:V - 2] = -np.inf
+    z = torch.as_tensor(z, dtype=torch.float32).to(dtype)
+    tok = rng.integers(0, V, N)
+    w = O.token_logprobs(z.double().numpy(), tok, top)
+    _check(_forward(kl, z.cuda(), _i(tok), top, stride), w, V)
+    assert kl.kl_device_status() == 0
+
+
 @pytest.mark.parametrize("V,top", [(700, 5), (40000, 20)])
 def test_forward_nonfinite(kl, V, top):
     rng = np.random.default_rng(1)
