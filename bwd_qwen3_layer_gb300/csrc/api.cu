@@ -1061,11 +1061,15 @@ kl_status kl_token_logprobs_bwd(int32_t N, int32_t V, int32_t dtype, const void*
   if (d_logprob) KL_TRY(check_arrays({d_logprob}, "token_logprobs_bwd d_logprob"));
   if (d_entropy) KL_TRY(check_arrays({d_entropy, entropy}, "token_logprobs_bwd entropy"));
   {
-    // in place each element is read before it is written by the same thread; any other overlap is not
+    // in place each element is read before it is written by the same thread; any other overlap is not. Rows of
+    // one pitch may lie side by side.
     const uintptr_t z0 = reinterpret_cast<uintptr_t>(z), d0 = reinterpret_cast<uintptr_t>(dz);
-    const uintptr_t zn = (static_cast<uintptr_t>(N - 1) * ldz + V) * dtype_size(dtype);
-    const uintptr_t dn = (static_cast<uintptr_t>(N - 1) * lddz + V) * dtype_size(dz_dtype);
-    if (z0 < d0 + dn && d0 < z0 + zn && !(z0 == d0 && dtype == dz_dtype && ldz == lddz))
+    const uintptr_t zr = static_cast<uintptr_t>(V) * dtype_size(dtype), dr = static_cast<uintptr_t>(V) * dtype_size(dz_dtype);
+    const uintptr_t zp = static_cast<uintptr_t>(ldz) * dtype_size(dtype), dp = static_cast<uintptr_t>(lddz) * dtype_size(dz_dtype);
+    const bool meet = z0 < d0 + (N - 1) * dp + dr && d0 < z0 + (N - 1) * zp + zr;
+    const uintptr_t off = z0 <= d0 ? (d0 - z0) % zp : (zp - (z0 - d0) % zp) % zp;       // of dz's row in z's
+    const bool beside = N > 1 && zp == dp && off >= zr && zp - off >= dr;
+    if (meet && !beside && !(z0 == d0 && dtype == dz_dtype && ldz == lddz))
       return set_error(KL_ERR_INVALID_ARG, "token_logprobs_bwd: dz overlaps the logits");
   }
   return token_logprobs_bwd(N, V, dtype, z, ldz, tokens, norm, entropy, d_logprob, d_entropy, dz_dtype, dz, lddz,

@@ -287,3 +287,27 @@ def test_offsets_past_32_bits(kl):
     assert kl.kl_device_status() == 0
     want = O.token_logprobs_bwd(rows, [7, 7], _host(a[-2:]), _host(a[-2:]))
     assert np.linalg.norm(_host(z[-2:]) - want) <= 2.0 ** -8 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("first", ["z", "dz"])
+def test_backward_side_by_side(kl, first):
+    """The gradient in the other half of the logits' rows: no overlap. Four columns further in is one."""
+    rng = np.random.default_rng(8)
+    N, V = 5, 1004
+    buf = torch.full((N, 2 * V), 7.0, device="cuda")
+    z, dz = (buf[:, :V], buf[:, V:]) if first == "z" else (buf[:, V:], buf[:, :V])
+    z.copy_(_logits(rng, N, V, torch.float32, "plain"))
+    tok = _i(rng.integers(0, V, N))
+    lp, ent, norm, _, _ = _forward(kl, z, tok, 0)
+    a, b = torch.randn(N, device="cuda"), torch.randn(N, device="cuda")
+    call = lambda g, ld, at: kl.kl_token_logprobs_bwd(N, V, kl.KL_F32, z.data_ptr(), 2 * V, tok.data_ptr(), norm.data_ptr(), ent.data_ptr(), a.data_ptr(), b.data_ptr(),
+                                                      kl.KL_F32, at, ld, None)
+    apart = torch.empty(N, V, device="cuda")
+    before = z.clone()
+    call(apart, V, apart.data_ptr())
+    call(dz, 2 * V, dz.data_ptr())
+    assert kl.kl_device_status() == 0
+    assert torch.equal(dz, apart) and torch.equal(z, before)
+    with pytest.raises(kl.KLError, match="overlaps"):
+        call(dz, 2 * V, dz.data_ptr() + (-16 if first == "z" else 16))
+    assert torch.equal(z, before)
