@@ -32,7 +32,7 @@
 // under way. The running maximum passes from one group to the other through shared memory;
 // O has one scale. Warp 12 looks up the scales, warps 13..15 split the next piece's queries
 // (the first piece's: the softmax warps, idle at first): done by the copy warps in between,
-// both held the copies up (124 us instead of LATER for a decoding batch).
+// both held the copies up (124 us instead of 116 for 64 decoding requests).
 // Scores stay in tensor memory and are read twice, for the maximum and for the weights, 32
 // columns at a time, so that a step's code is a few small loops: unrolled over 128 keys (30
 // KB a step, 170 KB in all) the instruction fetch took longer than the work, 3800 cycles a
@@ -138,12 +138,6 @@ __device__ __forceinline__ float a8_max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
 }
-__device__ __forceinline__ float4 a8_ld4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
-  return v;
-}
-
 // 32 lanes x 8 consecutive 32-bit columns from registers into TMEM
 __device__ __forceinline__ void a8_tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),

@@ -630,9 +630,10 @@ KL_API kl_status kl_ragged_qkv_rope8(const kl_ragged_cfg* rc, int32_t Hq, int32_
                                      const void* gamma_k, float eps, float rope_base, int32_t rope_interleaved,
                                      const int32_t* cu_rows, const int32_t* pos, const int32_t* slots, void* q_out,
                                      void* k_pool, void* v_pool, float* k_scale, float* v_scale, void* stream);
-/* kl_ragged_attention over such pools; q and o stay bf16 (dtype). Any positive,
- * finite, normal scale is taken. A block that is read as zero (see there) has no
- * scale. A NaN in a query, in a key that a row sees or in the scale of a block
+/* kl_ragged_attention over such pools; q and o stay bf16 (dtype). Key scales may be
+ * any positive, finite, normal numbers; value scales those from 2^-64 to 2^120 (what
+ * kl_ragged_qkv_rope8 writes), of which no two that a row sees are more than 2^100
+ * apart. A block that is read as zero (see there) has no scale. A NaN in a query, in a key that a row sees or in the scale of a block
  * that it sees makes the row's o and lse NaN, as an infinity in a query does; a
  * NaN in a value reaches rows as there. */
 KL_API size_t kl_ragged_attention8_ws_bytes(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d);
