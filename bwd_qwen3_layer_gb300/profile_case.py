@@ -27,6 +27,11 @@ Cases (T = 2048 tokens, hidden 5120, 64/8 heads of 128, intermediate 25600):
   ragged_decode attention of a ragged step: the paged_attn case
   ragged_chunk  attention of 4096 new tokens over 12288 cached ones
   ragged_qkv    norm, rotation and cache write of 8192 new tokens
+  ragged8_decode, ragged8_chunk, ragged8_qkv  the same over a cache of 8-bit codes
+                (the chunk: 1024 new tokens over 8192)
+  logprobs      log probabilities, entropy and 20 alternatives of 64 rows of
+                151936 classes, fp32
+  logprobs_bwd  their gradient on 1024 rows, bf16
   draft_verify  64 requests of four drafts, 151936 classes, fp32
 """
 from __future__ import annotations
@@ -184,6 +189,54 @@ def main():
                 K.kl_ragged_attention(rc, HQ, HKV, D, bf, q.data_ptr(), kp.data_ptr(), vp.data_ptr(),
                                       table.data_ptr(), cu.data_ptr(), ctx_t.data_ptr(), o.data_ptr(), 0,
                                       ws.data_ptr(), nb)
+    elif a.case in ("ragged8_decode", "ragged8_chunk", "ragged8_qkv"):
+        B, ctx, n, bs = {"ragged8_decode": (64, 4096, 1, 16), "ragged8_chunk": (1, 8192, 1024, 16),
+                         "ragged8_qkv": (8, 0, 1024, 16)}[a.case]
+        max_blocks = (ctx + n + bs - 1) // bs
+        n_blocks, R = B * max_blocks, B * n
+        kp, vp = (_rand((n_blocks, bs, HKV * D), 100.0).to(torch.float8_e4m3fn) for _ in range(2))
+        ks, vs = (torch.full((n_blocks, HKV), 2.0 ** -6, device="cuda") for _ in range(2))
+        table = torch.randperm(n_blocks, device="cuda").to(torch.int32).reshape(B, max_blocks)
+        ctx_t = torch.full((B,), ctx, dtype=torch.int32, device="cuda")
+        cu = torch.arange(B + 1, dtype=torch.int32, device="cuda") * n
+        q, o = _rand((R, HQ * D)), torch.empty(R, HQ * D, dtype=torch.bfloat16, device="cuda")
+        rc = K.RaggedCfg(B, R, bs, max_blocks, n_blocks)
+        if a.case == "ragged8_qkv":
+            k, v, g = _rand((R, HKV * D)), _rand((R, HKV * D)), _rand((D,))
+            pos = (torch.arange(R, device="cuda") % n).to(torch.int32)
+            req = torch.arange(R, device="cuda") // n
+            slots = (table[req, (pos // bs).long()] * bs + pos % bs).to(torch.int32)
+
+            def run():
+                K.kl_ragged_qkv_rope8(rc, HQ, HKV, D, bf, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                      g.data_ptr(), 1e-6, 1e6, 0, cu.data_ptr(), pos.data_ptr(), slots.data_ptr(),
+                                      o.data_ptr(), kp.data_ptr(), vp.data_ptr(), ks.data_ptr(), vs.data_ptr())
+        else:
+            nb = K.kl_ragged_attention8_ws_bytes(rc, HQ, HKV, D)
+            ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+
+            def run():
+                K.kl_ragged_attention8(rc, HQ, HKV, D, bf, q.data_ptr(), kp.data_ptr(), vp.data_ptr(), ks.data_ptr(),
+                                       vs.data_ptr(), table.data_ptr(), cu.data_ptr(), ctx_t.data_ptr(),
+                                       o.data_ptr(), 0, ws.data_ptr(), nb)
+    elif a.case in ("logprobs", "logprobs_bwd"):
+        N, V, top = (64, 151936, 20) if a.case == "logprobs" else (1024, 151936, 0)
+        dt = K.KL_F32 if a.case == "logprobs" else bf
+        z = _rand((N, V), 2.5, torch.float32 if a.case == "logprobs" else torch.bfloat16)
+        tok = torch.randint(0, V, (N,), device="cuda", dtype=torch.int32)
+        lp, ent, norm, da, de = (torch.randn(N, 2 if i == 2 else 1, device="cuda") for i in range(5))
+        ids, tlp = torch.empty(N, 20, dtype=torch.int32, device="cuda"), torch.empty(N, 20, device="cuda")
+        dz = torch.empty_like(z)
+
+        def run():
+            if a.case == "logprobs" or not run.forward:
+                K.kl_token_logprobs(N, V, dt, z.data_ptr(), V, tok.data_ptr(), top, lp.data_ptr(), ent.data_ptr(),
+                                    norm.data_ptr(), ids.data_ptr(), tlp.data_ptr())
+                run.forward = True
+            if a.case == "logprobs_bwd":
+                K.kl_token_logprobs_bwd(N, V, dt, z.data_ptr(), V, tok.data_ptr(), norm.data_ptr(), ent.data_ptr(),
+                                        da.data_ptr(), de.data_ptr(), dt, dz.data_ptr(), V)
+        run.forward = False
     elif a.case == "draft_verify":
         B, drafts, V = 64, 4, 151936
         R = B * (drafts + 1)
