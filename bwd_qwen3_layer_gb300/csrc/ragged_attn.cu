@@ -75,7 +75,11 @@ struct RaParams {
   const int32_t* table;
   const int32_t* cu;
   const int32_t* ctx;
-  RaJoin j;              // o, lse and the pieces of cut items
+  __nv_bfloat16* o;
+  float* lse;            // [T, Hq] or null
+  float* part_o;         // the pieces of cut items, as the joining kernel reads them
+  float* part_ml;
+  RaCut* cuts;
   int B, T, Hq, Hkv, G, TQ;
   int bs, max_blocks, n_blocks;
   int box_log;           // log2 of the rows per TMA box (8 .. 128)
@@ -402,7 +406,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
         cut.g = f.g;
         cut.first_slot = f.off - P >= 0 ? 0 : 1;
       }
-      p.j.cuts[cta] = cut;
+      p.cuts[cta] = cut;
     }
     __syncwarp();
     bool ok = true;
@@ -559,7 +563,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
           if (mine && whole) {
             // whole 32-byte sectors: rows lie apart, and an SM writes ~0.7 sectors a
             // cycle whether they are full or not (16-byte stores took twice as long)
-            __nv_bfloat16* orow_p = p.j.o + orow * RA_D + h * 32;
+            __nv_bfloat16* orow_p = p.o + orow * RA_D + h * 32;
 #pragma unroll
             for (int e = 0; e < 32; e += 16) {
               uint32_t x[8];
@@ -569,7 +573,7 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
               ra_st32(orow_p + e, x);
             }
           } else if (mine) {
-            float* po = p.j.part_o + (pslot * RA_D + h * 32) * RA_BQ + r * 4;      // lanes side by side
+            float* po = p.part_o + (pslot * RA_D + h * 32) * RA_BQ + r * 4;      // lanes side by side
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
               *reinterpret_cast<uint4*>(po + e * RA_BQ) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
@@ -578,9 +582,9 @@ __global__ void __launch_bounds__(RA_THREADS, 1) ragged_attn_kernel(const __grid
         }
         if (mine) {
           if (whole) {
-            if (p.j.lse) p.j.lse[orow] = (m + log2f(l)) * RA_LN2;
+            if (p.lse) p.lse[orow] = (m + log2f(l)) * RA_LN2;
           } else {
-            *reinterpret_cast<float2*>(p.j.part_ml + (pslot * RA_BQ + r) * 2) = make_float2(m, l);
+            *reinterpret_cast<float2*>(p.part_ml + (pslot * RA_BQ + r) * 2) = make_float2(m, l);
           }
         }
       }
@@ -693,7 +697,7 @@ kl_status ragged_attention(const kl_ragged_cfg& rc, int Hq, int Hkv, const void*
     return set_error(KL_ERR_NO_MEMORY, "ragged attention: workspace too small or not 256-byte aligned");
   RaParams p;
   memset(&p, 0, sizeof(p));
-  p.G = p.j.G = Hq / Hkv;
+  p.G = Hq / Hkv;
   p.TQ = RA_BQ / p.G;
   const bool tma = rc.block_size % 8 == 0;
   p.box_log = 7;
@@ -719,15 +723,15 @@ kl_status ragged_attention(const kl_ragged_cfg& rc, int Hq, int Hkv, const void*
   p.table = table;
   p.cu = cu;
   p.ctx = ctx;
-  p.j.o = static_cast<__nv_bfloat16*>(o);
-  p.j.lse = lse;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
   uint8_t* wb = static_cast<uint8_t*>(ws);
-  p.j.part_o = reinterpret_cast<float*>(wb + lay.o);
-  p.j.part_ml = reinterpret_cast<float*>(wb + lay.ml);
-  p.j.cuts = reinterpret_cast<RaCut*>(wb + lay.cuts);
+  p.part_o = reinterpret_cast<float*>(wb + lay.o);
+  p.part_ml = reinterpret_cast<float*>(wb + lay.ml);
+  p.cuts = reinterpret_cast<RaCut*>(wb + lay.cuts);
   p.B = rc.B;
   p.T = rc.T;
-  p.Hq = p.j.Hq = Hq;
+  p.Hq = Hq;
   p.Hkv = Hkv;
   p.bs = rc.block_size;
   p.max_blocks = rc.max_blocks;
@@ -753,7 +757,7 @@ kl_status ragged_attention(const kl_ragged_cfg& rc, int Hq, int Hkv, const void*
       launch_pdl(ragged_attn_kernel<false>, ctas, RA_THREADS, RA_SMEM, st, p);
   }
   KL_CUDA(cudaGetLastError());
-  return ragged_join(p.j, ctas, st);
+  return ragged_join({p.part_o, p.part_ml, p.cuts, p.o, p.lse, Hq, p.G}, ctas, st);
 }
 
 kl_status ragged_join(const RaJoin& j, int ctas, cudaStream_t st) {

@@ -281,7 +281,7 @@ template <int WARPS>
 __device__ __forceinline__ long long ra_find_run(const RaLens& p, int cta, int ctas, long long* wsum, RaFound* found,
                                                  RaPiece* first, RaWalk* walk) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = (p.B + 32 * WARPS - 1) / 32 * WARPS;
+  const int per = (p.B + 32 * WARPS - 1) / (32 * WARPS);
   const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
   long long mine = 0, units = 0;
   RaReq q = {0, 0, 0};
