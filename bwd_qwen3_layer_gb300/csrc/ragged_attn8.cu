@@ -47,6 +47,11 @@
 // the tile's keys (a lane 16), adds the parts. Weights likewise, in shared memory, from
 // where the P V product reads them: lanes r and 16 + r of O are added at the end.
 //
+// Measured (64 query heads, 8 kv heads, pages of 16): 64 requests of ~4096 keys 105 us, 0.76 of HBM's copy rate
+// (128-byte pieces 1 KB apart); one of 32768 22 us; 4095 rows over 12288 keys 1.9 to 2.0 ms, half of the
+// bf16 tensor peak that the doubled products come to: a step takes ~2300 cycles, of which the products need 1024, the
+// softmax warps' ~1150 instructions for each of two warps a scheduler the rest.
+//
 // Barriers, stages and buffers as in the bf16
 // kernel. A key tile of 16 KB is 16 groups of 8 keys x 128 bytes (one swizzle atom each);
 // with block_size a multiple of 8 it is 128 / box TMA boxes, box = gcd(block_size, 128),
@@ -78,7 +83,7 @@ constexpr uint32_t A8_OFF_P = A8_OFF_Q + 4 * A8_TILE;       // weights of few ro
 constexpr uint32_t A8_OFF_K = A8_OFF_P + A8_SB * A8_FEW_TILE;
 constexpr uint32_t A8_OFF_V = A8_OFF_K + A8_NST * A8_TILE;
 constexpr uint32_t A8_OFF_BAR = A8_OFF_V + A8_NST * A8_TILE;
-constexpr uint32_t A8_OFF_QS = A8_OFF_BAR + 3072;           // the rows' factors, of eight pieces
+constexpr uint32_t A8_OFF_QS = A8_OFF_BAR + 3 * 1024;       // the rows' factors, of eight pieces
 constexpr uint32_t A8_OFF_MX = A8_OFF_QS + A8_QR * RA_BQ * 4;   // the rows' maxima, of four steps
 constexpr uint32_t A8_OFF_L = A8_OFF_MX + 4 * RA_BQ * 4;    // the groups' sums, of two pieces
 constexpr uint32_t A8_OFF_SC = A8_OFF_L + 4 * RA_BQ * 4;    // the ring of scales
