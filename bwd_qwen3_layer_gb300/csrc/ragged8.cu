@@ -490,8 +490,7 @@ kl_status ragged_qkv_rope8(const kl_ragged_cfg& rc, int Hq, int Hkv, const void*
   while (parts < 2 * Hkv && busy * parts < 4 * num_sms()) parts *= 2;
   p.kv_parts = min(parts, 2 * Hkv);
   p.q_rows = rc.T < 2 * num_sms() ? 1 : max(1, min(R8_MAX * R8_UNITS / Hq, R8_QROWS));
-  const int64_t kv = static_cast<int64_t>(tiles) * p.kv_parts, grid = kv + (rc.T - 1) / p.q_rows + 1;
-  if (grid > 2147483647LL) return set_error(KL_ERR_UNSUPPORTED, "ragged_qkv_rope8: %d rows of %d kv heads", rc.T, Hkv);
+  const int64_t kv = static_cast<int64_t>(tiles) * p.kv_parts, grid = kv + (rc.T - 1) / p.q_rows + 1;    // below 2^31 for 2^24 rows
   p.kv_ctas = static_cast<int>(kv);
   ProfScope ps("ragged_qkv_rope8", st, 0.0, static_cast<double>(rc.T) * (4.0 * Hq + 6.0 * Hkv) * RQ_D);
   launch_pdl(ragged_qkv8_kernel, static_cast<int>(grid), R8_THREADS, 0, st, p);

@@ -123,7 +123,7 @@ def test_append_refusals(lib):
 
     assert call(d=64) == K.KL_ERR_UNSUPPORTED
     assert call(dtype=K.KL_F32) == K.KL_ERR_UNSUPPORTED
-    assert call(rc=_rc(T=1 << 24), Hq=256, Hkv=256) == K.KL_ERR_UNSUPPORTED       # more CTAs than a grid takes
+    assert call(rc=_rc(T=(1 << 24) + 1)) == K.KL_ERR_UNSUPPORTED
     for bad in (dict(Hq=6, Hkv=4), dict(rc=_rc(T=0)), dict(base=0.5), dict(eps=-1.0), dict(inter=2), dict(gq=0x1000)):
         assert call(**bad) == K.KL_ERR_INVALID_ARG, bad
     for n in ("q", "k", "v", "out", "kp", "vp"):
