@@ -139,6 +139,25 @@ def test_attention_of_values_of_any_size(kl):
     assert (np.abs(_host(lse) - want_lse) <= ltol).all()
 
 
+@pytest.mark.parametrize("k", [-60, 20, 100])
+def test_attention_scales_with_its_values(kl, k):
+    """All value scales times 2^k: the result times 2^k. The scores' logarithms are formed around k, off by 2^-17 there at most: 2^-17 of
+    a weight, beside the 2^-8 of its parts and the result's rounding of the one call and of the other; lse is a number of that size."""
+    Hq, Hkv, bs, reqs = 8, 2, 16, [(5, 300), (1, 1700), (40, 30)]
+    rng, n, ctx, table, maxb, nb, (kc, ks, vc, vs), cu, T = _step8(9, reqs, Hkv, bs)
+    vs = np.nan_to_num(vs, nan=1.0)
+    vs[vs * 2.0 ** k < 2.0 ** -64] = 2.0 ** (-64 - min(k, 0))
+    q = _dev(_bf(rng, T, Hq, D))
+    rc = kl.RaggedCfg(len(reqs), T, bs, maxb, nb)
+    tail = [_i(table), _i(cu), _i(ctx)]
+    o, lse = _attend(kl, rc, Hq, Hkv, q, _codes(kc), _f(ks), _codes(vc), _f(vs), *tail)
+    o2, lse2 = _attend(kl, rc, Hq, Hkv, q, _codes(kc), _f(ks), _codes(vc), _f(vs * 2.0 ** k), *tail)
+    assert kl.kl_device_status() == 0
+    A = O.ragged_attention(_host(q), O.dequantised(kc, ks), O.dequantised(vc, vs), table, cu, ctx)[2]
+    assert (np.abs(_host(o2) * 2.0 ** -k - _host(o)) <= (2.0 ** -7 + 2.0 ** -15) * A + 2.0 ** -7 * np.abs(_host(o))).all()
+    assert np.abs(_host(lse2) - _host(lse)).max() <= 1e-4
+
+
 @pytest.mark.parametrize("bs", [16, 5])
 def test_attention_reports_pages_outside_the_pool(kl, bs):
     """A bad table entry reads as zero keys and values and is reported; other requests are not touched by it."""
@@ -409,6 +428,74 @@ def test_append_matches_oracle(kl, Hq, Hkv, bs, reqs, norm, inter, inplace):
         assert kl.kl_device_status() == 0
         for t, w in zip((kpd, ksd, vpd, vsd), after):
             np.testing.assert_array_equal(_host(t), w)
+
+
+def _append(kl, rc, Hq, Hkv, q, k, v, cu, pos, slots, pools, out=None, stream=None, gains=(0, 0), inter=0):
+    out = torch.full_like(q, 7.0) if out is None else out
+    kl.kl_ragged_qkv_rope8(rc, Hq, Hkv, D, kl.KL_BF16, q.data_ptr(), k.data_ptr(), v.data_ptr(), *gains, 1e-6, 1e6, inter, cu.data_ptr(), pos.data_ptr(), slots.data_ptr(),
+                           out.data_ptr(), *[t.data_ptr() for t in pools], stream)
+    return out
+
+
+@pytest.mark.parametrize("Hq,Hkv,bs,n_max,B", [(1, 1, 16, 40, 60), (8, 2, 17, 40, 60), (6, 3, 16, 3, 200), (4, 1, 18, 50, 40), (2, 2, 32, 90, 30), (2, 1, 16, 9800, 1), (16, 8, 16, 1, 700)])
+def test_append_of_many_runs(kl, Hq, Hkv, bs, n_max, B):
+    """Runs of all lengths and beginnings, within a CTA's rows and across their ends; requests appended together or one after the other
+    leave the same bits."""
+    rng = np.random.default_rng(B + bs)
+    reqs = [(int(n), int(c)) for n, c in zip(rng.integers(min(n_max, 9800 if B == 1 else 1), n_max + 1, B), rng.integers(0, 3 * bs, B))]
+    rng, T, pos, slots, nb, (kc, ks, vc, vs), (qp, kp, v), cu = _append_case(B, reqs, Hq, Hkv, bs)
+    rc = kl.RaggedCfg(B, T + 2, bs, 4, nb)
+    x = [_dev(qp), _dev(kp), _dev(v)]
+    pools = [_codes(kc), _codes(vc), _f(ks), _f(vs)]
+    alone = [t.clone() for t in pools]
+    pd, sd = _i(np.concatenate([pos, [3, 4]])), _i(np.concatenate([slots, [0, 1]]))
+    out = _append(kl, rc, Hq, Hkv, *x, _i(cu), pd, sd, pools)
+    assert kl.kl_device_status() == 0
+    yq, yk = O.rope_at(qp[:T], pos, 1e6, False), O.rope_at(kp[:T], pos, 1e6, False)
+    mq, mk = (np.broadcast_to(2 * np.abs(t[:T]).max(-1, keepdims=True), t[:T].shape) for t in (qp, kp))
+    got_q = _host(out)
+    assert (np.abs(got_q[:T] - yq) <= 2.0 ** -8 * np.abs(yq) * (1 + 2.0 ** -7) + 2.0 ** -16 * mq).all() and (got_q[T:] == 7.0).all()
+    after = [_host(t) for t in pools]
+    _check_append(yk, mk, slots, (kc, ks), after[0], after[2])
+    _check_append(v[:T], np.zeros_like(yk), slots, (vc, vs), after[1], after[3], exact=True)
+    apart = torch.full_like(out, 7.0)
+    for b in range(min(B, 40)):
+        r = slice(int(cu[b]), int(cu[b + 1]))
+        rows = int(cu[b + 1] - cu[b])
+        _append(kl, kl.RaggedCfg(1, rows, bs, 4, nb), Hq, Hkv, *[t[r].contiguous() for t in x], _i([0, rows]), _i(pos[r]), _i(slots[r]), alone, apart[r])
+    assert kl.kl_device_status() == 0
+    done = np.unique(slots[:int(cu[min(B, 40)])] // bs)
+    assert torch.equal(apart[:int(cu[min(B, 40)])], out[:int(cu[min(B, 40)])])
+    for a, b in zip(alone, pools):
+        assert torch.equal(a[done].view(torch.uint8), b[done].view(torch.uint8))
+
+
+def test_append_in_two_graphs_and_on_two_streams(kl):
+    """Two captured appends, each with pools of its own, replayed at the same time on two streams: the bits of eager calls."""
+    sets = []
+    for seed, bs, reqs in ((71, 16, [(40, 5), (1, 77), (300, 30)]), (72, 24, [(1, 24 * i + 7) for i in range(50)])):
+        rng, T, pos, slots, nb, (kc, ks, vc, vs), (qp, kp, v), cu = _append_case(seed, reqs, 16, 4, bs)
+        rc = kl.RaggedCfg(len(reqs), T + 2, bs, 4, nb)
+        args = [_dev(qp), _dev(kp), _dev(v), _i(cu), _i(np.concatenate([pos, [0, 0]])), _i(np.concatenate([slots, [-1, -1]]))]
+        start = [_codes(kc), _codes(vc), _f(ks), _f(vs)]
+        eager, pools = [t.clone() for t in start], [t.clone() for t in start]
+        want = _append(kl, rc, 16, 4, *args, eager)
+        torch.cuda.synchronize()
+        st, out = torch.cuda.Stream(), torch.full_like(want, 7.0)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            for p_, s_ in zip(pools, start):
+                p_.view(torch.uint8).copy_(s_.view(torch.uint8))
+            _append(kl, rc, 16, 4, *args, pools, out, stream=st)
+        sets.append((graph, st, pools, eager, out, want, args, start))      # the graph reads the inputs
+    for _ in range(10):
+        for graph, st, *_ in sets:
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    assert kl.kl_device_status() == 0
+    for graph, st, pools, eager, out, want, *_ in sets:
+        assert torch.equal(out, want) and all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(pools, eager))
 
 
 def test_append_nonfinite_and_zeros(kl):
