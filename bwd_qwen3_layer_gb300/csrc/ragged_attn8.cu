@@ -723,9 +723,8 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       hi = a8_e4m3x4_h(h0 & KEEP, h1 & KEEP);
       lo = a8_e4m3x4_h(a8_sub_h(h0, h0 & KEEP), a8_sub_h(h1, h1 & KEEP));
     };
-    // What takes S to the score, S * factor(a); with keys cut off never zero, so that their -inf stays.
-    float least = 0.f;
-    auto factor = [&](float a) { return a8_max_nan(rs * a, least); };
+    // What takes S to the score, S * factor(a); never zero, so that the -inf of keys cut off stays.
+    auto factor = [&](float a) { return a8_max_nan(rs * a, 1.17549435e-38f); };
     // keys behind `last` of these do not count
     auto mask = [&](auto& sv, int last) {
       constexpr int N = sizeof(sv) / 4;
@@ -859,15 +858,24 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       tc_fence_after();
       const uint32_t sadr = tmem + lane_off + n % A8_SB * 128;
       const uint32_t sca = sc0 + (n & (A8_SCR - 1)) * 3 * NG * 4;
-      least = cut ? 1.17549435e-38f : 0.f;
-      const int last = lim - j * RA_BKV;           // keys 0 .. last of the tile are kept
+      if (cut) {
+        // keys behind the row's last one: -inf, in place (masks in the loops below were in the way of their code)
+#pragma unroll 1
+        for (int c = 0; c < RA_BKV; c += 16) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(sadr + c, v);
+          tmem_ld_wait();
+          mask(v, lim - j * RA_BKV - c);
+          tmem_st_32x32b_x16(sadr + c, v);
+        }
+        tmem_st_wait();
+      }
       float mx = -INFINITY;
       uint32_t sv[32];
       tmem_ld_32x32b_x32(sadr, sv);
 #pragma unroll 1
       for (int c = 0; c < RA_BKV; c += 32) {
         tmem_ld_wait();
-        if (cut) mask(sv, last - c);
         mx = fmaxf(mx, max_t(sv, sca + c / GRP * 4));
         tmem_ld_32x32b_x32(sadr + ((c + 32) & (RA_BKV - 1)), sv);     // at the end the first ones again
       }
@@ -878,7 +886,6 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
 #pragma unroll 1
       for (int c = 0; c < RA_BKV; c += 32) {       // P: 16 columns for 32 keys, high and low parts, where S has been read
         tmem_ld_wait();
-        if (cut) mask(sv, last - c);
         weigh(sv, sca + c / GRP * 4, neg, ph, pl, r0, r1);
         if (c < RA_BKV - 32) tmem_ld_32x32b_x32(sadr + c + 32, sv);
         a8_tmem_st8(sadr + c / 2, ph);
@@ -902,7 +909,6 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       tc_fence_after();
       const int first = quarter * 32 + (lane & 16);      // this lane's first key of the tile
       const uint32_t sca = sc0 + ((n & (A8_SCR - 1)) * 3 * NG + first / GRP) * 4;
-      least = cut ? 1.17549435e-38f : 0.f;
       uint32_t sw[32], sv[16];
       tmem_ld_32x32b_x32(tmem + lane_off + n % A8_SB * 128 + quarter * 32, sw);
       tmem_ld_wait();
