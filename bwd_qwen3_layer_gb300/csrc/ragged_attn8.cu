@@ -36,7 +36,7 @@
 // Scores stay in tensor memory and are read twice, for the maximum and for the weights, 32
 // columns at a time, so that a step's code is a few small loops: unrolled over 128 keys (30
 // KB a step, 170 KB in all) the instruction fetch took longer than the work, 3800 cycles a
-// step. P takes the columns of S that have been read; three such buffers keep the score
+// step. Keys cut off are marked in tensor memory beforehand for the same reason (1900 -> 1790 us on a chunk). P takes the columns of S that have been read; three such buffers keep the score
 // products two steps ahead.
 //
 // Few rows. A piece of at most 16 rows (decoding) would leave seven of eight TMEM lanes
@@ -47,9 +47,9 @@
 // the tile's keys (a lane 16), adds the parts. Weights likewise, in shared memory, from
 // where the P V product reads them: lanes r and 16 + r of O are added at the end.
 //
-// Measured (64 query heads, 8 kv heads, pages of 16): 64 requests of ~4096 keys 105 us, 0.76 of HBM's copy rate
-// (128-byte pieces 1 KB apart); one of 32768 22 us; 4095 rows over 12288 keys 1.9 to 2.0 ms, half of the
-// bf16 tensor peak that the doubled products come to: a step takes ~2300 cycles, of which the products need 1024, the
+// Measured (64 query heads, 8 kv heads, pages of 16): 64 requests of ~4096 keys 99-105 us, 0.76-0.80 of HBM's copy rate
+// (128-byte pieces 1 KB apart); one of 32768 22 us; 4095 rows over 12288 keys 1.77 to 1.87 ms, 0.55 to 0.58
+// of the bf16 tensor peak that the doubled products come to: a step takes ~2200 cycles, of which the products need 1024, the
 // softmax warps' ~1150 instructions for each of two warps a scheduler the rest.
 //
 // Barriers, stages and buffers as in the bf16
