@@ -179,6 +179,10 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
   const uint32_t sb = smem_u32(smem);
   const uint32_t bar = sb + A8_OFF_BAR;
   constexpr int A8_SCR = a8_scr(TMA);
+  // A wait by parity is right only if the phase before the one it means has ended. What says so: for the stages' and
+  // rings' producers and consumers (k_, v_, sc_, q_, p_full), that they wait for every phase in turn; for s_full(n) in the softmax,
+  // that S of step n - 2 was waited for; for v_full(n) and p_done(n - 1) there, that S of step n was, which was issued after the
+  // product of step n - 3; for told(t), that t - 1 was heard before; for sums and o_free, that every piece has one of each.
   // piece k's queries: eight, since with pieces of one tile the score products run three pieces ahead of
   // the softmax and the queries two more, and no waiter may be two phases behind
   auto q_full = [&](int k) { return bar + 576 + 8 * (k & (A8_QR - 1)); };
@@ -640,7 +644,11 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
     float* maxima = reinterpret_cast<float*>(smem + A8_OFF_MX);   // [step % 4][row]
     float* lsum = reinterpret_cast<float*>(smem + A8_OFF_L);      // [piece % 2][group][row]
     // The tile that holds the last key the query tile sees: its value rows behind it become zero
-    // (each of the group's four warps its 32).
+    // (each of the group's four warps its 32). Called once S of the step has been waited for, which was issued after the
+    // product of the third step before: that one's values, and those of the step before it, whose stage this is, had
+    // landed and been read, so that the wait by parity is for this step's. (Asked for before S, it passes while
+    // the values of four steps before are still on their way, and zeroes those.) Nothing waits in a circle: the copy
+    // needs the product of four steps before, no later one.
     auto clear_tail = [&](int end, int n) -> bool {
       if (end >= RA_BKV) return true;
       const int vs = n % A8_NST;
@@ -853,8 +861,8 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
     // Step j of the piece by a warp with rows. cut: some row of the tile ends inside its keys.
     auto step = [&](bool cut, int j) -> bool {
       const int n = n0 + j;
-      if (cut && TMA && !clear_tail(end - j * RA_BKV, n)) return false;
       if (!a8_wait(s_full(n), phase(n), p.err, abort_flag) || !a8_wait(sc_full(n), (n / A8_SCR) & 1, p.err, abort_flag)) return false;
+      if (cut && TMA && !clear_tail(end - j * RA_BKV, n)) return false;
       tc_fence_after();
       const uint32_t sadr = tmem + lane_off + n % A8_SB * 128;
       const uint32_t sca = sc0 + (n & (A8_SCR - 1)) * 3 * NG * 4;
@@ -904,8 +912,8 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
     // The same of a piece of few rows: this warp has 32 keys of the tile, a lane 16 of them.
     auto step_few = [&](bool cut, int j) -> bool {
       const int n = n0 + j;
-      if (cut && TMA && !clear_tail(end - j * RA_BKV, n)) return false;
       if (!a8_wait(s_full(n), phase(n), p.err, abort_flag) || !a8_wait(sc_full(n), (n / A8_SCR) & 1, p.err, abort_flag)) return false;
+      if (cut && TMA && !clear_tail(end - j * RA_BKV, n)) return false;
       tc_fence_after();
       const int first = quarter * 32 + (lane & 16);      // this lane's first key of the tile
       const uint32_t sca = sc0 + ((n & (A8_SCR - 1)) * 3 * NG + first / GRP) * 4;
@@ -966,7 +974,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
         // no real row: P stays whatever it is, its O rows are never read
         for (; ok && j < left; j += 2) {
           const int n = n0 + j;
-          ok = (!TMA || clear_tail(end - j * RA_BKV, n)) && a8_wait(s_full(n), phase(n), p.err, abort_flag);
+          ok = a8_wait(s_full(n), phase(n), p.err, abort_flag) && (!TMA || clear_tail(end - j * RA_BKV, n));
           __syncwarp();
           if (ok && lane == 0) {
             mbar_arrive(p_full(n));

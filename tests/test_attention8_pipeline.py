@@ -1,0 +1,144 @@
+"""The waits of the 8-bit attention's pipeline (CPU only), by a search over every order of its warps' steps.
+
+A wait by parity passes when the phase before the one it means has not completed yet either, so each wait needs an earlier one
+that says it has. The model is one item of several key tiles: the copies of keys and values (four stages each, landing as late
+as they like), the warps that issue the score products and the P V products (three buffers of scores and weights), and the two
+groups of softmax warps that take the steps in turn. At each wait that passes the phase must be the one that was meant."""
+import os
+import re
+
+import pytest
+
+SOURCE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "bwd_qwen3_layer_gb300", "csrc", "ragged_attn8.cu")
+STAGES, BUFFERS, TOLD, QUARTERS = 4, 3, 4, 2       # (two of the four quarters of the rows: all pairs of quarters look alike)
+
+
+def _of(done, slot, ring):
+    """Phases of a ring's barrier `slot` that are complete once steps 0 .. done - 1 have arrived."""
+    return max(0, -(-(done - slot) // ring))
+
+
+class Search:
+    """few: both quarters hear each other's maxima (few rows). idle: the last quarter has no rows. tail_first: the last tile's value
+    rows are cleared before the step's scores are waited for."""
+
+    def __init__(self, steps, few=False, idle=False, tail_first=False):
+        self.steps, self.few, self.idle, self.tail_first = steps, few, idle, tail_first
+        self.wrong = set()
+
+    def wait(self, name, phases, phase):
+        """Whether a wait for the end of phase `phase` (from 0) passes when `phases` have ended."""
+        if (phases & 1) != ((phase & 1) ^ 1):
+            return False
+        if phases != phase + 1:
+            self.wrong.add(name)
+        return True
+
+    def run(self):
+        n_told = 1 if self.few else QUARTERS
+        # keys and values landed, score products, P V products issued and done, each warp's place by quarter and
+        # group, arrivals at p_full and at told (arrivals of the open phase, phases ended)
+        start = (0, 0, 0, 0, 0, ((0, 0),) * QUARTERS, ((0, 0),) * BUFFERS, ((0, 0),) * (TOLD * n_told))
+        seen, todo = {start}, [start]
+        while todo:
+            s = todo.pop()
+            after = list(self.next(s))
+            if not after:
+                assert s[4] == self.steps, "the search ends in a state where everything waits"
+            for t in after:
+                if t not in seen:
+                    seen.add(t)
+                    todo.append(t)
+        return self.wrong
+
+    @staticmethod
+    def arrive(bars, i, count):
+        n, phases = bars[i]
+        b = (0, phases + 1) if n + 1 == count else (n + 1, phases)
+        return bars[:i] + (b,) + bars[i + 1:]
+
+    def next(self, s):
+        keys, values, scores, issued, done, at, p_full, told = s
+        if keys < self.steps and keys < scores + STAGES:
+            yield keys + 1, values, scores, issued, done, at, p_full, told
+        if values < self.steps and values < done + STAGES:
+            yield keys, values + 1, scores, issued, done, at, p_full, told
+        n = scores
+        if n < self.steps and (n < BUFFERS or self.wait("p_done for S", _of(done, n % BUFFERS, BUFFERS), n // BUFFERS - 1)) \
+                and self.wait("k_full", _of(keys, n % STAGES, STAGES), n // STAGES):
+            yield keys, values, scores + 1, issued, done, at, p_full, told
+        n = issued
+        if n < self.steps and self.wait("v_full", _of(values, n % STAGES, STAGES), n // STAGES) \
+                and self.wait("p_full", p_full[n % BUFFERS][1], n // BUFFERS):
+            if any(at[q][n & 1] < 6 * (n // 2 + 1) for q in range(QUARTERS)):
+                self.wrong.add("a product before its weights")
+            yield keys, values, scores, issued + 1, done, at, p_full, told
+        if done < issued:
+            yield keys, values, scores, issued, done + 1, at, p_full, told
+        for q in range(QUARTERS):
+            for g in range(2):
+                for t in self.softmax(s, q, g):
+                    yield t
+
+    def softmax(self, s, q, g):
+        """The next step of quarter q's warp of group g, whose steps are g, g + 2, ...: six places each."""
+        keys, values, scores, issued, done, at, p_full, told = s
+        own, part = divmod(at[q][g], 6)
+        n = 2 * own + g
+        if n >= self.steps:
+            return
+        busy = not (self.idle and q == QUARTERS - 1)
+        ring = 0 if self.few else q * TOLD
+        count = QUARTERS if self.few else 1
+
+        def to(place, p=p_full, m=told):
+            return keys, values, scores, issued, done, at[:q] + (at[q][:g] + (place,) + at[q][g + 1:],) + at[q + 1:], p, m
+
+        def tail():
+            return n + 1 < self.steps or self.wait("v_full of the tail", _of(values, n % STAGES, STAGES), n // STAGES)
+
+        def s_full():
+            return self.wait("s_full", _of(scores, n % BUFFERS, BUFFERS), n // BUFFERS)
+
+        base = 6 * own
+        if part == 0:                               # scores, and the values' tail
+            if not (tail() and s_full() if self.tail_first else s_full() and tail()):
+                return
+            yield to(base + 1) if busy else to(base + 2)
+        elif part == 1:                             # hears the step before, tells its own maxima
+            if n > 0 and not self.wait("told", told[ring + (n - 1) % TOLD][1], (n - 1) // TOLD):
+                return
+            yield to(base + 2, m=self.arrive(told, ring + n % TOLD, count))
+        elif part == 2:                             # (few rows: hears them all;) O at a new scale, weights
+            if busy and self.few and not self.wait("told", told[ring + n % TOLD][1], n // TOLD):
+                return
+            if busy and n > 0:                      # (only if the maximum is raised: the step goes on either way)
+                self.wait("p_done for O", _of(done, (n - 1) % BUFFERS, BUFFERS), (n - 1) // BUFFERS)
+            yield to(base + 6, p=self.arrive(p_full, n % BUFFERS, QUARTERS))
+
+
+KINDS = [dict(), dict(few=True), dict(idle=True)]
+
+
+def test_the_search_finds_a_tail_cleared_too_early():
+    assert "v_full of the tail" in Search(5, tail_first=True).run()
+    assert "v_full of the tail" in Search(5, few=True, tail_first=True).run()
+    assert not Search(4, tail_first=True).run()     # four tiles: no stage is used twice
+
+
+def _tail_first(text):
+    """Whether the kernel's steps (whole tiles', few rows', those of warps without rows) clear the tail before they wait for S."""
+    body = text[text.index("// Step j of the piece by a warp with rows"):]
+    tails = [m.start() for m in re.finditer(r"clear_tail\(end", body)]
+    waits = [m.start() for m in re.finditer(r"a8_wait\(s_full\(n\)", body)]
+    assert len(tails) == len(waits) == 3
+    return [t < w for t, w in zip(tails, waits)]
+
+
+@pytest.mark.parametrize("steps", [5, 7])
+@pytest.mark.parametrize("kind", range(len(KINDS)))
+def test_every_wait_is_for_the_phase_that_is_meant(kind, steps):
+    first = _tail_first(open(SOURCE).read())
+    # the step of warps without rows beside one with rows: either may be the early one
+    early = {0: first[0], 1: first[1], 2: first[0] or first[2]}[kind]
+    assert not Search(steps, tail_first=early, **KINDS[kind]).run()
