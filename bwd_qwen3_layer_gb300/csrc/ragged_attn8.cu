@@ -3,23 +3,29 @@
 //   o_i = sum_j softmax_j(q_i . (a_j kc_j) / sqrt(d)) b_j vc_j,
 // kc_j, vc_j the e4m3 codes of position j and a_j, b_j its page's scales.
 //
-// Exact products in 8 bits. Keys and values go to the tensor cores as they are cached,
+// Products in 8 bits. Keys and values go to the tensor cores as they are cached,
 // nothing is converted: half the bytes of a bf16 cache in HBM and in shared memory. The
 // other operands are split. A bf16 query has 8 significant bits, which two e4m3
 // numbers hold (row scaled by a power of two so that its largest element is in [128,
 // 256); hi is the nearest e4m3, the rest has 4 bits: exact down to 2^-10 of the
 // largest, off by 2^-17 of it below). e4m3 products run at twice the bf16 rate, so S =
-// hi K^T + lo K^T takes the time of one bf16 product. Weights likewise: 4 bits by
-// cutting, the rest rounded to 4, off by 2^-8 at most as a bf16 weight is.
+// hi K^T + lo K^T takes the time of one bf16 product. Weights are three e5m2 numbers:
+// that type is the upper byte of an f16 number, so two cuts of three bits and one rounding take
+// few instructions, and each weight is off by 2^-9 of itself and its f16's 2^-11.
+//
+// Range. Many small weights can outweigh a few large ones (a key at the start that takes half of the row,
+// 32768 others the rest): what each of them loses adds up, so no weight may be cut off early.
+// Here it is off by 2^-17 at most where the row's largest is 2^11 or more, 2^-28 of it. (Two e4m3 parts, 2^-14
+// of it: half of the row was lost in that example. One step of 64 x ~4096 keys took 98.7 us then and 109 now, the chunk
+// 1.75 and 2.0 ms, three products for two and three more instructions for four weights. Two e5m2 parts would be
+// off by 2^-7.)
 //
 // Scales. t_j = s_j a_j + log2 b_j is what the running maximum m is taken of, and P'_j =
-// 2^(t_j - m + 4) = 2^(4 - m) p_j b_j goes into the product with the values' codes: its
+// 2^(t_j - m + 11) = 2^(11 - m) p_j b_j goes into the product with the values' codes: its
 // range does not depend on how the pages' scales differ. The row's sum adds P'_j / b_j. m
 // is raised when t exceeds it by more than 4.7 in some row of a warp, so P' stays below
-// 2^8.7 < 448 (and then to the maximum of every row: O's columns are read and written once
-// for all). Codes below 2^-6 lose bits, each part by 2^-10 at most: a weight is off by 2^-13 of the row's
-// largest at most, where that is more than its own 2^-8. (Raised at 2.5, with P' up to 2^6,
-// a chunk's steps waited for the product before them a third of the time.)
+// 2^15.7, which e5m2 and f16 hold (and then to the maximum of every row: O's columns are read and written once
+// for all). (Raised at 2.5, a chunk's steps waited for the product before them a third of the time.)
 //
 // Work split, walk and join are those of the bf16 kernel (ragged_walk.cuh): query tiles
 // of floor(128 / G) tokens x G heads, runs of key tiles of 128 keys, one CTA per SM,
@@ -40,12 +46,14 @@
 // products two steps ahead.
 //
 // Few rows. A piece of at most 16 rows (decoding) would leave seven of eight TMEM lanes
-// and all but one softmax warp idle, and its products, which read 128 rows of both parts
+// and all but one softmax warp idle, and its products, which read 128 rows of each part
 // whatever they hold, would take more of shared memory's time than the copies. Both
 // parts of its queries are rows of one tile instead, row r's at lanes r and 16 + r of
 // each quarter of the lanes: half the products, and each quarter's warp, which takes 32 of
 // the tile's keys (a lane 16), adds the parts. Weights likewise, in shared memory, from
-// where the P V product reads them: lanes r and 16 + r of O are added at the end.
+// where the P V product reads them: up to ten rows' three parts at lanes r, 10 + r and 20 + r of O, added
+// at the end. Of more rows the third parts are a tile with zeros, and a second product (64 requests of two tokens: 114
+// us; as a tile of 128 rows 153).
 //
 // Measured (64 query heads, 8 kv heads, pages of 16): 64 requests of ~4096 keys 99-105 us, 0.76-0.80 of HBM's copy rate
 // (128-byte pieces 1 KB apart); one of 32768 22 us; 4095 rows over 12288 keys 1.77 to 1.87 ms, 0.55 to 0.58
@@ -75,12 +83,14 @@ constexpr int A8_QR = 8;                      // pieces in the ring of the rows'
 constexpr int a8_scr(bool tma) { return tma ? 8 : 4; }      // tiles in the ring of scales
 constexpr int A8_QW = 3;                      // warps that split queries
 constexpr int A8_SB = 3;                      // steps whose scores and weights are in tensor memory
-constexpr int A8_FEW = 16;                    // rows of a piece that has both parts in one tile
+constexpr int A8_FEW = 16;                    // rows at most of a piece that has the parts of its operands as rows of one tile
 constexpr uint32_t A8_FEW_TILE = 2 * A8_FEW * 128;          // 32 rows: a quarter of the lanes
+constexpr int A8_LEAST = 10;                  // rows whose three parts of weights are 32 rows, too
+constexpr uint32_t A8_P_BYTES = 4 * A8_FEW_TILE;
 constexpr uint32_t A8_OFF_Q = 0;              // two pieces' queries, high and low parts
-constexpr uint32_t A8_OFF_P = A8_OFF_Q + 4 * A8_TILE;       // weights of few rows, three steps (the product reads 128
-                                              // rows: what lies behind gives rows that nobody reads)
-constexpr uint32_t A8_OFF_K = A8_OFF_P + A8_SB * A8_FEW_TILE;
+constexpr uint32_t A8_OFF_P = A8_OFF_Q + 4 * A8_TILE;       // weights of few rows: three steps of 32 rows or two of 64
+                                              // (the product reads 128: what lies behind gives rows that nobody reads)
+constexpr uint32_t A8_OFF_K = A8_OFF_P + A8_P_BYTES;
 constexpr uint32_t A8_OFF_V = A8_OFF_K + A8_NST * A8_TILE;
 constexpr uint32_t A8_OFF_BAR = A8_OFF_V + A8_NST * A8_TILE;
 constexpr uint32_t A8_OFF_QS = A8_OFF_BAR + 3 * 1024;       // the rows' factors, of eight pieces
@@ -91,8 +101,8 @@ constexpr size_t a8_smem(bool tma) { return 1024 + A8_OFF_SC + a8_scr(tma) * 3 *
 static_assert(a8_smem(false) <= 232448, "shared memory");
 // Tensor memory: S of three steps, whose columns P takes as they are read, and O: all 512 columns.
 constexpr uint32_t A8_TM_O = 384;
-constexpr float A8_LIFT = 4.0f;               // P' of the running maximum is 2^4 ...
-constexpr float A8_LAG = 4.7f;                // ... to 2^8.7
+constexpr float A8_LIFT = 11.0f;              // P' of the running maximum is 2^11 ...
+constexpr float A8_LAG = 4.7f;                // ... to 2^15.7
 
 struct A8Params {
   CUtensorMap tmK, tmV;
@@ -118,21 +128,23 @@ __device__ __forceinline__ uint64_t a8_desc_k(uint32_t base, int kk) { return sm
 // Values as the MN-major B operand: n = head dim, 128 bytes; k-step kk of 32 keys = four groups
 __device__ __forceinline__ uint64_t a8_desc_v(uint32_t base, int kk) { return smem_desc_sw128(base + kk * 4096, 1024, 1024); }
 
-// Pairs of f16 in one register, and four of them as e4m3.
+// Pairs of f16 in one register (the largest finite one for what is above), and four of them as e5m2: cut, which
+// is their upper bytes, or rounded.
 __device__ __forceinline__ uint32_t a8_f16x2(uint32_t lo, uint32_t hi) {
   uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
   return d;
 }
+__device__ __forceinline__ uint32_t a8_e5m2x4_cut(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7531); }
 __device__ __forceinline__ uint32_t a8_sub_h(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-__device__ __forceinline__ uint32_t a8_e4m3x4_h(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t a8_e5m2x4_h(uint32_t a, uint32_t b) {
   uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(a));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(b));
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(lo) : "r"(a));
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(hi) : "r"(b));
   uint32_t d;
   asm("mov.b32 %0, {%1, %2};" : "=r"(d) : "h"(lo), "h"(hi));
   return d;
@@ -279,6 +291,8 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
   // the parity that piece k's queries' barrier is waited for with (q_full(0) serves from piece 8 on)
   auto q_phase = [&](int k) -> uint32_t { return k ? ((k - (k & (A8_QR - 1) ? 0 : A8_QR)) / A8_QR) & 1 : 0; };
   auto token_of = [&](int r) { return (r * p.inv_g) >> 16; };
+  // where few rows' weights of step n are
+  auto few_p = [&](bool least, int n) { return sb + A8_OFF_P + (least ? n % 3 : 2 * (n & 1)) * A8_FEW_TILE; };
   // Queries, four rows at a time, 8 lanes of 16 elements each: row r0 + (lane >> 3) of a piece with `rows` ...
   auto load_q = [&](const RaPiece& c, int rows, int r0, uint4 (&x)[2]) {
     const int r = r0 + (lane >> 3), tok = token_of(r);
@@ -444,7 +458,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
   } else if (warp == 2) {
     // ---------- S_n = hi K_n^T + lo K_n^T into S[n % 3] (whole warp; the elected lane issues) ----------
     const bool el = elect_one();
-    const uint32_t idesc = idesc_e4m3_f32(128, 128, 0, 0);
+    const uint32_t idesc = idesc_f8_f32(128, 128, 0, 0, 0);
     int n = 0, ks = 0;                        // step, K stage
     uint32_t kph = 0;
     bool ok = true;
@@ -465,7 +479,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
           const uint32_t kb = sb + A8_OFF_K + ks * A8_TILE;
 #pragma unroll 1
           for (int kk = 0; kk < (few ? 4 : 8); ++kk)      // high parts, then low ones
-            umma_e4m3(tmem + n % A8_SB * 128, a8_desc_k(qb + (kk >> 2) * A8_TILE, kk & 3), a8_desc_k(kb, kk & 3), idesc, kk > 0);
+            umma_f8(tmem + n % A8_SB * 128, a8_desc_k(qb + (kk >> 2) * A8_TILE, kk & 3), a8_desc_k(kb, kk & 3), idesc, kk > 0);
           umma_commit(s_full(n));
           umma_commit(k_empty(ks));
           if (j == tiles - 1) umma_commit(q_empty(k));   // the piece's last use of Q
@@ -482,15 +496,16 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
     __syncwarp();
     mbar_wait(drain, 0, p.err);
   } else if (warp == 3) {
-    // ---------- O (+)= P_n V_n, both parts (whole warp; the elected lane issues) ----------
+    // ---------- O (+)= P_n V_n, all parts (whole warp; the elected lane issues) ----------
     const bool el = elect_one();
-    const uint32_t idesc = idesc_e4m3_f32(128, 128, 0, 1);
+    const uint32_t idesc = idesc_f8_f32(128, 128, 1, 0, 1);
     int n = 0, vs = 0;                        // step, V stage
     uint32_t vph = 0;
     bool ok = true;
     for (int k = 0; ok && find(k); ++k) {
       const int tiles = piece(k).tb - piece(k).ta;
-      const bool few = piece(k).toks * p.G <= A8_FEW;
+      const int rows = piece(k).toks * p.G;
+      const bool few = rows <= A8_FEW, least = rows <= A8_LEAST;
       if (k > 0 && !a8_wait(o_free, (k - 1) & 1, p.err, abort_flag)) { ok = false; break; }
       for (int j = 0; j < tiles; ++j, ++n) {
         if (!a8_wait(v_full(vs), vph, p.err, abort_flag) || !a8_wait(p_full(n), phase(n), p.err, abort_flag)) {
@@ -499,13 +514,20 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
         }
         tc_fence_after();
         if (el) {
-          const uint32_t vb = sb + A8_OFF_V + vs * A8_TILE, pb = sb + A8_OFF_P + n % A8_SB * A8_FEW_TILE;
-          const uint32_t pt = tmem + n % A8_SB * 128;     // 16 columns for 32 keys: high parts, low parts
+          const uint32_t vb = sb + A8_OFF_V + vs * A8_TILE, pb = few_p(least, n);
+          const uint32_t pt = tmem + n % A8_SB * 128;     // 24 columns for 32 keys: the three parts
 #pragma unroll 1
-          for (int kk = 0; kk < (few ? 4 : 8); ++kk) {
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t v = a8_desc_v(vb, kk);
             const uint32_t acc = j > 0 || kk > 0;
-            if (few) umma_e4m3(tmO, a8_desc_k(pb, kk), a8_desc_v(vb, kk), idesc, acc);
-            else umma_e4m3_ta(tmO, pt + kk * 8, a8_desc_v(vb, kk >> 1), idesc, acc);
+            if (few) {                             // (more than A8_LEAST: two parts, then the third beside zeros)
+              umma_f8(tmO, a8_desc_k(pb, kk), v, idesc, acc);
+              if (!least) umma_f8(tmO, a8_desc_k(pb + A8_FEW_TILE, kk), v, idesc, 1);
+            } else {
+              umma_f8_ta(tmO, pt + kk * 24, v, idesc, acc);
+              umma_f8_ta(tmO, pt + kk * 24 + 8, v, idesc, 1);
+              umma_f8_ta(tmO, pt + kk * 24 + 16, v, idesc, 1);
+            }
           }
           umma_commit(p_done(n));
           umma_commit(v_empty(vs));
@@ -700,6 +722,8 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
     float rs = 0.f;                                // the row's factor: score in log2 units = S * rs * a
     int lim = 0, end = 0;                          // from the piece's first key: the row's last key; the end of the query tile's
     bool real = false;                             // this lane's row is one of the piece's
+    bool least = true;                             // (few rows) all parts of the weights are 32 rows ...
+    int apart = A8_LEAST;                          // ... and so far apart
     // The maximum after one more step, which only moves when some row's would by more than A8_LAG (the
     // final O / l cancels a stale one). All warps that have these rows come to the same answer.
     auto raised = [&](float m, float mx) { return __any_sync(0xffffffffu, real && mx > m + A8_LAG) ? fmaxf(m, mx) : m; };
@@ -716,20 +740,23 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       }
       return true;
     };
-    // Four weights' exponents -> their values (pairs), and both parts: as f16, of whose 11 bits four are kept
-    // and the rest is rounded to four. (In fp32 the masks and differences took four instructions more for
-    // four weights, and one warp 11.8 cycles a weight, 7.9 so.)
-    auto weights = [&](uint64_t x0, uint64_t x1, uint64_t& y0, uint64_t& y1, uint32_t& hi, uint32_t& lo) {
+    // Four weights' exponents -> their values (pairs), and three parts: as f16, of whose 11 bits three are kept,
+    // of the rest three again, and what is left is rounded to three. (In fp32 the masks and differences took four
+    // instructions more for four weights and two parts, and one warp 11.8 cycles a weight, 7.9 so.)
+    auto weights = [&](uint64_t x0, uint64_t x1, uint64_t& y0, uint64_t& y1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
       float p0, p1, p2, p3;
       ra_unpair(x0, p0, p1);
       ra_unpair(x1, p2, p3);
       const uint32_t u0 = __float_as_uint(ra_ex2(p0)), u1 = __float_as_uint(ra_ex2(p1)), u2 = __float_as_uint(ra_ex2(p2)), u3 = __float_as_uint(ra_ex2(p3));
       y0 = ra_pair(u0, u1);
       y1 = ra_pair(u2, u3);
-      const uint32_t h0 = a8_f16x2(u0, u1), h1 = a8_f16x2(u2, u3);
-      constexpr uint32_t KEEP = 0xff80ff80u;
-      hi = a8_e4m3x4_h(h0 & KEEP, h1 & KEEP);
-      lo = a8_e4m3x4_h(a8_sub_h(h0, h0 & KEEP), a8_sub_h(h1, h1 & KEEP));
+      constexpr uint32_t KEEP = 0xff00ff00u;
+      uint32_t h0 = a8_f16x2(u0, u1), h1 = a8_f16x2(u2, u3);
+      hi = a8_e5m2x4_cut(h0, h1);
+      h0 = a8_sub_h(h0, h0 & KEEP);
+      h1 = a8_sub_h(h1, h1 & KEEP);
+      mid = a8_e5m2x4_cut(h0, h1);
+      lo = a8_e5m2x4_h(a8_sub_h(h0, h0 & KEEP), a8_sub_h(h1, h1 & KEEP));
     };
     // What takes S to the score, S * factor(a); never zero, so that the -inf of keys cut off stays.
     auto factor = [&](float a) { return a8_max_nan(rs * a, 1.17549435e-38f); };
@@ -776,8 +803,8 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       }
       return mx;
     };
-    // N keys' weights, four to a word of each part; their sum goes into r0, r1.
-    auto weigh = [&](auto& sv, uint32_t sc, float neg, auto& ph, auto& pl, uint64_t& r0, uint64_t& r1) {
+    // N keys' weights, four to a word of each of three parts; their sum goes into r0, r1.
+    auto weigh = [&](auto& sv, uint32_t sc, float neg, auto& ph, auto& pm, auto& pl, uint64_t& r0, uint64_t& r1) {
       constexpr int N = sizeof(sv) / 4, GV = N < 32 ? 2 : 4;
       if (TMA) {
         float a4[4], l4[4], i4[4];
@@ -790,8 +817,8 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
           const uint32_t fu = __float_as_uint(factor(a4[g])), cu = __float_as_uint(l4[g] + neg), iu = __float_as_uint(i4[g]);
           const uint64_t f2 = ra_pair(fu, fu), c2 = ra_pair(cu, cu), iv = ra_pair(iu, iu);
           uint64_t y0, y1, y2, y3;
-          weights(ra_fma2(ra_pair(v[0], v[1]), f2, c2), ra_fma2(ra_pair(v[2], v[3]), f2, c2), y0, y1, ph[2 * g], pl[2 * g]);
-          weights(ra_fma2(ra_pair(v[4], v[5]), f2, c2), ra_fma2(ra_pair(v[6], v[7]), f2, c2), y2, y3, ph[2 * g + 1], pl[2 * g + 1]);
+          weights(ra_fma2(ra_pair(v[0], v[1]), f2, c2), ra_fma2(ra_pair(v[2], v[3]), f2, c2), y0, y1, ph[2 * g], pm[2 * g], pl[2 * g]);
+          weights(ra_fma2(ra_pair(v[4], v[5]), f2, c2), ra_fma2(ra_pair(v[6], v[7]), f2, c2), y2, y3, ph[2 * g + 1], pm[2 * g + 1], pl[2 * g + 1]);
           r0 = ra_fma2(ra_add2(y0, y1), iv, r0);
           r1 = ra_fma2(ra_add2(y2, y3), iv, r1);
         }
@@ -806,7 +833,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
           uint64_t y0, y1;
           weights(ra_fma2(ra_pair(sv[e], sv[e + 1]), two(factor(a4[0]), factor(a4[1])), two(l4[0] + neg, l4[1] + neg)),
                   ra_fma2(ra_pair(sv[e + 2], sv[e + 3]), two(factor(a4[2]), factor(a4[3])), two(l4[2] + neg, l4[3] + neg)), y0, y1,
-                  ph[e / 4], pl[e / 4]);
+                  ph[e / 4], pm[e / 4], pl[e / 4]);
           r0 = ra_fma2(y0, two(i4[0], i4[1]), r0);
           r1 = ra_fma2(y1, two(i4[2], i4[3]), r1);
         }
@@ -837,7 +864,8 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       if (j > 0 && (!FEW || quarter == 0) && __any_sync(0xffffffffu, m2 > m1)) {
         // O at the new scale, after the product of the step before (its barrier is at no earlier phase: S_n was
         // computed after the product of step n - 3)
-        const float alpha = m2 > m1 ? ra_ex2(m1 - m2) : 1.0f;
+        float alpha = m2 > m1 ? ra_ex2(m1 - m2) : 1.0f;
+        if (FEW) alpha = __shfl_sync(0xffffffffu, alpha, lane % apart);       // O's lane is a part of that row
         if (!a8_wait(p_done(n0 + j - 1), phase(n0 + j - 1), p.err, abort_flag)) return false;
         tc_fence_after();
 #pragma unroll 1
@@ -890,14 +918,16 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       if (!agree(std::false_type(), j, mx)) return false;
       const float neg = m > -INFINITY ? A8_LIFT - m : 0.f;
       uint64_t r0 = 0, r1 = 0;
-      uint32_t ph[8], pl[8];
+      uint32_t ph[8], pm[8], pl[8];
 #pragma unroll 1
-      for (int c = 0; c < RA_BKV; c += 32) {       // P: 16 columns for 32 keys, high and low parts, where S has been read
+      for (int c = 0; c < RA_BKV; c += 32) {       // P: 24 columns for 32 keys, the three parts, where S has been read
         tmem_ld_wait();
-        weigh(sv, sca + c / GRP * 4, neg, ph, pl, r0, r1);
+        weigh(sv, sca + c / GRP * 4, neg, ph, pm, pl, r0, r1);
         if (c < RA_BKV - 32) tmem_ld_32x32b_x32(sadr + c + 32, sv);
-        a8_tmem_st8(sadr + c / 2, ph);
-        a8_tmem_st8(sadr + c / 2 + 8, pl);
+        const uint32_t at = sadr + c / 32 * 24;
+        a8_tmem_st8(at, ph);
+        a8_tmem_st8(at + 8, pm);
+        a8_tmem_st8(at + 16, pl);
       }
       sum_up(r0, r1);
       tmem_st_wait();
@@ -930,12 +960,19 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       if (!agree(std::true_type(), j, max_t(sv, sca))) return false;
       const float neg = m > -INFINITY ? A8_LIFT - m : 0.f;
       uint64_t r0 = 0, r1 = 0;
-      uint32_t ph[4], pl[4];
-      weigh(sv, sca, neg, ph, pl, r0, r1);
-      // row lane & 15, its low parts 16 rows further on; 16 keys: one 16-byte chunk of its 128 bytes
-      const uint32_t at = sb + A8_OFF_P + n % A8_SB * A8_FEW_TILE + (lane & 15) * 128 + ((2 * quarter + (lane >> 4)) ^ (lane & 7)) * 16;
-      st_shared_v4(at, ph[0], ph[1], ph[2], ph[3]);
-      st_shared_v4(at + A8_FEW * 128, pl[0], pl[1], pl[2], pl[3]);
+      uint32_t ph[4], pm[4], pl[4];
+      weigh(sv, sca, neg, ph, pm, pl, r0, r1);
+      // with two buffers this step's is free once the product of two steps before is done (at no earlier phase: as in agree)
+      if (!least && n >= 2 && !a8_wait(p_done(n - 2), phase(n - 2), p.err, abort_flag)) return false;
+      // a row's three parts, `apart` rows from each other; 16 keys: one 16-byte chunk of a row's 128 bytes
+      auto put = [&](int row, const uint32_t (&x)[4]) {
+        st_shared_v4(few_p(least, n) + row * 128 + ((2 * quarter + (lane >> 4)) ^ (row & 7)) * 16, x[0], x[1], x[2], x[3]);
+      };
+      if ((lane & 15) < apart) {
+        put(lane & 15, ph);
+        put((lane & 15) + apart, pm);
+        put((lane & 15) + 2 * apart, pl);
+      }
       sum_up(r0, r1);
       fence_async_shared();
       tmem_st_wait();                              // O's, if the maximum was raised
@@ -961,6 +998,10 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       const bool few = rows <= A8_FEW;
       const bool busy = few || quarter * 32 < rows;      // some row of this warp is real
       real = (few ? lane & (A8_FEW - 1) : r) < rows;
+      least = rows <= A8_LEAST;
+      apart = least ? A8_LEAST : A8_FEW;
+      // the zeros beside the third parts (nobody reads the buffers between two pieces)
+      if (few && !least) st_shared_v4(few_p(false, grp) + A8_FEW_TILE + A8_FEW * 128 + r * 16, 0u, 0u, 0u, 0u);
       m = -INFINITY;
       l = 0.f;
       if (!a8_wait(k ? q_full(k) : q_first, q_phase(k), p.err, abort_flag)) { ok = false; break; }
@@ -1027,9 +1068,13 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
           uint32_t v[32];
           tmem_ld_32x32b_x32(oadr + grp * 64 + h * 32, v);
           tmem_ld_wait();
-          if (few) {                               // the low parts' share
+          if (few) {                               // the other parts' share (more than A8_LEAST rows: one other lane's)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(__shfl_down_sync(0xffffffffu, v[e], 16)));
+            for (int e = 0; e < 32; ++e) {
+              const float b = __uint_as_float(__shfl_down_sync(0xffffffffu, v[e], apart));
+              const float c = __uint_as_float(__shfl_down_sync(0xffffffffu, v[e], 2 * A8_LEAST));
+              v[e] = __float_as_uint(__uint_as_float(v[e]) + (least ? b + c : b));
+            }
           }
           if (mine && all) {
             __nv_bfloat16* orow_p = p.j.o + orow * RA_D + grp * 64 + h * 32;

@@ -635,7 +635,10 @@ KL_API kl_status kl_ragged_qkv_rope8(const kl_ragged_cfg* rc, int32_t Hq, int32_
  * kl_ragged_qkv_rope8 writes), of which no two that a row sees are more than 2^100
  * apart. A block that is read as zero (see there) has no scale. A NaN in a query, in a key that a row sees or in the scale of a block
  * that it sees makes the row's o and lse NaN, as an infinity in a query does; a
- * NaN in a value reaches rows as there. */
+ * NaN in a value reaches rows as there.
+ * Precision, beside fp32 sums and o's rounding to bf16: a query's element is off by 2^-17
+ * of its row and head's largest one at most; a softmax weight times its value scale by 2^-8.6 of
+ * itself, and by 2^-28 of the largest such product of the row for each of the row's keys. */
 KL_API size_t kl_ragged_attention8_ws_bytes(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d);
 KL_API kl_status kl_ragged_attention8(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
                                       const void* q, const void* k_pool, const void* v_pool, const float* k_scale,

@@ -19,11 +19,11 @@ def _of(done, slot, ring):
 
 
 class Search:
-    """few: both quarters hear each other's maxima (few rows). idle: the last quarter has no rows. tail_first: the last tile's value
+    """few: both quarters hear each other's maxima (few rows). pairs: their weights have two buffers. idle: the last quarter has no rows. tail_first: the last tile's value
     rows are cleared before the step's scores are waited for."""
 
-    def __init__(self, steps, few=False, idle=False, tail_first=False):
-        self.steps, self.few, self.idle, self.tail_first = steps, few, idle, tail_first
+    def __init__(self, steps, few=False, pairs=False, idle=False, tail_first=False):
+        self.steps, self.few, self.pairs, self.idle, self.tail_first = steps, few, pairs, idle, tail_first
         self.wrong = set()
 
     def wait(self, name, phases, phase):
@@ -112,12 +112,14 @@ class Search:
         elif part == 2:                             # (few rows: hears them all;) O at a new scale, weights
             if busy and self.few and not self.wait("told", told[ring + n % TOLD][1], n // TOLD):
                 return
+            if self.pairs and n > 1 and not self.wait("p_done for P", _of(done, (n - 2) % BUFFERS, BUFFERS), (n - 2) // BUFFERS):
+                return
             if busy and n > 0:                      # (only if the maximum is raised: the step goes on either way)
                 self.wait("p_done for O", _of(done, (n - 1) % BUFFERS, BUFFERS), (n - 1) // BUFFERS)
             yield to(base + 6, p=self.arrive(p_full, n % BUFFERS, QUARTERS))
 
 
-KINDS = [dict(), dict(few=True), dict(idle=True)]
+KINDS = [dict(), dict(few=True), dict(idle=True), dict(few=True, pairs=True)]
 
 
 def test_the_search_finds_a_tail_cleared_too_early():
@@ -140,5 +142,5 @@ def _tail_first(text):
 def test_every_wait_is_for_the_phase_that_is_meant(kind, steps):
     first = _tail_first(open(SOURCE).read())
     # the step of warps without rows beside one with rows: either may be the early one
-    early = {0: first[0], 1: first[1], 2: first[0] or first[2]}[kind]
+    early = [first[0], first[1], first[0] or first[2], first[1]][kind]
     assert not Search(steps, tail_first=early, **KINDS[kind]).run()

@@ -108,3 +108,58 @@ def test_attention_of_long_caches(kl, reqs):
         different += (o.view(torch.int16) != first.view(torch.int16)).any()
     assert kl.kl_device_status() == 0
     assert int(different) == 0 and not bool(torch.isnan(first).any())
+
+
+def _sink(cache, mass, lift=1.0):
+    """Each request's first key takes `mass` of its rows' weight and has a small value; the rest is spread evenly over the other keys. lift:
+    the second value's size, which says how coarse the first page's scale is."""
+    u = cache.rand(D).sign() * 0.5
+    cache.q = u + 0.05 * cache.rand(int(cache.cu[-1]), cache.Hq, D)
+    cache.k *= 0.05
+    for b, (n, c) in enumerate(cache.reqs):
+        page = int(cache.table[b, 0])
+        score = math.log(mass / (1 - mass) * (n + c))
+        cache.k[page, 0] = u * (score * math.sqrt(D) / float(u @ u))
+        cache.v[page, 0] = 0.01 * cache.v[page, 0]
+        if cache.bs > 1:
+            cache.v[page, 1] *= lift
+    return cache.codes()
+
+
+def _check_relative(cache, o, rows=None):
+    """All values positive: the result is off by what a weight is, 2^-9 and 2^-11 of itself, by twice what a score is (below 2^-10), the
+    running sums' 2^-9, the rounding to bf16, 2^-8: below 2^-6.2 of it in all. And for each key by half of 2^-16, the least step of the weights'
+    parts, where the row's largest weight times scale is held as 2^11 or more: 2^-28 of that, times the key's code."""
+    for r, h, want, size, top, codes, dz in cache.exact(rows):
+        assert float(dz.max()) < 2.0 ** -10
+        err = (o[r, h].double() - want).abs()
+        tol = 2.0 ** -6 * want + 2.0 ** -28 * top * codes
+        assert (err <= tol).all(), (r[0], h, float((err / tol).max()))
+
+
+@pytest.mark.parametrize("mass,lift", [(0.3, 1.0), (0.5, 64.0), (0.9, 1.0), (0.95, 8.0)])
+@pytest.mark.parametrize("Hq,Hkv,bs,reqs", [
+    (64, 8, 16, [(1, 32768), (1, 8191), (1, 2000)]),
+    (10, 1, 16, [(1, 9000)]), (11, 1, 16, [(1, 9000)]), (16, 1, 16, [(1, 30000), (1, 700)]),       # 10 rows, 11, 16
+    (16, 2, 5, [(1, 8192), (9, 3000)]),
+    (64, 8, 16, [(300, 8000)]), (16, 2, 24, [(40, 2000), (1, 17000), (3, 5000)]),
+])
+def test_attention_with_a_key_that_outweighs_the_others(kl, Hq, Hkv, bs, reqs, mass, lift):
+    """What the many small weights add up to is there, in whatever pieces a request is cut: alone, and in a batch."""
+    cache = _sink(Cache(len(reqs) + reqs[0][1], reqs, Hq, Hkv, bs), mass, lift)
+    rc = cache.cfg(kl)
+    o, _ = _attend(kl, rc, Hq, Hkv, *cache.args)
+    assert kl.kl_device_status() == 0
+    rows = sorted(set(np.random.default_rng(1).integers(0, len(o), 60).tolist()) | set(int(c) for c in cache.cu[:-1]))
+    _check_relative(cache, o, rows)
+    # the first request alone, and beside 39 others: cut in other places
+    n, c = reqs[0]
+    q, kc, ks, vc, vs, table, cu, ctx = cache.args
+    one = kl.RaggedCfg(1, n, bs, cache.maxb, cache.nb)
+    o1, _ = _attend(kl, one, Hq, Hkv, q[:n].contiguous(), kc, ks, vc, vs, table[:1].contiguous(), _i([0, n]), _i([c]))
+    many = kl.RaggedCfg(40, 40 * n, bs, cache.maxb, cache.nb)
+    o40, _ = _attend(kl, many, Hq, Hkv, q[:n].repeat(40, 1, 1), kc, ks, vc, vs, table[:1].repeat(40, 1), _i(np.arange(41) * n), _i([c] * 40))
+    assert kl.kl_device_status() == 0
+    _check_relative(cache, o1, [r for r in rows if r < n])
+    for b in (0, 17, 39):
+        _check_relative(cache, o40[b * n:(b + 1) * n], [r for r in rows if r < n])
