@@ -194,7 +194,9 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
   // A wait by parity is right only if the phase before the one it means has ended. What says so: for the stages' and
   // rings' producers and consumers (k_, v_, sc_, q_, p_full), that they wait for every phase in turn; for s_full(n) in the softmax,
   // that S of step n - 2 was waited for; for v_full(n) and p_done(n - 1) there, that S of step n was, which was issued after the
-  // product of step n - 3; for told(t), that t - 1 was heard before; for sums and o_free, that every piece has one of each.
+  // product of step n - 3; for told(t), that t - 1 was heard before; for sums and o_free, that every piece has one of each. Arrivals, too, count
+  // for the phase that is open: sc_empty(n) comes before p_full(n), so that a warp without rows, which waits for S alone,
+  // cannot arrive for a later tile of that place before the others have for this one.
   // piece k's queries: eight, since with pieces of one tile the score products run three pieces ahead of
   // the softmax and the queries two more, and no waiter may be two phases behind
   auto q_full = [&](int k) { return bar + 576 + 8 * (k & (A8_QR - 1)); };
@@ -934,8 +936,8 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(p_full(n));
         mbar_arrive(sc_empty(n));
+        mbar_arrive(p_full(n));
       }
       return true;
     };
@@ -979,8 +981,8 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(p_full(n));
         mbar_arrive(sc_empty(n));
+        mbar_arrive(p_full(n));
       }
       return true;
     };
@@ -1018,8 +1020,8 @@ __global__ void __launch_bounds__(A8_THREADS, 1) ragged_attn8_kernel(const __gri
           ok = a8_wait(s_full(n), phase(n), p.err, abort_flag) && (!TMA || clear_tail(end - j * RA_BKV, n));
           __syncwarp();
           if (ok && lane == 0) {
-            mbar_arrive(p_full(n));
             mbar_arrive(sc_empty(n));
+            mbar_arrive(p_full(n));
           }
         }
       }
