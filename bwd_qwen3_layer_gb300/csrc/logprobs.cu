@@ -479,6 +479,7 @@ struct LpBwdParams {
 // where dz's lie as z's do they are written whole, else (rows of other strides or types whose alignment
 // differs) class by class.
 constexpr int LB_U = 4;                        // vectors a thread has under way
+constexpr float LB_FAR = -1e4f;                // as LP_FAR: p is 0, and the entropy's weight times this is finite (up to 3e34)
 constexpr int LB_PART = LP_THREADS * 8 * LB_U; // classes a CTA takes
 
 template <typename T, typename U>
@@ -496,7 +497,7 @@ __global__ void __launch_bounds__(LP_THREADS) token_logprobs_bwd_kernel(const __
   }
   const float a = t >= 0 && p.dlp ? p.dlp[n] : 0.f, b = p.dent ? p.dent[n] : 0.f, H = p.dent ? p.entropy[n] : 0.f;
   auto grad = [&](float zj, int j) {
-    const float x = lp_max_nan(zj - m - ls, LP_FAR), q = lp_ex2(x * LP_LOG2E);
+    const float x = lp_max_nan(zj - m - ls, LB_FAR), q = lp_ex2(x * LP_LOG2E);
     float d = -q * fmaf(b, x + H, a);
     if (j == t) d += a;
     return empty ? 0.f : d;
