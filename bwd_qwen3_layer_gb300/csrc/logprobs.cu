@@ -489,18 +489,19 @@ __global__ void __launch_bounds__(LP_THREADS) token_logprobs_bwd_kernel(const __
   const T* z = static_cast<const T*>(p.z) + static_cast<int64_t>(n) * p.ldz;
   U* dz = static_cast<U*>(p.dz) + static_cast<int64_t>(n) * p.lddz;
   const float m = p.norm[2 * static_cast<int64_t>(n)], ls = p.norm[2 * static_cast<int64_t>(n) + 1];
-  const bool empty = m == -INFINITY && ls == -INFINITY;
   int t = p.tokens[n];
   if (t < -1 || t >= p.V) {
     if (threadIdx.x == 0 && part == 0) record_error(p.err, KL_DEVERR_TARGET);
     t = -1;
   }
   const float a = t >= 0 && p.dlp ? p.dlp[n] : 0.f, b = p.dent ? p.dent[n] : 0.f, H = p.dent ? p.entropy[n] : 0.f;
+  // zeros: no logit above -inf, or no weight, whatever the logits are (padding may hold NaN)
+  const bool none = (m == -INFINITY && ls == -INFINITY) || (a == 0.f && b == 0.f);
   auto grad = [&](float zj, int j) {
     const float x = lp_max_nan(zj - m - ls, LB_FAR), q = lp_ex2(x * LP_LOG2E);
     float d = -q * fmaf(b, x + H, a);
     if (j == t) d += a;
-    return empty ? 0.f : d;
+    return none ? 0.f : d;
   };
   constexpr int ZA = 8 * sizeof(T), DA = 8 * sizeof(U);         // bytes of a vector
   const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(z) & (ZA - 1)) / sizeof(T));

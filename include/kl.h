@@ -684,7 +684,8 @@ KL_API kl_status kl_token_logprobs(int32_t N, int32_t V, int32_t dtype, const vo
  * from the forward's norm and entropy. d_logprob or d_entropy may be NULL (zero;
  * entropy is read with d_entropy only). Rows without a token get nothing from d_logprob
  * (a token outside [0, V) but for -1 is reported), rows without any logit above
- * -infinity zeros, as every class with p = 0 (of an entropy weight below 1e34). dz [N, V] (dz_dtype fp32 or bf16, row
+ * -infinity zeros, as every class with p = 0 (of an entropy weight below 1e34). A row whose
+ * weights are both zero or absent gets zeros whatever it holds, NaN too. dz [N, V] (dz_dtype fp32 or bf16, row
  * stride lddz) is overwritten; it may be z itself (same type and stride), else it
  * must not overlap z. */
 KL_API kl_status kl_token_logprobs_bwd(int32_t N, int32_t V, int32_t dtype, const void* z, int64_t ldz,
