@@ -633,9 +633,10 @@ KL_API kl_status kl_ragged_qkv_rope8(const kl_ragged_cfg* rc, int32_t Hq, int32_
 /* kl_ragged_attention over such pools; q and o stay bf16 (dtype). Key scales may be
  * any positive, finite, normal numbers; value scales those from 2^-64 to 2^120 (what
  * kl_ragged_qkv_rope8 writes), of which no two that a row sees are more than 2^100
- * apart. A block that is read as zero (see there) has no scale. A NaN in a query, in a key that a row sees or in the scale of a block
- * that it sees makes the row's o and lse NaN, as an infinity in a query does; a
- * NaN in a value reaches rows as there.
+ * apart. A block that is read as zero (see there) has no scale. A NaN in a query, in a
+ * key that a row sees or in the scale of a block that it sees makes the row's o and lse
+ * NaN, as an infinity in a query does. A NaN in a value reaches rows as there, and so does one in
+ * a scale, their lse too: every row of a query tile of which some row sees the block.
  * Precision, beside fp32 sums and o's rounding to bf16: a query's element is off by 2^-17
  * of its row and head's largest one at most; a softmax weight times its value scale by 2^-8.6 of
  * itself, and by 2^-28 of the largest such product of the row for each of the row's keys. */

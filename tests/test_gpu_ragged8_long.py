@@ -163,3 +163,21 @@ def test_attention_with_a_key_that_outweighs_the_others(kl, Hq, Hkv, bs, reqs, m
     _check_relative(cache, o1, [r for r in rows if r < n])
     for b in (0, 17, 39):
         _check_relative(cache, o40[b * n:(b + 1) * n], [r for r in rows if r < n])
+
+
+@pytest.mark.parametrize("which", ["key", "value"])
+@pytest.mark.parametrize("bs", [16, 5])
+def test_attention_of_a_block_without_a_scale(kl, bs, which):
+    """A NaN scale of a block that only a request's last rows see: these are NaN, the rows of other query tiles, heads and requests as they
+    were. (Rows of the same tile before the block may be NaN, too.)"""
+    reqs, Hq, Hkv = [(100, 60), (3, 400), (9, 0)], 4, 2          # two heads a group: tiles of 64 tokens
+    cache = Cache(3, reqs, Hq, Hkv, bs).codes()
+    rc = cache.cfg(kl)
+    base, blse = _attend(kl, rc, Hq, Hkv, *cache.args)
+    first = 145 // bs * bs                                       # rows from here on see the block: in the second tile
+    (cache.ks if which == "key" else cache.vs)[cache.table[0, first // bs], 1] = float("nan")
+    o, lse = _attend(kl, rc, Hq, Hkv, *cache.args)
+    assert kl.kl_device_status() == 0
+    assert torch.isnan(o[first - 60:100, 2:]).all() and torch.isnan(lse[first - 60:100, 2:]).all()
+    for a, b in ((o, base), (lse, blse)):
+        assert torch.equal(a[:64], b[:64]) and torch.equal(a[100:], b[100:]) and torch.equal(a[:, :2], b[:, :2])
