@@ -25,12 +25,16 @@
 #include <float.h>
 
 #include "e4m3.cuh"
-#include "ragged_rope.cuh"
+#include "internal.h"
+#include "kl_common.cuh"
+#include "rope.cuh"
 
 namespace kl {
 namespace {
 
 constexpr int R8_THREADS = 128;
+constexpr int RQ_D = 128;
+constexpr int RQ_LANES = 8;                      // threads per head: 8 planes (16 elements) each
 constexpr int R8_UNITS = R8_THREADS / RQ_LANES;  // heads that a CTA has in flight at a time
 constexpr int R8_TILE = 16;                      // rows whose runs a CTA takes
 constexpr int R8_AHEAD = 4;                      // steps whose rows are on their way to a CTA of the first kind
