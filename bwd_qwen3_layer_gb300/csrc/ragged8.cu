@@ -19,7 +19,7 @@
 // A CTA of the first kind takes the runs that begin in 16 rows, head by head, the rows of
 // the next heads on their way: 16 rows from the first run's on, an eighth of one to a
 // thread, its angles in registers, which meet for the runs' largest sizes. Where the runs
-// have more rows these are read twice, 16 at a time (the prompts in blocks of 64: 83 us).
+// have more rows these are read twice, 16 at a time (the prompts in blocks of 64: 84 us, and their angles formed twice for each head).
 // Before, a CTA for each row and head, of which one of 16 found a run, formed the angles
 // eight times over: 143 us (9000 decoding rows 348 against 71).
 #include <float.h>
@@ -62,13 +62,19 @@ struct Rope8Params {
   RopeFreq f;
 };
 
-// rope_cos_sin with the hardware's functions: off by 2^-21 at most within half a turn, far below half a step of
-// the results (2^-9 of a bf16 number, 2^-4 of a code), at an eighth of the instructions.
+// rope_cos_sin in fewer instructions: the phase's upper bits give the quarter of a turn, exactly, and the rest is
+// within an eighth, where the power series of sine and cosine are off by 2^-29 after five and six terms. 2^-23.3 in
+// all, sincosf's precision; the hardware's functions (2^-21) left some codes and queries a step away.
 __device__ __forceinline__ void r8_cos_sin(int pos, uint64_t turn, float* c, float* s) {
-  const uint64_t phase = static_cast<uint64_t>(pos) * turn;          // turns mod 1, in 2^-64 units
-  const float r = static_cast<float>(static_cast<int32_t>(static_cast<uint32_t>(phase >> 32))) * 1.46291807926715968e-09f;   // 2 pi / 2^32
-  *c = __cosf(r);
-  *s = __sinf(r);
+  const uint32_t t = static_cast<uint32_t>((static_cast<uint64_t>(pos) * turn) >> 32);   // turns mod 1, in 2^-32 units
+  const uint32_t k = (t + 0x20000000u) >> 30;
+  const float r = static_cast<float>(static_cast<int32_t>(t - (k << 30))) * 1.46291807926715968e-09f;   // 2 pi / 2^32
+  const float x = r * r;
+  const float sn = fmaf(r * x, fmaf(x, fmaf(x, fmaf(x, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), r);
+  const float cs = fmaf(x, fmaf(x, fmaf(x, fmaf(x, fmaf(x, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
+  const float a = k & 1 ? -sn : cs, b = k & 1 ? cs : sn;
+  *c = k & 2 ? -a : a;
+  *s = k & 2 ? -b : b;
 }
 // The least power of two w >= 2^-64 with a / w <= 448 = 1.75 * 2^8, for finite a >= 0.
 __device__ __forceinline__ float scale_for(float a) {
