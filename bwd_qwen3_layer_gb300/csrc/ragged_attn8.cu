@@ -16,8 +16,8 @@
 // Range. Many small weights can outweigh a few large ones (a key at the start that takes half of the row,
 // 32768 others the rest): what each of them loses adds up, so no weight may be cut off early.
 // Here it is off by 2^-17 at most where the row's largest is 2^11 or more, 2^-28 of it. (Two e4m3 parts, 2^-14
-// of it: half of the row was lost in that example. One step of 64 x ~4096 keys took 98.7 us then and 109 now, the chunk
-// 1.75 and 2.0 ms, three products for two and three more instructions for four weights. Two e5m2 parts would be
+// of it, lost half of the row in that example. On one GPU 64 x ~4096 keys took 98.7 us so and take 109, the chunk
+// 1.75 and 2.0 ms: three products for two and three more instructions for four weights. Two e5m2 parts would be
 // off by 2^-7.)
 //
 // Scales. t_j = s_j a_j + log2 b_j is what the running maximum m is taken of, and P'_j =
@@ -42,8 +42,8 @@
 // Scores stay in tensor memory and are read twice, for the maximum and for the weights, 32
 // columns at a time, so that a step's code is a few small loops: unrolled over 128 keys (30
 // KB a step, 170 KB in all) the instruction fetch took longer than the work, 3800 cycles a
-// step. Keys cut off are marked in tensor memory beforehand for the same reason (1900 -> 1790 us on a chunk). P takes the columns of S that have been read; three such buffers keep the score
-// products two steps ahead.
+// step. Keys cut off are marked in tensor memory beforehand for the same reason (6 % of a chunk). P takes the columns of S
+// that have been read; three such buffers keep the score products two steps ahead.
 //
 // Few rows. A piece of at most 16 rows (decoding) would leave seven of eight TMEM lanes
 // and all but one softmax warp idle, and its products, which read 128 rows of each part
@@ -55,10 +55,10 @@
 // at the end. Of more rows the third parts are a tile with zeros, and a second product (64 requests of two tokens: 114
 // us; as a tile of 128 rows 153).
 //
-// Measured (64 query heads, 8 kv heads, pages of 16): 64 requests of ~4096 keys 99-105 us, 0.76-0.80 of HBM's copy rate
-// (128-byte pieces 1 KB apart); one of 32768 22 us; 4095 rows over 12288 keys 1.77 to 1.87 ms, 0.55 to 0.58
-// of the bf16 tensor peak that the doubled products come to: a step takes ~2200 cycles, of which the products need 1024, the
-// softmax warps' ~1150 instructions for each of two warps a scheduler the rest.
+// Measured (64 query heads, 8 kv heads, pages of 16): 64 requests of ~4096 keys 108-110 us, 0.73-0.74 of HBM's copy rate
+// (128-byte pieces 1 KB apart, and a chain of waits from a tile's scores to its product); one of 32768 23-24 us; 4095 rows over
+// 12288 keys 1.95 to 2.07 ms: a step takes ~2400 cycles, of which the products (two for the scores, three for the
+// values) need 1280, the softmax warps' instructions for two warps a scheduler the rest.
 //
 // Barriers, stages and buffers as in the bf16
 // kernel. A key tile of 16 KB is 16 groups of 8 keys x 128 bytes (one swizzle atom each);

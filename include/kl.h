@@ -639,7 +639,9 @@ KL_API kl_status kl_ragged_qkv_rope8(const kl_ragged_cfg* rc, int32_t Hq, int32_
  * a scale, their lse too: every row of a query tile of which some row sees the block.
  * Precision, beside fp32 sums and o's rounding to bf16: a query's element is off by 2^-17
  * of its row and head's largest one at most; a softmax weight times its value scale by 2^-8.6 of
- * itself, and by 2^-28 of the largest such product of the row for each of the row's keys. */
+ * itself, and by 2^-28 of the largest such product of the row for each of the row's keys.
+ * lse is formed beside the value scales' logarithms: off by 2^-21 of the largest |log2| of
+ * one, too. */
 KL_API size_t kl_ragged_attention8_ws_bytes(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d);
 KL_API kl_status kl_ragged_attention8(const kl_ragged_cfg* rc, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
                                       const void* q, const void* k_pool, const void* v_pool, const float* k_scale,

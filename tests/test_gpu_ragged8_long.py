@@ -181,3 +181,24 @@ def test_attention_of_a_block_without_a_scale(kl, bs, which):
     assert torch.isnan(o[first - 60:100, 2:]).all() and torch.isnan(lse[first - 60:100, 2:]).all()
     for a, b in ((o, base), (lse, blse)):
         assert torch.equal(a[:64], b[:64]) and torch.equal(a[100:], b[100:]) and torch.equal(a[:, :2], b[:, :2])
+
+
+@pytest.mark.parametrize("k", [-60, 0, 60, 110])
+def test_lse_beside_value_scales_of_any_size(kl, k):
+    """lse does not depend on the value scales but for rounding: 2^-21 of their largest |log2|, beside what a score is off by, the sum's
+    2^-24 a key and 2^-22 of the result."""
+    reqs, Hq, Hkv, bs = [(3, 500), (40, 100), (1, 2000)], 8, 2, 16
+    cache = Cache(5, reqs, Hq, Hkv, bs).codes()
+    cache.vs *= 2.0 ** k * (1 + 0.9 * torch.rand(cache.vs.shape, generator=cache.gen, device="cuda"))
+    o, lse = _attend(kl, cache.cfg(kl), Hq, Hkv, *cache.args)
+    assert kl.kl_device_status() == 0
+    for r, h, want, size, top, codes, dz in cache.exact():
+        b = int(np.searchsorted(cache.cu, r[0], side="right")) - 1
+        p = torch.arange(sum(reqs[b]), device="cuda")
+        page, g = cache.table[b, p // bs], h.start // (Hq // Hkv)
+        keys = cache.kc[page, p % bs, g].double() * cache.ks[page, g].double()[:, None] / math.sqrt(D)
+        z = cache.q[r, h].double() @ keys.T
+        seen = p[None, :] <= torch.tensor([reqs[b][1] + x - int(cache.cu[b]) for x in r], device="cuda")[:, None]
+        exact = torch.logsumexp(z.masked_fill(~seen[:, None, :], -math.inf), -1)
+        tol = dz[..., 0] + 2.0 ** -22 * exact.abs() + len(p) * 2.0 ** -24 + 2.0 ** -21 * cache.vs[page, g].log2().abs().max().double() + 1e-6
+        assert ((lse[r, h].double() - exact).abs() <= tol).all()
